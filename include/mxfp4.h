@@ -402,10 +402,69 @@ mxfp4_status mxfp4_linear_fprop_noalloc(const void* x, const void* w, int64_t M,
 /* Size in bytes of the scratch area used by mxfp4_linear_fprop_noalloc. */
 size_t mxfp4_noalloc_scratch_bytes(void);
 
+/* ------------------------------------------------------------------------------------
+ * The two ends of a training step: the embedding lookup in front of the first linear
+ * layer, the output layer's cross entropy behind the last one, and the clipping of the
+ * gradients that the step leaves.  Numbers here may be any bf16 / fp32 values: infinities
+ * and NaN go through the formulas, except where a token is ignored (its values are then
+ * never read).  Token ids and targets are device arrays; one outside the vocabulary is
+ * treated as ignored and reported by mxfp4_device_status as MXFP4_ERR_INVALID_ARG.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { MXFP4_IDS_I32 = 0, MXFP4_IDS_I64 = 1 } mxfp4_ids_dtype;
+
+/* Embedding lookup y[t, :] = scale * w[ids[t], :], computed in fp32 and rounded once.
+ * ids: device [tokens] (ids_dtype); w: device [vocab, dim] (ldw elements between rows);
+ * y: device [tokens, dim] (ldy).  w_dtype / y_dtype: MXFP4_OUT_F32 or MXFP4_OUT_BF16.
+ * Any dim and pitch; rows of a multiple of 16 bytes are moved as vectors.  An id outside
+ * [0, vocab) gives a row of zeros. */
+mxfp4_status mxfp4_embedding(const void* ids, int ids_dtype, int64_t tokens, const void* w, int w_dtype,
+                             int64_t vocab, int64_t dim, int64_t ldw, float scale, void* y, int y_dtype, int64_t ldy,
+                             mxfp4_stream_t stream);
+
+/* Workspace bytes of mxfp4_embedding_grad. */
+size_t mxfp4_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+
+/* Gradient of mxfp4_embedding's table: dw[v, :] = scale * sum of dy[t, :] over the tokens
+ * with ids[t] == v; added to dw when accumulate is 1, otherwise dw is written whole (rows
+ * of tokens that do not occur become 0).  Tokens whose id is padding_id are left out
+ * (padding_id < 0: none).  The tokens are sorted by id (stable), each row's sum is taken in
+ * fp32 in an order that the ids alone determine, and rounded once: no atomic additions,
+ * the same bits on every run.
+ * dy: device [tokens, dim] (lddy) and dw: device [vocab, dim] (lddw), fp32 or bf16 each.
+ * ws: device, 256-byte aligned, mxfp4_embedding_grad_workspace_bytes bytes. */
+mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int64_t tokens, const void* dy, int dy_dtype,
+                                  int64_t lddy, int64_t vocab, int64_t dim, float scale, int64_t padding_id, void* dw,
+                                  int dw_dtype, int64_t lddw, int accumulate, void* ws, size_t ws_bytes,
+                                  mxfp4_stream_t stream);
+
+/* One gradient of mxfp4_clip_grad_norm. */
+typedef struct {
+    const void* grad; /* device, numel contiguous elements (may be NULL when numel == 0) */
+    void* out;        /* device: the clipped gradient, same dtype; grad itself for in place */
+    int64_t numel;
+    int32_t dtype;    /* MXFP4_OUT_F32 or MXFP4_OUT_BF16 */
+    int32_t reserved; /* 0 */
+} mxfp4_grad;
+
+/* Workspace bytes of mxfp4_clip_grad_norm for n gradients. */
+size_t mxfp4_clip_grad_norm_workspace_bytes(int n);
+
+/* Global 2-norm of n gradients and clipping: norm = sqrt(sum of all squares),
+ * c = min(1, max_norm / (norm + 1e-6)), out = c * grad (fp32 arithmetic, rounded once).
+ * *norm (device fp32) receives the norm before clipping.  Where c == 1, gradients that
+ * are clipped in place are left as they are.  A NaN or infinite norm makes c NaN or 0 and
+ * goes into every output, as the formula says.  The squares are summed in fp32 per thread and
+ * in fp64 across threads, in an order fixed by the sizes.  Any alignment of the element
+ * type; n >= 0.  grads is read on the host during the call.  out must be grad or not
+ * overlap any gradient.  ws: device, 256-byte aligned. */
+mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,
+                                  size_t ws_bytes, mxfp4_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the current device's status word:
  * MXFP4_OK, MXFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last call,
  * or MXFP4_ERR_CUDA if a GEMM kernel found its shared memory misaligned for its tile
- * layout.  In both error cases that kernel returned early and its output is invalid. */
+ * layout.  In both error cases that kernel returned early and its output is invalid.
+ * MXFP4_ERR_INVALID_ARG if a token id or target was outside the vocabulary. */
 mxfp4_status mxfp4_device_status(mxfp4_stream_t stream);
 
 /* Bounded-wait limit in nanoseconds for kernels launched afterwards by this host

@@ -6,6 +6,7 @@ and events.  If the library is missing, every call raises -- there is no fallbac
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -24,6 +25,7 @@ SCALE_FLOOR, SCALE_CEIL = 0, 1
 LAYOUT_ROW, LAYOUT_COLT, LAYOUT_2D = 1, 2, 4
 OUT_F32, OUT_BF16 = 0, 1
 SF_PLAIN, SF_MMA = 0, 1
+IDS_I32, IDS_I64 = 0, 1
 OP_FPROP, OP_DGRAD, OP_WGRAD, OP_BACKWARD = 0, 1, 2, 3
 
 STATUS = {0: "MXFP4_OK", 1: "MXFP4_ERR_INVALID_ARG", 2: "MXFP4_ERR_UNSUPPORTED_SHAPE", 3: "MXFP4_ERR_MISALIGNED",
@@ -80,6 +82,7 @@ def lib():
                                    "g.build()'` (there is no CPU fallback)")
             L = ctypes.CDLL(LIB_PATH)
             P, I64, I, U, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+            F = ctypes.c_float
             T = ctypes.POINTER(MxTensorC)
             CF = ctypes.POINTER(MxConfigC)
             sig = {
@@ -105,6 +108,11 @@ def lib():
                 "mxfp4_noalloc_scratch_bytes": ([], S),
                 "mxfp4_error_decomposition": ([P, I64, I64, I64, I, I, P, P], I),
                 "mxfp4_mma_peak_probe": ([I, I64, ctypes.POINTER(ctypes.c_double)], I),
+                "mxfp4_embedding": ([P, I, I64, P, I, I64, I64, I64, F, P, I, I64, P], I),
+                "mxfp4_embedding_grad_workspace_bytes": ([I64, I64, I64], S),
+                "mxfp4_embedding_grad": ([P, I, I64, P, I, I64, I64, I64, F, I64, P, I, I64, I, P, S, P], I),
+                "mxfp4_clip_grad_norm_workspace_bytes": ([I], S),
+                "mxfp4_clip_grad_norm": ([P, I, F, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
                 "mxfp4_set_wait_limit_ns": ([ctypes.c_uint64], None),
                 "mxfp4_test_inject_gemm_fault": ([I], None),
@@ -523,6 +531,117 @@ def linear_backward(dy: torch.Tensor, wT: QTensor, xT: QTensor, cfg: Config, dx:
     _check(lib().mxfp4_linear_backward(_ptr(dy), ctypes.byref(cw), ctypes.byref(cx), M, N, K, ctypes.byref(c),
                                        _ptr(dx), _ptr(dw), _ptr(buf), nb, _stream(stream)))
     return dx, dw
+
+
+# ----------------------------------------------------------------- the ends of a training step
+_FLOAT_OF = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16}
+_OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_IDS_OF = {torch.int32: IDS_I32, torch.int64: IDS_I64}
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream` (None: the current one): the allocator ties a block's
+    reuse to the stream it was allocated on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _float_matrix(x: torch.Tensor, name: str) -> int:
+    """Checks a CUDA fp32 / bf16 matrix with unit column stride; returns its leading dimension."""
+    if x.dtype not in _OUT_OF or not x.is_cuda or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA fp32 or bf16 matrix with unit column stride")
+    # a row count of one or less leaves the row stride without meaning
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _token_ids(ids: torch.Tensor, name: str) -> int:
+    if ids.dtype not in _IDS_OF or not ids.is_cuda or not ids.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 or int64 tensor")
+    return _IDS_OF[ids.dtype]
+
+
+def _given(out: torch.Tensor, shape, dtype, name: str) -> int:
+    """Checks a caller's output matrix; returns its leading dimension."""
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} of {dtype}")
+    return _float_matrix(out, name)
+
+
+def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, out_dtype: int | None = None,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """mxfp4_embedding: scale * w[ids] for a table w [vocab, dim] (fp32 or bf16) and ids of any
+    shape; returns [*ids.shape, dim] in out_dtype (default: w's).  `out`, if given, is a
+    matrix [ids.numel(), dim]."""
+    kind = _token_ids(ids, "ids")
+    ldw = _float_matrix(w, "w")
+    vocab, dim = w.shape
+    w_kind = _OUT_OF[w.dtype]
+    if out_dtype is None:
+        out_dtype = w_kind
+    n = ids.numel()
+    if out is None:
+        y, ldy = _empty((*ids.shape, dim), _FLOAT_OF[out_dtype], w.device, stream), dim
+    else:
+        y, ldy = out, _given(out, (n, dim), _FLOAT_OF[out_dtype], "out")
+    _check(lib().mxfp4_embedding(ids.data_ptr(), kind, n, w.data_ptr(), w_kind, vocab, dim, ldw, scale, y.data_ptr(),
+                                 out_dtype, ldy, _stream(stream)))
+    return y
+
+
+def embedding_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float = 1.0, padding_id: int = -1,
+                   out_dtype: int | None = None, accumulate: bool = False, dw: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """mxfp4_embedding_grad: the table's gradient [vocab, dim] from dy [ids.numel(), dim] (fp32 or
+    bf16), in out_dtype (default: dw's type if given, else dy's).  accumulate adds to dw, which
+    must then be given; tokens with padding_id are left out."""
+    kind = _token_ids(ids, "ids")
+    lddy = _float_matrix(dy, "dy")
+    n, dim = dy.shape
+    if ids.numel() != n:
+        raise ValueError(f"dy has {n} rows for {ids.numel()} ids")
+    if out_dtype is None:
+        out_dtype = _OUT_OF[dw.dtype if dw is not None and dw.dtype in _OUT_OF else dy.dtype]
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw, lddw = _empty((vocab, dim), _FLOAT_OF[out_dtype], dy.device, stream), dim
+    else:
+        lddw = _given(dw, (vocab, dim), _FLOAT_OF[out_dtype], "dw")
+    L = lib()
+    nb = L.mxfp4_embedding_grad_workspace_bytes(n, vocab, dim)
+    ws = _empty(nb, torch.uint8, dy.device, stream)
+    _check(L.mxfp4_embedding_grad(ids.data_ptr(), kind, n, dy.data_ptr(), _OUT_OF[dy.dtype], lddy, vocab, dim, scale,
+                                  padding_id, dw.data_ptr(), out_dtype, lddw, int(accumulate), ws.data_ptr(), nb,
+                                  _stream(stream)))
+    return dw
+
+
+def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
+    """mxfp4_clip_grad_norm over a sequence of contiguous CUDA fp32 / bf16 tensors: clips them in
+    place, or into `outs` (same shapes and types; gradients left as they are).  Returns the
+    norm before clipping as a 1-element fp32 CUDA tensor."""
+    outs = grads if outs is None else outs
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
+    flat = []
+    for g, o in zip(grads, outs):
+        kind = _OUT_OF.get(g.dtype)
+        if kind is None or not g.is_cuda or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
+            raise ValueError("outs must be contiguous CUDA tensors of their gradients' shapes and types")
+        flat += (g.data_ptr(), o.data_ptr(), g.numel(), kind)  # an mxfp4_grad: two pointers, numel, (dtype, 0)
+    table = array.array("q", flat)
+    device = grads[0].device if flat else torch.device("cuda", torch.cuda.current_device())
+    L = lib()
+    nb = L.mxfp4_clip_grad_norm_workspace_bytes(len(grads))
+    norm = _empty(1, torch.float32, device, stream)
+    ws = _empty(nb, torch.uint8, device, stream)
+    _check(L.mxfp4_clip_grad_norm(table.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), nb,
+                                  _stream(stream)))
+    return norm
 
 
 DECOMP_KEYS = ("e2", "scale2", "dz2", "grid2", "scale_grid", "n_deadzone", "n")

@@ -1,0 +1,609 @@
+// embedding.cu -- embedding lookup with scaling, and the table's gradient by sorted tokens.
+//
+//   y[t, :]  = s * w[id_t, :]
+//   dw[v, :] (+)= s * sum over { t : id_t = v } of dy[t, :]      (fp32, t in a fixed order)
+//
+// Both only move data: the lookup reads and writes tokens x dim elements, the gradient reads
+// them once and writes the table (or reads and writes the rows that occur, when it adds to
+// the table).  HBM bandwidth bounds every long call, launch latency the short ones.
+//
+// The gradient is three launches.
+//   1. Sort.  One cluster of eight CTAs sorts (id, token) pairs by id, stably, with a
+//      least-significant-digit radix sort of 9 bits a pass (two passes up to 262143 ids): each
+//      warp owns a contiguous run of tokens and counts its digits with match.any, so that the
+//      order within a digit is the order of the tokens.  The other clusters of the launch
+//      meanwhile clear the table with bulk copies of a zeroed shared-memory buffer.
+//   2. Sum.  The sorted tokens are cut into chunks of kChunk.  A CTA owns one chunk and one slab
+//      of columns and adds its rows up in registers; a row of the table whose tokens all lie in
+//      the chunk is finished there.  A run that crosses a chunk's border leaves an fp32 partial
+//      sum, so a very frequent token is shared out over many CTAs.
+//   3. Join.  Where a crossing run starts, its partial sums are added in chunk order.
+// Which additions are made in which order depends on the ids alone, never on timing.
+#include <algorithm>
+
+#include "element.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// ---------------------------------------------------------------- lookup
+constexpr int kLookupThreads = 256;
+constexpr int kLookupUnits = 4;  // units (8 elements, or one) in flight per lane
+
+// One warp per row segment of 32 * kLookupUnits units.
+template <class W, class Y, bool VEC>
+__global__ void __launch_bounds__(kLookupThreads)
+    lookup_kernel(const void* ids, int is64, int64_t tokens, const W* w, int64_t vocab, int64_t dim, int64_t ldw,
+                  float scale, Y* y, int64_t ldy, uint32_t segs, uint32_t* status) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t wid = (int64_t)blockIdx.x * (kLookupThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = wid / segs;
+    if (t >= tokens) return;
+    const int64_t seg = wid - t * segs;
+    const int64_t id = load_id(ids, is64, t);
+    const bool good = id >= 0 && id < vocab;
+    if (!good && seg == 0 && lane == 0) atomicOr(status, kStatusBadIndex);
+    const W* src = w + (good ? id : 0) * ldw;
+    Y* dst = y + t * ldy;
+    constexpr int U = VEC ? 8 : 1;
+    const int64_t units = VEC ? dim / 8 : dim;
+    const int64_t u0 = seg * (32 * kLookupUnits) + lane;
+    if constexpr (VEC) {
+        Raw8<W> r[kLookupUnits];
+#pragma unroll
+        for (int i = 0; i < kLookupUnits; ++i)
+            if (good && u0 + i * 32 < units) r[i] = load8(src + (u0 + i * 32) * U);
+#pragma unroll
+        for (int i = 0; i < kLookupUnits; ++i) {
+            if (u0 + i * 32 >= units) break;
+            float v[8] = {};
+            if (good) {
+                unpack8(r[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= scale;
+            }
+            store8(dst + (u0 + i * 32) * U, v);
+        }
+    } else {
+        float v[kLookupUnits];
+#pragma unroll
+        for (int i = 0; i < kLookupUnits; ++i) v[i] = good && u0 + i * 32 < units ? load1(src + u0 + i * 32) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kLookupUnits; ++i)
+            if (u0 + i * 32 < units) store1(dst + u0 + i * 32, good ? v[i] * scale : 0.f);
+    }
+}
+
+// ---------------------------------------------------------------- sort (and clear)
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCtas = 8;  // the portable cluster size
+constexpr int kBits = 9;
+constexpr int kBins = 1 << kBits;
+// counters [warp][bin], this CTA's bin totals, the cluster-wide offsets, scan scratch
+constexpr int kSortSmem = (kSortWarps * kBins + 2 * kBins + 32) * 4;
+constexpr uint32_t kClearBytes = 32 * 1024;  // zeroed buffer of a clearing CTA (inside the same shared memory)
+static_assert(kClearBytes <= kSortSmem, "shared memory");
+
+struct SortParams {
+    const void* ids;
+    int32_t is64;
+    int32_t passes;
+    uint32_t tokens;
+    int64_t vocab, padding_id;
+    uint2* buf[2];  // (key, token); the last pass writes buf[0]
+    uint32_t* status;
+    // clearing: rows of row_bytes, pitch_bytes apart
+    uint8_t* dw;
+    int64_t rows, row_bytes, pitch_bytes;
+    int32_t clear_vec;  // 16-byte aligned rows
+};
+
+// The key that a token sorts by: its id, or `vocab` (behind every row) when it is left out.
+__device__ __forceinline__ uint32_t token_key(const SortParams& p, uint32_t t) {
+    const int64_t id = load_id(p.ids, p.is64, t);
+    if (id == p.padding_id && id >= 0) return (uint32_t)p.vocab;
+    if (id < 0 || id >= p.vocab) {
+        atomicOr(p.status, kStatusBadIndex);
+        return (uint32_t)p.vocab;
+    }
+    return (uint32_t)id;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
+    uint32_t* count = smem;                       // [kSortWarps][kBins]
+    uint32_t* total = count + kSortWarps * kBins;  // [kBins]
+    uint32_t* base = total + kBins;                // [kBins]
+    uint32_t* wsum = base + kBins;                 // [32]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank();
+    // contiguous run of tokens of this warp, a multiple of 32 long
+    const uint32_t per_warp = ((p.tokens + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
+    const uint64_t first = (uint64_t)(rank * kSortWarps + warp) * per_warp;
+    const uint32_t begin = (uint32_t)(first < p.tokens ? first : p.tokens);
+    const uint32_t end = (uint32_t)(first + per_warp < p.tokens ? first + per_warp : p.tokens);
+    uint32_t* mine = count + warp * kBins;
+
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * kBits;
+        const uint2* in = p.buf[(p.passes - pass) & 1];
+        uint2* out = p.buf[(p.passes - pass - 1) & 1];
+        for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) count[i] = 0;
+        __syncthreads();
+        for (uint32_t t0 = begin; t0 < end; t0 += 32) {
+            const uint32_t t = t0 + lane;
+            const bool on = t < end;
+            const uint32_t mask = __ballot_sync(0xffffffffu, on);
+            if (on) {
+                const uint32_t key = pass == 0 ? token_key(p, t) : __ldcg(&in[t]).x;
+                const uint32_t d = (key >> shift) & (kBins - 1);
+                const uint32_t peers = __match_any_sync(mask, d);
+                if ((peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+            }
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < kBins) {  // exclusive over the warps of this CTA
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = count[w * kBins + tid];
+                count[w * kBins + tid] = run;
+                run += c;
+            }
+            total[tid] = run;
+        }
+        cluster_sync();
+        uint32_t before = 0, all = 0;
+        if (tid < kBins) {
+            const uint32_t a = smem_u32(total + tid);
+            uint32_t c[kSortCtas];
+#pragma unroll
+            for (int r = 0; r < kSortCtas; ++r) c[r] = ld_cluster_u32(mapa_shared(a, r));
+#pragma unroll
+            for (int r = 0; r < kSortCtas; ++r) {
+                before += r < (int)rank ? c[r] : 0u;
+                all += c[r];
+            }
+        }
+        // exclusive scan of `all` over the bins (16 warps of 32 bins)
+        uint32_t inc = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += n;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        if (tid < kBins) {
+            uint32_t lower = 0;
+            for (int w = 0; w < warp; ++w) lower += wsum[w];
+            base[tid] = lower + inc - all + before;
+        }
+        __syncthreads();
+        for (uint32_t t0 = begin; t0 < end; t0 += 32) {
+            const uint32_t t = t0 + lane;
+            const bool on = t < end;
+            const uint32_t mask = __ballot_sync(0xffffffffu, on);
+            uint32_t d = 0, peers = 0, at = 0;
+            if (on) {
+                const uint2 kv = pass == 0 ? make_uint2(token_key(p, t), t) : __ldcg(&in[t]);
+                d = (kv.x >> shift) & (kBins - 1);
+                peers = __match_any_sync(mask, d);
+                at = base[d] + mine[d] + __popc(peers & ((1u << lane) - 1));
+                out[at] = kv;
+            }
+            __syncwarp();
+            if (on && (peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+            __syncwarp();
+        }
+        // The pass's output is visible to the whole cluster, and no CTA's totals are still
+        // being read, before the next pass starts.
+        cluster_sync();
+    }
+}
+
+// Zeroes the table from CTA `part` of `parts`.
+__device__ void clear_table(const SortParams& p, uint32_t part, uint32_t parts, uint32_t* smem) {
+    const int tid = threadIdx.x;
+    if (!p.clear_vec) {  // rows that are not 16-byte aligned: two-byte stores (every element is a multiple of two)
+        for (int64_t r = part; r < p.rows; r += parts) {
+            uint16_t* row = reinterpret_cast<uint16_t*>(p.dw + r * p.pitch_bytes);
+            for (int64_t i = tid; i < p.row_bytes / 2; i += kSortThreads) row[i] = 0;
+        }
+        return;
+    }
+    for (uint32_t i = tid; i < kClearBytes / 16; i += kSortThreads)
+        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        if (p.pitch_bytes == p.row_bytes) {
+            const int64_t all = p.rows * p.row_bytes, bytes = all & ~int64_t(15);
+            if (part == 0)  // the last bytes of a table that does not fill 16
+                for (int64_t o = bytes; o < all; o += 2) *reinterpret_cast<uint16_t*>(p.dw + o) = 0;
+            for (int64_t o = (int64_t)part * kClearBytes; o < bytes; o += (int64_t)parts * kClearBytes)
+                bulk_store(p.dw + o, smem, (uint32_t)(bytes - o < kClearBytes ? bytes - o : kClearBytes));
+        } else {
+            for (int64_t r = part; r < p.rows; r += parts)
+                for (int64_t o = 0; o < p.row_bytes; o += kClearBytes)
+                    bulk_store(p.dw + r * p.pitch_bytes + o, smem,
+                               (uint32_t)(p.row_bytes - o < kClearBytes ? p.row_bytes - o : kClearBytes));
+        }
+        bulk_commit();
+        bulk_wait_all();
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_clear_kernel(const SortParams p) {
+    extern __shared__ __align__(16) uint32_t smem[];
+    grid_dependency_wait();
+    if (blockIdx.x < kSortCtas)
+        sort_cluster(p, smem);
+    else
+        clear_table(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas, smem);
+}
+
+// ---------------------------------------------------------------- sum and join
+constexpr int kChunk = 32;
+constexpr int kAhead = 8;  // rows loaded before they are added
+constexpr int kSumThreads = 128;
+
+struct SumParams {
+    const uint2* sorted;
+    uint32_t tokens;
+    int64_t vocab, dim, lddy, lddw;
+    float scale;
+    int32_t accumulate;
+    float* part;  // [chunks][2][dim]: a run that came in from the left, a run that goes out to the right
+};
+
+template <class DW>
+__device__ __forceinline__ void finish(DW* dst, float sum, const SumParams& p) {
+    const float v = p.scale * sum;
+    store1(dst, p.accumulate ? load1(dst) + v : v);
+}
+template <class DW>
+__device__ __forceinline__ void finish8(DW* dst, float (&sum)[8], const SumParams& p) {
+    float v[8];
+    if (p.accumulate) {
+        unpack8(load8(dst), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(p.scale, sum[j], v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p.scale * sum[j];
+    }
+    store8(dst, v);
+}
+
+// One chunk of sorted tokens x one slab of columns (8 per thread, or one).
+template <class DY, class DW, bool VEC>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, const DY* dy, DW* dw) {
+    constexpr int U = VEC ? 8 : 1;
+    __shared__ uint2 kv[kChunk + 2];  // with the neighbours' keys on both sides
+    grid_dependency_wait();
+    const uint32_t chunk = blockIdx.x;
+    const uint32_t begin = chunk * kChunk;
+    const uint32_t n = min((uint32_t)kChunk, p.tokens - begin);
+    for (int i = threadIdx.x; i < (int)n + 2; i += kSumThreads) {
+        const int64_t at = (int64_t)begin + i - 1;
+        kv[i] = at >= 0 && at < p.tokens ? p.sorted[at] : make_uint2(0xffffffffu, 0);
+    }
+    __syncthreads();
+    const int64_t col = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * U;
+    if (col >= p.dim || kv[1].x == (uint32_t)p.vocab) return;
+
+    float acc[U] = {};
+    for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
+        Raw8<DY> raw[VEC ? kAhead : 1];
+        float one[VEC ? 1 : kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const bool on = i0 + a < n && kv[1 + i0 + a].x != (uint32_t)p.vocab;
+            const DY* src = dy + (int64_t)kv[1 + (on ? i0 + a : 0)].y * p.lddy + col;
+            if constexpr (VEC) {
+                if (on) raw[a] = load8(src);
+            } else {
+                if (on) one[a] = load1(src);
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const uint32_t i = i0 + a;
+            if (i >= n || kv[1 + i].x == (uint32_t)p.vocab) break;
+            if constexpr (VEC) {
+                float v[8];
+                unpack8(raw[a], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += v[j];
+            } else {
+                acc[0] += one[a];
+            }
+            const uint32_t key = kv[1 + i].x;
+            const bool last = kv[2 + i].x != key;
+            if (!last && i + 1 < n) continue;  // the run goes on inside the chunk
+            // The run ends here, or the chunk does.  It came in from the left if the chunk's
+            // first key and the one before it are the same.
+            const bool from_left = kv[0].x == key;
+            if (last && !from_left) {
+                if constexpr (VEC)
+                    finish8(dw + (int64_t)key * p.lddw + col, acc, p);
+                else
+                    finish(dw + (int64_t)key * p.lddw + col, acc[0], p);
+            } else {
+                float* to = p.part + ((int64_t)chunk * 2 + (from_left ? 0 : 1)) * p.dim + col;
+                if constexpr (VEC)
+                    store8(to, acc);
+                else
+                    to[0] = acc[0];
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) acc[j] = 0.f;
+        }
+    }
+}
+
+// Joins the run that starts in chunk blockIdx.x and goes out to the right: kJoinGroups
+// groups of lanes take the following chunks in turn, and their sums are added in group order.
+constexpr int kJoinGroups = 8;
+constexpr int kJoinThreads = kJoinGroups * 32;
+
+template <class DW, bool VEC>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, DW* dw) {
+    constexpr int U = VEC ? 4 : 1;
+    __shared__ float part[kJoinGroups][32 * U];
+    __shared__ uint32_t run_end;
+    grid_dependency_wait();
+    const uint32_t chunk = blockIdx.x;
+    const uint32_t last = chunk * kChunk + kChunk - 1;  // the grid has no block for the last chunk
+    const uint32_t key = p.sorted[last].x;
+    if (key == (uint32_t)p.vocab || p.sorted[last + 1].x != key) return;
+    if (chunk > 0 && p.sorted[chunk * kChunk - 1].x == key) return;  // it started further left
+    // the first chunk behind the run: chunks whose first key is `key` hold partial sums of it
+    const uint32_t chunks = (p.tokens + kChunk - 1) / kChunk;
+    if (threadIdx.x == 0) {
+        uint32_t lo = chunk + 1, hi = chunks;  // first key of lo is `key`
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (p.sorted[(uint64_t)mid * kChunk].x == key)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        run_end = hi;
+    }
+    __syncthreads();
+    const uint32_t end = run_end;
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t col = ((int64_t)blockIdx.y * 32 + lane) * U;
+    float acc[U] = {};
+    if (col < p.dim) {
+        // chunk c of the run: slot 1 (going out) where it starts, slot 0 (coming in) after that
+#pragma unroll 4
+        for (uint32_t c = chunk + g; c < end; c += kJoinGroups) {
+            const float* src = p.part + ((int64_t)c * 2 + (c == chunk ? 1 : 0)) * p.dim + col;
+            if constexpr (VEC) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+            } else {
+                acc[0] += src[0];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) part[g][lane * U + j] = acc[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * U; i += kJoinThreads) {
+        const int64_t c = (int64_t)blockIdx.y * 32 * U + i;
+        if (c >= p.dim) break;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kJoinGroups; ++k) sum += part[k][i];
+        finish(dw + (int64_t)key * p.lddw + c, sum, p);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+template <class W, class Y, bool VEC>
+cudaError_t launch_lookup(const void* ids, int is64, int64_t tokens, const void* w, int64_t vocab, int64_t dim,
+                          int64_t ldw, float scale, void* y, int64_t ldy, cudaStream_t s) {
+    const int64_t units = VEC ? dim / 8 : dim;
+    const int64_t segs = (units + 32 * kLookupUnits - 1) / (32 * kLookupUnits);
+    const int64_t blocks = (tokens * segs + kLookupThreads / 32 - 1) / (kLookupThreads / 32);
+    if (blocks > INT32_MAX || segs > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(lookup_kernel<W, Y, VEC>, dim3((unsigned)blocks), dim3(kLookupThreads), 0, s, 1, true, ids,
+                             is64, tokens, static_cast<const W*>(w), vocab, dim, ldw, scale, static_cast<Y*>(y), ldy,
+                             (uint32_t)segs, device_status_ptr());
+}
+
+template <class DY, class DW, bool VEC>
+cudaError_t launch_sum(const SumParams& p, const void* dy, void* dw, cudaStream_t s) {
+    constexpr int per = kSumThreads * (VEC ? 8 : 1);
+    const unsigned chunks = (p.tokens + kChunk - 1) / kChunk;
+    cudaError_t e = launch_overlapped(sum_kernel<DY, DW, VEC>, dim3(chunks, (unsigned)((p.dim + per - 1) / per)),
+                                      dim3(kSumThreads), 0, s, 1, true, p, static_cast<const DY*>(dy),
+                                      static_cast<DW*>(dw));
+    if (e != cudaSuccess || chunks < 2) return e;
+    constexpr int per_join = VEC ? 128 : 32;
+    return launch_overlapped(join_kernel<DW, VEC>, dim3(chunks - 1, (unsigned)((p.dim + per_join - 1) / per_join)),
+                             dim3(kJoinThreads), 0, s, 1, true, p, static_cast<DW*>(dw));
+}
+
+cudaError_t launch_sort(const SortParams& p, bool clear, cudaStream_t s) {
+    static DeviceSlots slots;
+    int sms = 0;
+    cudaError_t e = per_device_setting(slots, &sms, [&](int dev, int* n) {
+        cudaError_t r =
+            cudaFuncSetAttribute(sort_clear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+        return r != cudaSuccess ? r : cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    });
+    if (e != cudaSuccess) return e;
+    // two CTAs fit an SM; the clearing ones cover the device beside the sorting cluster
+    const int64_t clear_ctas = std::min<int64_t>((p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes, 2 * sms);
+    const unsigned clusters = 1 + (clear ? (unsigned)((clear_ctas + kSortCtas - 1) / kSortCtas) : 0u);
+    return launch_overlapped(sort_clear_kernel, dim3(clusters * kSortCtas), dim3(kSortThreads), kSortSmem, s, kSortCtas,
+                             true, p);
+}
+
+bool valid_float(int t) { return t == MXFP4_OUT_F32 || t == MXFP4_OUT_BF16; }
+int64_t esize(int t) { return t == MXFP4_OUT_BF16 ? 2 : 4; }
+bool element_aligned(const void* p, int t) { return reinterpret_cast<uintptr_t>(p) % esize(t) == 0; }
+
+constexpr int64_t kMaxDim = int64_t(1) << 20;  // the slabs of the sum and join grids fit in gridDim.y
+
+int sort_passes(int64_t vocab) {
+    int bits = 1;
+    while ((vocab >> bits) != 0) ++bits;  // keys 0 .. vocab
+    return (bits + kBits - 1) / kBits;
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+size_t sorted_bytes(int64_t tokens) { return up256((size_t)tokens * sizeof(uint2)); }
+
+mxfp4_status check_table(const char* what, int ids_dtype, int64_t tokens, int64_t vocab, int64_t dim) {
+    if (ids_dtype != MXFP4_IDS_I32 && ids_dtype != MXFP4_IDS_I64)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad ids_dtype %d", what, ids_dtype);
+    if (tokens < 0 || vocab < 0 || dim < 0) return record_error(MXFP4_ERR_INVALID_ARG, "%s: negative size", what);
+    if (tokens > INT32_MAX || vocab >= INT32_MAX || dim > kMaxDim)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens and vocab must be below 2^31, dim at most %lld",
+                            what, (long long)kMaxDim);
+    return MXFP4_OK;
+}
+
+// A typed pointer with a leading dimension: non-NULL, aligned to its element, ld >= dim.
+mxfp4_status check_matrix(const char* what, const char* name, const void* p, int dtype, int64_t dim, int64_t ld) {
+    if (!valid_float(dtype)) return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad dtype %d of %s", what, dtype, name);
+    if (!p) return record_error(MXFP4_ERR_INVALID_ARG, "%s: %s is NULL", what, name);
+    if (!element_aligned(p, dtype))
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: %s not aligned to its element type", what, name);
+    if (ld < dim) return record_error(MXFP4_ERR_INVALID_ARG, "%s: leading dimension of %s below dim", what, name);
+    return MXFP4_OK;
+}
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" mxfp4_status mxfp4_embedding(const void* ids, int ids_dtype, int64_t tokens, const void* w, int w_dtype,
+                                        int64_t vocab, int64_t dim, int64_t ldw, float scale, void* y, int y_dtype,
+                                        int64_t ldy, mxfp4_stream_t stream) {
+    const char* what = "embedding";
+    mxfp4_status st = check_table(what, ids_dtype, tokens, vocab, dim);
+    if (st) return st;
+    if (!valid_float(w_dtype) || !valid_float(y_dtype))
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad dtype (%d, %d)", what, w_dtype, y_dtype);
+    if (tokens == 0 || dim == 0) return record_error(MXFP4_OK, "%s", "");
+    if (vocab == 0) return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: an empty table", what);
+    if (!ids) return record_error(MXFP4_ERR_INVALID_ARG, "%s: ids is NULL", what);
+    if (reinterpret_cast<uintptr_t>(ids) % (ids_dtype == MXFP4_IDS_I64 ? 8 : 4))
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: ids not aligned to their type", what);
+    if ((st = check_matrix(what, "w", w, w_dtype, dim, ldw))) return st;
+    if ((st = check_matrix(what, "y", y, y_dtype, dim, ldy))) return st;
+    if ((st = ensure_device())) return st;
+    const bool vec = vector_rows(w, ldw, dim, esize(w_dtype)) && vector_rows(y, ldy, dim, esize(y_dtype));
+    const int is64 = ids_dtype == MXFP4_IDS_I64;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto go = [&](auto wt, auto yt) {
+        using W = decltype(wt);
+        using Y = decltype(yt);
+        return vec ? launch_lookup<W, Y, true>(ids, is64, tokens, w, vocab, dim, ldw, scale, y, ldy, s)
+                   : launch_lookup<W, Y, false>(ids, is64, tokens, w, vocab, dim, ldw, scale, y, ldy, s);
+    };
+    const bool wb = w_dtype == MXFP4_OUT_BF16, yb = y_dtype == MXFP4_OUT_BF16;
+    const cudaError_t e = wb ? (yb ? go(bf16{}, bf16{}) : go(bf16{}, float{})) : (yb ? go(float{}, bf16{}) : go(float{}, float{}));
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return record_error(MXFP4_OK, "%s", "");
+}
+
+extern "C" size_t mxfp4_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
+    if (tokens <= 0 || vocab <= 0 || dim <= 0 || tokens > INT32_MAX || vocab >= INT32_MAX || dim > kMaxDim) return 0;
+    const size_t chunks = (size_t)((tokens + kChunk - 1) / kChunk);
+    return 2 * sorted_bytes(tokens) + up256(chunks * 2 * (size_t)dim * sizeof(float));
+}
+
+extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int64_t tokens, const void* dy,
+                                             int dy_dtype, int64_t lddy, int64_t vocab, int64_t dim, float scale,
+                                             int64_t padding_id, void* dw, int dw_dtype, int64_t lddw, int accumulate,
+                                             void* ws, size_t ws_bytes, mxfp4_stream_t stream) {
+    const char* what = "embedding_grad";
+    mxfp4_status st = check_table(what, ids_dtype, tokens, vocab, dim);
+    if (st) return st;
+    if (!valid_float(dy_dtype) || !valid_float(dw_dtype))
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad dtype (%d, %d)", what, dy_dtype, dw_dtype);
+    if (accumulate != 0 && accumulate != 1)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: accumulate must be 0 or 1", what);
+    if (vocab == 0 || dim == 0) return record_error(MXFP4_OK, "%s", "");
+    if ((st = check_matrix(what, "dw", dw, dw_dtype, dim, lddw))) return st;
+    if (tokens > 0) {
+        if (!ids) return record_error(MXFP4_ERR_INVALID_ARG, "%s: ids is NULL", what);
+        if (reinterpret_cast<uintptr_t>(ids) % (ids_dtype == MXFP4_IDS_I64 ? 8 : 4))
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: ids not aligned to their type", what);
+        if ((st = check_matrix(what, "dy", dy, dy_dtype, dim, lddy))) return st;
+        const size_t need = mxfp4_embedding_grad_workspace_bytes(tokens, vocab, dim);
+        if (!ws || ws_bytes < need)
+            return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, need);
+        if (reinterpret_cast<uintptr_t>(ws) % 256)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: workspace not 256-byte aligned", what);
+    } else if (accumulate) {
+        return record_error(MXFP4_OK, "%s", "");
+    }
+    if ((st = ensure_device())) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t wsz = esize(dw_dtype);
+
+    SortParams sp{};
+    sp.ids = ids;
+    sp.is64 = ids_dtype == MXFP4_IDS_I64;
+    sp.passes = tokens > 0 ? sort_passes(vocab) : 0;
+    sp.tokens = (uint32_t)tokens;
+    sp.vocab = vocab;
+    sp.padding_id = padding_id;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    sp.buf[0] = reinterpret_cast<uint2*>(at);
+    sp.buf[1] = tokens > 0 ? reinterpret_cast<uint2*>(at + sorted_bytes(tokens)) : nullptr;
+    sp.status = device_status_ptr();
+    sp.dw = static_cast<uint8_t*>(dw);
+    sp.rows = vocab;
+    sp.row_bytes = dim * wsz;
+    sp.pitch_bytes = lddw * wsz;
+    // a contiguous table is cleared as one run of bytes, whatever its rows' length
+    sp.clear_vec = reinterpret_cast<uintptr_t>(dw) % 16 == 0 &&
+                   (sp.pitch_bytes == sp.row_bytes || (sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0));
+    cudaError_t e = launch_sort(sp, !accumulate, s);
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s sort launch: %s", what, cudaGetErrorString(e));
+    if (tokens == 0) return record_error(MXFP4_OK, "%s", "");
+
+    SumParams p{};
+    p.sorted = sp.buf[0];
+    p.tokens = (uint32_t)tokens;
+    p.vocab = vocab;
+    p.dim = dim;
+    p.lddy = lddy;
+    p.lddw = lddw;
+    p.scale = scale;
+    p.accumulate = accumulate;
+    p.part = reinterpret_cast<float*>(at + 2 * sorted_bytes(tokens));
+    const bool vec = vector_rows(dy, lddy, dim, esize(dy_dtype)) && vector_rows(dw, lddw, dim, wsz);
+    auto go = [&](auto yt, auto wt) {
+        using DY = decltype(yt);
+        using DW = decltype(wt);
+        return vec ? launch_sum<DY, DW, true>(p, dy, dw, s) : launch_sum<DY, DW, false>(p, dy, dw, s);
+    };
+    const bool yb = dy_dtype == MXFP4_OUT_BF16, wb = dw_dtype == MXFP4_OUT_BF16;
+    e = yb ? (wb ? go(bf16{}, bf16{}) : go(bf16{}, float{})) : (wb ? go(float{}, bf16{}) : go(float{}, float{}));
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return record_error(MXFP4_OK, "%s", "");
+}

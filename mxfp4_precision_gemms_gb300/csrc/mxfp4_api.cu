@@ -144,6 +144,13 @@ mxfp4_status record_error(mxfp4_status st, const char* fmt, ...) {
     return st;
 }
 
+mxfp4_status ensure_device() {
+    int dev;
+    return check_device(&dev);
+}
+
+uint64_t wait_limit_ns() { return wait_limit(); }
+
 uint32_t* device_status_ptr() {
     int dev = 0;
     cudaGetDevice(&dev);
@@ -177,6 +184,20 @@ bool encode_out_map(CUtensorMap* map, void* c, int64_t rows, int64_t cols, int64
     return (t_encode_result = f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c, dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)) == CUDA_SUCCESS;
+}
+
+bool encode_bf16_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, uint32_t box_cols,
+                     uint32_t box_rows) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return (t_encode_result = f(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)) ==
+           CUDA_SUCCESS;
 }
 
 // 2D tensor map over MMA-order scale factors of a [rows, cols] operand, viewed as
@@ -311,6 +332,8 @@ mxfp4_status mxfp4_device_status(mxfp4_stream_t stream) {
     if (word & kStatusSmemLayout)
         return fail(MXFP4_ERR_CUDA, "a kernel's shared memory was not 1024-byte aligned; it returned early (status 0x%x)",
                     word);
+    if (word & kStatusBadIndex)
+        return fail(MXFP4_ERR_INVALID_ARG, "a token id or target was outside the vocabulary (status 0x%x)", word);
     return ok();
 }
 

@@ -14,6 +14,8 @@ constexpr uint32_t kStatusTimeout = 1u;
 // A kernel found its dynamic shared memory misaligned for its layout and returned
 // without touching memory.
 constexpr uint32_t kStatusSmemLayout = 2u;
+// A token id or target outside the vocabulary (and not the ignored / padding one).
+constexpr uint32_t kStatusBadIndex = 4u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -119,6 +121,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
     asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                  "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+// SMEM -> global copy of `bytes` (both addresses 16-byte aligned, bytes a multiple of 16);
+// completion is tracked with bulk groups of the issuing thread.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+                 "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }

@@ -1,0 +1,95 @@
+"""Refusals of the embedding, cross-entropy and clipping entry points that need no GPU: every argument
+is checked on the host before the device is touched."""
+import array
+import ctypes
+
+import pytest
+
+import __graft_entry__
+from mxfp4_precision_gemms_gb300 import binding as mx
+
+P = ctypes.c_void_p
+INVALID, SHAPE, MISALIGNED, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    __graft_entry__.build()
+    return mx.lib()
+
+
+def _lookup(L, **kw):
+    a = dict(ids=0x1000, it=1, n=4, w=0x2000, wt=1, vocab=10, dim=8, ldw=8, scale=1.0, y=0x3000, yt=1, ldy=8)
+    a.update(kw)
+    return L.mxfp4_embedding(P(a["ids"]), a["it"], a["n"], P(a["w"]), a["wt"], a["vocab"], a["dim"], a["ldw"],
+                             a["scale"], P(a["y"]), a["yt"], a["ldy"], None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(it=2), INVALID), (dict(wt=2), INVALID), (dict(yt=-1), INVALID), (dict(n=-1), INVALID),
+    (dict(vocab=-1), INVALID), (dict(dim=-1), INVALID), (dict(ids=None), INVALID), (dict(w=None), INVALID),
+    (dict(y=None), INVALID), (dict(ldw=7), INVALID), (dict(ldy=7), INVALID), (dict(vocab=0), SHAPE),
+    (dict(n=1 << 31), SHAPE), (dict(vocab=(1 << 31) - 1), SHAPE), (dict(dim=(1 << 20) + 1, ldw=1 << 21, ldy=1 << 21), SHAPE),
+    (dict(ids=0x1004), MISALIGNED), (dict(w=0x2001), MISALIGNED), (dict(y=0x3002, yt=0), MISALIGNED),
+    (dict(n=0), 0), (dict(dim=0, ldw=0, ldy=0), 0)])
+def test_embedding_refuses(L, change, want):
+    assert _lookup(L, **change) == want
+    assert (L.mxfp4_last_error() == b"") == (want == 0)
+
+
+def _grad(L, **kw):
+    need = L.mxfp4_embedding_grad_workspace_bytes(4, 10, 8)
+    a = dict(ids=0x1000, it=0, n=4, dy=0x2000, dyt=1, lddy=8, vocab=10, dim=8, pad=-1, dw=0x3000, dwt=0, lddw=8, acc=0,
+             ws=0x4000, wsb=need)
+    a.update(kw)
+    return L.mxfp4_embedding_grad(P(a["ids"]), a["it"], a["n"], P(a["dy"]), a["dyt"], a["lddy"], a["vocab"], a["dim"],
+                                  1.0, a["pad"], P(a["dw"]), a["dwt"], a["lddw"], a["acc"], P(a["ws"]), a["wsb"], None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(it=5), INVALID), (dict(dyt=2), INVALID), (dict(dwt=2), INVALID), (dict(acc=2), INVALID), (dict(n=-1), INVALID),
+    (dict(dw=None), INVALID), (dict(dy=None), INVALID), (dict(ids=None), INVALID), (dict(lddw=7), INVALID),
+    (dict(lddy=7), INVALID), (dict(ws=None), WORKSPACE), (dict(wsb=100), WORKSPACE), (dict(ws=0x4010), MISALIGNED),
+    (dict(dw=0x3002), MISALIGNED), (dict(ids=0x1002), MISALIGNED), (dict(n=0, acc=1), 0), (dict(vocab=0), 0)])
+def test_embedding_grad_refuses(L, change, want):
+    assert _grad(L, **change) == want
+
+
+def test_embedding_grad_workspace(L):
+    f = L.mxfp4_embedding_grad_workspace_bytes
+    assert f(0, 10, 8) == 0 and f(-1, 10, 8) == 0 and f(4, 10, 1 << 21) == 0
+    # two (id, token) arrays and two fp32 rows for each chunk of 32 tokens
+    assert f(8192, 128256, 4096) == 2 * 8192 * 8 + 256 * 2 * 4096 * 4
+
+
+def _clip(L, entries, n=None, max_norm=1.0, norm=0x5000, ws=0x6000, wsb=None):
+    flat = array.array("q", [x for e in entries for x in e])
+    wsb = L.mxfp4_clip_grad_norm_workspace_bytes(len(entries)) if wsb is None else wsb
+    return L.mxfp4_clip_grad_norm(P(flat.buffer_info()[0]) if entries else None, len(entries) if n is None else n,
+                                  max_norm, P(norm), P(ws), wsb, None)
+
+
+@pytest.mark.parametrize("entry,want", [
+    ((0x1000, 0x2000, 8, 2), INVALID), ((0x1000, 0x2000, -1, 0), INVALID), ((0, 0x2000, 8, 0), INVALID),
+    ((0x1000, 0, 8, 0), INVALID), ((0x1000, 0x2000, 8, 1 << 32), INVALID), ((0x1002, 0x2000, 8, 0), MISALIGNED),
+    ((0x1000, 0x2001, 8, 1), MISALIGNED), ((0x1000, 0x2000, 1 << 45, 0), SHAPE)])
+def test_clip_refuses_a_gradient(L, entry, want):
+    assert _clip(L, [(0x1000, 0x1000, 8, 0), entry]) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(n=-1), INVALID), (dict(max_norm=-1.0), INVALID), (dict(max_norm=float("nan")), INVALID),
+    (dict(norm=None), INVALID), (dict(norm=0x5002), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(wsb=8), WORKSPACE),
+    (dict(ws=0x6008), MISALIGNED), (dict(n=1 << 21), SHAPE)])
+def test_clip_refuses(L, change, want):
+    assert _clip(L, [(0x1000, 0x1000, 8, 0)], **change) == want
+
+
+def test_binding_refuses_before_the_library():
+    import torch
+
+    ids, w = torch.zeros(3, dtype=torch.int64), torch.zeros(4, 8)
+    for call in (lambda: mx.embedding(ids, w), lambda: mx.embedding_grad(ids, torch.zeros(3, 8), 4),
+                 lambda: mx.clip_grad_norm([w], 1.0), lambda: mx.clip_grad_norm([w], 1.0, outs=[])):
+        with pytest.raises(ValueError):
+            call()

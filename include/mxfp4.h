@@ -437,6 +437,42 @@ mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int64_t tokens
                                   int dw_dtype, int64_t lddw, int accumulate, void* ws, size_t ws_bytes,
                                   mxfp4_stream_t stream);
 
+/* How the losses of the tokens become one: NONE keeps them, SUM adds them, MEAN divides the
+ * sum by the number of tokens counted (0 when none is). */
+typedef enum { MXFP4_REDUCE_NONE = 0, MXFP4_REDUCE_SUM = 1, MXFP4_REDUCE_MEAN = 2 } mxfp4_reduction;
+
+/* Softmax cross entropy of a linear output layer, without its logits z = h w^T in memory:
+ *   lse[t] = log sum over v of exp(z[t, v]),  loss[t] = lse[t] - z[t, targets[t]].
+ * h: device bf16 [tokens, dim] (ldh); w: device bf16 [vocab, dim] (ldw, 16-byte aligned,
+ * ldw % 8 == 0); dim % 8 == 0, vocab and tokens any.  Products in bf16 on the tensor cores, sums
+ * and softmax statistics in fp32.
+ * targets: device [tokens] (ids_dtype).  A token whose target is ignore_index does not
+ * count: its row of h is not read, its loss and lse are 0.
+ * loss: device fp32, [tokens] for MXFP4_REDUCE_NONE, else [1]; lse: device fp32 [tokens], what
+ * mxfp4_linear_ce_grad takes.
+ * ws: device, 256-byte aligned, mxfp4_linear_ce_workspace_bytes bytes (a copy of the counted
+ * rows of h, and two fp32 statistics for each token and 128 columns of the vocabulary). */
+size_t mxfp4_linear_ce_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t dim, int64_t ldh, const void* w, int64_t vocab,
+                             int64_t ldw, const void* targets, int ids_dtype, int64_t ignore_index, int reduction,
+                             float* loss, float* lse, void* ws, size_t ws_bytes, mxfp4_stream_t stream);
+
+/* Gradients of mxfp4_linear_ce.  With dz[t, v] = g[t] (exp(z[t, v] - lse[t]) - [v == targets[t]])
+ *   dh = dz w  (rows of ignored tokens are 0),  dw = dz^T h  (added to dw when accumulate is 1).
+ * The logits are made again piece by piece of the vocabulary; dz of one piece is held in the
+ * workspace, rounded to bf16 (before the factor that all tokens share).
+ * h, w, targets, ignore_index, reduction, lse: as given to / returned by mxfp4_linear_ce.
+ * dloss: device fp32, the gradient of the loss: [tokens] for MXFP4_REDUCE_NONE, else [1].
+ * dh: device [tokens, dim] (lddh), fp32 or bf16, or NULL.  dw: device [vocab, dim] (lddw,
+ * 16-byte aligned, rows a multiple of 16 bytes), fp32 or bf16, or NULL; accumulate needs fp32.
+ * Sums in fp32 in a fixed order, rounded once: the same bits on every run. */
+size_t mxfp4_linear_ce_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int64_t dim, int64_t ldh, const void* w,
+                                  int64_t vocab, int64_t ldw, const void* targets, int ids_dtype,
+                                  int64_t ignore_index, int reduction, const float* lse, const float* dloss, void* dh,
+                                  int dh_dtype, int64_t lddh, void* dw, int dw_dtype, int64_t lddw, int accumulate,
+                                  void* ws, size_t ws_bytes, mxfp4_stream_t stream);
+
 /* One gradient of mxfp4_clip_grad_norm. */
 typedef struct {
     const void* grad; /* device, numel contiguous elements (may be NULL when numel == 0) */

@@ -26,6 +26,7 @@ LAYOUT_ROW, LAYOUT_COLT, LAYOUT_2D = 1, 2, 4
 OUT_F32, OUT_BF16 = 0, 1
 SF_PLAIN, SF_MMA = 0, 1
 IDS_I32, IDS_I64 = 0, 1
+REDUCE_NONE, REDUCE_SUM, REDUCE_MEAN = 0, 1, 2
 OP_FPROP, OP_DGRAD, OP_WGRAD, OP_BACKWARD = 0, 1, 2, 3
 
 STATUS = {0: "MXFP4_OK", 1: "MXFP4_ERR_INVALID_ARG", 2: "MXFP4_ERR_UNSUPPORTED_SHAPE", 3: "MXFP4_ERR_MISALIGNED",
@@ -111,6 +112,11 @@ def lib():
                 "mxfp4_embedding": ([P, I, I64, P, I, I64, I64, I64, F, P, I, I64, P], I),
                 "mxfp4_embedding_grad_workspace_bytes": ([I64, I64, I64], S),
                 "mxfp4_embedding_grad": ([P, I, I64, P, I, I64, I64, I64, F, I64, P, I, I64, I, P, S, P], I),
+                "mxfp4_linear_ce_workspace_bytes": ([I64, I64, I64], S),
+                "mxfp4_linear_ce": ([P, I64, I64, I64, P, I64, I64, P, I, I64, I, P, P, P, S, P], I),
+                "mxfp4_linear_ce_grad_workspace_bytes": ([I64, I64, I64], S),
+                "mxfp4_linear_ce_grad": ([P, I64, I64, I64, P, I64, I64, P, I, I64, I, P, P, P, I, I64, P, I, I64, I,
+                                          P, S, P], I),
                 "mxfp4_clip_grad_norm_workspace_bytes": ([I], S),
                 "mxfp4_clip_grad_norm": ([P, I, F, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
@@ -616,6 +622,72 @@ def embedding_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float
                                   padding_id, dw.data_ptr(), out_dtype, lddw, int(accumulate), ws.data_ptr(), nb,
                                   _stream(stream)))
     return dw
+
+
+def _ce_operands(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor) -> tuple[int, int, int]:
+    """Checks the operands of the linear cross entropy; returns (ids dtype, ldh, ldw)."""
+    kind = _token_ids(targets, "targets")
+    if h.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise ValueError("h and w must be bf16")
+    ldh, ldw = _float_matrix(h, "h"), _float_matrix(w, "w")
+    if h.shape[1] != w.shape[1] or targets.numel() != h.shape[0]:
+        raise ValueError(f"h {tuple(h.shape)}, w {tuple(w.shape)} and {targets.numel()} targets do not fit together")
+    return kind, ldh, ldw
+
+
+def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+              reduction: int = REDUCE_MEAN, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """mxfp4_linear_ce: softmax cross entropy of the logits h w^T (h [tokens, dim], w [vocab, dim], both
+    bf16) at `targets`, without the logits in memory.  Returns (loss, lse): loss [tokens] for
+    REDUCE_NONE, else [1]; lse [tokens], which linear_ce_grad takes; both fp32."""
+    kind, ldh, ldw = _ce_operands(h, w, targets)
+    (n, dim), vocab = h.shape, w.shape[0]
+    loss = _empty(n if reduction == REDUCE_NONE else 1, torch.float32, h.device, stream)
+    lse = _empty(n, torch.float32, h.device, stream)
+    L = lib()
+    nb = L.mxfp4_linear_ce_workspace_bytes(n, vocab, dim)
+    ws = _empty(nb, torch.uint8, h.device, stream)
+    _check(L.mxfp4_linear_ce(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), kind, ignore_index,
+                             reduction, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb, _stream(stream)))
+    return loss, lse
+
+
+def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
+                   ignore_index: int = -100, reduction: int = REDUCE_MEAN, dh_dtype: int | None = OUT_BF16,
+                   dw_dtype: int | None = OUT_BF16, accumulate: bool = False, dh: torch.Tensor | None = None,
+                   dw: torch.Tensor | None = None, stream=None):
+    """mxfp4_linear_ce_grad: gradients (dh [tokens, dim], dw [vocab, dim]) of linear_ce's loss.  dloss: the
+    loss's gradient, fp32, [tokens] for REDUCE_NONE, else one element.  dh_dtype / dw_dtype None
+    leaves that gradient out (None is returned for it); accumulate adds to dw (fp32, given)."""
+    kind, ldh, ldw = _ce_operands(h, w, targets)
+    (n, dim), vocab = h.shape, w.shape[0]
+    for x, size, name in ((lse, n, "lse"), (dloss, n if reduction == REDUCE_NONE else 1, "dloss")):
+        if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous() or x.numel() != size:
+            raise ValueError(f"{name} must be {size} contiguous fp32 CUDA elements")
+    lddh = lddw = dim
+    if dh_dtype is None:
+        dh = None
+    elif dh is None:
+        dh = _empty((n, dim), _FLOAT_OF[dh_dtype], h.device, stream)
+    else:
+        lddh = _given(dh, (n, dim), _FLOAT_OF[dh_dtype], "dh")
+    if dw_dtype is None:
+        dw = None
+    elif dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw = _empty((vocab, dim), _FLOAT_OF[dw_dtype], h.device, stream)
+    else:
+        lddw = _given(dw, (vocab, dim), _FLOAT_OF[dw_dtype], "dw")
+    L = lib()
+    nb = L.mxfp4_linear_ce_grad_workspace_bytes(n, vocab, dim)
+    ws = _empty(nb, torch.uint8, h.device, stream)
+    _check(L.mxfp4_linear_ce_grad(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), kind,
+                                  ignore_index, reduction, lse.data_ptr(), dloss.data_ptr(),
+                                  None if dh is None else dh.data_ptr(), dh_dtype or 0, lddh,
+                                  None if dw is None else dw.data_ptr(), dw_dtype or 0, lddw, int(accumulate),
+                                  ws.data_ptr(), nb, _stream(stream)))
+    return dh, dw
 
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:

@@ -1,0 +1,1109 @@
+// linear_ce.cu -- softmax cross entropy of a linear output layer, without its logits in memory,
+// and its gradients.
+//
+//   z = h w^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_{t, y_t}
+//   dz_tv = g_t (exp(z_tv - lse_t) - [v = y_t]),  dh = dz w,  dw = dz^T h
+//
+// Everything of size tokens x vocab lives in tensor memory and registers, except one piece of dz
+// (all tokens x a range of the vocabulary, bf16) between the kernel that makes it and the one
+// that multiplies it.  The forward pass is one matrix product (2 T V D operations), the backward
+// pass three: the logits are made again (the price of not keeping them), and two gradients.
+// All of them are compute-bound for T above a few hundred tokens; for few tokens the read of w (and
+// the write of dw) from HBM bounds them.
+//
+//   gather    copies the counted rows of h together (ignored rows are never read, so what they
+//             hold cannot reach a sum, and cost no multiplication), zero-fills up to a tile's rows
+//   stats     logits tile by tile; each thread reduces 128 columns of one row to (max, sum)
+//   combine   joins the tiles' statistics, writes lse and the losses
+//   dlogits   logits of one piece again -> dz in bf16
+//   products  dh += dz w and dw = dz^T h of that piece, in one launch
+//   scatter   adds up the parts of dh and puts its rows back in the tokens' order
+//
+// The three matrix kernels share one structure, a persistent kernel of CTA pairs with 256 x 256
+// tiles (tcgen05.mma.cta_group::2.kind::f16, K = 64 per stage):
+//   warp 0     TMA producer of this CTA's 128 rows of A and 128 of B, six stages deep
+//   warp 1     allocates TMEM; in the even CTA one thread issues the pair's MMAs
+//   warps 2-9  epilogue of this CTA's 128 rows, two warps per lane quadrant
+// Two accumulators (all 512 columns of TMEM): an epilogue overlaps the next tile's MMAs.
+// Operands lie in shared memory as the tensors lie in HBM, with 128-byte rows along K (h, w, and dz
+// as rows of tokens) or along M / N (w and h as summands, dz for dw): nothing is transposed.
+#include <algorithm>
+
+#include "element.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kTile = 256;    // rows and columns of a pair's tile
+constexpr int kK = 64;        // K per stage: 128 bytes of bf16
+constexpr int kStages = 6;
+constexpr int kOpBytes = 128 * kK * 2;  // one CTA's half of an operand's stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBoxBytes = 32 * 64;  // staging box of a TMA store: 32 rows x 64 bytes, 64-byte swizzle
+constexpr int kBoxes = 2;           // per epilogue warp
+constexpr int kOffA = 0;
+constexpr int kOffB = kOffA + kStages * kOpBytes;
+constexpr int kOffBox = kOffB + kStages * kOpBytes;
+constexpr int kOffBar = kOffBox + kEpiWarps * kBoxes * kBoxBytes;
+constexpr int kNumBars = 2 * kStages + 5;
+constexpr int kOffTmem = kOffBar + kNumBars * 8;
+constexpr int kSmem = kOffTmem + 16;
+constexpr uint32_t kTxPair = 2 * 2 * kOpBytes;
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(2 * kSmem > 228 * 1024, "one CTA per SM: two pairs never compete for TMEM");
+static_assert(kOffBox % 1024 == 0 && kOffBar % 8 == 0, "alignment");
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What the gather kernel leaves for the others.
+struct Header {
+    int32_t count;  // tokens that count
+    float gscale;   // factor that every token's gradient shares
+};
+
+// One matrix product C[M, N] (+)= A[M, K] . B[N, K]^T, or a launch's share of two.
+struct Product {
+    CUtensorMap map_a, map_b, map_c;
+    int32_t a_mn, b_mn;     // the operand's rows in memory run over K, its M / N index is contiguous
+    int32_t m_counted;      // M is the number of counted tokens (rounded up to a tile)
+    int32_t k_counted;      // K is the number of counted tokens
+    int32_t M, N, K;
+    int32_t splits;         // K is cut into this many parts, each with its own output
+    int32_t k_per_split;    // stages of a part
+    int32_t slot_rows;      // rows of C between the parts' outputs
+    int32_t out_bf16, add;  // output type; add to what is there (fp32)
+    int32_t scaled;         // multiply by Header::gscale
+};
+
+struct CeParams {
+    Product prod[2];
+    int32_t count;
+    const Header* header;
+    const int32_t* target;  // [rows] of the counted tokens, relative to nothing: vocabulary index
+    int32_t col0;           // first vocabulary index of this launch's columns
+    int32_t rows;           // pitch of the statistics: padded token count
+    float2* stats;          // [tile * 2 + half][rows]: (max * log2 e, sum of 2^(z log2 e - max))
+    float* target_logit;    // [rows]
+    const float* lse2;      // [rows] lse * log2 e
+    const float* ratio;     // [rows] factor of this token's gradient
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+enum Kind { kStats = 0, kDlogits = 1, kProducts = 2 };
+
+__host__ __device__ inline int32_t pad_rows(int32_t n) { return n <= 0 ? kTile : (n + kTile - 1) / kTile * kTile; }
+
+struct Tile {
+    int prob;
+    int32_t m0, n0, k0, stages, slot;
+};
+
+// Where tile `t` of the launch lies; false past the last one.  Within a product, consecutive
+// tiles (which run at the same time) walk the dimension with fewer tiles first: the operand along
+// it is read in every wave and stays in L2 while the other one streams through once.
+__device__ __forceinline__ bool locate(const CeParams& p, int32_t count, int64_t t, Tile& out) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (i >= p.count) return false;
+        const Product& q = p.prod[i];
+        const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
+        const int32_t num_n = (q.N + kTile - 1) / kTile;
+        const int64_t per = (int64_t)num_m * num_n;
+        if (t < per * q.splits) {
+            const int32_t slot = (int32_t)(t / per);
+            const int32_t lt = (int32_t)(t - slot * per);
+            out.prob = i;
+            out.slot = slot;
+            if (num_n > num_m) {
+                out.m0 = (lt % num_m) * kTile;
+                out.n0 = (lt / num_m) * kTile;
+            } else {
+                out.m0 = (lt / num_n) * kTile;
+                out.n0 = (lt % num_n) * kTile;
+            }
+            const int32_t k = q.k_counted ? max(count, 1) : q.K;
+            const int32_t all = (k + kK - 1) / kK;
+            out.k0 = slot * q.k_per_split;
+            out.stages = q.splits > 1 ? min(q.k_per_split, all - out.k0) : all;
+            return true;
+        }
+        t -= per * q.splits;
+    }
+    return false;
+}
+
+// Lane i writes its row's 64 bytes into a staging box (16-byte piece j of row r at
+// j ^ ((r >> 1) & 3): the 64-byte swizzle, conflict-free).
+__device__ __forceinline__ void write_box(uint8_t* box, int lane, const uint32_t* w) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// A warp's staging boxes, used in turn: a box is written again once the store before the last
+// has read it.
+struct Boxes {
+    uint8_t* base;
+    int turn;
+    __device__ __forceinline__ void store(const CUtensorMap* map, int lane, const uint32_t* w, int32_t x, int32_t y,
+                                          bool inside, bool add) {
+        if (lane == 0) bulk_wait_read<kBoxes - 1>();
+        __syncwarp();
+        uint8_t* box = base + turn * kBoxBytes;
+        turn = turn + 1 == kBoxes ? 0 : turn + 1;
+        write_box(box, lane, w);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (inside) {
+                if (add)
+                    tma_reduce_add_2d(map, box, x, y);
+                else
+                    tma_store_2d(map, box, x, y);
+            }
+            bulk_commit();
+        }
+    }
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_constant__ CeParams p) {
+    extern __shared__ uint8_t smem[];
+    // The swizzled tiles need 1024-byte alignment.  Both CTAs of a pair see the same base, so
+    // both return here, before any cluster barrier.
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemLayout);
+        return;
+    }
+    uint8_t* sA = smem + kOffA;
+    uint8_t* sB = smem + kOffB;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // used in the leader
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;   // [2]
+    uint64_t* acc_empty = acc_full + 2;     // [2], used in the leader: both CTAs' epilogues arrive
+    uint64_t* mma_done = acc_empty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffTmem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t cluster = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        for (int i = 0; i < p.count; ++i) {
+            prefetch_tmap(&p.prod[i].map_a);
+            prefetch_tmap(&p.prod[i].map_b);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    // The set-up above touches no global memory, so it overlaps the previous kernel.
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int32_t count = *reinterpret_cast<const volatile int32_t*>(&p.header->count);
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs)
+        if (elect_one()) {
+            const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+            uint32_t armed[kStages];  // phases issued per stage
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) armed[s] = 0;
+            uint32_t s = 0, round = 0;
+            bool ok = true;
+            Tile t;
+            for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
+                const Product& q = p.prod[t.prob];
+                const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * 128;
+                for (int32_t i = 0; i < t.stages; ++i) {
+                    if (round > 0 && !wait_bounded(&empty[s], (round - 1) & 1u, p.wait_ns, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], kTxPair);
+                    const uint32_t bar = full_leader + s * 8u;
+                    const int32_t k = (t.k0 + i) * kK;
+                    uint8_t* a = sA + s * kOpBytes;
+                    uint8_t* b = sB + s * kOpBytes;
+                    if (q.a_mn) {  // two boxes of 64 rows (K) x 64 columns (M)
+                        tma_load_2d_pair(a, &q.map_a, bar, ya, k);
+                        tma_load_2d_pair(a + kOpBytes / 2, &q.map_a, bar, ya + 64, k);
+                    } else {  // one box of 128 rows (M) x 64 columns (K)
+                        tma_load_2d_pair(a, &q.map_a, bar, k, ya);
+                    }
+                    if (q.b_mn) {
+                        tma_load_2d_pair(b, &q.map_b, bar, yb, k);
+                        tma_load_2d_pair(b + kOpBytes / 2, &q.map_b, bar, yb + 64, k);
+                    } else {
+                        tma_load_2d_pair(b, &q.map_b, bar, k, yb);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kStages; ++j)
+                        if (j == (int)s) armed[j] = round + 1;
+                    if (++s == kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            // Drain: the leader waits until the last armed phase of every stage has landed, both
+            // CTAs until the MMAs have released every stage they were given.
+#pragma unroll
+            for (int j = 0; j < kStages; ++j) {
+                if (!armed[j]) continue;
+                if (rank == 0) wait_bounded(&full[j], (armed[j] - 1u) & 1u, p.wait_ns, p.status);
+                wait_bounded(&empty[j], (armed[j] - 1u) & 1u, p.wait_ns, p.status);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- tensor-core issuer (leader CTA)
+        if (elect_one()) {
+            if (rank == 0) {
+                uint32_t s = 0, phase = 0, tcount = 0;
+                bool ok = true;
+                Tile t;
+                for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters, ++tcount) {
+                    const Product& q = p.prod[t.prob];
+                    const uint32_t idesc = idesc_bf16(256, 256, q.a_mn != 0, q.b_mn != 0);
+                    // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
+                    // Between 64-column blocks of M / N: half a stage's operand.
+                    const uint32_t a_step = q.a_mn ? 2048 : 32, b_step = q.b_mn ? 2048 : 32;
+                    const uint32_t a_lbo = q.a_mn ? kOpBytes / 2 : 16, b_lbo = q.b_mn ? kOpBytes / 2 : 16;
+                    const uint32_t ab = tcount & 1u;
+                    if (tcount >= 2 && !wait_bounded(&acc_empty[ab], ((tcount >> 1) - 1u) & 1u, p.wait_ns, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + ab * 256;
+                    for (int32_t i = 0; i < t.stages; ++i) {
+                        if (!wait_bounded(&full[s], phase, p.wait_ns, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = smem_u32(sA + s * kOpBytes), b = smem_u32(sB + s * kOpBytes);
+#pragma unroll
+                        for (int k = 0; k < kK / 16; ++k)
+                            tc_mma_bf16_pair(d, smem_desc(a + k * a_step, a_lbo, 1024, kSwizzle128B),
+                                             smem_desc(b + k * b_step, b_lbo, 1024, kSwizzle128B), idesc,
+                                             (i | k) != 0);
+                        tc_commit_pair(&empty[s], 0x3);
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) tc_commit_pair(&acc_full[ab], 0x3);
+                }
+                tc_commit_pair(mma_done, 0x3);
+            }
+            // Both CTAs: every MMA of the pair has completed before TMEM is released.
+            wait_bounded(mma_done, 0, p.wait_ns, p.status);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs): this CTA's 128 rows of the tile
+        const int quad = warp & 3;
+        const int half = (warp - 2) >> 2;
+        Boxes boxes{smem + kOffBox + (warp - 2) * kBoxes * kBoxBytes, 0};
+        const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+        const float gscale = KIND == kProducts ? *reinterpret_cast<const volatile float*>(&p.header->gscale) : 1.f;
+        uint32_t tcount = 0;
+        Tile t;
+        for (int64_t tile = cluster; locate(p, count, tile, t); tile += num_clusters, ++tcount) {
+            const Product& q = p.prod[t.prob];
+            const uint32_t ab = tcount & 1u;
+            const int32_t row0 = t.m0 + (int32_t)rank * 128 + quad * 32;
+            const int32_t row = row0 + lane;
+            const int32_t c0 = t.n0 + half * 128;
+            // per-row values first: their latency hides behind the wait for the accumulator
+            int32_t tgt = -1;
+            float lse2 = 0.f, ratio = 0.f;
+            if constexpr (KIND != kProducts) {
+                tgt = __ldcg(p.target + row) - p.col0;
+                if constexpr (KIND == kDlogits) {
+                    lse2 = __ldcg(p.lse2 + row);
+                    ratio = __ldcg(p.ratio + row);
+                }
+            }
+            if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) break;
+            tc_fence_after();
+            const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + ab * 256 + (uint32_t)(half * 128);
+            float m = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(src + c * 32, v);
+                tmem_ld_wait();
+                if (c == 3) {  // the accumulator has been read out; the arrive only reports it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
+                }
+                const int32_t col = c0 + c * 32;
+                if constexpr (KIND == kStats) {
+                    const int32_t left = q.N - col;
+                    if (left < 32) {  // past the vocabulary's end
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= left) v[j] = 0xff800000u;
+                    }
+                    const int32_t hit = tgt - col;
+                    if (hit >= 0 && hit < 32) {
+                        float z = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j == hit) z = __uint_as_float(v[j]);
+                        p.target_logit[row] = z;
+                    }
+                    float top = m;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]) * kLog2e);
+                    // all -inf so far: any finite reference leaves the terms 0
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float s4[4] = {sum * exp2_approx(m - ref), 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        s4[j & 3] += exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
+                    sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    m = top;
+                } else if constexpr (KIND == kDlogits) {
+                    const int32_t hit = tgt - col;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float x[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
+                            x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
+                        }
+                        w[j] = row < count ? pack_bf16(x[0], x[1]) : 0u;
+                    }
+                    boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
+                } else {
+                    const int32_t y = t.slot * q.slot_rows + row0;
+                    const bool in_m = q.m_counted || row0 < q.M;
+                    if (q.scaled) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * gscale);
+                    }
+                    if (q.out_bf16) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        boxes.store(&q.map_c, lane, w, col, y, in_m && col < q.N, false);
+                    } else {
+                        boxes.store(&q.map_c, lane, v, col, y, in_m && col < q.N, q.add);
+                        boxes.store(&q.map_c, lane, v + 16, col + 16, y, in_m && col + 16 < q.N, q.add);
+                    }
+                }
+            }
+            if constexpr (KIND == kStats) {
+                if (row < count)
+                    p.stats[(int64_t)((t.n0 / kTile) * 2 + half) * p.rows + row] = make_float2(m, sum);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA frees TMEM or exits while the pair may still use it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- gather
+constexpr int kGatherThreads = 512;
+constexpr int kGatherWarps = kGatherThreads / 32;
+
+struct GatherParams {
+    const bf16* h;
+    int64_t ldh;
+    int32_t tokens, dim, vocab;
+    int32_t vec;  // rows of h can be read in 16-byte vectors
+    const void* targets;
+    int32_t is64;
+    int64_t ignore;
+    int32_t reduction;
+    // gradient only
+    const float* lse;
+    const float* dloss;
+    // outputs
+    Header* header;
+    bf16* rows;        // [padded tokens][dim]
+    int32_t* target;   // [padded tokens]
+    int32_t* source;   // [padded tokens]: token of a gathered row
+    int32_t* place;    // [tokens]: gathered row of a token, or -1
+    float* lse2;
+    float* ratio;
+    float* loss;       // forward: zero for ignored tokens
+    float* lse_out;
+    uint32_t* status;
+};
+
+// The target of token t, or -1 when it does not count.
+__device__ __forceinline__ int32_t counted_target(const GatherParams& p, int32_t t, bool report) {
+    const int64_t y = load_id(p.targets, p.is64, t);
+    if (y == p.ignore) return -1;
+    if (y < 0 || y >= p.vocab) {
+        if (report) atomicOr(p.status, kStatusBadIndex);
+        return -1;
+    }
+    return (int32_t)y;
+}
+
+// Each CTA gathers a contiguous range of tokens.  Where its rows go follows from the number of
+// counted tokens in front of them, which it counts by itself: the targets are short beside
+// the rows, and no CTA waits for another.
+template <bool GRAD>
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
+    __shared__ int32_t warp_n[2][kGatherWarps];
+    __shared__ int32_t list_src[kGatherThreads];
+    __shared__ int32_t n_list;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t per = (p.tokens + (int32_t)gridDim.x - 1) / (int32_t)gridDim.x;
+    const int32_t begin = (int32_t)min((int64_t)blockIdx.x * per, (int64_t)p.tokens);
+    const int32_t end = (int32_t)min((int64_t)begin + per, (int64_t)p.tokens);
+
+    int32_t before = 0, total = 0;
+#pragma unroll 4
+    for (int32_t t = tid; t < p.tokens; t += kGatherThreads) {
+        const int32_t on = counted_target(p, t, blockIdx.x == 0) >= 0;
+        total += on;
+        before += t < begin ? on : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) warp_n[0][warp] = before, warp_n[1][warp] = total;
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < kGatherWarps; ++w) before += warp_n[0][w], total += warp_n[1][w];
+
+    if (blockIdx.x == 0 && tid == 0) {
+        p.header->count = total;
+        float g = 1.f;
+        if (GRAD && p.reduction != MXFP4_REDUCE_NONE) {
+            g = p.dloss[0];
+            if (p.reduction == MXFP4_REDUCE_MEAN) g /= (float)max(total, 1);
+        }
+        p.header->gscale = g;
+    }
+
+    const int units = p.dim / 8;
+    for (int32_t t0 = begin; t0 < end; t0 += kGatherThreads) {
+        const int32_t t = t0 + tid;
+        const int32_t y = t < end ? counted_target(p, t, false) : -1;
+        const uint32_t on = __ballot_sync(0xffffffffu, y >= 0);
+        __syncthreads();  // the counts and the list of the round before have been read
+        if (lane == 0) warp_n[0][warp] = __popc(on);
+        __syncthreads();
+        int32_t lower = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kGatherWarps; ++w) {
+            lower += w < warp ? warp_n[0][w] : 0;
+            all += warp_n[0][w];
+        }
+        const int32_t at = lower + __popc(on & ((1u << lane) - 1));
+        if (t < end) {
+            p.place[t] = y >= 0 ? before + at : -1;
+            if (y >= 0) {
+                const int32_t r = before + at;
+                list_src[at] = t;
+                p.target[r] = y;
+                p.source[r] = t;
+                if constexpr (GRAD) {
+                    p.lse2[r] = p.lse[t] * kLog2e;
+                    p.ratio[r] = p.reduction == MXFP4_REDUCE_NONE ? p.dloss[t] : 1.f;
+                }
+            } else if constexpr (!GRAD) {
+                p.lse_out[t] = 0.f;
+                p.loss[t] = 0.f;
+            }
+        }
+        if (tid == 0) n_list = all;
+        __syncthreads();
+        for (int32_t i = warp; i < n_list; i += kGatherWarps) {
+            const bf16* src = p.h + (int64_t)list_src[i] * p.ldh;
+            bf16* dst = p.rows + (int64_t)(before + i) * p.dim;
+            if (p.vec) {
+#pragma unroll 8
+                for (int u = lane; u < units; u += 32)
+                    reinterpret_cast<uint4*>(dst)[u] = reinterpret_cast<const uint4*>(src)[u];
+            } else {
+                for (int c = lane; c < p.dim; c += 32) dst[c] = src[c];
+            }
+        }
+        before += all;
+    }
+    // rows up to the end of the last tile: zeros that count for nothing
+    const int32_t padded = pad_rows(total);
+    for (int32_t r = total + (int32_t)blockIdx.x * kGatherWarps + warp; r < padded; r += (int32_t)gridDim.x * kGatherWarps) {
+        bf16* dst = p.rows + (int64_t)r * p.dim;
+        for (int u = lane; u < units; u += 32) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0, 0, 0, 0);
+        if (lane == 0) {
+            p.target[r] = -1;
+            if constexpr (GRAD) p.lse2[r] = 0.f, p.ratio[r] = 0.f;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine
+constexpr int kCombineThreads = 256;
+
+// ROWS rows per CTA, 256 / ROWS threads to each.
+template <int ROWS>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_kernel(const Header* header, const float2* stats, int32_t parts, int32_t rows, const float* target_logit,
+                   const int32_t* source, float* lse_out, float* loss) {
+    constexpr int GROUPS = kCombineThreads / ROWS;
+    __shared__ float2 sh[GROUPS][ROWS];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int32_t count = *reinterpret_cast<const volatile int32_t*>(&header->count);
+    const int r = threadIdx.x % ROWS, g = threadIdx.x / ROWS;
+    const int32_t row = blockIdx.x * ROWS + r;
+    if ((int32_t)blockIdx.x * ROWS >= count) return;
+    float m = -INFINITY, s = 0.f;
+    auto join = [&](float2 o) {
+        const float top = fmaxf(m, o.x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        s = s * exp2_approx(m - ref) + o.y * exp2_approx(o.x - ref);
+        m = top;
+    };
+    if (row < count) {
+        int32_t i = g;
+        for (; i + 3 * GROUPS < parts; i += 4 * GROUPS) {  // four loads in flight
+            float2 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = __ldcg(&stats[(int64_t)(i + k * GROUPS) * rows + row]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) join(o[k]);
+        }
+        for (; i < parts; i += GROUPS) join(__ldcg(&stats[(int64_t)i * rows + row]));
+    }
+    sh[g][r] = make_float2(m, s);
+    __syncthreads();
+    if (g == 0 && row < count) {
+        for (int k = 1; k < GROUPS; ++k) join(sh[k][r]);
+        const float lse = (m + log2f(s)) * kLn2;
+        const int32_t t = source[row];
+        lse_out[t] = lse;
+        loss[t] = lse - target_logit[row];
+    }
+}
+
+// Sum or mean of the tokens' losses, in one CTA: a fixed order.
+constexpr int kReduceThreads = 1024;
+__global__ void __launch_bounds__(kReduceThreads)
+    reduce_kernel(const Header* header, const float* loss, int32_t tokens, int32_t mean, float* out) {
+    __shared__ float warp_sum[kReduceThreads / 32];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    float s = 0.f;
+#pragma unroll 4
+    for (int32_t t = threadIdx.x; t < tokens; t += kReduceThreads) s += __ldcg(loss + t);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        s = warp_sum[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) out[0] = mean ? s / (float)max(header->count, 1) : s;
+    }
+}
+
+// ---------------------------------------------------------------- scatter
+constexpr int kScatterThreads = 256;
+
+// dh[t] = gscale * sum over the parts of row place[t]; one warp per token and 256 columns.
+template <class DH>
+__global__ void __launch_bounds__(kScatterThreads)
+    scatter_kernel(const Header* header, const int32_t* place, const float* parts, int32_t splits, int64_t slot_elems,
+                   int32_t tokens, int32_t dim, uint32_t segs, DH* dh, int64_t lddh, int32_t vec) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t wid = (int64_t)blockIdx.x * (kScatterThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = wid / segs;
+    const int32_t u = (int32_t)(wid - t * segs) * 32 + (threadIdx.x & 31);
+    if (t >= tokens || u * 8 >= dim) return;
+    const int32_t r = place[t];
+    const float gscale = header->gscale;
+    float v[8] = {};
+    if (r >= 0) {
+        const float* src = parts + (int64_t)r * dim + u * 8;
+        for (int32_t k = 0; k < splits; ++k) {
+            float x[8];
+            unpack8(load8(src + k * slot_elems), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += x[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= gscale;
+    }
+    DH* dst = dh + t * lddh + u * 8;
+    if (vec) {
+        store8(dst, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store1(dst + j, v[j]);
+    }
+}
+
+// ---------------------------------------------------------------- host
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// The dz of one piece: at most this many bytes (or kMinPiece columns), so that a long batch
+// needs no more scratch than a short one.  16384 columns at 8192 tokens: a piece's three products
+// are then long enough that their launches' ends cost little.
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr int32_t kMinPiece = 2048;
+
+int32_t piece_columns(int32_t padded, int64_t vocab) {
+    const int64_t fit = std::max<int64_t>(kMinPiece, (int64_t)(kPieceBytes / (2 * (size_t)padded)) / kTile * kTile);
+    const int64_t pieces = (vocab + fit - 1) / fit;
+    const int64_t even = (vocab + pieces - 1) / pieces;
+    return (int32_t)((even + kTile - 1) / kTile * kTile);
+}
+
+constexpr int kClustersMost = 76;  // pairs of SMs
+
+// Parts that dh's contraction over a piece's columns is cut into.  With fewer tiles than pairs of
+// SMs the parts fill the device; each costs a pass over its fp32 output, written here as four
+// stages of the tile loop.  The number with the shortest schedule is taken, and lowered to the
+// parts that get work; every piece of the vocabulary uses at most as many.
+int32_t split_count(int32_t padded, int64_t dim, int32_t columns) {
+    const int64_t tiles = (int64_t)(padded / kTile) * ((dim + kTile - 1) / kTile);
+    const int32_t stages = (columns + kK - 1) / kK;
+    if (tiles >= kClustersMost) return 1;
+    int32_t best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int32_t s = 1; s <= 16 && s <= stages; ++s) {
+        const int64_t per = (stages + s - 1) / s;
+        const int64_t cost = (tiles * s + kClustersMost - 1) / kClustersMost * (per + 4);
+        if (cost < best_cost) best = s, best_cost = cost;
+    }
+    const int32_t per = (stages + best - 1) / best;
+    return (stages + per - 1) / per;
+}
+
+struct Layout {
+    int32_t padded;
+    size_t header, target, source, place, lse2, ratio, target_logit, token_loss, rows, stats, dz, parts, bytes;
+    int32_t piece, splits;
+};
+
+Layout lay_out(int64_t tokens, int64_t vocab, int64_t dim, bool grad) {
+    Layout l{};
+    l.padded = pad_rows((int32_t)tokens);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    const size_t n = (size_t)l.padded;
+    l.header = take(sizeof(Header));
+    l.target = take(n * 4);
+    l.source = take(n * 4);
+    l.place = take(n * 4);
+    l.rows = take(n * (size_t)dim * 2);
+    if (!grad) {
+        l.target_logit = take(n * 4);
+        l.token_loss = take(n * 4);
+        l.stats = take((size_t)((vocab + kTile - 1) / kTile) * 2 * n * sizeof(float2));
+    } else {
+        l.lse2 = take(n * 4);
+        l.ratio = take(n * 4);
+        l.piece = piece_columns(l.padded, vocab);
+        l.splits = split_count(l.padded, dim, (int32_t)std::min<int64_t>(l.piece, vocab));
+        l.dz = take(n * (size_t)l.piece * 2);
+        l.parts = take((size_t)l.splits * n * (size_t)dim * 4);
+    }
+    l.bytes = at;
+    return l;
+}
+
+bool sizes_fit(int64_t tokens, int64_t vocab, int64_t dim) {
+    return tokens >= 0 && vocab >= 0 && dim >= 0 && tokens <= (1 << 24) && vocab <= (1 << 28) && dim <= (1 << 20);
+}
+
+template <int KIND>
+cudaError_t launch_matrix(const CeParams& p, int64_t tiles, cudaStream_t s) {
+    auto kern = ce_matrix_kernel<KIND>;
+    static DeviceSlots slots;
+    int clusters = 0;
+    cudaError_t e = per_device_setting(slots, &clusters, [&](int dev, int* n) {
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (r != cudaSuccess) return r;
+        int sms = 0;
+        r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (r != cudaSuccess) return r;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t probe = {};
+        probe.gridDim = dim3((unsigned)(sms & ~1));
+        probe.blockDim = dim3(kThreads);
+        probe.dynamicSmemBytes = kSmem;
+        probe.attrs = attr;
+        probe.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(n, kern, &probe);
+    });
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorNotSupported;
+    const int64_t grid = 2 * std::min<int64_t>(tiles, clusters);
+    return launch_overlapped(kern, dim3((unsigned)grid), dim3(kThreads), kSmem, s, 2, true, p);
+}
+
+int64_t tiles_of(int64_t m, int64_t n) { return ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile); }
+
+cudaError_t gather_grid(int64_t tokens, int* grid) {
+    static DeviceSlots slots;
+    int sms = 0;
+    cudaError_t e = per_device_setting(
+        slots, &sms, [&](int dev, int* n) { return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev); });
+    *grid = (int)std::min<int64_t>(2 * sms, std::max<int64_t>(1, (tokens + 7) / 8));
+    return e;
+}
+
+// Checks what the two calls share.  *empty: there is no token or no element.
+mxfp4_status check_common(const char* what, const void* h, int64_t tokens, int64_t dim, int64_t ldh, const void* w,
+                          int64_t vocab, int64_t ldw, const void* targets, int ids_dtype, int reduction) {
+    if (tokens < 0 || vocab < 0 || dim < 0) return record_error(MXFP4_ERR_INVALID_ARG, "%s: negative size", what);
+    if (ids_dtype != MXFP4_IDS_I32 && ids_dtype != MXFP4_IDS_I64)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad ids_dtype %d", what, ids_dtype);
+    if (reduction < MXFP4_REDUCE_NONE || reduction > MXFP4_REDUCE_MEAN)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad reduction %d", what, reduction);
+    if (vocab == 0 || dim == 0)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: vocab and dim must be positive", what);
+    if (dim % 8) return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: dim (%lld) %% 8 != 0", what, (long long)dim);
+    if (!sizes_fit(tokens, vocab, dim))
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tokens, 2^28 ids or 2^20 columns", what);
+    if (!w) return record_error(MXFP4_ERR_INVALID_ARG, "%s: w is NULL", what);
+    if (reinterpret_cast<uintptr_t>(w) % 16 || ldw % 8)
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: w must be 16-byte aligned with ldw %% 8 == 0", what);
+    if (ldw < dim) return record_error(MXFP4_ERR_INVALID_ARG, "%s: ldw below dim", what);
+    if (tokens == 0) return MXFP4_OK;
+    if (!h || !targets) return record_error(MXFP4_ERR_INVALID_ARG, "%s: h or targets is NULL", what);
+    if (ldh < dim) return record_error(MXFP4_ERR_INVALID_ARG, "%s: ldh below dim", what);
+    if (reinterpret_cast<uintptr_t>(h) % 2 ||
+        reinterpret_cast<uintptr_t>(targets) % (ids_dtype == MXFP4_IDS_I64 ? 8 : 4))
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: h or targets not aligned to its type", what);
+    return MXFP4_OK;
+}
+
+mxfp4_status check_ws(const char* what, const void* ws, size_t have, size_t need) {
+    if (!ws || have < need) return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, need);
+    if (reinterpret_cast<uintptr_t>(ws) % 256)
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: workspace not 256-byte aligned", what);
+    return MXFP4_OK;
+}
+
+mxfp4_status launch_failed(const char* what, const char* step, cudaError_t e) {
+    return record_error(MXFP4_ERR_CUDA, "%s: %s: %s", what, step, cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" size_t mxfp4_linear_ce_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
+    if (tokens <= 0 || vocab <= 0 || dim <= 0 || !sizes_fit(tokens, vocab, dim)) return 0;
+    return lay_out(tokens, vocab, dim, false).bytes;
+}
+
+extern "C" size_t mxfp4_linear_ce_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
+    if (tokens <= 0 || vocab <= 0 || dim <= 0 || !sizes_fit(tokens, vocab, dim)) return 0;
+    return lay_out(tokens, vocab, dim, true).bytes;
+}
+
+extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t dim, int64_t ldh, const void* w,
+                                        int64_t vocab, int64_t ldw, const void* targets, int ids_dtype,
+                                        int64_t ignore_index, int reduction, float* loss, float* lse, void* ws,
+                                        size_t ws_bytes, mxfp4_stream_t stream) {
+    const char* what = "linear_ce";
+    mxfp4_status st = check_common(what, h, tokens, dim, ldh, w, vocab, ldw, targets, ids_dtype, reduction);
+    if (st) return st;
+    const bool reduced = reduction != MXFP4_REDUCE_NONE;
+    if (tokens > 0 || reduced) {
+        if (!loss || (tokens > 0 && !lse)) return record_error(MXFP4_ERR_INVALID_ARG, "%s: loss or lse is NULL", what);
+        if ((reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(lse)) % 4)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: loss or lse misaligned", what);
+    }
+    if (tokens > 0 && (st = check_ws(what, ws, ws_bytes, mxfp4_linear_ce_workspace_bytes(tokens, vocab, dim)))) return st;
+    if (tokens == 0 && !reduced) return record_error(MXFP4_OK, "%s", "");
+    if ((st = ensure_device())) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        const cudaError_t e = cudaMemsetAsync(loss, 0, sizeof(float), s);
+        return e != cudaSuccess ? launch_failed(what, "clear", e) : record_error(MXFP4_OK, "%s", "");
+    }
+    const Layout l = lay_out(tokens, vocab, dim, false);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    float* token_loss = reduced ? reinterpret_cast<float*>(base + l.token_loss) : loss;
+
+    GatherParams g{};
+    g.h = static_cast<const bf16*>(h);
+    g.ldh = ldh;
+    g.tokens = (int32_t)tokens;
+    g.dim = (int32_t)dim;
+    g.vocab = (int32_t)vocab;
+    g.vec = vector_rows(h, ldh, dim, 2);
+    g.targets = targets;
+    g.is64 = ids_dtype == MXFP4_IDS_I64;
+    g.ignore = ignore_index;
+    g.reduction = reduction;
+    g.header = reinterpret_cast<Header*>(base + l.header);
+    g.rows = reinterpret_cast<bf16*>(base + l.rows);
+    g.target = reinterpret_cast<int32_t*>(base + l.target);
+    g.source = reinterpret_cast<int32_t*>(base + l.source);
+    g.place = reinterpret_cast<int32_t*>(base + l.place);
+    g.loss = token_loss;
+    g.lse_out = lse;
+    g.status = device_status_ptr();
+
+    CeParams p{};
+    Product& q = p.prod[0];
+    if (!encode_bf16_map(&q.map_a, g.rows, l.padded, dim, dim, kK, 128) ||
+        !encode_bf16_map(&q.map_b, w, vocab, dim, ldw, kK, 128))
+        return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+    q.m_counted = 1;
+    q.M = l.padded;
+    q.N = (int32_t)vocab;
+    q.K = (int32_t)dim;
+    q.splits = 1;
+    p.count = 1;
+    p.header = g.header;
+    p.target = g.target;
+    p.rows = l.padded;
+    p.stats = reinterpret_cast<float2*>(base + l.stats);
+    p.target_logit = reinterpret_cast<float*>(base + l.target_logit);
+    p.status = g.status;
+    p.wait_ns = wait_limit_ns();
+
+    int grid = 1;
+    cudaError_t e = gather_grid(tokens, &grid);
+    if (e == cudaSuccess)
+        e = launch_overlapped(gather_kernel<false>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
+    if (e != cudaSuccess) return launch_failed(what, "gather", e);
+    e = launch_matrix<kStats>(p, tiles_of(l.padded, vocab), s);
+    if (e != cudaSuccess) return launch_failed(what, "statistics", e);
+    const int32_t parts = (int32_t)((vocab + kTile - 1) / kTile) * 2;
+    // Few rows: more threads to each, since the walk over the parts is a chain of loads.
+    if (tokens <= 1024)
+        e = launch_overlapped(combine_kernel<4>, dim3((unsigned)((tokens + 3) / 4)), dim3(kCombineThreads), 0, s, 1, true,
+                              (const Header*)g.header, (const float2*)p.stats, parts, l.padded,
+                              (const float*)p.target_logit, (const int32_t*)g.source, lse, token_loss);
+    else
+        e = launch_overlapped(combine_kernel<32>, dim3((unsigned)((tokens + 31) / 32)), dim3(kCombineThreads), 0, s, 1,
+                              true, (const Header*)g.header, (const float2*)p.stats, parts, l.padded,
+                              (const float*)p.target_logit, (const int32_t*)g.source, lse, token_loss);
+    if (e != cudaSuccess) return launch_failed(what, "combine", e);
+    if (reduced) {
+        e = launch_overlapped(reduce_kernel, dim3(1), dim3(kReduceThreads), 0, s, 1, true, (const Header*)g.header,
+                              (const float*)token_loss, (int32_t)tokens, (int32_t)(reduction == MXFP4_REDUCE_MEAN), loss);
+        if (e != cudaSuccess) return launch_failed(what, "reduce", e);
+    }
+    return record_error(MXFP4_OK, "%s", "");
+}
+
+extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int64_t dim, int64_t ldh, const void* w,
+                                             int64_t vocab, int64_t ldw, const void* targets, int ids_dtype,
+                                             int64_t ignore_index, int reduction, const float* lse, const float* dloss,
+                                             void* dh, int dh_dtype, int64_t lddh, void* dw, int dw_dtype,
+                                             int64_t lddw, int accumulate, void* ws, size_t ws_bytes,
+                                             mxfp4_stream_t stream) {
+    const char* what = "linear_ce_grad";
+    mxfp4_status st = check_common(what, h, tokens, dim, ldh, w, vocab, ldw, targets, ids_dtype, reduction);
+    if (st) return st;
+    for (int t : {dh ? dh_dtype : 0, dw ? dw_dtype : 0})
+        if (t != MXFP4_OUT_F32 && t != MXFP4_OUT_BF16)
+            return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad output dtype %d", what, t);
+    if (accumulate != 0 && accumulate != 1)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: accumulate must be 0 or 1", what);
+    if (dw && accumulate && dw_dtype != MXFP4_OUT_F32)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: accumulate needs fp32 output", what);
+    const int64_t hsz = dh_dtype == MXFP4_OUT_BF16 ? 2 : 4, wsz = dw_dtype == MXFP4_OUT_BF16 ? 2 : 4;
+    if (dw) {
+        if (lddw < dim) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lddw below dim", what);
+        if (reinterpret_cast<uintptr_t>(dw) % 16 || lddw * wsz % 16)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: dw must be 16-byte aligned with rows of 16 bytes", what);
+    }
+    if (tokens > 0) {
+        if (!lse || !dloss) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse or dloss is NULL", what);
+        if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(dloss)) % 4)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: lse or dloss misaligned", what);
+        if (dh && lddh < dim) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lddh below dim", what);
+        if (dh && reinterpret_cast<uintptr_t>(dh) % hsz)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: dh not aligned to its type", what);
+        if ((dh || dw) &&
+            (st = check_ws(what, ws, ws_bytes, mxfp4_linear_ce_grad_workspace_bytes(tokens, vocab, dim))))
+            return st;
+    }
+    if ((!dh && !dw) || (tokens == 0 && (!dw || accumulate))) return record_error(MXFP4_OK, "%s", "");
+    if ((st = ensure_device())) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (tokens == 0) {
+        e = cudaMemset2DAsync(dw, (size_t)(lddw * wsz), 0, (size_t)(dim * wsz), (size_t)vocab, s);
+        return e != cudaSuccess ? launch_failed(what, "clear", e) : record_error(MXFP4_OK, "%s", "");
+    }
+    const Layout l = lay_out(tokens, vocab, dim, true);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+
+    GatherParams g{};
+    g.h = static_cast<const bf16*>(h);
+    g.ldh = ldh;
+    g.tokens = (int32_t)tokens;
+    g.dim = (int32_t)dim;
+    g.vocab = (int32_t)vocab;
+    g.vec = vector_rows(h, ldh, dim, 2);
+    g.targets = targets;
+    g.is64 = ids_dtype == MXFP4_IDS_I64;
+    g.ignore = ignore_index;
+    g.reduction = reduction;
+    g.lse = lse;
+    g.dloss = dloss;
+    g.header = reinterpret_cast<Header*>(base + l.header);
+    g.rows = reinterpret_cast<bf16*>(base + l.rows);
+    g.target = reinterpret_cast<int32_t*>(base + l.target);
+    g.source = reinterpret_cast<int32_t*>(base + l.source);
+    g.place = reinterpret_cast<int32_t*>(base + l.place);
+    g.lse2 = reinterpret_cast<float*>(base + l.lse2);
+    g.ratio = reinterpret_cast<float*>(base + l.ratio);
+    g.status = device_status_ptr();
+    int grid = 1;
+    e = gather_grid(tokens, &grid);
+    if (e == cudaSuccess)
+        e = launch_overlapped(gather_kernel<true>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
+    if (e != cudaSuccess) return launch_failed(what, "gather", e);
+
+    bf16* dz = reinterpret_cast<bf16*>(base + l.dz);
+    float* parts = reinterpret_cast<float*>(base + l.parts);
+    for (int64_t v0 = 0; v0 < vocab; v0 += l.piece) {
+        const int32_t cols = (int32_t)std::min<int64_t>(l.piece, vocab - v0);
+        const uint8_t* w_piece = static_cast<const uint8_t*>(w) + v0 * ldw * 2;
+        CeParams p{};
+        p.header = g.header;
+        p.target = g.target;
+        p.col0 = (int32_t)v0;
+        p.rows = l.padded;
+        p.lse2 = g.lse2;
+        p.ratio = g.ratio;
+        p.status = g.status;
+        p.wait_ns = wait_limit_ns();
+        {
+            Product& q = p.prod[0];
+            q.m_counted = 1;
+            q.M = l.padded;
+            q.N = cols;
+            q.K = (int32_t)dim;
+            q.splits = 1;
+            q.out_bf16 = 1;
+            if (!encode_bf16_map(&q.map_a, g.rows, l.padded, dim, dim, kK, 128) ||
+                !encode_bf16_map(&q.map_b, w_piece, cols, dim, ldw, kK, 128) ||
+                !encode_out_map(&q.map_c, dz, l.padded, cols, l.piece, true))
+                return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+            p.count = 1;
+            e = launch_matrix<kDlogits>(p, tiles_of(l.padded, cols), s);
+            if (e != cudaSuccess) return launch_failed(what, "dlogits", e);
+        }
+        int n = 0;
+        int64_t tiles = 0;
+        if (dh) {  // the longer contraction first: the schedule ends on the shorter tiles
+            Product& q = p.prod[n++];
+            q = Product{};
+            q.m_counted = 1;
+            q.b_mn = 1;
+            q.M = l.padded;
+            q.N = (int32_t)dim;
+            q.K = cols;
+            const int32_t stages = (cols + kK - 1) / kK;
+            q.k_per_split = (stages + l.splits - 1) / l.splits;
+            q.splits = (stages + q.k_per_split - 1) / q.k_per_split;
+            q.slot_rows = l.padded;
+            q.add = v0 > 0;
+            if (!encode_bf16_map(&q.map_a, dz, l.padded, cols, l.piece, kK, 128) ||
+                !encode_bf16_map(&q.map_b, w_piece, cols, dim, ldw, 64, kK) ||
+                !encode_out_map(&q.map_c, parts, (int64_t)l.splits * l.padded, dim, dim, false))
+                return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+            tiles += tiles_of(l.padded, dim) * q.splits;
+        }
+        if (dw) {
+            Product& q = p.prod[n++];
+            q = Product{};
+            q.a_mn = q.b_mn = 1;
+            q.k_counted = 1;
+            q.M = cols;
+            q.N = (int32_t)dim;
+            q.K = l.padded;
+            q.splits = 1;
+            q.scaled = 1;
+            q.out_bf16 = dw_dtype == MXFP4_OUT_BF16;
+            q.add = accumulate;
+            if (!encode_bf16_map(&q.map_a, dz, l.padded, cols, l.piece, 64, kK) ||
+                !encode_bf16_map(&q.map_b, g.rows, l.padded, dim, dim, 64, kK) ||
+                !encode_out_map(&q.map_c, static_cast<uint8_t*>(dw) + v0 * lddw * wsz, cols, dim, lddw, q.out_bf16))
+                return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+            tiles += tiles_of(cols, dim);
+        }
+        p.count = n;
+        e = launch_matrix<kProducts>(p, tiles, s);
+        if (e != cudaSuccess) return launch_failed(what, "products", e);
+    }
+    if (dh) {
+        const uint32_t segs = (uint32_t)((dim / 8 + 31) / 32);
+        const int64_t blocks = (tokens * segs + kScatterThreads / 32 - 1) / (kScatterThreads / 32);
+        const int64_t slot = (int64_t)l.padded * dim;
+        if (dh_dtype == MXFP4_OUT_BF16)
+            e = launch_overlapped(scatter_kernel<bf16>, dim3((unsigned)blocks), dim3(kScatterThreads), 0, s, 1, true,
+                                  (const Header*)g.header, (const int32_t*)g.place, (const float*)parts, l.splits, slot,
+                                  (int32_t)tokens, (int32_t)dim, segs, static_cast<bf16*>(dh), lddh,
+                                  (int32_t)vector_rows(dh, lddh, dim, 2));
+        else
+            e = launch_overlapped(scatter_kernel<float>, dim3((unsigned)blocks), dim3(kScatterThreads), 0, s, 1, true,
+                                  (const Header*)g.header, (const int32_t*)g.place, (const float*)parts, l.splits, slot,
+                                  (int32_t)tokens, (int32_t)dim, segs, static_cast<float*>(dh), lddh,
+                                  (int32_t)vector_rows(dh, lddh, dim, 4));
+        if (e != cudaSuccess) return launch_failed(what, "scatter", e);
+    }
+    return record_error(MXFP4_OK, "%s", "");
+}

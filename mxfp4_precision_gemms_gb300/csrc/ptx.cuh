@@ -133,6 +133,11 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until the shared-memory sources of all committed bulk groups have been read.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// The same for all but the N most recently committed groups.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 // Waits until all committed bulk groups have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -255,6 +260,17 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc
         : "memory");
 }
 
+// bf16 operands (kind::f16), fp32 accumulation, issued for a CTA pair.
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading / stride
 // byte offsets (16-byte units), version 1, swizzle mode in bits 61-63.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
@@ -279,6 +295,16 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N) {
            | (1u << 23)         // scale type: UE8M0
            | ((M >> 4) << 24);  // M / 16
 }
+// Instruction descriptor for kind::f16 with bf16 A/B and fp32 accumulation.  a_mn / b_mn: that
+// operand's M (N) index runs along its shared-memory rows instead of K.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+    return (1u << 4)                // D format: fp32
+           | (1u << 7)              // A format: bf16
+           | (1u << 10)             // B format: bf16
+           | (a_mn << 15) | (b_mn << 16)
+           | ((N >> 3) << 17)       // N / 8
+           | ((M >> 4) << 24);      // M / 16
+}
 __device__ __forceinline__ uint32_t idesc_with_sf_ids(uint32_t idesc, uint32_t a_id, uint32_t b_id) {
     return idesc | (b_id << 4) | (a_id << 29);
 }
@@ -300,6 +326,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ conversions
+// 2^x (ex2.approx: about 2 ulp, 2^-inf = 0, subnormal results flushed).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Eight fp32 -> eight E2M1 codes packed in 32 bits (value i in nibble i), round to
 // nearest even, saturating.  A pure conversion (no side effects), so not volatile: the
 // compiler may schedule it among the surrounding arithmetic.

@@ -90,6 +90,58 @@ def test_binding_refuses_before_the_library():
 
     ids, w = torch.zeros(3, dtype=torch.int64), torch.zeros(4, 8)
     for call in (lambda: mx.embedding(ids, w), lambda: mx.embedding_grad(ids, torch.zeros(3, 8), 4),
+                 lambda: mx.linear_ce(w, w, ids), lambda: mx.linear_ce_grad(w, w, ids, w[:, 0], w[0, :1]),
                  lambda: mx.clip_grad_norm([w], 1.0), lambda: mx.clip_grad_norm([w], 1.0, outs=[])):
         with pytest.raises(ValueError):
             call()
+
+
+def _ce(L, **kw):
+    need = L.mxfp4_linear_ce_workspace_bytes(4, 100, 64)
+    a = dict(h=0x1000, n=4, dim=64, ldh=64, w=0x2000, vocab=100, ldw=64, y=0x3000, it=1, red=2, loss=0x4000, lse=0x5000,
+             ws=0x6000, wsb=need)
+    a.update(kw)
+    return L.mxfp4_linear_ce(P(a["h"]), a["n"], a["dim"], a["ldh"], P(a["w"]), a["vocab"], a["ldw"], P(a["y"]), a["it"],
+                             -100, a["red"], P(a["loss"]), P(a["lse"]), P(a["ws"]), a["wsb"], None)
+
+
+CE_BAD = [(dict(h=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(it=2), INVALID),
+          (dict(red=3), INVALID), (dict(red=-1), INVALID), (dict(n=-1), INVALID), (dict(vocab=-1), INVALID),
+          (dict(dim=-8), INVALID), (dict(vocab=0), SHAPE), (dict(dim=0), SHAPE), (dict(dim=60), SHAPE),
+          (dict(n=(1 << 24) + 1), SHAPE), (dict(vocab=(1 << 28) + 1), SHAPE), (dict(ldh=63), INVALID),
+          (dict(ldw=56), INVALID), (dict(ldw=68), MISALIGNED), (dict(w=0x2008), MISALIGNED), (dict(h=0x1001), MISALIGNED),
+          (dict(y=0x3004), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(wsb=64), WORKSPACE),
+          (dict(ws=0x6010), MISALIGNED)]
+
+
+@pytest.mark.parametrize("change,want", CE_BAD + [(dict(loss=None), INVALID), (dict(lse=None), INVALID),
+                                                  (dict(loss=0x4002), MISALIGNED), (dict(n=0, red=0), 0)])
+def test_linear_ce_refuses(L, change, want):
+    assert _ce(L, **change) == want
+
+
+def _ce_grad(L, **kw):
+    need = L.mxfp4_linear_ce_grad_workspace_bytes(4, 100, 64)
+    a = dict(h=0x1000, n=4, dim=64, ldh=64, w=0x2000, vocab=100, ldw=64, y=0x3000, it=1, red=2, lse=0x5000, g=0x4000,
+             dh=0x7000, ht=1, lddh=64, dw=0x8000, wt=0, lddw=64, acc=0, ws=0x6000, wsb=need)
+    a.update(kw)
+    return L.mxfp4_linear_ce_grad(P(a["h"]), a["n"], a["dim"], a["ldh"], P(a["w"]), a["vocab"], a["ldw"], P(a["y"]),
+                                  a["it"], -100, a["red"], P(a["lse"]), P(a["g"]), P(a["dh"]), a["ht"], a["lddh"],
+                                  P(a["dw"]), a["wt"], a["lddw"], a["acc"], P(a["ws"]), a["wsb"], None)
+
+
+@pytest.mark.parametrize("change,want", CE_BAD + [
+    (dict(lse=None), INVALID), (dict(g=None), INVALID), (dict(ht=2), INVALID), (dict(wt=2), INVALID),
+    (dict(acc=2), INVALID), (dict(acc=1, wt=1), INVALID), (dict(lddh=63), INVALID), (dict(lddw=63), INVALID),
+    (dict(lddw=66), MISALIGNED), (dict(dw=0x8008), MISALIGNED), (dict(dh=0x7001), MISALIGNED),
+    (dict(lse=0x5002), MISALIGNED), (dict(dh=None, dw=None), 0), (dict(n=0, acc=1), 0), (dict(n=0, dw=None), 0)])
+def test_linear_ce_grad_refuses(L, change, want):
+    assert _ce_grad(L, **change) == want
+
+
+def test_linear_ce_workspace_holds_no_logits(L):
+    """At 8192 x 128256 x 4096 the logits would be 4.2 GB in fp32; one piece of dz is at most 256 MiB."""
+    T, V, D = 8192, 128256, 4096
+    assert L.mxfp4_linear_ce_workspace_bytes(T, V, D) < 2 * T * D + 8 * T * (2 * 501) + (1 << 20)
+    assert L.mxfp4_linear_ce_grad_workspace_bytes(T, V, D) < (256 << 20) + 6 * T * D + (1 << 20)
+    assert L.mxfp4_linear_ce_workspace_bytes(0, V, D) == 0 and L.mxfp4_linear_ce_grad_workspace_bytes(T, -1, D) == 0

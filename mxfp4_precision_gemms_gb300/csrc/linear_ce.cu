@@ -98,6 +98,14 @@ struct CeParams {
 
 enum Kind { kStats = 0, kDlogits = 1, kProducts = 2 };
 
+// Stages that one accumulator takes.  The tensor cores cut each step's sum off towards zero, and the
+// loss of a long contraction would carry that one-sided error: the logits of dim = 4096 came out
+// smaller by 4.2e-6 of themselves (1.0e-6 at 1024), ten times an fp32 product's error.  So the
+// statistics' logits are summed in runs of K = 512, joined in fp32 by the epilogue, which has the time:
+// a run is 4096 cycles of MMAs and about 500 of read-out.  dz is rounded to bf16 anyway, and the
+// gradients' sums carry that rounding: they are taken in one run.
+constexpr int kStatsRun = 8;
+
 __host__ __device__ inline int32_t pad_rows(int32_t n) { return n <= 0 ? kTile : (n + kTile - 1) / kTile * kTile; }
 
 struct Tile {
@@ -192,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     uint64_t* mma_done = acc_empty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffTmem);
 
+    constexpr int32_t kRun = KIND == kStats ? kStatsRun : 1 << 30;  // stages per accumulator
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int64_t cluster = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
@@ -286,21 +295,26 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 uint32_t s = 0, phase = 0, tcount = 0;
                 bool ok = true;
                 Tile t;
-                for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters, ++tcount) {
+                for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
                     const Product& q = p.prod[t.prob];
                     const uint32_t idesc = idesc_bf16(256, 256, q.a_mn != 0, q.b_mn != 0);
                     // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
                     // Between 64-column blocks of M / N: half a stage's operand.
                     const uint32_t a_step = q.a_mn ? 2048 : 32, b_step = q.b_mn ? 2048 : 32;
                     const uint32_t a_lbo = q.a_mn ? kOpBytes / 2 : 16, b_lbo = q.b_mn ? kOpBytes / 2 : 16;
-                    const uint32_t ab = tcount & 1u;
-                    if (tcount >= 2 && !wait_bounded(&acc_empty[ab], ((tcount >> 1) - 1u) & 1u, p.wait_ns, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + ab * 256;
+                    uint32_t d = 0;
                     for (int32_t i = 0; i < t.stages; ++i) {
+                        const bool first = (i & (kRun - 1)) == 0;
+                        if (first) {  // a new accumulator
+                            const uint32_t ab = tcount & 1u;
+                            if (tcount >= 2 &&
+                                !wait_bounded(&acc_empty[ab], ((tcount >> 1) - 1u) & 1u, p.wait_ns, p.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            d = tmem + ab * 256;
+                        }
                         if (!wait_bounded(&full[s], phase, p.wait_ns, p.status)) {
                             ok = false;
                             break;
@@ -311,14 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         for (int k = 0; k < kK / 16; ++k)
                             tc_mma_bf16_pair(d, smem_desc(a + k * a_step, a_lbo, 1024, kSwizzle128B),
                                              smem_desc(b + k * b_step, b_lbo, 1024, kSwizzle128B), idesc,
-                                             (i | k) != 0);
+                                             !first || k != 0);
                         tc_commit_pair(&empty[s], 0x3);
                         if (++s == kStages) {
                             s = 0;
                             phase ^= 1u;
                         }
+                        if ((i & (kRun - 1)) == kRun - 1 || i + 1 == t.stages) {
+                            tc_commit_pair(&acc_full[tcount & 1u], 0x3);
+                            ++tcount;
+                        }
                     }
-                    if (ok) tc_commit_pair(&acc_full[ab], 0x3);
                 }
                 tc_commit_pair(mma_done, 0x3);
             }
@@ -333,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
         const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
         const float gscale = KIND == kProducts ? *reinterpret_cast<const volatile float*>(&p.header->gscale) : 1.f;
         uint32_t tcount = 0;
+        bool ok = true;
         Tile t;
-        for (int64_t tile = cluster; locate(p, count, tile, t); tile += num_clusters, ++tcount) {
+        for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
             const Product& q = p.prod[t.prob];
-            const uint32_t ab = tcount & 1u;
             const int32_t row0 = t.m0 + (int32_t)rank * 128 + quad * 32;
             const int32_t row = row0 + lane;
             const int32_t c0 = t.n0 + half * 128;
@@ -350,83 +367,121 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     ratio = __ldcg(p.ratio + row);
                 }
             }
-            if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) break;
-            tc_fence_after();
-            const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + ab * 256 + (uint32_t)(half * 128);
-            float m = -INFINITY, sum = 0.f;
+            const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
+            if constexpr (KIND == kStats) {
+                // The logits are the sums of their runs' accumulators, added up here.
+                uint32_t z[4][32];
+                for (int32_t i = 0; i < t.stages; i += kRun, ++tcount) {
+                    const uint32_t ab = tcount & 1u;
+                    if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (i == 0) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(src + c * 32, v);
-                tmem_ld_wait();
-                if (c == 3) {  // the accumulator has been read out; the arrive only reports it
+                        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(src + ab * 256 + c * 32, z[c]);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {  // 16 columns at a time: 168 registers is the limit
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(src + ab * 256 + c * 16, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                uint32_t& x = z[c / 2][(c & 1) * 16 + j];
+                                x = __float_as_uint(__uint_as_float(x) + __uint_as_float(v[j]));
+                            }
+                        }
+                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
                 }
-                const int32_t col = c0 + c * 32;
-                if constexpr (KIND == kStats) {
+                if (!ok) break;
+                float m = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int32_t col = c0 + c * 32;
                     const int32_t left = q.N - col;
                     if (left < 32) {  // past the vocabulary's end
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j >= left) v[j] = 0xff800000u;
+                            if (j >= left) z[c][j] = 0xff800000u;
                     }
                     const int32_t hit = tgt - col;
                     if (hit >= 0 && hit < 32) {
-                        float z = 0.f;
+                        float x = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j == hit) z = __uint_as_float(v[j]);
-                        p.target_logit[row] = z;
+                            if (j == hit) x = __uint_as_float(z[c][j]);
+                        p.target_logit[row] = x;
                     }
-                    float top = m;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]) * kLog2e);
-                    // all -inf so far: any finite reference leaves the terms 0
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float s4[4] = {sum * exp2_approx(m - ref), 0.f, 0.f, 0.f};
+                    for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(z[c][j]));
+                }
+                m *= kLog2e;
+                // all -inf: any finite reference leaves the terms 0
+                const float ref = m == -INFINITY ? 0.f : m;
+                float s4[4] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        s4[j & 3] += exp2_approx(fmaf(__uint_as_float(v[j]), kLog2e, -ref));
-                    sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    m = top;
-                } else if constexpr (KIND == kDlogits) {
-                    const int32_t hit = tgt - col;
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float x[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
-                            x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
-                        }
-                        w[j] = row < count ? pack_bf16(x[0], x[1]) : 0u;
-                    }
-                    boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
-                } else {
-                    const int32_t y = t.slot * q.slot_rows + row0;
-                    const bool in_m = q.m_counted || row0 < q.M;
-                    if (q.scaled) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * gscale);
-                    }
-                    if (q.out_bf16) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        boxes.store(&q.map_c, lane, w, col, y, in_m && col < q.N, false);
-                    } else {
-                        boxes.store(&q.map_c, lane, v, col, y, in_m && col < q.N, q.add);
-                        boxes.store(&q.map_c, lane, v + 16, col + 16, y, in_m && col + 16 < q.N, q.add);
-                    }
-                }
-            }
-            if constexpr (KIND == kStats) {
+                        s4[j & 3] += exp2_approx(fmaf(__uint_as_float(z[c][j]), kLog2e, -ref));
+                sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 if (row < count)
                     p.stats[(int64_t)((t.n0 / kTile) * 2 + half) * p.rows + row] = make_float2(m, sum);
+            } else {
+                const uint32_t ab = tcount & 1u;
+                if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) break;
+                ++tcount;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(src + ab * 256 + c * 32, v);
+                    tmem_ld_wait();
+                    if (c == 3) {  // the accumulator has been read out; the arrive only reports it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
+                    }
+                    const int32_t col = c0 + c * 32;
+                    if constexpr (KIND == kDlogits) {
+                        const int32_t hit = tgt - col;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float x[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
+                                x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
+                            }
+                            w[j] = row < count ? pack_bf16(x[0], x[1]) : 0u;
+                        }
+                        boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
+                    } else {
+                        const int32_t y = t.slot * q.slot_rows + row0;
+                        const bool in_m = q.m_counted || row0 < q.M;
+                        if (q.scaled) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * gscale);
+                        }
+                        if (q.out_bf16) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            boxes.store(&q.map_c, lane, w, col, y, in_m && col < q.N, false);
+                        } else {
+                            boxes.store(&q.map_c, lane, v, col, y, in_m && col < q.N, q.add);
+                            boxes.store(&q.map_c, lane, v + 16, col + 16, y, in_m && col + 16 < q.N, q.add);
+                        }
+                    }
+                }
             }
         }
         if (lane == 0) bulk_wait_all();

@@ -406,8 +406,8 @@ size_t mxfp4_noalloc_scratch_bytes(void);
  * The two ends of a training step: the embedding lookup in front of the first linear
  * layer, the output layer's cross entropy behind the last one, and the clipping of the
  * gradients that the step leaves.  Numbers here may be any bf16 / fp32 values: infinities
- * and NaN go through the formulas, except where a token is ignored (its values are then
- * never read).  Token ids and targets are device arrays; one outside the vocabulary is
+ * and NaN go through the formulas, except where a token is ignored (its values then reach
+ * nothing).  Token ids and targets are device arrays; one outside the vocabulary is
  * treated as ignored and reported by mxfp4_device_status as MXFP4_ERR_INVALID_ARG.
  * ---------------------------------------------------------------------------------- */
 typedef enum { MXFP4_IDS_I32 = 0, MXFP4_IDS_I64 = 1 } mxfp4_ids_dtype;
@@ -447,7 +447,7 @@ typedef enum { MXFP4_REDUCE_NONE = 0, MXFP4_REDUCE_SUM = 1, MXFP4_REDUCE_MEAN = 
  * ldw % 8 == 0); dim % 8 == 0, vocab and tokens any.  Products in bf16 on the tensor cores, sums
  * and softmax statistics in fp32.
  * targets: device [tokens] (ids_dtype).  A token whose target is ignore_index does not
- * count: its row of h is not read, its loss and lse are 0.
+ * count: its loss and lse are 0, and nothing depends on its row of h (which may hold NaN).
  * loss: device fp32, [tokens] for MXFP4_REDUCE_NONE, else [1]; lse: device fp32 [tokens], what
  * mxfp4_linear_ce_grad takes.
  * ws: device, 256-byte aligned, mxfp4_linear_ce_workspace_bytes bytes (a copy of the counted
@@ -489,8 +489,8 @@ size_t mxfp4_clip_grad_norm_workspace_bytes(int n);
  * c = min(1, max_norm / (norm + 1e-6)), out = c * grad (fp32 arithmetic, rounded once).
  * *norm (device fp32) receives the norm before clipping.  Where c == 1, gradients that
  * are clipped in place are left as they are.  A NaN or infinite norm makes c NaN or 0 and
- * goes into every output, as the formula says.  The squares are summed in fp32 per thread and
- * in fp64 across threads, in an order fixed by the sizes.  Any alignment of the element
+ * goes into every output, as the formula says.  The squares are summed in fp32, in an order
+ * fixed by the sizes (a norm above 1.8e19 overflows to infinity).  Any alignment of the element
  * type; n >= 0.  grads is read on the host during the call.  out must be grad or not
  * overlap any gradient.  ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,

@@ -76,6 +76,8 @@ _lib = None
 def lib():
     """Loads libmxfp4.so (built by ``__graft_entry__.build()``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -699,19 +701,19 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse:
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
     """mxfp4_clip_grad_norm over a sequence of contiguous CUDA fp32 / bf16 tensors: clips them in
-    place, or into `outs` (same shapes and types; gradients left as they are).  Returns the
+    place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
     norm before clipping as a 1-element fp32 CUDA tensor."""
     outs = grads if outs is None else outs
     if len(outs) != len(grads):
         raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
     flat = []
     for g, o in zip(grads, outs):
-        kind = _OUT_OF.get(g.dtype)
+        kind, n = _OUT_OF.get(g.dtype), g.numel()
         if kind is None or not g.is_cuda or not g.is_contiguous():
             raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
-            raise ValueError("outs must be contiguous CUDA tensors of their gradients' shapes and types")
-        flat += (g.data_ptr(), o.data_ptr(), g.numel(), kind)  # an mxfp4_grad: two pointers, numel, (dtype, 0)
+        if o is not g and (o.dtype is not g.dtype or o.numel() != n or not o.is_cuda or not o.is_contiguous()):
+            raise ValueError("outs must be contiguous CUDA tensors of their gradients' sizes and types")
+        flat += (g.data_ptr(), o.data_ptr(), n, kind)  # an mxfp4_grad: two pointers, numel, (dtype, 0)
     table = array.array("q", flat)
     device = grads[0].device if flat else torch.device("cuda", torch.cuda.current_device())
     L = lib()

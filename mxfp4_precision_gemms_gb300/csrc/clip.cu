@@ -4,14 +4,20 @@
 //
 // Two launches.  The table of tensors travels in the kernels' parameters, so nothing is
 // copied to the device and a captured graph replays it.  The tensors are cut into chunks of
-// equal size that the CTAs take in turn.
-//   1. Each CTA sums the squares of its chunks -- fp32 over a thread's elements of one chunk, fp64
-//      from there on -- and writes one partial sum.
+// equal bytes.
+//   1. Persistent CTAs sum the squares of their chunks in fp32 -- a thread's elements of one chunk, its
+//      chunks, then trees over threads and CTAs, so that no chain of additions is long -- and
+//      write one partial sum each.  (fp64 sums cost 20 us a call: every CTA of the second pass took
+//      part in them, at 2 fp64 operations per SM and cycle.)
 //   2. Each CTA adds the partial sums up in the same order, so that all have the same norm with
 //      no atomics and no counter to reset, then scales its chunks, last read first: what the 129 MB
-//      L2 still holds from the first pass is read from there.  A gradient that is clipped in
-//      place by c == 1 is left as it is.
+//      L2 still holds from the first pass is read from there.  Gradients that are clipped in
+//      place by c == 1 are left as they are.
 // HBM bandwidth bounds both passes of long calls, the two launches short ones.
+// Out of place, the second pass has a CTA for each chunk: CTAs that take one and end keep the accesses in
+// address order (872 MB: 248 us against 272 for persistent ones and 257 for cudaMemcpy), and each
+// loads its chunk before it adds up the norm.  In place it is persistent and looks at the norm
+// first, because the ordinary step ends there: 5700 CTAs would take 15 us to find that out.
 #include <algorithm>
 
 #include "element.cuh"
@@ -24,9 +30,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kClipThreads = 256;
-constexpr int kClipCtasPerSm = 8;
+constexpr int kClipCtasPerSm = 4;
 constexpr int kMaxParts = 2048;  // partial sums of one call's launches together
-constexpr int64_t kMaxChunk = 16384, kMinChunk = 2048;  // elements of a chunk (a power of two)
+constexpr int kBatch = 8;        // 16-byte units that a thread loads before it uses them
+constexpr int kMinChunk = 12, kMaxChunk = 15;  // log2 of a chunk's bytes: one unit a thread .. kBatch
+static_assert((1 << kMinChunk) == 16 * kClipThreads && (1 << kMaxChunk) == 16 * kClipThreads * kBatch, "units");
 
 // Up to N tensors of one launch; chunk c of the launch belongs to the tensor i with
 // first[i] <= c < first[i + 1].
@@ -38,7 +46,8 @@ struct ClipTable {
     uint32_t first[N + 1];
     uint8_t is_bf16[N];
     int32_t n;
-    int32_t chunk_log2;
+    int32_t chunk_log2;  // of its bytes
+    int32_t in_place;  // every tensor is
 };
 // Kernel parameters hold 32764 bytes.  The small table is for the usual few tensors: a launch
 // copies its parameters, all of them.
@@ -59,116 +68,157 @@ __device__ __forceinline__ int find_tensor(const ClipTable<N>& t, uint32_t chunk
 }
 
 
-// Sum of squares of n elements at p over the CTA's threads (this thread's share).
-template <class T>
-__device__ __forceinline__ float chunk_squares(const T* p, int64_t n) {
-    float s0 = 0.f, s1 = 0.f;
-    int64_t done = 0;
-    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        const int64_t units = n / 8;
-#pragma unroll 4
-        for (int64_t u = threadIdx.x; u < units; u += kClipThreads) {
-            float v[8];
-            unpack8(load8(p + u * 8), v);
+// Chunk `chunk` of a launch: its tensor and the bytes of it.
+struct Chunk {
+    const uint8_t* in;
+    uint8_t* out;
+    int32_t bytes;
+    bool is_bf16, vec;  // vec: 16-byte aligned
+};
+template <int N>
+__device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, uint32_t chunk) {
+    const int i = find_tensor(t, chunk);
+    Chunk c;
+    c.is_bf16 = t.is_bf16[i];
+    const int64_t at = (int64_t)(chunk - t.first[i]) << t.chunk_log2;
+    c.in = static_cast<const uint8_t*>(t.in[i]) + at;
+    c.out = static_cast<uint8_t*>(t.out[i]) + at;
+    c.bytes = (int32_t)min(int64_t(1) << t.chunk_log2, t.numel[i] * (c.is_bf16 ? 2 : 4) - at);
+    c.vec = ((reinterpret_cast<uintptr_t>(c.in) | reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
+    return c;
+}
+
+// This thread's units of a chunk (at most kBatch).
+__device__ __forceinline__ void load_units(const Chunk& c, uint4 (&r)[kBatch]) {
+    const int units = c.vec ? c.bytes / 16 : 0;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                s0 = fmaf(v[j], v[j], s0);
-                s1 = fmaf(v[j + 1], v[j + 1], s1);
+    for (int k = 0; k < kBatch; ++k) {
+        const int u = threadIdx.x + k * kClipThreads;
+        if (u < units) r[k] = reinterpret_cast<const uint4*>(c.in)[u];
+    }
+}
+
+// f(element pointer index) over the elements that load_units leaves out.
+template <class F>
+__device__ __forceinline__ void for_rest(const Chunk& c, F&& f) {
+    const int esz = c.is_bf16 ? 2 : 4;
+    const int n = c.bytes / esz, first = c.vec ? c.bytes / 16 * (16 / esz) : 0;
+    for (int i = first + threadIdx.x; i < n; i += kClipThreads) f(i);
+}
+
+__device__ __forceinline__ float chunk_squares(const Chunk& c) {
+    uint4 r[kBatch];
+    load_units(c, r);
+    const int units = c.vec ? c.bytes / 16 : 0;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        if (threadIdx.x + k * kClipThreads >= units) break;
+        const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (c.is_bf16) {
+                const float a = bf16_lo(w[j]), b = bf16_hi(w[j]);
+                s0 = fmaf(a, a, s0);
+                s1 = fmaf(b, b, s1);
+            } else {
+                const float a = __uint_as_float(w[j]);
+                if (j & 1)
+                    s1 = fmaf(a, a, s1);
+                else
+                    s0 = fmaf(a, a, s0);
             }
         }
-        done = units * 8;
     }
-#pragma unroll 4
-    for (int64_t i = done + threadIdx.x; i < n; i += kClipThreads) {
-        const float v = load1(p + i);
+    for_rest(c, [&](int i) {
+        const float v = c.is_bf16 ? load1(reinterpret_cast<const bf16*>(c.in) + i)
+                                  : load1(reinterpret_cast<const float*>(c.in) + i);
         s0 = fmaf(v, v, s0);
-    }
+    });
     return s0 + s1;
 }
 
-template <class T>
-__device__ __forceinline__ void chunk_scale(const T* p, T* q, int64_t n, float c) {
-    int64_t done = 0;
-    if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0) {
-        const int64_t units = n / 8;
-#pragma unroll 4
-        for (int64_t u = threadIdx.x; u < units; u += kClipThreads) {
-            float v[8];
-            unpack8(load8(p + u * 8), v);
+// The chunk's units (loaded before) and its other elements, times x.
+__device__ __forceinline__ void chunk_scale(const Chunk& c, const uint4 (&r)[kBatch], float x) {
+    const int units = c.vec ? c.bytes / 16 : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= c;
-            store8(q + u * 8, v);
+    for (int k = 0; k < kBatch; ++k) {
+        const int u = threadIdx.x + k * kClipThreads;
+        if (u >= units) break;
+        uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = c.is_bf16 ? pack_bf16(bf16_lo(w[j]) * x, bf16_hi(w[j]) * x)
+                             : __float_as_uint(__uint_as_float(w[j]) * x);
+        reinterpret_cast<uint4*>(c.out)[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for_rest(c, [&](int i) {
+        if (c.is_bf16) {
+            const bf16* p = reinterpret_cast<const bf16*>(c.in) + i;
+            store1(reinterpret_cast<bf16*>(c.out) + i, load1(p) * x);
+        } else {
+            const float* p = reinterpret_cast<const float*>(c.in) + i;
+            store1(reinterpret_cast<float*>(c.out) + i, load1(p) * x);
         }
-        done = units * 8;
+    });
+}
+
+// Sum over the CTA, the same value in every thread.
+__device__ __forceinline__ float cta_sum(float v) {
+    __shared__ float warp_sum[kClipThreads / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = warp_sum[threadIdx.x & (kClipThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kClipThreads / 64; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
+    squares_kernel(const __grid_constant__ ClipTable<N> t, float* part) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    float sum = 0.f;
+    const uint32_t chunks = t.first[t.n];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) sum += chunk_squares(chunk_at(t, c));
+    sum = cta_sum(sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
+    scale_kernel(const __grid_constant__ ClipTable<N> t, const float* part, int parts, float max_norm, float* norm) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const uint32_t chunks = t.first[t.n];
+    // This CTA's chunks from the last one down; the first of them is loaded beside the partial
+    // sums, unless an in-place call may have nothing to do.
+    int64_t ch = (int64_t)chunks - 1 - blockIdx.x;
+    Chunk c;
+    uint4 r[kBatch];
+    if (ch >= 0) {
+        c = chunk_at(t, (uint32_t)ch);
+        if (!t.in_place) load_units(c, r);
     }
+    // The norm from the partial sums, the same in every CTA.
+    float sum = 0.f;
 #pragma unroll 4
-    for (int64_t i = done + threadIdx.x; i < n; i += kClipThreads) store1(q + i, load1(p + i) * c);
-}
-
-template <int N>
-__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
-    squares_kernel(const __grid_constant__ ClipTable<N> t, double* part) {
-    __shared__ double warp_sum[kClipThreads / 32];
-    grid_dependency_wait();
-    double sum = 0.0;
-    const uint32_t chunks = t.first[t.n];
-    const int64_t len = int64_t(1) << t.chunk_log2;
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = find_tensor(t, c);
-        const int64_t at = (int64_t)(c - t.first[i]) << t.chunk_log2;
-        const int64_t n = min(len, t.numel[i] - at);
-        sum += t.is_bf16[i] ? chunk_squares(static_cast<const bf16*>(t.in[i]) + at, n)
-                            : chunk_squares(static_cast<const float*>(t.in[i]) + at, n);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-#pragma unroll
-        for (int w = 0; w < kClipThreads / 32; ++w) all += warp_sum[w];
-        part[blockIdx.x] = all;
-    }
-}
-
-// The norm from the partial sums, the same in every CTA.
-__device__ __forceinline__ float norm_of(const double* part, int parts) {
-    __shared__ double warp_sum[kClipThreads / 32];
-    double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kClipThreads) sum += __ldcg(part + i);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    double all = 0.0;
-#pragma unroll
-    for (int w = 0; w < kClipThreads / 32; ++w) all += warp_sum[w];
-    return (float)sqrt(all);
-}
-
-template <int N>
-__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
-    scale_kernel(const __grid_constant__ ClipTable<N> t, const double* part, int parts, float max_norm, float* norm) {
-    grid_dependency_wait();
-    const float n = norm_of(part, parts);
+    const float n = sqrtf(cta_sum(sum));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-    const float r = max_norm / (n + 1e-6f);
-    const float c = r > 1.f ? 1.f : r;  // NaN stays NaN
-    const uint32_t chunks = t.first[t.n];
-    const int64_t len = int64_t(1) << t.chunk_log2;
-    if (blockIdx.x >= chunks) return;
-    const uint32_t turns = (chunks - 1 - blockIdx.x) / gridDim.x;
-    for (int64_t k = turns; k >= 0; --k) {
-        const uint32_t ch = blockIdx.x + (uint32_t)k * gridDim.x;
-        const int i = find_tensor(t, ch);
-        if (c == 1.f && t.in[i] == t.out[i]) continue;
-        const int64_t at = (int64_t)(ch - t.first[i]) << t.chunk_log2;
-        const int64_t m = min(len, t.numel[i] - at);
-        if (t.is_bf16[i])
-            chunk_scale(static_cast<const bf16*>(t.in[i]) + at, static_cast<bf16*>(t.out[i]) + at, m, c);
-        else
-            chunk_scale(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, m, c);
+    const float q = max_norm / (n + 1e-6f);
+    const float x = q > 1.f ? 1.f : q;  // NaN stays NaN
+    if (ch < 0 || (x == 1.f && t.in_place)) return;
+    if (t.in_place) load_units(c, r);
+    for (;;) {
+        if (x != 1.f || c.in != c.out) chunk_scale(c, r, x);
+        ch -= gridDim.x;
+        if (ch < 0) return;
+        c = chunk_at(t, (uint32_t)ch);
+        load_units(c, r);
     }
 }
 
@@ -176,14 +226,17 @@ template <int N>
 void fill_table(ClipTable<N>& t, const mxfp4_grad* g, int n, int chunk_log2) {
     t.n = n;
     t.chunk_log2 = chunk_log2;
+    t.in_place = 1;
     uint32_t chunk = 0;
     for (int i = 0; i < n; ++i) {
         t.in[i] = g[i].grad;
         t.out[i] = g[i].out;
         t.numel[i] = g[i].numel;
+        if (g[i].grad != g[i].out) t.in_place = 0;
         t.is_bf16[i] = g[i].dtype == MXFP4_OUT_BF16;
         t.first[i] = chunk;
-        chunk += (uint32_t)((g[i].numel + (int64_t(1) << chunk_log2) - 1) >> chunk_log2);
+        const int64_t bytes = g[i].numel * (t.is_bf16[i] ? 2 : 4);
+        chunk += (uint32_t)((bytes + (int64_t(1) << chunk_log2) - 1) >> chunk_log2);
     }
     t.first[n] = chunk;
 }
@@ -197,7 +250,7 @@ cudaError_t sm_count(int* sms) {
 
 // Launches both passes over tables of N tensors each (several where n > N).
 template <int N>
-cudaError_t launch_clip(const mxfp4_grad* g, int n, int chunk_log2, int ctas, float max_norm, float* norm, double* part,
+cudaError_t launch_clip(const mxfp4_grad* g, int n, int chunk_log2, int ctas, float max_norm, float* norm, float* part,
                         cudaStream_t s) {
     const int tables = n > N ? (n + N - 1) / N : 1;
     const int most = std::min(ctas, kMaxParts / tables);
@@ -212,14 +265,16 @@ cudaError_t launch_clip(const mxfp4_grad* g, int n, int chunk_log2, int ctas, fl
     }
     for (int k = tables - 1; k >= 0; --k) {  // last read first
         if (tables > 1) fill_table(t, g + k * N, std::min(N, n - k * N), chunk_log2);
-        const int grid = (int)std::max<uint32_t>(1u, std::min<uint32_t>((uint32_t)ctas, t.first[t.n]));
+        const uint32_t chunks = t.first[t.n];
+        const uint32_t grid = std::max<uint32_t>(1u, t.in_place ? std::min<uint32_t>((uint32_t)ctas, chunks) : chunks);
         cudaError_t e = launch_overlapped(scale_kernel<N>, dim3(grid), dim3(kClipThreads), 0, s, 1, true, t,
-                                          const_cast<const double*>(part), parts, max_norm, norm);
+                                          const_cast<const float*>(part), parts, max_norm, norm);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
+constexpr int64_t kMaxElements = int64_t(1) << 42;  // chunks stay within 31 bits
 constexpr int kMaxGrads = 1 << 20;  // 1024 tables: still two partial sums each
 
 }  // namespace
@@ -228,7 +283,7 @@ constexpr int kMaxGrads = 1 << 20;  // 1024 tables: still two partial sums each
 using namespace mx;
 
 extern "C" size_t mxfp4_clip_grad_norm_workspace_bytes(int n) {
-    return n < 0 || n > kMaxGrads ? 0 : kMaxParts * sizeof(double);
+    return n < 0 || n > kMaxGrads ? 0 : kMaxParts * sizeof(float);
 }
 
 extern "C" mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,
@@ -252,12 +307,12 @@ extern "C" mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, flo
         const uintptr_t esz = g.dtype == MXFP4_OUT_BF16 ? 2 : 4;
         if (reinterpret_cast<uintptr_t>(g.grad) % esz || reinterpret_cast<uintptr_t>(g.out) % esz)
             return record_error(MXFP4_ERR_MISALIGNED, "%s: gradient %d not aligned to its type", what, i);
-        if (g.numel > (int64_t(1) << 44) || total > (int64_t(1) << 44))
-            return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^44 elements", what);
+        if (g.numel > kMaxElements || total > kMaxElements)
+            return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^42 elements", what);
         total += g.numel;
     }
-    if (!ws || ws_bytes < kMaxParts * sizeof(double))
-        return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, kMaxParts * sizeof(double));
+    if (!ws || ws_bytes < kMaxParts * sizeof(float))
+        return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, kMaxParts * sizeof(float));
     if (reinterpret_cast<uintptr_t>(ws) % 256)
         return record_error(MXFP4_ERR_MISALIGNED, "%s: workspace not 256-byte aligned", what);
     mxfp4_status st = ensure_device();
@@ -266,14 +321,11 @@ extern "C" mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, flo
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     const int ctas = std::min(kMaxParts, sms * kClipCtasPerSm);
-    // Chunks of kMaxChunk elements where there is enough work, shorter ones (down to one vector
-    // a thread) where that spreads a short call over more CTAs, longer ones past 2^45 elements
-    // in sight of the 32-bit chunk index.
-    int chunk_log2 = 11;
-    while ((int64_t(1) << chunk_log2) < kMaxChunk && (total >> chunk_log2) > 2 * ctas) ++chunk_log2;
-    while ((total >> chunk_log2) > (int64_t(1) << 30)) ++chunk_log2;
-    static_assert(kMinChunk == 1 << 11 && kMinChunk == 8 * kClipThreads, "one vector a thread");
-    double* part = static_cast<double*>(ws);
+    // Chunks of kBatch units a thread where there is work enough, shorter ones where that spreads a
+    // short call over more CTAs.
+    int chunk_log2 = kMinChunk;
+    while (chunk_log2 < kMaxChunk && (total * 4 >> chunk_log2) > 2 * ctas) ++chunk_log2;
+    float* part = static_cast<float*>(ws);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     e = n <= kSmallTable ? launch_clip<kSmallTable>(grads, n, chunk_log2, ctas, max_norm, norm, part, s)
                          : launch_clip<kLargeTable>(grads, n, chunk_log2, ctas, max_norm, norm, part, s);

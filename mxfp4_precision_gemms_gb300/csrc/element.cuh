@@ -1,6 +1,8 @@
 // element.cuh -- typed element access shared by the memory-bound kernels (embedding,
-// gradient clipping, the cross entropy's gather and scatter): eight elements of bf16 or
-// fp32 as 16-byte vectors, or one at a time where rows are not 16-byte aligned.
+// gradient clipping, the cross entropy's gather and scatter): eight elements at a time --
+// bf16 as one 16-byte, fp32 as one 32-byte access -- or one where rows are not aligned to that.
+// (fp32 as two 16-byte accesses leaves each instruction with half of every 32-byte sector:
+// measured, 5.0 against 6.4 TB/s for a scaled copy of 872 MB.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,31 +25,37 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-    uint4 a, b;
+    float v[8];
 };
 
 __device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16* p) {
     return {*reinterpret_cast<const uint4*>(p)};
 }
 __device__ __forceinline__ Raw8<float> load8(const float* p) {
-    return {reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<const uint4*>(p)[1]};
+    Raw8<float> r;
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[2]), "=f"(r.v[3]), "=f"(r.v[4]), "=f"(r.v[5]), "=f"(r.v[6]),
+                   "=f"(r.v[7])
+                 : "l"(p)
+                 : "memory");
+    return r;
 }
 __device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
     v[0] = bf16_lo(r.a.x), v[1] = bf16_hi(r.a.x), v[2] = bf16_lo(r.a.y), v[3] = bf16_hi(r.a.y);
     v[4] = bf16_lo(r.a.z), v[5] = bf16_hi(r.a.z), v[6] = bf16_lo(r.a.w), v[7] = bf16_hi(r.a.w);
 }
 __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
-    v[0] = __uint_as_float(r.a.x), v[1] = __uint_as_float(r.a.y), v[2] = __uint_as_float(r.a.z),
-    v[3] = __uint_as_float(r.a.w), v[4] = __uint_as_float(r.b.x), v[5] = __uint_as_float(r.b.y),
-    v[6] = __uint_as_float(r.b.z), v[7] = __uint_as_float(r.b.w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = r.v[j];
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -60,9 +68,10 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int is64, int64_t i)
 }
 
 // Whether every row of a matrix (ld elements of esz bytes apart, dim long) can be moved in
-// units of eight elements.
+// units of eight
+// elements.
 inline bool vector_rows(const void* p, int64_t ld, int64_t dim, int64_t esz) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * esz % 16 == 0 && dim % 8 == 0;
+    return reinterpret_cast<uintptr_t>(p) % (8 * esz) == 0 && ld % 8 == 0 && dim % 8 == 0;
 }
 
 }  // namespace mx

@@ -12,12 +12,12 @@
 //      least-significant-digit radix sort of 9 bits a pass (two passes up to 262143 ids): each
 //      warp owns a contiguous run of tokens and counts its digits with match.any, so that the
 //      order within a digit is the order of the tokens.  The other clusters of the launch
-//      meanwhile clear the table with bulk copies of a zeroed shared-memory buffer.
+//      meanwhile clear the table.
 //   2. Sum.  The sorted tokens are cut into chunks of kChunk.  A CTA owns one chunk and one slab
 //      of columns and adds its rows up in registers; a row of the table whose tokens all lie in
 //      the chunk is finished there.  A run that crosses a chunk's border leaves an fp32 partial
 //      sum, so a very frequent token is shared out over many CTAs.
-//   3. Join.  Where a crossing run starts, its partial sums are added in chunk order.
+//   3. Join.  The partial sums of each crossing run are added in chunk order.
 // Which additions are made in which order depends on the ids alone, never on timing.
 #include <algorithm>
 
@@ -87,8 +87,17 @@ constexpr int kBits = 9;
 constexpr int kBins = 1 << kBits;
 // counters [warp][bin], this CTA's bin totals, the cluster-wide offsets, scan scratch
 constexpr int kSortSmem = (kSortWarps * kBins + 2 * kBins + 32) * 4;
-constexpr uint32_t kClearBytes = 32 * 1024;  // zeroed buffer of a clearing CTA (inside the same shared memory)
-static_assert(kClearBytes <= kSortSmem, "shared memory");
+// Bytes that a clearing CTA clears, two 16-byte stores a thread.  CTAs that each clear one stretch and
+// end keep the stores in address order: 7.65 TB/s over a 1.05 GB table, where persistent CTAs
+// reached 6.4 with plain stores and 6.3 to 6.9 with bulk copies of a zeroed buffer.
+constexpr int64_t kClearBytes = 2 * 16 * kSortThreads;
+constexpr int kSortItems = 4;  // tokens of a lane that are loaded together
+constexpr int kChunk = 32;     // sorted tokens of a chunk
+
+// A run of one id that crosses a chunk's border: its first chunk, and the one behind its last.
+struct Run {
+    uint32_t key, first, end;
+};
 
 struct SortParams {
     const void* ids;
@@ -97,11 +106,14 @@ struct SortParams {
     uint32_t tokens;
     int64_t vocab, padding_id;
     uint2* buf[2];  // (key, token); the last pass writes buf[0]
+    Run* runs;
+    uint32_t* num_runs;
     uint32_t* status;
     // clearing: rows of row_bytes, pitch_bytes apart
     uint8_t* dw;
     int64_t rows, row_bytes, pitch_bytes;
-    int32_t clear_vec;  // 16-byte aligned rows
+    int32_t clear_flat;  // contiguous and 16-byte aligned: one run of bytes
+    int32_t clear_vec;   // 16-byte aligned rows of a multiple of 16 bytes
 };
 
 // The key that a token sorts by: its id, or `vocab` (behind every row) when it is left out.
@@ -122,6 +134,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 
 __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
+    if (p.tokens == 0) return;  // nothing to sort, and no workspace: the launch only clears
     uint32_t* count = smem;                       // [kSortWarps][kBins]
     uint32_t* total = count + kSortWarps * kBins;  // [kBins]
     uint32_t* base = total + kBins;                // [kBins]
@@ -141,17 +154,24 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
         uint2* out = p.buf[(p.passes - pass - 1) & 1];
         for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) count[i] = 0;
         __syncthreads();
-        for (uint32_t t0 = begin; t0 < end; t0 += 32) {
-            const uint32_t t = t0 + lane;
-            const bool on = t < end;
-            const uint32_t mask = __ballot_sync(0xffffffffu, on);
-            if (on) {
-                const uint32_t key = pass == 0 ? token_key(p, t) : __ldcg(&in[t]).x;
-                const uint32_t d = (key >> shift) & (kBins - 1);
-                const uint32_t peers = __match_any_sync(mask, d);
-                if ((peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+        for (uint32_t t0 = begin; t0 < end; t0 += 32 * kSortItems) {
+            uint32_t key[kSortItems];
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                const uint32_t t = t0 + k * 32 + lane;
+                key[k] = t < end ? (pass == 0 ? token_key(p, t) : __ldcg(&in[t]).x) : 0u;
             }
-            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                const bool on = t0 + k * 32 + lane < end;
+                const uint32_t mask = __ballot_sync(0xffffffffu, on);
+                if (on) {
+                    const uint32_t d = (key[k] >> shift) & (kBins - 1);
+                    const uint32_t peers = __match_any_sync(mask, d);
+                    if ((peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+                }
+                __syncwarp();
+            }
         }
         __syncthreads();
         if (tid < kBins) {  // exclusive over the warps of this CTA
@@ -192,71 +212,107 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
             base[tid] = lower + inc - all + before;
         }
         __syncthreads();
-        for (uint32_t t0 = begin; t0 < end; t0 += 32) {
-            const uint32_t t = t0 + lane;
-            const bool on = t < end;
-            const uint32_t mask = __ballot_sync(0xffffffffu, on);
-            uint32_t d = 0, peers = 0, at = 0;
-            if (on) {
-                const uint2 kv = pass == 0 ? make_uint2(token_key(p, t), t) : __ldcg(&in[t]);
-                d = (kv.x >> shift) & (kBins - 1);
-                peers = __match_any_sync(mask, d);
-                at = base[d] + mine[d] + __popc(peers & ((1u << lane) - 1));
-                out[at] = kv;
+        for (uint32_t t0 = begin; t0 < end; t0 += 32 * kSortItems) {
+            uint2 kv[kSortItems];
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                const uint32_t t = t0 + k * 32 + lane;
+                kv[k] = t < end ? (pass == 0 ? make_uint2(token_key(p, t), t) : __ldcg(&in[t])) : make_uint2(0u, 0u);
             }
-            __syncwarp();
-            if (on && (peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
-            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                const bool on = t0 + k * 32 + lane < end;
+                const uint32_t mask = __ballot_sync(0xffffffffu, on);
+                uint32_t d = 0, peers = 0;
+                if (on) {
+                    d = (kv[k].x >> shift) & (kBins - 1);
+                    peers = __match_any_sync(mask, d);
+                    out[base[d] + mine[d] + __popc(peers & ((1u << lane) - 1))] = kv[k];
+                }
+                __syncwarp();
+                if (on && (peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
+                __syncwarp();
+            }
         }
         // The pass's output is visible to the whole cluster, and no CTA's totals are still
         // being read, before the next pass starts.
         cluster_sync();
     }
+    if (rank != 0) return;
+    // The runs that cross a chunk's border, in the order of their ids.
+    const uint2* sorted = p.buf[0];
+    const uint32_t chunks = (p.tokens + kChunk - 1) / kChunk;
+    uint32_t found = 0;
+    for (uint32_t c0 = 0; c0 + 1 < chunks; c0 += kSortThreads) {
+        const uint32_t c = c0 + tid;
+        bool starts = false;
+        uint32_t key = 0;
+        if (c + 1 < chunks) {  // the last key of chunk c goes on in the next, and did not come from the one before
+            key = __ldcg(&sorted[(uint64_t)c * kChunk + kChunk - 1]).x;
+            starts = key != (uint32_t)p.vocab && __ldcg(&sorted[(uint64_t)(c + 1) * kChunk]).x == key &&
+                     (c == 0 || __ldcg(&sorted[(uint64_t)c * kChunk - 1]).x != key);
+        }
+        const uint32_t votes = __ballot_sync(0xffffffffu, starts);
+        __syncthreads();  // the round before has read wsum
+        if (lane == 0) wsum[warp] = __popc(votes);
+        __syncthreads();
+        uint32_t lower = 0, all = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            lower += w < warp ? wsum[w] : 0u;
+            all += wsum[w];
+        }
+        if (starts) {
+            uint32_t lo = c + 1, hi = chunks;  // the first key of chunk lo is `key`
+            while (hi - lo > 1) {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                if (__ldcg(&sorted[(uint64_t)mid * kChunk]).x == key)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            p.runs[found + lower + __popc(votes & ((1u << lane) - 1))] = {key, c, hi};
+        }
+        found += all;
+    }
+    if (tid == 0) *p.num_runs = found;
 }
 
-// Zeroes the table from CTA `part` of `parts`.
-__device__ void clear_table(const SortParams& p, uint32_t part, uint32_t parts, uint32_t* smem) {
-    const int tid = threadIdx.x;
-    if (!p.clear_vec) {  // rows that are not 16-byte aligned: two-byte stores (every element is a multiple of two)
-        for (int64_t r = part; r < p.rows; r += parts) {
-            uint16_t* row = reinterpret_cast<uint16_t*>(p.dw + r * p.pitch_bytes);
-            for (int64_t i = tid; i < p.row_bytes / 2; i += kSortThreads) row[i] = 0;
+// Zeroes the table's part of CTA `part` of `parts`.
+__device__ __forceinline__ void clear_table(const SortParams& p, uint32_t part, uint32_t parts) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (p.clear_flat) {  // one run of bytes, kClearBytes of it here
+        const int64_t all = p.rows * p.row_bytes;
+        const int64_t at = part * kClearBytes + threadIdx.x * 16;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t o = at + k * 16 * kSortThreads;
+            if (o + 16 <= all)
+                *reinterpret_cast<uint4*>(p.dw + o) = zero;
+            else  // the last bytes of a table that does not fill 16; every element is a multiple of two
+                for (int64_t b = o; b < all; b += 2) *reinterpret_cast<uint16_t*>(p.dw + b) = 0;
         }
         return;
     }
-    for (uint32_t i = tid; i < kClearBytes / 16; i += kSortThreads)
-        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-    fence_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-        if (p.pitch_bytes == p.row_bytes) {
-            const int64_t all = p.rows * p.row_bytes, bytes = all & ~int64_t(15);
-            if (part == 0)  // the last bytes of a table that does not fill 16
-                for (int64_t o = bytes; o < all; o += 2) *reinterpret_cast<uint16_t*>(p.dw + o) = 0;
-            for (int64_t o = (int64_t)part * kClearBytes; o < bytes; o += (int64_t)parts * kClearBytes)
-                bulk_store(p.dw + o, smem, (uint32_t)(bytes - o < kClearBytes ? bytes - o : kClearBytes));
-        } else {
-            for (int64_t r = part; r < p.rows; r += parts)
-                for (int64_t o = 0; o < p.row_bytes; o += kClearBytes)
-                    bulk_store(p.dw + r * p.pitch_bytes + o, smem,
-                               (uint32_t)(p.row_bytes - o < kClearBytes ? p.row_bytes - o : kClearBytes));
-        }
-        bulk_commit();
-        bulk_wait_all();
+    for (int64_t r = part; r < p.rows; r += parts) {
+        uint8_t* row = p.dw + r * p.pitch_bytes;
+        if (p.clear_vec)
+            for (int64_t i = threadIdx.x; i < p.row_bytes / 16; i += kSortThreads) reinterpret_cast<uint4*>(row)[i] = zero;
+        else
+            for (int64_t i = threadIdx.x; i < p.row_bytes / 2; i += kSortThreads) reinterpret_cast<uint16_t*>(row)[i] = 0;
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_clear_kernel(const SortParams p) {
+__global__ void __launch_bounds__(kSortThreads, 2) sort_clear_kernel(const __grid_constant__ SortParams p) {
     extern __shared__ __align__(16) uint32_t smem[];
     grid_dependency_wait();
+    allow_dependent_launch();
     if (blockIdx.x < kSortCtas)
         sort_cluster(p, smem);
     else
-        clear_table(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas, smem);
+        clear_table(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
 }
 
 // ---------------------------------------------------------------- sum and join
-constexpr int kChunk = 32;
 constexpr int kAhead = 8;  // rows loaded before they are added
 constexpr int kSumThreads = 128;
 
@@ -267,6 +323,9 @@ struct SumParams {
     float scale;
     int32_t accumulate;
     float* part;  // [chunks][2][dim]: a run that came in from the left, a run that goes out to the right
+    const Run* runs;
+    const uint32_t* num_runs;
+    uint32_t chunks;
 };
 
 template <class DW>
@@ -294,7 +353,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
     constexpr int U = VEC ? 8 : 1;
     __shared__ uint2 kv[kChunk + 2];  // with the neighbours' keys on both sides
     grid_dependency_wait();
-    const uint32_t chunk = blockIdx.x;
+    allow_dependent_launch();
+    const uint32_t slab = blockIdx.x / p.chunks, chunk = blockIdx.x - slab * p.chunks;
     const uint32_t begin = chunk * kChunk;
     const uint32_t n = min((uint32_t)kChunk, p.tokens - begin);
     for (int i = threadIdx.x; i < (int)n + 2; i += kSumThreads) {
@@ -302,7 +362,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
         kv[i] = at >= 0 && at < p.tokens ? p.sorted[at] : make_uint2(0xffffffffu, 0);
     }
     __syncthreads();
-    const int64_t col = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * U;
+    const int64_t col = ((int64_t)slab * kSumThreads + threadIdx.x) * U;
     if (col >= p.dim || kv[1].x == (uint32_t)p.vocab) return;
 
     float acc[U] = {};
@@ -355,63 +415,49 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
     }
 }
 
-// Joins the run that starts in chunk blockIdx.x and goes out to the right: kJoinGroups
-// groups of lanes take the following chunks in turn, and their sums are added in group order.
+// Joins the crossing runs, one run and one slab of columns at a time: kJoinGroups groups of
+// lanes take the run's chunks in turn, and their sums are added in group order.
 constexpr int kJoinGroups = 8;
 constexpr int kJoinThreads = kJoinGroups * 32;
 
 template <class DW, bool VEC>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, DW* dw) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, DW* dw, uint32_t slabs) {
     constexpr int U = VEC ? 4 : 1;
     __shared__ float part[kJoinGroups][32 * U];
-    __shared__ uint32_t run_end;
     grid_dependency_wait();
-    const uint32_t chunk = blockIdx.x;
-    const uint32_t last = chunk * kChunk + kChunk - 1;  // the grid has no block for the last chunk
-    const uint32_t key = p.sorted[last].x;
-    if (key == (uint32_t)p.vocab || p.sorted[last + 1].x != key) return;
-    if (chunk > 0 && p.sorted[chunk * kChunk - 1].x == key) return;  // it started further left
-    // the first chunk behind the run: chunks whose first key is `key` hold partial sums of it
-    const uint32_t chunks = (p.tokens + kChunk - 1) / kChunk;
-    if (threadIdx.x == 0) {
-        uint32_t lo = chunk + 1, hi = chunks;  // first key of lo is `key`
-        while (hi - lo > 1) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (p.sorted[(uint64_t)mid * kChunk].x == key)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        run_end = hi;
-    }
-    __syncthreads();
-    const uint32_t end = run_end;
+    allow_dependent_launch();
+    const uint64_t items = (uint64_t)*p.num_runs * slabs;
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int64_t col = ((int64_t)blockIdx.y * 32 + lane) * U;
-    float acc[U] = {};
-    if (col < p.dim) {
-        // chunk c of the run: slot 1 (going out) where it starts, slot 0 (coming in) after that
+    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t slab = (uint32_t)(item % slabs);
+        const Run run = p.runs[item / slabs];
+        const int64_t col = ((int64_t)slab * 32 + lane) * U;
+        float acc[U] = {};
+        if (col < p.dim) {
+            // chunk c of the run: slot 1 (going out) where it starts, slot 0 (coming in) after that
 #pragma unroll 4
-        for (uint32_t c = chunk + g; c < end; c += kJoinGroups) {
-            const float* src = p.part + ((int64_t)c * 2 + (c == chunk ? 1 : 0)) * p.dim + col;
-            if constexpr (VEC) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-            } else {
-                acc[0] += src[0];
+            for (uint32_t c = run.first + g; c < run.end; c += kJoinGroups) {
+                const float* src = p.part + ((int64_t)c * 2 + (c == run.first ? 1 : 0)) * p.dim + col;
+                if constexpr (VEC) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+                } else {
+                    acc[0] += src[0];
+                }
             }
         }
-    }
+        __syncthreads();  // the item before has been read
 #pragma unroll
-    for (int j = 0; j < U; ++j) part[g][lane * U + j] = acc[j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * U; i += kJoinThreads) {
-        const int64_t c = (int64_t)blockIdx.y * 32 * U + i;
-        if (c >= p.dim) break;
-        float sum = 0.f;
+        for (int j = 0; j < U; ++j) part[g][lane * U + j] = acc[j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * U; i += kJoinThreads) {
+            const int64_t at = (int64_t)slab * 32 * U + i;
+            if (at >= p.dim) break;
+            float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kJoinGroups; ++k) sum += part[k][i];
-        finish(dw + (int64_t)key * p.lddw + c, sum, p);
+            for (int k = 0; k < kJoinGroups; ++k) sum += part[k][i];
+            finish(dw + (int64_t)run.key * p.lddw + at, sum, p);
+        }
     }
 }
 
@@ -428,32 +474,42 @@ cudaError_t launch_lookup(const void* ids, int is64, int64_t tokens, const void*
                              (uint32_t)segs, device_status_ptr());
 }
 
-template <class DY, class DW, bool VEC>
-cudaError_t launch_sum(const SumParams& p, const void* dy, void* dw, cudaStream_t s) {
-    constexpr int per = kSumThreads * (VEC ? 8 : 1);
-    const unsigned chunks = (p.tokens + kChunk - 1) / kChunk;
-    cudaError_t e = launch_overlapped(sum_kernel<DY, DW, VEC>, dim3(chunks, (unsigned)((p.dim + per - 1) / per)),
-                                      dim3(kSumThreads), 0, s, 1, true, p, static_cast<const DY*>(dy),
-                                      static_cast<DW*>(dw));
-    if (e != cudaSuccess || chunks < 2) return e;
-    constexpr int per_join = VEC ? 128 : 32;
-    return launch_overlapped(join_kernel<DW, VEC>, dim3(chunks - 1, (unsigned)((p.dim + per_join - 1) / per_join)),
-                             dim3(kJoinThreads), 0, s, 1, true, p, static_cast<DW*>(dw));
+cudaError_t sm_count(int* sms) {
+    static DeviceSlots slots;
+    return per_device_setting(slots, sms, [&](int dev, int* n) {
+        return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    });
 }
 
-cudaError_t launch_sort(const SortParams& p, bool clear, cudaStream_t s) {
+template <class DY, class DW, bool VEC>
+cudaError_t launch_sum(SumParams p, const void* dy, void* dw, int sms, cudaStream_t s) {
+    constexpr int per = kSumThreads * (VEC ? 8 : 1);
+    p.chunks = (p.tokens + kChunk - 1) / kChunk;
+    const int64_t ctas = (int64_t)p.chunks * ((p.dim + per - 1) / per);
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaError_t e = launch_overlapped(sum_kernel<DY, DW, VEC>, dim3((unsigned)ctas), dim3(kSumThreads), 0, s, 1, true, p,
+                                      static_cast<const DY*>(dy), static_cast<DW*>(dw));
+    if (e != cudaSuccess || p.chunks < 2) return e;
+    constexpr int per_join = VEC ? 128 : 32;
+    const uint32_t slabs = (uint32_t)((p.dim + per_join - 1) / per_join);
+    const int64_t most = (int64_t)(p.chunks - 1) * slabs;  // runs are at most one for each border
+    return launch_overlapped(join_kernel<DW, VEC>, dim3((unsigned)std::min<int64_t>(most, 4 * sms)), dim3(kJoinThreads),
+                             0, s, 1, true, p, static_cast<DW*>(dw), slabs);
+}
+
+cudaError_t launch_sort(const SortParams& p, bool clear, int sms, cudaStream_t s) {
     static DeviceSlots slots;
-    int sms = 0;
-    cudaError_t e = per_device_setting(slots, &sms, [&](int dev, int* n) {
-        cudaError_t r =
-            cudaFuncSetAttribute(sort_clear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-        return r != cudaSuccess ? r : cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    int set = 0;
+    cudaError_t e = per_device_setting(slots, &set, [&](int, int* n) {
+        *n = 1;
+        return cudaFuncSetAttribute(sort_clear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     });
     if (e != cudaSuccess) return e;
-    // two CTAs fit an SM; the clearing ones cover the device beside the sorting cluster
-    const int64_t clear_ctas = std::min<int64_t>((p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes, 2 * sms);
-    const unsigned clusters = 1 + (clear ? (unsigned)((clear_ctas + kSortCtas - 1) / kSortCtas) : 0u);
-    return launch_overlapped(sort_clear_kernel, dim3(clusters * kSortCtas), dim3(kSortThreads), kSortSmem, s, kSortCtas,
+    const int64_t stretches = (p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes;
+    const int64_t clear_ctas = p.clear_flat ? stretches : std::min<int64_t>(stretches, 8 * sms);
+    const int64_t clusters = 1 + (clear ? (clear_ctas + kSortCtas - 1) / kSortCtas : 0);
+    if (clusters * kSortCtas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(sort_clear_kernel, dim3((unsigned)(clusters * kSortCtas)), dim3(kSortThreads), kSortSmem, s, kSortCtas,
                              true, p);
 }
 
@@ -471,6 +527,9 @@ int sort_passes(int64_t vocab) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 size_t sorted_bytes(int64_t tokens) { return up256((size_t)tokens * sizeof(uint2)); }
+size_t chunks_of(int64_t tokens) { return (size_t)((tokens + kChunk - 1) / kChunk); }
+// the number of runs (16 bytes) and the runs
+size_t runs_bytes(int64_t tokens) { return up256(16 + chunks_of(tokens) * sizeof(Run)); }
 
 mxfp4_status check_table(const char* what, int ids_dtype, int64_t tokens, int64_t vocab, int64_t dim) {
     if (ids_dtype != MXFP4_IDS_I32 && ids_dtype != MXFP4_IDS_I64)
@@ -530,8 +589,7 @@ extern "C" mxfp4_status mxfp4_embedding(const void* ids, int ids_dtype, int64_t 
 
 extern "C" size_t mxfp4_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
     if (tokens <= 0 || vocab <= 0 || dim <= 0 || tokens > INT32_MAX || vocab >= INT32_MAX || dim > kMaxDim) return 0;
-    const size_t chunks = (size_t)((tokens + kChunk - 1) / kChunk);
-    return 2 * sorted_bytes(tokens) + up256(chunks * 2 * (size_t)dim * sizeof(float));
+    return 2 * sorted_bytes(tokens) + runs_bytes(tokens) + up256(chunks_of(tokens) * 2 * (size_t)dim * sizeof(float));
 }
 
 extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int64_t tokens, const void* dy,
@@ -574,15 +632,21 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     uint8_t* at = static_cast<uint8_t*>(ws);
     sp.buf[0] = reinterpret_cast<uint2*>(at);
     sp.buf[1] = tokens > 0 ? reinterpret_cast<uint2*>(at + sorted_bytes(tokens)) : nullptr;
+    if (tokens > 0) {
+        sp.num_runs = reinterpret_cast<uint32_t*>(at + 2 * sorted_bytes(tokens));
+        sp.runs = reinterpret_cast<Run*>(at + 2 * sorted_bytes(tokens) + 16);
+    }
     sp.status = device_status_ptr();
     sp.dw = static_cast<uint8_t*>(dw);
     sp.rows = vocab;
     sp.row_bytes = dim * wsz;
     sp.pitch_bytes = lddw * wsz;
-    // a contiguous table is cleared as one run of bytes, whatever its rows' length
-    sp.clear_vec = reinterpret_cast<uintptr_t>(dw) % 16 == 0 &&
-                   (sp.pitch_bytes == sp.row_bytes || (sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0));
-    cudaError_t e = launch_sort(sp, !accumulate, s);
+    const bool base16 = reinterpret_cast<uintptr_t>(dw) % 16 == 0;
+    sp.clear_flat = base16 && sp.pitch_bytes == sp.row_bytes;
+    sp.clear_vec = base16 && sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = launch_sort(sp, !accumulate, sms, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s sort launch: %s", what, cudaGetErrorString(e));
     if (tokens == 0) return record_error(MXFP4_OK, "%s", "");
 
@@ -595,12 +659,14 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     p.lddw = lddw;
     p.scale = scale;
     p.accumulate = accumulate;
-    p.part = reinterpret_cast<float*>(at + 2 * sorted_bytes(tokens));
+    p.runs = sp.runs;
+    p.num_runs = sp.num_runs;
+    p.part = reinterpret_cast<float*>(at + 2 * sorted_bytes(tokens) + runs_bytes(tokens));
     const bool vec = vector_rows(dy, lddy, dim, esize(dy_dtype)) && vector_rows(dw, lddw, dim, wsz);
     auto go = [&](auto yt, auto wt) {
         using DY = decltype(yt);
         using DW = decltype(wt);
-        return vec ? launch_sum<DY, DW, true>(p, dy, dw, s) : launch_sum<DY, DW, false>(p, dy, dw, s);
+        return vec ? launch_sum<DY, DW, true>(p, dy, dw, sms, s) : launch_sum<DY, DW, false>(p, dy, dw, sms, s);
     };
     const bool yb = dy_dtype == MXFP4_OUT_BF16, wb = dw_dtype == MXFP4_OUT_BF16;
     e = yb ? (wb ? go(bf16{}, bf16{}) : go(bf16{}, float{})) : (wb ? go(float{}, bf16{}) : go(float{}, float{}));

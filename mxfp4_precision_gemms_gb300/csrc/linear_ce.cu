@@ -11,8 +11,8 @@
 // All of them are compute-bound for T above a few hundred tokens; for few tokens the read of w (and
 // the write of dw) from HBM bounds them.
 //
-//   gather    copies the counted rows of h together (ignored rows are never read, so what they
-//             hold cannot reach a sum, and cost no multiplication), zero-fills up to a tile's rows
+//   gather    copies the counted rows of h together: ignored rows cost no multiplication, and what they
+//             hold cannot reach a sum (left out before the loss of at most 256 tokens)
 //   stats     logits tile by tile; each thread reduces 128 columns of one row to (max, sum)
 //   combine   joins the tiles' statistics, writes lse and the losses
 //   dlogits   logits of one piece again -> dz in bf16
@@ -61,11 +61,21 @@ static_assert(kOffBox % 1024 == 0 && kOffBar % 8 == 0, "alignment");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// What the gather kernel leaves for the others.
+// What the gather kernel leaves for the others.  The forward pass of at most one tile of tokens has
+// none: its rows are read where they lie (a row's values reach no other row's logits).
 struct Header {
     int32_t count;  // tokens that count
     float gscale;   // factor that every token's gradient shares
 };
+
+// Read as volatile, by value: as an lvalue next to a kernel parameter in a conditional expression it
+// would make the parameter's own read volatile too, which parameter memory does not take (a fault).
+__device__ __forceinline__ int32_t counted_tokens(const Header* h) {
+    return *reinterpret_cast<const volatile int32_t*>(&h->count);
+}
+__device__ __forceinline__ float shared_factor(const Header* h) {
+    return *reinterpret_cast<const volatile float*>(&h->gscale);
+}
 
 // One matrix product C[M, N] (+)= A[M, K] . B[N, K]^T, or a launch's share of two.
 struct Product {
@@ -74,6 +84,7 @@ struct Product {
     int32_t m_counted;      // M is the number of counted tokens (rounded up to a tile)
     int32_t k_counted;      // K is the number of counted tokens
     int32_t M, N, K;
+    int32_t tile_n;         // columns of a tile: kTile, or less where N divides better (a multiple of 32)
     int32_t splits;         // K is cut into this many parts, each with its own output
     int32_t k_per_split;    // stages of a part
     int32_t slot_rows;      // rows of C between the parts' outputs
@@ -85,7 +96,10 @@ struct CeParams {
     Product prod[2];
     int32_t count;
     const Header* header;
-    const int32_t* target;  // [rows] of the counted tokens, relative to nothing: vocabulary index
+    const int32_t* target;  // [rows] targets of the counted tokens
+    // forward pass without a gather: all tokens are rows, their targets as the caller has them
+    int32_t direct, tokens, is64;
+    const void* targets;
     int32_t col0;           // first vocabulary index of this launch's columns
     int32_t rows;           // pitch of the statistics: padded token count
     float2* stats;          // [tile * 2 + half][rows]: (max * log2 e, sum of 2^(z log2 e - max))
@@ -113,6 +127,13 @@ struct Tile {
     int32_t m0, n0, k0, stages, slot;
 };
 
+// A tile's columns for N columns in all: as few tiles as 256-column ones, cut evenly.  The MMA's time
+// goes with the columns (dim = 1032: five tiles of 224 instead of 256, an eighth less).
+inline int32_t even_tile(int64_t n) {
+    const int64_t tiles = (n + kTile - 1) / kTile;
+    return (int32_t)(((n + tiles - 1) / tiles + 31) / 32 * 32);
+}
+
 // Where tile `t` of the launch lies; false past the last one.  Within a product, consecutive
 // tiles (which run at the same time) walk the dimension with fewer tiles first: the operand along
 // it is read in every wave and stays in L2 while the other one streams through once.
@@ -131,10 +152,10 @@ __device__ __forceinline__ bool locate(const CeParams& p, int32_t count, int64_t
             out.slot = slot;
             if (num_n > num_m) {
                 out.m0 = (lt % num_m) * kTile;
-                out.n0 = (lt / num_m) * kTile;
+                out.n0 = (lt / num_m) * q.tile_n;
             } else {
                 out.m0 = (lt / num_n) * kTile;
-                out.n0 = (lt % num_n) * kTile;
+                out.n0 = (lt % num_n) * q.tile_n;
             }
             const int32_t k = q.k_counted ? max(count, 1) : q.K;
             const int32_t all = (k + kK - 1) / kK;
@@ -233,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     // The set-up above touches no global memory, so it overlaps the previous kernel.
     grid_dependency_wait();
     allow_dependent_launch();
-    const int32_t count = *reinterpret_cast<const volatile int32_t*>(&p.header->count);
+    int32_t count = p.tokens;
+    if (KIND != kStats || !p.direct) count = counted_tokens(p.header);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs)
@@ -247,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             Tile t;
             for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
                 const Product& q = p.prod[t.prob];
-                const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * 128;
+                const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * (q.tile_n / 2);
                 for (int32_t i = 0; i < t.stages; ++i) {
                     if (round > 0 && !wait_bounded(&empty[s], (round - 1) & 1u, p.wait_ns, p.status)) {
                         ok = false;
@@ -297,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 Tile t;
                 for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
                     const Product& q = p.prod[t.prob];
-                    const uint32_t idesc = idesc_bf16(256, 256, q.a_mn != 0, q.b_mn != 0);
+                    const uint32_t idesc = idesc_bf16(256, (uint32_t)q.tile_n, q.a_mn != 0, q.b_mn != 0);
                     // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
                     // Between 64-column blocks of M / N: half a stage's operand.
                     const uint32_t a_step = q.a_mn ? 2048 : 32, b_step = q.b_mn ? 2048 : 32;
@@ -348,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
         const int half = (warp - 2) >> 2;
         Boxes boxes{smem + kOffBox + (warp - 2) * kBoxes * kBoxBytes, 0};
         const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
-        const float gscale = KIND == kProducts ? *reinterpret_cast<const volatile float*>(&p.header->gscale) : 1.f;
+        float gscale = 1.f;
+        if constexpr (KIND == kProducts) gscale = shared_factor(p.header);
         uint32_t tcount = 0;
         bool ok = true;
         Tile t;
@@ -361,7 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             int32_t tgt = -1;
             float lse2 = 0.f, ratio = 0.f;
             if constexpr (KIND != kProducts) {
-                tgt = __ldcg(p.target + row) - p.col0;
+                if (KIND == kStats && p.direct) {  // one that does not count hits no column, or its value is not used
+                    const int64_t y = row < count ? load_id(p.targets, p.is64, row) : -1;
+                    tgt = y >= 0 && y < q.N ? (int32_t)y : -1;
+                } else {
+                    tgt = __ldcg(p.target + row) - p.col0;
+                }
                 if constexpr (KIND == kDlogits) {
                     lse2 = __ldcg(p.lse2 + row);
                     ratio = __ldcg(p.ratio + row);
@@ -449,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
                     }
                     const int32_t col = c0 + c * 32;
+                    if (KIND == kProducts && half * 128 + c * 32 >= q.tile_n) continue;  // past a narrow tile's columns
                     if constexpr (KIND == kDlogits) {
                         const int32_t hit = tgt - col;
                         uint32_t w[16];
@@ -623,11 +652,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
         }
         before += all;
     }
-    // rows up to the end of the last tile: zeros that count for nothing
-    const int32_t padded = pad_rows(total);
+    // Behind the counted rows: their dz is 0 up to the end of the last tile, whatever their logits are,
+    // but rows that share dw's last stage with them are multiplied by that 0 and must be finite.
+    const int32_t padded = pad_rows(total), stage_end = (max(total, 1) + kK - 1) / kK * kK;
     for (int32_t r = total + (int32_t)blockIdx.x * kGatherWarps + warp; r < padded; r += (int32_t)gridDim.x * kGatherWarps) {
-        bf16* dst = p.rows + (int64_t)r * p.dim;
-        for (int u = lane; u < units; u += 32) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0, 0, 0, 0);
+        if (GRAD && r < stage_end) {
+            bf16* dst = p.rows + (int64_t)r * p.dim;
+            for (int u = lane; u < units; u += 32) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0, 0, 0, 0);
+        }
         if (lane == 0) {
             p.target[r] = -1;
             if constexpr (GRAD) p.lse2[r] = 0.f, p.ratio[r] = 0.f;
@@ -637,20 +669,34 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 
 // ---------------------------------------------------------------- combine
 constexpr int kCombineThreads = 256;
+constexpr int kCombineRows = 8;  // 64 bytes of each tile's statistics
+constexpr int kCombineGroups = kCombineThreads / kCombineRows;
 
-// ROWS rows per CTA, 256 / ROWS threads to each.
-template <int ROWS>
-__global__ void __launch_bounds__(kCombineThreads)
-    combine_kernel(const Header* header, const float2* stats, int32_t parts, int32_t rows, const float* target_logit,
-                   const int32_t* source, float* lse_out, float* loss) {
-    constexpr int GROUPS = kCombineThreads / ROWS;
-    __shared__ float2 sh[GROUPS][ROWS];
+struct CombineParams {
+    const Header* header;
+    const float2* stats;
+    int32_t parts, rows;
+    const float* target_logit;
+    const int32_t* source;
+    float* lse;
+    float* loss;
+    // without a gather: the tokens' own targets decide what counts
+    int32_t direct, tokens, vocab, is64;
+    const void* targets;
+    int64_t ignore;
+    uint32_t* status;
+};
+
+// kCombineRows rows per CTA, a group of threads to each: the walk over the tiles is a chain of loads.
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
+    __shared__ float2 sh[kCombineThreads / 32][kCombineRows];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int32_t count = *reinterpret_cast<const volatile int32_t*>(&header->count);
-    const int r = threadIdx.x % ROWS, g = threadIdx.x / ROWS;
-    const int32_t row = blockIdx.x * ROWS + r;
-    if ((int32_t)blockIdx.x * ROWS >= count) return;
+    int32_t count = p.tokens;
+    if (!p.direct) count = counted_tokens(p.header);
+    const int r = threadIdx.x % kCombineRows, g = threadIdx.x / kCombineRows;
+    const int32_t row = blockIdx.x * kCombineRows + r;
+    if ((int32_t)blockIdx.x * kCombineRows >= count) return;
     float m = -INFINITY, s = 0.f;
     auto join = [&](float2 o) {
         const float top = fmaxf(m, o.x);
@@ -659,37 +705,67 @@ __global__ void __launch_bounds__(kCombineThreads)
         m = top;
     };
     if (row < count) {
-        int32_t i = g;
-        for (; i + 3 * GROUPS < parts; i += 4 * GROUPS) {  // four loads in flight
-            float2 o[4];
+        constexpr int kFlight = 8;  // loads in flight
+        for (int32_t i = g; i < p.parts; i += kFlight * kCombineGroups) {
+            float2 o[kFlight];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = __ldcg(&stats[(int64_t)(i + k * GROUPS) * rows + row]);
+            for (int k = 0; k < kFlight; ++k) {
+                const int32_t at = i + k * kCombineGroups;
+                o[k] = at < p.parts ? __ldcg(&p.stats[(int64_t)at * p.rows + row]) : make_float2(-INFINITY, 0.f);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) join(o[k]);
+            for (int k = 0; k < kFlight; ++k) join(o[k]);
         }
-        for (; i < parts; i += GROUPS) join(__ldcg(&stats[(int64_t)i * rows + row]));
     }
-    sh[g][r] = make_float2(m, s);
+    // Groups are joined pairwise: lanes 8 and 16 apart, then the warps in order.
+#pragma unroll
+    for (int o = kCombineRows; o < 32; o <<= 1)
+        join(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+    if ((threadIdx.x & 31) < kCombineRows) sh[threadIdx.x >> 5][r] = make_float2(m, s);
     __syncthreads();
-    if (g == 0 && row < count) {
-        for (int k = 1; k < GROUPS; ++k) join(sh[k][r]);
-        const float lse = (m + log2f(s)) * kLn2;
-        const int32_t t = source[row];
-        lse_out[t] = lse;
-        loss[t] = lse - target_logit[row];
+    if (threadIdx.x >= kCombineRows || row >= count) return;
+    m = sh[0][r].x, s = sh[0][r].y;
+#pragma unroll
+    for (int k = 1; k < kCombineThreads / 32; ++k) join(sh[k][r]);
+    float lse = (m + log2f(s)) * kLn2, loss = 0.f;
+    int32_t t = row;
+    bool counts = true;
+    if (p.direct) {
+        const int64_t y = load_id(p.targets, p.is64, row);
+        counts = y != p.ignore && y >= 0 && y < p.vocab;
+        if (!counts && y != p.ignore) atomicOr(p.status, kStatusBadIndex);
+    } else {
+        t = p.source[row];
     }
+    if (counts)
+        loss = lse - p.target_logit[row];
+    else
+        lse = 0.f;
+    p.lse[t] = lse;
+    p.loss[t] = loss;
 }
 
 // Sum or mean of the tokens' losses, in one CTA: a fixed order.
 constexpr int kReduceThreads = 1024;
 __global__ void __launch_bounds__(kReduceThreads)
-    reduce_kernel(const Header* header, const float* loss, int32_t tokens, int32_t mean, float* out) {
+    reduce_kernel(const CombineParams p, int32_t mean, float* out) {
     __shared__ float warp_sum[kReduceThreads / 32];
     grid_dependency_wait();
     allow_dependent_launch();
     float s = 0.f;
 #pragma unroll 4
-    for (int32_t t = threadIdx.x; t < tokens; t += kReduceThreads) s += __ldcg(loss + t);
+    for (int32_t t = threadIdx.x; t < p.tokens; t += kReduceThreads) s += __ldcg(p.loss + t);
+    int32_t count = 0;
+    if (!p.direct) {
+        count = counted_tokens(p.header);
+    } else if (mean) {  // at most one tile of tokens, and the CTA has more threads
+        bool on = false;
+        if (threadIdx.x < p.tokens) {
+            const int64_t y = load_id(p.targets, p.is64, threadIdx.x);
+            on = y != p.ignore && y >= 0 && y < p.vocab;
+        }
+        count = __syncthreads_count(on);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
@@ -698,7 +774,7 @@ __global__ void __launch_bounds__(kReduceThreads)
         s = warp_sum[threadIdx.x];
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (threadIdx.x == 0) out[0] = mean ? s / (float)max(header->count, 1) : s;
+        if (threadIdx.x == 0) out[0] = mean ? s / (float)max(count, 1) : s;
     }
 }
 
@@ -717,7 +793,7 @@ __global__ void __launch_bounds__(kScatterThreads)
     const int32_t u = (int32_t)(wid - t * segs) * 32 + (threadIdx.x & 31);
     if (t >= tokens || u * 8 >= dim) return;
     const int32_t r = place[t];
-    const float gscale = header->gscale;
+    const float gscale = shared_factor(header);
     float v[8] = {};
     if (r >= 0) {
         const float* src = parts + (int64_t)r * dim + u * 8;
@@ -934,67 +1010,89 @@ extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t d
     const Layout l = lay_out(tokens, vocab, dim, false);
     uint8_t* base = static_cast<uint8_t*>(ws);
     float* token_loss = reduced ? reinterpret_cast<float*>(base + l.token_loss) : loss;
-
-    GatherParams g{};
-    g.h = static_cast<const bf16*>(h);
-    g.ldh = ldh;
-    g.tokens = (int32_t)tokens;
-    g.dim = (int32_t)dim;
-    g.vocab = (int32_t)vocab;
-    g.vec = vector_rows(h, ldh, dim, 2);
-    g.targets = targets;
-    g.is64 = ids_dtype == MXFP4_IDS_I64;
-    g.ignore = ignore_index;
-    g.reduction = reduction;
-    g.header = reinterpret_cast<Header*>(base + l.header);
-    g.rows = reinterpret_cast<bf16*>(base + l.rows);
-    g.target = reinterpret_cast<int32_t*>(base + l.target);
-    g.source = reinterpret_cast<int32_t*>(base + l.source);
-    g.place = reinterpret_cast<int32_t*>(base + l.place);
-    g.loss = token_loss;
-    g.lse_out = lse;
-    g.status = device_status_ptr();
+    const int is64 = ids_dtype == MXFP4_IDS_I64;
+    // One tile of tokens that TMA can read: gathering would cost a launch (5 of 31 us for 7 tokens of
+    // a 32000 x 1024 layer) and save no tile.
+    const bool direct = tokens <= kTile && vector_rows(h, ldh, dim, 2);
+    Header* header = reinterpret_cast<Header*>(base + l.header);
 
     CeParams p{};
     Product& q = p.prod[0];
-    if (!encode_bf16_map(&q.map_a, g.rows, l.padded, dim, dim, kK, 128) ||
+    bf16* rows = reinterpret_cast<bf16*>(base + l.rows);
+    if (!(direct ? encode_bf16_map(&q.map_a, h, tokens, dim, ldh, kK, 128)
+                 : encode_bf16_map(&q.map_a, rows, l.padded, dim, dim, kK, 128)) ||
         !encode_bf16_map(&q.map_b, w, vocab, dim, ldw, kK, 128))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     q.m_counted = 1;
     q.M = l.padded;
     q.N = (int32_t)vocab;
+    q.tile_n = kTile;
     q.K = (int32_t)dim;
     q.splits = 1;
     p.count = 1;
-    p.header = g.header;
-    p.target = g.target;
+    p.header = header;
+    p.target = reinterpret_cast<int32_t*>(base + l.target);
+    p.direct = direct;
+    p.tokens = (int32_t)tokens;
+    p.is64 = is64;
+    p.targets = targets;
     p.rows = l.padded;
     p.stats = reinterpret_cast<float2*>(base + l.stats);
     p.target_logit = reinterpret_cast<float*>(base + l.target_logit);
-    p.status = g.status;
+    p.status = device_status_ptr();
     p.wait_ns = wait_limit_ns();
 
-    int grid = 1;
-    cudaError_t e = gather_grid(tokens, &grid);
-    if (e == cudaSuccess)
-        e = launch_overlapped(gather_kernel<false>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
-    if (e != cudaSuccess) return launch_failed(what, "gather", e);
+    cudaError_t e;
+    if (!direct) {
+        GatherParams g{};
+        g.h = static_cast<const bf16*>(h);
+        g.ldh = ldh;
+        g.tokens = (int32_t)tokens;
+        g.dim = (int32_t)dim;
+        g.vocab = (int32_t)vocab;
+        g.vec = vector_rows(h, ldh, dim, 2);
+        g.targets = targets;
+        g.is64 = is64;
+        g.ignore = ignore_index;
+        g.reduction = reduction;
+        g.header = header;
+        g.rows = rows;
+        g.target = reinterpret_cast<int32_t*>(base + l.target);
+        g.source = reinterpret_cast<int32_t*>(base + l.source);
+        g.place = reinterpret_cast<int32_t*>(base + l.place);
+        g.loss = token_loss;
+        g.lse_out = lse;
+        g.status = p.status;
+        int grid = 1;
+        e = gather_grid(tokens, &grid);
+        if (e == cudaSuccess)
+            e = launch_overlapped(gather_kernel<false>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
+        if (e != cudaSuccess) return launch_failed(what, "gather", e);
+    }
     e = launch_matrix<kStats>(p, tiles_of(l.padded, vocab), s);
     if (e != cudaSuccess) return launch_failed(what, "statistics", e);
-    const int32_t parts = (int32_t)((vocab + kTile - 1) / kTile) * 2;
-    // Few rows: more threads to each, since the walk over the parts is a chain of loads.
-    if (tokens <= 1024)
-        e = launch_overlapped(combine_kernel<4>, dim3((unsigned)((tokens + 3) / 4)), dim3(kCombineThreads), 0, s, 1, true,
-                              (const Header*)g.header, (const float2*)p.stats, parts, l.padded,
-                              (const float*)p.target_logit, (const int32_t*)g.source, lse, token_loss);
-    else
-        e = launch_overlapped(combine_kernel<32>, dim3((unsigned)((tokens + 31) / 32)), dim3(kCombineThreads), 0, s, 1,
-                              true, (const Header*)g.header, (const float2*)p.stats, parts, l.padded,
-                              (const float*)p.target_logit, (const int32_t*)g.source, lse, token_loss);
+    CombineParams c{};
+    c.header = header;
+    c.stats = p.stats;
+    c.parts = (int32_t)((vocab + kTile - 1) / kTile) * 2;
+    c.rows = l.padded;
+    c.target_logit = p.target_logit;
+    c.source = reinterpret_cast<int32_t*>(base + l.source);
+    c.lse = lse;
+    c.loss = token_loss;
+    c.direct = direct;
+    c.tokens = (int32_t)tokens;
+    c.vocab = (int32_t)vocab;
+    c.is64 = is64;
+    c.targets = targets;
+    c.ignore = ignore_index;
+    c.status = p.status;
+    e = launch_overlapped(combine_kernel, dim3((unsigned)((tokens + kCombineRows - 1) / kCombineRows)),
+                          dim3(kCombineThreads), 0, s, 1, true, c);
     if (e != cudaSuccess) return launch_failed(what, "combine", e);
     if (reduced) {
-        e = launch_overlapped(reduce_kernel, dim3(1), dim3(kReduceThreads), 0, s, 1, true, (const Header*)g.header,
-                              (const float*)token_loss, (int32_t)tokens, (int32_t)(reduction == MXFP4_REDUCE_MEAN), loss);
+        e = launch_overlapped(reduce_kernel, dim3(1), dim3(kReduceThreads), 0, s, 1, true, c,
+                              (int32_t)(reduction == MXFP4_REDUCE_MEAN), loss);
         if (e != cudaSuccess) return launch_failed(what, "reduce", e);
     }
     return record_error(MXFP4_OK, "%s", "");
@@ -1090,6 +1188,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.m_counted = 1;
             q.M = l.padded;
             q.N = cols;
+            q.tile_n = kTile;
             q.K = (int32_t)dim;
             q.splits = 1;
             q.out_bf16 = 1;
@@ -1110,6 +1209,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.b_mn = 1;
             q.M = l.padded;
             q.N = (int32_t)dim;
+            q.tile_n = even_tile(dim);
             q.K = cols;
             const int32_t stages = (cols + kK - 1) / kK;
             q.k_per_split = (stages + l.splits - 1) / l.splits;
@@ -1129,6 +1229,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.k_counted = 1;
             q.M = cols;
             q.N = (int32_t)dim;
+            q.tile_n = even_tile(dim);
             q.K = l.padded;
             q.splits = 1;
             q.scaled = 1;

@@ -1,7 +1,8 @@
 """Global gradient norm and clipping (mxfp4_clip_grad_norm) against the formula in 64 bits.
-Tolerances: a thread adds at most 64 squares of a chunk in fp32 (two sums of 32, then their sum), so the sum
-of squares is off by less than 40 * 2^-24 of itself and the norm by half of that, plus its rounding to
-fp32; the coefficient adds three roundings, and each output one more (2^-9 of its binade in bf16)."""
+Tolerances: the sum of squares is one of fp32 additions, none of whose chains is longer here than 64 squares of
+a chunk in a thread (two sums of 32), 8 chunks, and trees of 8 levels over a CTA and 8 + 8 over the CTAs: it
+is off by less than 58 * 2^-24 of itself, and the norm by half of that, plus its rounding to fp32; the
+coefficient adds three roundings, and each output one more (2^-9 of its binade in bf16)."""
 import math
 
 import pytest
@@ -10,7 +11,7 @@ from tests.gpu_util import gpu_ready
 
 pytestmark = pytest.mark.gpu
 
-REL = 24 * 2.0 ** -24
+REL = 30 * 2.0 ** -24
 
 
 def _setup():

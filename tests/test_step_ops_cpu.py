@@ -58,8 +58,8 @@ def test_embedding_grad_refuses(L, change, want):
 def test_embedding_grad_workspace(L):
     f = L.mxfp4_embedding_grad_workspace_bytes
     assert f(0, 10, 8) == 0 and f(-1, 10, 8) == 0 and f(4, 10, 1 << 21) == 0
-    # two (id, token) arrays and two fp32 rows for each chunk of 32 tokens
-    assert f(8192, 128256, 4096) == 2 * 8192 * 8 + 256 * 2 * 4096 * 4
+    # two (id, token) arrays, the list of runs, and two fp32 rows for each chunk of 32 tokens
+    assert f(8192, 128256, 4096) == 2 * 8192 * 8 + (16 + 256 * 12 + 255) // 256 * 256 + 256 * 2 * 4096 * 4
 
 
 def _clip(L, entries, n=None, max_norm=1.0, norm=0x5000, ws=0x6000, wsb=None):

@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import array
 import ctypes
+import itertools
+import operator
 import os
 import re
 import threading
@@ -554,6 +556,10 @@ _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 _IDS_OF = {torch.int32: IDS_I32, torch.int64: IDS_I64}
 
 
+_data_ptr, _numel, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+_dtype_of, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+
+
 def _empty(shape, dtype, device, stream):
     """torch.empty for a call on `stream` (None: the current one): the allocator ties a block's
     reuse to the stream it was allocated on."""
@@ -706,16 +712,22 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
     outs = grads if outs is None else outs
     if len(outs) != len(grads):
         raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
-    flat = []
-    for g, o in zip(grads, outs):
-        kind, n = _OUT_OF.get(g.dtype), g.numel()
-        if kind is None or not g.is_cuda or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
-        if o is not g and (o.dtype is not g.dtype or o.numel() != n or not o.is_cuda or not o.is_contiguous()):
+    # Whole-list passes of the tensors' own C methods: a call may come with hundreds of gradients.
+    kinds = [_OUT_OF.get(d) for d in map(_dtype_of, grads)]
+    sizes = list(map(_numel, grads))
+    if None in kinds or not all(map(_is_cuda, grads)) or not all(map(_is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
+    at = list(map(_data_ptr, grads))
+    to = at
+    if outs is not grads:
+        if (kinds != [_OUT_OF.get(d) for d in map(_dtype_of, outs)] or sizes != list(map(_numel, outs))
+                or not all(map(_is_cuda, outs)) or not all(map(_is_contiguous, outs))):
             raise ValueError("outs must be contiguous CUDA tensors of their gradients' sizes and types")
-        flat += (g.data_ptr(), o.data_ptr(), n, kind)  # an mxfp4_grad: two pointers, numel, (dtype, 0)
+        to = list(map(_data_ptr, outs))
+    # mxfp4_grad entries: two pointers, numel, (dtype, 0)
+    flat = list(itertools.chain.from_iterable(zip(at, to, sizes, kinds)))
     table = array.array("q", flat)
-    device = grads[0].device if flat else torch.device("cuda", torch.cuda.current_device())
+    device = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
     L = lib()
     nb = L.mxfp4_clip_grad_norm_workspace_bytes(len(grads))
     norm = _empty(1, torch.float32, device, stream)

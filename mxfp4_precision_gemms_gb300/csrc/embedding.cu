@@ -93,6 +93,7 @@ constexpr int kSortSmem = (kSortWarps * kBins + 2 * kBins + 32) * 4;
 constexpr int64_t kClearBytes = 2 * 16 * kSortThreads;
 constexpr int kSortItems = 4;  // tokens of a lane that are loaded together
 constexpr int kChunk = 32;     // sorted tokens of a chunk
+constexpr uint32_t kLongRun = 16;  // chunks
 
 // A run of one id that crosses a chunk's border: its first chunk, and the one behind its last.
 struct Run {
@@ -106,12 +107,15 @@ struct SortParams {
     uint32_t tokens;
     int64_t vocab, padding_id;
     uint2* buf[2];  // (key, token); the last pass writes buf[0]
-    Run* runs;
-    uint32_t* num_runs;
+    Run* runs;           // short runs from the front, long ones from the back
+    uint32_t* num_runs;  // [2]: short, long
     uint32_t* status;
     // clearing: rows of row_bytes, pitch_bytes apart
     uint8_t* dw;
     int64_t rows, row_bytes, pitch_bytes;
+    int32_t clear;       // otherwise the CTAs beside the sorting ones fetch dy into L2
+    const uint8_t* fetch;
+    int64_t fetch_bytes;
     int32_t clear_flat;  // contiguous and 16-byte aligned: one run of bytes
     int32_t clear_vec;   // 16-byte aligned rows of a multiple of 16 bytes
 };
@@ -242,27 +246,27 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
     // The runs that cross a chunk's border, in the order of their ids.
     const uint2* sorted = p.buf[0];
     const uint32_t chunks = (p.tokens + kChunk - 1) / kChunk;
-    uint32_t found = 0;
+    uint32_t found[2] = {0, 0};
     for (uint32_t c0 = 0; c0 + 1 < chunks; c0 += kSortThreads) {
         const uint32_t c = c0 + tid;
         bool starts = false;
-        uint32_t key = 0;
+        uint32_t key = 0, end = 0;
         if (c + 1 < chunks) {  // the last key of chunk c goes on in the next, and did not come from the one before
             key = __ldcg(&sorted[(uint64_t)c * kChunk + kChunk - 1]).x;
             starts = key != (uint32_t)p.vocab && __ldcg(&sorted[(uint64_t)(c + 1) * kChunk]).x == key &&
                      (c == 0 || __ldcg(&sorted[(uint64_t)c * kChunk - 1]).x != key);
         }
-        const uint32_t votes = __ballot_sync(0xffffffffu, starts);
-        __syncthreads();  // the round before has read wsum
-        if (lane == 0) wsum[warp] = __popc(votes);
-        __syncthreads();
-        uint32_t lower = 0, all = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            lower += w < warp ? wsum[w] : 0u;
-            all += wsum[w];
-        }
         if (starts) {
-            uint32_t lo = c + 1, hi = chunks;  // the first key of chunk lo is `key`
+            // The first key of chunk lo is `key`, that of chunk hi is not.  Most runs end soon: strides
+            // that double first, then halving between the last two.
+            uint32_t lo = c + 1, hi = chunks;
+            for (uint32_t step = 1; lo + step < hi; step *= 2) {
+                if (__ldcg(&sorted[(uint64_t)(lo + step) * kChunk]).x != key) {
+                    hi = lo + step;
+                    break;
+                }
+                lo += step;
+            }
             while (hi - lo > 1) {
                 const uint32_t mid = lo + (hi - lo) / 2;
                 if (__ldcg(&sorted[(uint64_t)mid * kChunk]).x == key)
@@ -270,11 +274,27 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
                 else
                     hi = mid;
             }
-            p.runs[found + lower + __popc(votes & ((1u << lane) - 1))] = {key, c, hi};
+            end = hi;
         }
-        found += all;
+        for (int kind = 0; kind < 2; ++kind) {
+            const bool mine_is = starts && (end - c > kLongRun) == (kind == 1);
+            const uint32_t votes = __ballot_sync(0xffffffffu, mine_is);
+            __syncthreads();  // the round before has read wsum
+            if (lane == 0) wsum[warp] = __popc(votes);
+            __syncthreads();
+            uint32_t lower = 0, all = 0;
+            for (int w = 0; w < kSortWarps; ++w) {
+                lower += w < warp ? wsum[w] : 0u;
+                all += wsum[w];
+            }
+            if (mine_is) {
+                const uint32_t at = found[kind] + lower + __popc(votes & ((1u << lane) - 1));
+                p.runs[kind ? chunks - 1 - at : at] = {key, c, end};
+            }
+            found[kind] += all;
+        }
     }
-    if (tid == 0) *p.num_runs = found;
+    if (tid < 2) p.num_runs[tid] = found[tid];
 }
 
 // Zeroes the table's part of CTA `part` of `parts`.
@@ -302,12 +322,24 @@ __device__ __forceinline__ void clear_table(const SortParams& p, uint32_t part, 
     }
 }
 
+// While the sort of a call that adds to the table keeps eight SMs busy, the others bring the
+// first rows of dy into L2, a CTA's threads kFetchBytes each.
+constexpr int64_t kFetchBytes = 4096;
+constexpr int64_t kFetchMost = int64_t(64) << 20;  // half of L2
+__device__ __forceinline__ void fetch_rows(const SortParams& p, uint32_t part, uint32_t parts) {
+    for (int64_t o = ((int64_t)part * kSortThreads + threadIdx.x) * kFetchBytes; o < p.fetch_bytes;
+         o += (int64_t)parts * kSortThreads * kFetchBytes)
+        l2_prefetch(p.fetch + o, (uint32_t)(p.fetch_bytes - o < kFetchBytes ? p.fetch_bytes - o : kFetchBytes));
+}
+
 __global__ void __launch_bounds__(kSortThreads, 2) sort_clear_kernel(const __grid_constant__ SortParams p) {
     extern __shared__ __align__(16) uint32_t smem[];
     grid_dependency_wait();
     allow_dependent_launch();
     if (blockIdx.x < kSortCtas)
         sort_cluster(p, smem);
+    else if (!p.clear)
+        fetch_rows(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
     else
         clear_table(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
 }
@@ -415,49 +447,62 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
     }
 }
 
-// Joins the crossing runs, one run and one slab of columns at a time: kJoinGroups groups of
-// lanes take the run's chunks in turn, and their sums are added in group order.
-constexpr int kJoinGroups = 8;
-constexpr int kJoinThreads = kJoinGroups * 32;
+// Joins the crossing runs, one run and one slab of 32 units at a time: a short run's chunks are
+// added by one warp in turn, a long run's by the CTA's warps, each taking every eighth, and their
+// sums in the warps' order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
 template <class DW, bool VEC>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, DW* dw, uint32_t slabs) {
     constexpr int U = VEC ? 4 : 1;
-    __shared__ float part[kJoinGroups][32 * U];
+    __shared__ float part[kJoinWarps][32 * U];
     grid_dependency_wait();
     allow_dependent_launch();
-    const uint64_t items = (uint64_t)*p.num_runs * slabs;
-    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint64_t shorts = (uint64_t)p.num_runs[0] * slabs, longs = (uint64_t)p.num_runs[1] * slabs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // chunk c of a run: slot 1 (going out) where it starts, slot 0 (coming in) after that
+    auto add = [&](float (&acc)[U], const Run& run, uint32_t c, int64_t col) {
+        const float* src = p.part + ((int64_t)c * 2 + (c == run.first ? 1 : 0)) * p.dim + col;
+        if constexpr (VEC) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+        } else {
+            acc[0] += src[0];
+        }
+    };
+    for (uint64_t item = blockIdx.x; item < longs; item += gridDim.x) {
         const uint32_t slab = (uint32_t)(item % slabs);
-        const Run run = p.runs[item / slabs];
-        const int64_t col = ((int64_t)slab * 32 + lane) * U;
+        const Run run = p.runs[p.chunks - 1 - item / slabs];
+        const int64_t col0 = (int64_t)slab * 32 * U, col = col0 + lane * U;
         float acc[U] = {};
         if (col < p.dim) {
-            // chunk c of the run: slot 1 (going out) where it starts, slot 0 (coming in) after that
 #pragma unroll 4
-            for (uint32_t c = run.first + g; c < run.end; c += kJoinGroups) {
-                const float* src = p.part + ((int64_t)c * 2 + (c == run.first ? 1 : 0)) * p.dim + col;
-                if constexpr (VEC) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-                } else {
-                    acc[0] += src[0];
-                }
-            }
+            for (uint32_t c = run.first + warp; c < run.end; c += kJoinWarps) add(acc, run, c, col);
         }
         __syncthreads();  // the item before has been read
 #pragma unroll
-        for (int j = 0; j < U; ++j) part[g][lane * U + j] = acc[j];
+        for (int j = 0; j < U; ++j) part[warp][lane * U + j] = acc[j];
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * U; i += kJoinThreads) {
-            const int64_t at = (int64_t)slab * 32 * U + i;
-            if (at >= p.dim) break;
+            if (col0 + i >= p.dim) break;
             float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kJoinGroups; ++k) sum += part[k][i];
-            finish(dw + (int64_t)run.key * p.lddw + at, sum, p);
+            for (int k = 0; k < kJoinWarps; ++k) sum += part[k][i];
+            finish(dw + (int64_t)run.key * p.lddw + col0 + i, sum, p);
         }
+    }
+    for (uint64_t item = (uint64_t)blockIdx.x * kJoinWarps + warp; item < shorts; item += (uint64_t)gridDim.x * kJoinWarps) {
+        const uint32_t slab = (uint32_t)(item % slabs);
+        const Run run = p.runs[item / slabs];
+        const int64_t col = ((int64_t)slab * 32 + lane) * U;
+        if (col >= p.dim) continue;
+        float acc[U] = {};
+#pragma unroll 4
+        for (uint32_t c = run.first; c < run.end; ++c) add(acc, run, c, col);
+        DW* dst = dw + (int64_t)run.key * p.lddw + col;
+#pragma unroll
+        for (int j = 0; j < U; ++j) finish(dst + j, acc[j], p);
     }
 }
 
@@ -490,14 +535,14 @@ cudaError_t launch_sum(SumParams p, const void* dy, void* dw, int sms, cudaStrea
     cudaError_t e = launch_overlapped(sum_kernel<DY, DW, VEC>, dim3((unsigned)ctas), dim3(kSumThreads), 0, s, 1, true, p,
                                       static_cast<const DY*>(dy), static_cast<DW*>(dw));
     if (e != cudaSuccess || p.chunks < 2) return e;
-    constexpr int per_join = VEC ? 128 : 32;
+    constexpr int per_join = 32 * (VEC ? 4 : 1);
     const uint32_t slabs = (uint32_t)((p.dim + per_join - 1) / per_join);
     const int64_t most = (int64_t)(p.chunks - 1) * slabs;  // runs are at most one for each border
     return launch_overlapped(join_kernel<DW, VEC>, dim3((unsigned)std::min<int64_t>(most, 4 * sms)), dim3(kJoinThreads),
                              0, s, 1, true, p, static_cast<DW*>(dw), slabs);
 }
 
-cudaError_t launch_sort(const SortParams& p, bool clear, int sms, cudaStream_t s) {
+cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
     static DeviceSlots slots;
     int set = 0;
     cudaError_t e = per_device_setting(slots, &set, [&](int, int* n) {
@@ -507,7 +552,8 @@ cudaError_t launch_sort(const SortParams& p, bool clear, int sms, cudaStream_t s
     if (e != cudaSuccess) return e;
     const int64_t stretches = (p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes;
     const int64_t clear_ctas = p.clear_flat ? stretches : std::min<int64_t>(stretches, 8 * sms);
-    const int64_t clusters = 1 + (clear ? (clear_ctas + kSortCtas - 1) / kSortCtas : 0);
+    const int64_t fetch_ctas = (p.fetch_bytes + kSortThreads * kFetchBytes - 1) / (kSortThreads * kFetchBytes);
+    const int64_t clusters = 1 + ((p.clear ? clear_ctas : fetch_ctas) + kSortCtas - 1) / kSortCtas;
     if (clusters * kSortCtas > INT32_MAX) return cudaErrorInvalidConfiguration;
     return launch_overlapped(sort_clear_kernel, dim3((unsigned)(clusters * kSortCtas)), dim3(kSortThreads), kSortSmem, s, kSortCtas,
                              true, p);
@@ -644,9 +690,15 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     const bool base16 = reinterpret_cast<uintptr_t>(dw) % 16 == 0;
     sp.clear_flat = base16 && sp.pitch_bytes == sp.row_bytes;
     sp.clear_vec = base16 && sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0;
+    sp.clear = !accumulate;
+    const int64_t dsz = esize(dy_dtype);
+    if (accumulate && lddy == dim && reinterpret_cast<uintptr_t>(dy) % 16 == 0) {
+        sp.fetch = static_cast<const uint8_t*>(dy);
+        sp.fetch_bytes = std::min<int64_t>(tokens * dim * dsz, kFetchMost) / 16 * 16;
+    }
     int sms = 0;
     cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess) e = launch_sort(sp, !accumulate, sms, s);
+    if (e == cudaSuccess) e = launch_sort(sp, sms, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s sort launch: %s", what, cudaGetErrorString(e));
     if (tokens == 0) return record_error(MXFP4_OK, "%s", "");
 

@@ -53,7 +53,6 @@ constexpr int kOffBar = kOffBox + kEpiWarps * kBoxes * kBoxBytes;
 constexpr int kNumBars = 2 * kStages + 5;
 constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kSmem = kOffTmem + 16;
-constexpr uint32_t kTxPair = 2 * 2 * kOpBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(2 * kSmem > 228 * 1024, "one CTA per SM: two pairs never compete for TMEM");
 static_assert(kOffBox % 1024 == 0 && kOffBar % 8 == 0, "alignment");
@@ -84,7 +83,8 @@ struct Product {
     int32_t m_counted;      // M is the number of counted tokens (rounded up to a tile)
     int32_t k_counted;      // K is the number of counted tokens
     int32_t M, N, K;
-    int32_t tile_n;         // columns of a tile: kTile, or less where N divides better (a multiple of 32)
+    int32_t tile_n;         // columns of a tile: kTile, or less where that divides better (a multiple of 32)
+    uint32_t tx;            // bytes of a stage, both CTAs
     int32_t splits;         // K is cut into this many parts, each with its own output
     int32_t k_per_split;    // stages of a part
     int32_t slot_rows;      // rows of C between the parts' outputs
@@ -134,20 +134,42 @@ inline int32_t even_tile(int64_t n) {
     return (int32_t)(((n + tiles - 1) / tiles + 31) / 32 * 32);
 }
 
+inline uint32_t stage_bytes(int32_t b_columns) { return 2u * (128u + (uint32_t)b_columns / 2) * kK * 2; }
+
+constexpr int kClustersMost = 76;  // pairs of SMs
+
+// A tile's columns of the vocabulary where the tiles fill the device few times over: the width whose
+// schedule is shortest.  A stage costs two cycles a column, or its bytes at 72 a cycle (what L2
+// gives an SM), and a tile some 600 cycles more.  (64 tokens, 65536 x 4096: 256 tiles of 256 columns are
+// four rounds of 76, 293 of 224 too: 115 -> 101 us.)
+inline int32_t vocab_tile(int64_t num_m, int64_t n, int64_t k) {
+    if (num_m * ((n + kTile - 1) / kTile) >= 8 * kClustersMost) return kTile;
+    int32_t best = kTile;
+    int64_t best_cost = INT64_MAX;
+    for (int32_t w = kTile; w >= 128; w -= 32) {
+        const int64_t rounds = (num_m * ((n + w - 1) / w) + kClustersMost - 1) / kClustersMost;
+        const int64_t stage = std::max<int64_t>(2 * w, stage_bytes(w) / 2 / 72);
+        const int64_t cost = rounds * (stage * ((k + kK - 1) / kK) + 600);
+        if (cost < best_cost) best = w, best_cost = cost;
+    }
+    return best;
+}
+
 // Where tile `t` of the launch lies; false past the last one.  Within a product, consecutive
 // tiles (which run at the same time) walk the dimension with fewer tiles first: the operand along
 // it is read in every wave and stays in L2 while the other one streams through once.
-__device__ __forceinline__ bool locate(const CeParams& p, int32_t count, int64_t t, Tile& out) {
+template <int KIND>
+__device__ __forceinline__ bool locate(const CeParams& p, int32_t count, int32_t t, Tile& out) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (KIND == kProducts ? 2 : 1); ++i) {
         if (i >= p.count) return false;
         const Product& q = p.prod[i];
         const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
-        const int32_t num_n = (q.N + kTile - 1) / kTile;
-        const int64_t per = (int64_t)num_m * num_n;
+        const int32_t num_n = (q.N + q.tile_n - 1) / q.tile_n;
+        const int32_t per = num_m * num_n;
         if (t < per * q.splits) {
-            const int32_t slot = (int32_t)(t / per);
-            const int32_t lt = (int32_t)(t - slot * per);
+            const int32_t slot = q.splits > 1 ? t / per : 0;
+            const int32_t lt = t - slot * per;
             out.prob = i;
             out.slot = slot;
             if (num_n > num_m) {
@@ -224,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     constexpr int32_t kRun = KIND == kStats ? kStatsRun : 1 << 30;  // stages per accumulator
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int64_t cluster = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
+    const int32_t cluster = (int32_t)(blockIdx.x >> 1), num_clusters = (int32_t)(gridDim.x >> 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -267,15 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             uint32_t s = 0, round = 0;
             bool ok = true;
             Tile t;
-            for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
-                const Product& q = p.prod[t.prob];
+            for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+                const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                 const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * (q.tile_n / 2);
                 for (int32_t i = 0; i < t.stages; ++i) {
                     if (round > 0 && !wait_bounded(&empty[s], (round - 1) & 1u, p.wait_ns, p.status)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], kTxPair);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], q.tx);
                     const uint32_t bar = full_leader + s * 8u;
                     const int32_t k = (t.k0 + i) * kK;
                     uint8_t* a = sA + s * kOpBytes;
@@ -317,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 uint32_t s = 0, phase = 0, tcount = 0;
                 bool ok = true;
                 Tile t;
-                for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
-                    const Product& q = p.prod[t.prob];
+                for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+                    const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                     const uint32_t idesc = idesc_bf16(256, (uint32_t)q.tile_n, q.a_mn != 0, q.b_mn != 0);
                     // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
                     // Between 64-column blocks of M / N: half a stage's operand.
@@ -375,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
         uint32_t tcount = 0;
         bool ok = true;
         Tile t;
-        for (int64_t tile = cluster; ok && locate(p, count, tile, t); tile += num_clusters) {
-            const Product& q = p.prod[t.prob];
+        for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+            const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
             const int32_t row0 = t.m0 + (int32_t)rank * 128 + quad * 32;
             const int32_t row = row0 + lane;
             const int32_t c0 = t.n0 + half * 128;
@@ -412,13 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         tmem_ld_wait();
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {  // 16 columns at a time: 168 registers is the limit
-                            uint32_t v[16];
-                            tmem_ld_32x32b_x16(src + ab * 256 + c * 16, v);
+                        for (int c = 0; c < 16; ++c) {  // 8 columns at a time: 168 registers is the limit
+                            uint32_t v[8];
+                            tmem_ld_32x32b_x8(src + ab * 256 + c * 8, v);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                uint32_t& x = z[c / 2][(c & 1) * 16 + j];
+                            for (int j = 0; j < 8; ++j) {
+                                uint32_t& x = z[c / 4][(c & 3) * 8 + j];
                                 x = __float_as_uint(__uint_as_float(x) + __uint_as_float(v[j]));
                             }
                         }
@@ -432,14 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int32_t col = c0 + c * 32;
-                    const int32_t left = q.N - col;
-                    if (left < 32) {  // past the vocabulary's end
+                    // columns of this tile that are left: the vocabulary's end, or a narrow tile's
+                    const int32_t left = min(q.N - t.n0, q.tile_n) - (half * 128 + c * 32);
+                    if (left < 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j >= left) z[c][j] = 0xff800000u;
                     }
                     const int32_t hit = tgt - col;
-                    if (hit >= 0 && hit < 32) {
+                    if (hit >= 0 && hit < min(left, 32)) {
                         float x = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -460,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         s4[j & 3] += exp2_approx(fmaf(__uint_as_float(z[c][j]), kLog2e, -ref));
                 sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 if (row < count)
-                    p.stats[(int64_t)((t.n0 / kTile) * 2 + half) * p.rows + row] = make_float2(m, sum);
+                    p.stats[(int64_t)((t.n0 / q.tile_n) * 2 + half) * p.rows + row] = make_float2(m, sum);
             } else {
                 const uint32_t ab = tcount & 1u;
                 if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) break;
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
                     }
                     const int32_t col = c0 + c * 32;
-                    if (KIND == kProducts && half * 128 + c * 32 >= q.tile_n) continue;  // past a narrow tile's columns
+                    if (half * 128 + c * 32 >= q.tile_n) continue;  // past a narrow tile's columns
                     if constexpr (KIND == kDlogits) {
                         const int32_t hit = tgt - col;
                         uint32_t w[16];
@@ -819,9 +842,11 @@ __global__ void __launch_bounds__(kScatterThreads)
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // The dz of one piece: at most this many bytes (or kMinPiece columns), so that a long batch
-// needs no more scratch than a short one.  16384 columns at 8192 tokens: a piece's three products
-// are then long enough that their launches' ends cost little.
-constexpr size_t kPieceBytes = size_t(256) << 20;
+// needs no more scratch than a short one.  A piece's products are then long enough that the ends of
+// their launches cost little: of 8192 tokens of a 128256 x 512 layer the gradients take 2258 us with pieces
+// of 256 MB, 2107 with 512 and 1994 with 1024.  (Pieces of 48 MB, whose dz would stay in L2, were slower
+// throughout: 65536 x 256, 759 us against 1301.)
+constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int32_t kMinPiece = 2048;
 
 int32_t piece_columns(int32_t padded, int64_t vocab) {
@@ -830,8 +855,6 @@ int32_t piece_columns(int32_t padded, int64_t vocab) {
     const int64_t even = (vocab + pieces - 1) / pieces;
     return (int32_t)((even + kTile - 1) / kTile * kTile);
 }
-
-constexpr int kClustersMost = 76;  // pairs of SMs
 
 // Parts that dh's contraction over a piece's columns is cut into.  With fewer tiles than pairs of
 // SMs the parts fill the device; each costs a pass over its fp32 output, written here as four
@@ -855,6 +878,7 @@ int32_t split_count(int32_t padded, int64_t dim, int32_t columns) {
 struct Layout {
     int32_t padded;
     size_t header, target, source, place, lse2, ratio, target_logit, token_loss, rows, stats, dz, parts, bytes;
+    int32_t tile_n;  // of the forward pass
     int32_t piece, splits;
 };
 
@@ -876,7 +900,8 @@ Layout lay_out(int64_t tokens, int64_t vocab, int64_t dim, bool grad) {
     if (!grad) {
         l.target_logit = take(n * 4);
         l.token_loss = take(n * 4);
-        l.stats = take((size_t)((vocab + kTile - 1) / kTile) * 2 * n * sizeof(float2));
+        l.tile_n = vocab_tile(l.padded / kTile, vocab, dim);
+        l.stats = take((size_t)((vocab + l.tile_n - 1) / l.tile_n) * 2 * n * sizeof(float2));
     } else {
         l.lse2 = take(n * 4);
         l.ratio = take(n * 4);
@@ -919,11 +944,12 @@ cudaError_t launch_matrix(const CeParams& p, int64_t tiles, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorNotSupported;
+    if (tiles > INT32_MAX - 1024) return cudaErrorInvalidConfiguration;  // the kernel counts them in 32 bits
     const int64_t grid = 2 * std::min<int64_t>(tiles, clusters);
     return launch_overlapped(kern, dim3((unsigned)grid), dim3(kThreads), kSmem, s, 2, true, p);
 }
 
-int64_t tiles_of(int64_t m, int64_t n) { return ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile); }
+int64_t tiles_of(int64_t m, int64_t n, int64_t width) { return ((m + kTile - 1) / kTile) * ((n + width - 1) / width); }
 
 cudaError_t gather_grid(int64_t tokens, int* grid) {
     static DeviceSlots slots;
@@ -1021,12 +1047,13 @@ extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t d
     bf16* rows = reinterpret_cast<bf16*>(base + l.rows);
     if (!(direct ? encode_bf16_map(&q.map_a, h, tokens, dim, ldh, kK, 128)
                  : encode_bf16_map(&q.map_a, rows, l.padded, dim, dim, kK, 128)) ||
-        !encode_bf16_map(&q.map_b, w, vocab, dim, ldw, kK, 128))
+        !encode_bf16_map(&q.map_b, w, vocab, dim, ldw, kK, (uint32_t)l.tile_n / 2))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     q.m_counted = 1;
     q.M = l.padded;
     q.N = (int32_t)vocab;
-    q.tile_n = kTile;
+    q.tile_n = l.tile_n;
+    q.tx = stage_bytes(l.tile_n);
     q.K = (int32_t)dim;
     q.splits = 1;
     p.count = 1;
@@ -1069,12 +1096,12 @@ extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t d
             e = launch_overlapped(gather_kernel<false>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
         if (e != cudaSuccess) return launch_failed(what, "gather", e);
     }
-    e = launch_matrix<kStats>(p, tiles_of(l.padded, vocab), s);
+    e = launch_matrix<kStats>(p, tiles_of(l.padded, vocab, l.tile_n), s);
     if (e != cudaSuccess) return launch_failed(what, "statistics", e);
     CombineParams c{};
     c.header = header;
     c.stats = p.stats;
-    c.parts = (int32_t)((vocab + kTile - 1) / kTile) * 2;
+    c.parts = (int32_t)((vocab + l.tile_n - 1) / l.tile_n) * 2;
     c.rows = l.padded;
     c.target_logit = p.target_logit;
     c.source = reinterpret_cast<int32_t*>(base + l.source);
@@ -1178,7 +1205,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
         p.header = g.header;
         p.target = g.target;
         p.col0 = (int32_t)v0;
-        p.rows = l.padded;
+            p.rows = l.padded;
         p.lse2 = g.lse2;
         p.ratio = g.ratio;
         p.status = g.status;
@@ -1188,16 +1215,17 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.m_counted = 1;
             q.M = l.padded;
             q.N = cols;
-            q.tile_n = kTile;
+            q.tile_n = vocab_tile(l.padded / kTile, cols, dim);
+            q.tx = stage_bytes(q.tile_n);
             q.K = (int32_t)dim;
             q.splits = 1;
             q.out_bf16 = 1;
             if (!encode_bf16_map(&q.map_a, g.rows, l.padded, dim, dim, kK, 128) ||
-                !encode_bf16_map(&q.map_b, w_piece, cols, dim, ldw, kK, 128) ||
+                !encode_bf16_map(&q.map_b, w_piece, cols, dim, ldw, kK, (uint32_t)q.tile_n / 2) ||
                 !encode_out_map(&q.map_c, dz, l.padded, cols, l.piece, true))
                 return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
             p.count = 1;
-            e = launch_matrix<kDlogits>(p, tiles_of(l.padded, cols), s);
+            e = launch_matrix<kDlogits>(p, tiles_of(l.padded, cols, q.tile_n), s);
             if (e != cudaSuccess) return launch_failed(what, "dlogits", e);
         }
         int n = 0;
@@ -1210,6 +1238,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.M = l.padded;
             q.N = (int32_t)dim;
             q.tile_n = even_tile(dim);
+            q.tx = stage_bytes(kTile);
             q.K = cols;
             const int32_t stages = (cols + kK - 1) / kK;
             q.k_per_split = (stages + l.splits - 1) / l.splits;
@@ -1220,7 +1249,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
                 !encode_bf16_map(&q.map_b, w_piece, cols, dim, ldw, 64, kK) ||
                 !encode_out_map(&q.map_c, parts, (int64_t)l.splits * l.padded, dim, dim, false))
                 return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
-            tiles += tiles_of(l.padded, dim) * q.splits;
+            tiles += tiles_of(l.padded, dim, q.tile_n) * q.splits;
         }
         if (dw) {
             Product& q = p.prod[n++];
@@ -1230,6 +1259,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.M = cols;
             q.N = (int32_t)dim;
             q.tile_n = even_tile(dim);
+            q.tx = stage_bytes(kTile);
             q.K = l.padded;
             q.splits = 1;
             q.scaled = 1;
@@ -1239,7 +1269,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
                 !encode_bf16_map(&q.map_b, g.rows, l.padded, dim, dim, 64, kK) ||
                 !encode_out_map(&q.map_c, static_cast<uint8_t*>(dw) + v0 * lddw * wsz, cols, dim, lddw, q.out_bf16))
                 return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
-            tiles += tiles_of(cols, dim);
+            tiles += tiles_of(cols, dim, q.tile_n);
         }
         p.count = n;
         e = launch_matrix<kProducts>(p, tiles, s);

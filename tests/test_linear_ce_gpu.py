@@ -152,7 +152,7 @@ def test_loss_and_gradients(T, V, D, ignored):
 def test_several_pieces_and_accumulation():
     """A vocabulary of several pieces (2048 columns at the least) with a long batch, and dw added to."""
     torch, mx = _setup()
-    T, V, D = 40000, 5001, 64
+    T, V, D = 40000, 15001, 64
     h, w, y = _inputs(torch, T, V, D, 5, 0.1)
     L = mx.lib()
     # the workspace holds one piece of dz, not tokens x vocab

@@ -155,9 +155,8 @@ _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 def _stream(stream=None):
     if stream is None and _raw_stream is not None and _raw_device is not None:
-        return ctypes.c_void_p(_raw_stream(_raw_device()))
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+        return _raw_stream(_raw_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _ptr(t: torch.Tensor):
@@ -551,43 +550,54 @@ def linear_backward(dy: torch.Tensor, wT: QTensor, xT: QTensor, cfg: Config, dx:
 
 
 # ----------------------------------------------------------------- the ends of a training step
+# These calls may be short, so what a call costs on the host is kept low: a tensor's shape and
+# strides are asked for once, and the current stream is read without an object around it.
 _FLOAT_OF = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16}
 _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 _IDS_OF = {torch.int32: IDS_I32, torch.int64: IDS_I64}
-
-
 _data_ptr, _numel, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 _dtype_of, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_torch_empty = torch.empty
 
 
 def _empty(shape, dtype, device, stream):
     """torch.empty for a call on `stream` (None: the current one): the allocator ties a block's
     reuse to the stream it was allocated on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch_empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch_empty(shape, dtype=dtype, device=device)
 
 
-def _float_matrix(x: torch.Tensor, name: str) -> int:
-    """Checks a CUDA fp32 / bf16 matrix with unit column stride; returns its leading dimension."""
-    if x.dtype not in _OUT_OF or not x.is_cuda or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be a CUDA fp32 or bf16 matrix with unit column stride")
-    # a row count of one or less leaves the row stride without meaning
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+def _matrix(x: torch.Tensor, name: str) -> tuple[int, int, int, int]:
+    """Checks a CUDA fp32 / bf16 matrix with unit column stride; returns (rows, columns, leading
+    dimension, dtype)."""
+    kind = _OUT_OF.get(x.dtype)
+    if kind is not None and x.is_cuda and x.dim() == 2:
+        rows, cols = x.shape
+        ld, inner = x.stride()
+        if inner == 1 or cols <= 1:
+            return rows, cols, (ld if rows > 1 else cols), kind  # of a single row the stride has no meaning
+    raise ValueError(f"{name} must be a CUDA fp32 or bf16 matrix with unit column stride")
 
 
 def _token_ids(ids: torch.Tensor, name: str) -> int:
-    if ids.dtype not in _IDS_OF or not ids.is_cuda or not ids.is_contiguous():
+    kind = _IDS_OF.get(ids.dtype)
+    if kind is None or not ids.is_cuda or not ids.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA int32 or int64 tensor")
-    return _IDS_OF[ids.dtype]
+    return kind
 
 
-def _given(out: torch.Tensor, shape, dtype, name: str) -> int:
-    """Checks a caller's output matrix; returns its leading dimension."""
+def _output(out, shape, kind: int, name: str, device, stream):
+    """A caller's output matrix, checked, or a new one; returns (tensor, leading dimension)."""
+    dtype = _FLOAT_OF.get(kind)
+    if dtype is None:
+        raise ValueError(f"{name}: the output type must be OUT_F32 or OUT_BF16")
+    if out is None:
+        return _empty(shape, dtype, device, stream), shape[-1]
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
         raise ValueError(f"{name} must be {tuple(shape)} of {dtype}")
-    return _float_matrix(out, name)
+    return out, _matrix(out, name)[2]
 
 
 def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, out_dtype: int | None = None,
@@ -595,19 +605,13 @@ def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, out_dtype:
     """mxfp4_embedding: scale * w[ids] for a table w [vocab, dim] (fp32 or bf16) and ids of any
     shape; returns [*ids.shape, dim] in out_dtype (default: w's).  `out`, if given, is a
     matrix [ids.numel(), dim]."""
-    kind = _token_ids(ids, "ids")
-    ldw = _float_matrix(w, "w")
-    vocab, dim = w.shape
-    w_kind = _OUT_OF[w.dtype]
-    if out_dtype is None:
-        out_dtype = w_kind
+    ids_kind = _token_ids(ids, "ids")
+    vocab, dim, ldw, w_kind = _matrix(w, "w")
+    y_kind = w_kind if out_dtype is None else out_dtype
     n = ids.numel()
-    if out is None:
-        y, ldy = _empty((*ids.shape, dim), _FLOAT_OF[out_dtype], w.device, stream), dim
-    else:
-        y, ldy = out, _given(out, (n, dim), _FLOAT_OF[out_dtype], "out")
-    _check(lib().mxfp4_embedding(ids.data_ptr(), kind, n, w.data_ptr(), w_kind, vocab, dim, ldw, scale, y.data_ptr(),
-                                 out_dtype, ldy, _stream(stream)))
+    y, ldy = _output(out, (*ids.shape, dim) if out is None else (n, dim), y_kind, "out", w.device, stream)
+    _check(lib().mxfp4_embedding(ids.data_ptr(), ids_kind, n, w.data_ptr(), w_kind, vocab, dim, ldw, scale, y.data_ptr(),
+                                 y_kind, ldy, _stream(stream)))
     return y
 
 
@@ -617,37 +621,35 @@ def embedding_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, scale: float
     """mxfp4_embedding_grad: the table's gradient [vocab, dim] from dy [ids.numel(), dim] (fp32 or
     bf16), in out_dtype (default: dw's type if given, else dy's).  accumulate adds to dw, which
     must then be given; tokens with padding_id are left out."""
-    kind = _token_ids(ids, "ids")
-    lddy = _float_matrix(dy, "dy")
-    n, dim = dy.shape
+    ids_kind = _token_ids(ids, "ids")
+    n, dim, lddy, dy_kind = _matrix(dy, "dy")
     if ids.numel() != n:
         raise ValueError(f"dy has {n} rows for {ids.numel()} ids")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
     if out_dtype is None:
-        out_dtype = _OUT_OF[dw.dtype if dw is not None and dw.dtype in _OUT_OF else dy.dtype]
-    if dw is None:
-        if accumulate:
-            raise ValueError("accumulate needs dw")
-        dw, lddw = _empty((vocab, dim), _FLOAT_OF[out_dtype], dy.device, stream), dim
-    else:
-        lddw = _given(dw, (vocab, dim), _FLOAT_OF[out_dtype], "dw")
+        out_dtype = dy_kind if dw is None else _OUT_OF.get(dw.dtype, dy_kind)
+    device = dy.device
+    dw, lddw = _output(dw, (vocab, dim), out_dtype, "dw", device, stream)
     L = lib()
     nb = L.mxfp4_embedding_grad_workspace_bytes(n, vocab, dim)
-    ws = _empty(nb, torch.uint8, dy.device, stream)
-    _check(L.mxfp4_embedding_grad(ids.data_ptr(), kind, n, dy.data_ptr(), _OUT_OF[dy.dtype], lddy, vocab, dim, scale,
+    ws = _empty(nb, torch.uint8, device, stream)
+    _check(L.mxfp4_embedding_grad(ids.data_ptr(), ids_kind, n, dy.data_ptr(), dy_kind, lddy, vocab, dim, scale,
                                   padding_id, dw.data_ptr(), out_dtype, lddw, int(accumulate), ws.data_ptr(), nb,
                                   _stream(stream)))
     return dw
 
 
-def _ce_operands(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor) -> tuple[int, int, int]:
-    """Checks the operands of the linear cross entropy; returns (ids dtype, ldh, ldw)."""
-    kind = _token_ids(targets, "targets")
-    if h.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+def _ce_operands(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor) -> tuple[int, int, int, int, int, int]:
+    """Checks the operands of the linear cross entropy; returns (tokens, dim, ldh, vocab, ldw, ids dtype)."""
+    ids_kind = _token_ids(targets, "targets")
+    n, dim, ldh, h_kind = _matrix(h, "h")
+    vocab, w_dim, ldw, w_kind = _matrix(w, "w")
+    if h_kind != OUT_BF16 or w_kind != OUT_BF16:
         raise ValueError("h and w must be bf16")
-    ldh, ldw = _float_matrix(h, "h"), _float_matrix(w, "w")
-    if h.shape[1] != w.shape[1] or targets.numel() != h.shape[0]:
+    if dim != w_dim or targets.numel() != n:
         raise ValueError(f"h {tuple(h.shape)}, w {tuple(w.shape)} and {targets.numel()} targets do not fit together")
-    return kind, ldh, ldw
+    return n, dim, ldh, vocab, ldw, ids_kind
 
 
 def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
@@ -655,15 +657,16 @@ def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_in
     """mxfp4_linear_ce: softmax cross entropy of the logits h w^T (h [tokens, dim], w [vocab, dim], both
     bf16) at `targets`, without the logits in memory.  Returns (loss, lse): loss [tokens] for
     REDUCE_NONE, else [1]; lse [tokens], which linear_ce_grad takes; both fp32."""
-    kind, ldh, ldw = _ce_operands(h, w, targets)
-    (n, dim), vocab = h.shape, w.shape[0]
-    loss = _empty(n if reduction == REDUCE_NONE else 1, torch.float32, h.device, stream)
-    lse = _empty(n, torch.float32, h.device, stream)
+    n, dim, ldh, vocab, ldw, ids_kind = _ce_operands(h, w, targets)
+    device = h.device
     L = lib()
     nb = L.mxfp4_linear_ce_workspace_bytes(n, vocab, dim)
-    ws = _empty(nb, torch.uint8, h.device, stream)
-    _check(L.mxfp4_linear_ce(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), kind, ignore_index,
-                             reduction, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb, _stream(stream)))
+    loss = _empty(n if reduction == REDUCE_NONE else 1, torch.float32, device, stream)
+    lse = _empty(n, torch.float32, device, stream)
+    ws = _empty(nb, torch.uint8, device, stream)
+    _check(L.mxfp4_linear_ce(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), ids_kind,
+                             ignore_index, reduction, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb,
+                             _stream(stream)))
     return loss, lse
 
 
@@ -674,34 +677,31 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse:
     """mxfp4_linear_ce_grad: gradients (dh [tokens, dim], dw [vocab, dim]) of linear_ce's loss.  dloss: the
     loss's gradient, fp32, [tokens] for REDUCE_NONE, else one element.  dh_dtype / dw_dtype None
     leaves that gradient out (None is returned for it); accumulate adds to dw (fp32, given)."""
-    kind, ldh, ldw = _ce_operands(h, w, targets)
-    (n, dim), vocab = h.shape, w.shape[0]
+    n, dim, ldh, vocab, ldw, ids_kind = _ce_operands(h, w, targets)
     for x, size, name in ((lse, n, "lse"), (dloss, n if reduction == REDUCE_NONE else 1, "dloss")):
-        if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous() or x.numel() != size:
+        if x.dtype is not torch.float32 or not x.is_cuda or not x.is_contiguous() or x.numel() != size:
             raise ValueError(f"{name} must be {size} contiguous fp32 CUDA elements")
+    device = h.device
+    dh_at = dw_at = None
     lddh = lddw = dim
     if dh_dtype is None:
         dh = None
-    elif dh is None:
-        dh = _empty((n, dim), _FLOAT_OF[dh_dtype], h.device, stream)
     else:
-        lddh = _given(dh, (n, dim), _FLOAT_OF[dh_dtype], "dh")
+        dh, lddh = _output(dh, (n, dim), dh_dtype, "dh", device, stream)
+        dh_at = dh.data_ptr()
     if dw_dtype is None:
         dw = None
-    elif dw is None:
-        if accumulate:
-            raise ValueError("accumulate needs dw")
-        dw = _empty((vocab, dim), _FLOAT_OF[dw_dtype], h.device, stream)
+    elif accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
     else:
-        lddw = _given(dw, (vocab, dim), _FLOAT_OF[dw_dtype], "dw")
+        dw, lddw = _output(dw, (vocab, dim), dw_dtype, "dw", device, stream)
+        dw_at = dw.data_ptr()
     L = lib()
     nb = L.mxfp4_linear_ce_grad_workspace_bytes(n, vocab, dim)
-    ws = _empty(nb, torch.uint8, h.device, stream)
-    _check(L.mxfp4_linear_ce_grad(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), kind,
-                                  ignore_index, reduction, lse.data_ptr(), dloss.data_ptr(),
-                                  None if dh is None else dh.data_ptr(), dh_dtype or 0, lddh,
-                                  None if dw is None else dw.data_ptr(), dw_dtype or 0, lddw, int(accumulate),
-                                  ws.data_ptr(), nb, _stream(stream)))
+    ws = _empty(nb, torch.uint8, device, stream)
+    _check(L.mxfp4_linear_ce_grad(h.data_ptr(), n, dim, ldh, w.data_ptr(), vocab, ldw, targets.data_ptr(), ids_kind,
+                                  ignore_index, reduction, lse.data_ptr(), dloss.data_ptr(), dh_at, dh_dtype or 0, lddh,
+                                  dw_at, dw_dtype or 0, lddw, int(accumulate), ws.data_ptr(), nb, _stream(stream)))
     return dh, dw
 
 
@@ -710,8 +710,9 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
     place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
     norm before clipping as a 1-element fp32 CUDA tensor."""
     outs = grads if outs is None else outs
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
+    n = len(grads)
+    if len(outs) != n:
+        raise ValueError(f"{len(outs)} outs for {n} gradients")
     # Whole-list passes of the tensors' own C methods: a call may come with hundreds of gradients.
     kinds = [_OUT_OF.get(d) for d in map(_dtype_of, grads)]
     sizes = list(map(_numel, grads))
@@ -725,14 +726,13 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
             raise ValueError("outs must be contiguous CUDA tensors of their gradients' sizes and types")
         to = list(map(_data_ptr, outs))
     # mxfp4_grad entries: two pointers, numel, (dtype, 0)
-    flat = list(itertools.chain.from_iterable(zip(at, to, sizes, kinds)))
-    table = array.array("q", flat)
-    device = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
+    table = array.array("q", itertools.chain.from_iterable(zip(at, to, sizes, kinds)))
+    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
     L = lib()
-    nb = L.mxfp4_clip_grad_norm_workspace_bytes(len(grads))
+    nb = L.mxfp4_clip_grad_norm_workspace_bytes(n)
     norm = _empty(1, torch.float32, device, stream)
     ws = _empty(nb, torch.uint8, device, stream)
-    _check(L.mxfp4_clip_grad_norm(table.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), nb,
+    _check(L.mxfp4_clip_grad_norm(table.buffer_info()[0], n, max_norm, norm.data_ptr(), ws.data_ptr(), nb,
                                   _stream(stream)))
     return norm
 

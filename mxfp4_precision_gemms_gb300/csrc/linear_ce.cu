@@ -915,7 +915,7 @@ Layout lay_out(int64_t tokens, int64_t vocab, int64_t dim, bool grad) {
 }
 
 bool sizes_fit(int64_t tokens, int64_t vocab, int64_t dim) {
-    return tokens >= 0 && vocab >= 0 && dim >= 0 && tokens <= (1 << 24) && vocab <= (1 << 28) && dim <= (1 << 20);
+    return tokens >= 0 && vocab >= 0 && dim >= 0 && tokens <= (1 << 24) && vocab <= (1 << 28) && dim <= (1 << 16);
 }
 
 template <int KIND>
@@ -972,7 +972,7 @@ mxfp4_status check_common(const char* what, const void* h, int64_t tokens, int64
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: vocab and dim must be positive", what);
     if (dim % 8) return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: dim (%lld) %% 8 != 0", what, (long long)dim);
     if (!sizes_fit(tokens, vocab, dim))
-        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tokens, 2^28 ids or 2^20 columns", what);
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tokens, 2^28 ids or 2^16 columns", what);
     if (!w) return record_error(MXFP4_ERR_INVALID_ARG, "%s: w is NULL", what);
     if (reinterpret_cast<uintptr_t>(w) % 16 || ldw % 8)
         return record_error(MXFP4_ERR_MISALIGNED, "%s: w must be 16-byte aligned with ldw %% 8 == 0", what);

@@ -155,40 +155,81 @@ inline int32_t vocab_tile(int64_t num_m, int64_t n, int64_t k) {
     return best;
 }
 
-// Where tile `t` of the launch lies; false past the last one.  Within a product, consecutive
-// tiles (which run at the same time) walk the dimension with fewer tiles first: the operand along
-// it is read in every wave and stays in L2 while the other one streams through once.
+// Tile `lt` of product `i`.  Consecutive tiles (which run at the same time) walk the dimension with
+// fewer tiles first: the operand along it is read in every wave and stays in L2 while the other
+// one streams through once.
+__device__ __forceinline__ void locate(const CeParams& p, int32_t count, int i, int32_t lt, Tile& out) {
+    const Product& q = p.prod[i];
+    const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
+    const int32_t num_n = (q.N + q.tile_n - 1) / q.tile_n;
+    out.prob = i;
+    out.slot = 0;
+    if (q.splits > 1) {
+        out.slot = lt / (num_m * num_n);
+        lt -= out.slot * (num_m * num_n);
+    }
+    if (num_n > num_m) {
+        out.m0 = (lt % num_m) * kTile;
+        out.n0 = (lt / num_m) * q.tile_n;
+    } else {
+        out.m0 = (lt / num_n) * kTile;
+        out.n0 = (lt % num_n) * q.tile_n;
+    }
+    const int32_t k = q.k_counted ? max(count, 1) : q.K;
+    const int32_t all = (k + kK - 1) / kK;
+    out.k0 = out.slot * q.k_per_split;
+    out.stages = q.splits > 1 ? min(q.k_per_split, all - out.k0) : all;
+}
+__device__ __forceinline__ int32_t tiles_in(const CeParams& p, int32_t count, int i) {
+    const Product& q = p.prod[i];
+    const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
+    return num_m * ((q.N + q.tile_n - 1) / q.tile_n) * q.splits;
+}
+
+// The tiles of one cluster, in order; every role of both CTAs walks the same ones.  One product:
+// every num_clusters-th tile.  Two: the first one's tiles (the longer contraction) that way, and
+// while `rest` clusters have one of them more than the others, those others take `lead` rounds of the
+// second one's tiles; then all clusters take turns again.
 template <int KIND>
-__device__ __forceinline__ bool locate(const CeParams& p, int32_t count, int32_t t, Tile& out) {
-#pragma unroll
-    for (int i = 0; i < (KIND == kProducts ? 2 : 1); ++i) {
-        if (i >= p.count) return false;
-        const Product& q = p.prod[i];
-        const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
-        const int32_t num_n = (q.N + q.tile_n - 1) / q.tile_n;
-        const int32_t per = num_m * num_n;
-        if (t < per * q.splits) {
-            const int32_t slot = q.splits > 1 ? t / per : 0;
-            const int32_t lt = t - slot * per;
-            out.prob = i;
-            out.slot = slot;
-            if (num_n > num_m) {
-                out.m0 = (lt % num_m) * kTile;
-                out.n0 = (lt / num_m) * q.tile_n;
-            } else {
-                out.m0 = (lt / num_n) * kTile;
-                out.n0 = (lt % num_n) * q.tile_n;
-            }
+struct Walk {
+    int32_t cluster, clusters, tiles0, tiles1, rest, lead, turn;
+    __device__ __forceinline__ void start(const CeParams& p, int32_t count, int32_t c, int32_t n) {
+        cluster = c, clusters = n, turn = 0;
+        tiles0 = tiles_in(p, count, 0);
+        tiles1 = rest = lead = 0;
+        if (KIND == kProducts && p.count == 2) {
+            tiles1 = tiles_in(p, count, 1);
+            rest = tiles0 % n;
+            // A tile's time in stages: its own and two of hand-off, but no less than storing it takes
+            // (128 KB at a pair's share of HBM: six stages, twelve for fp32).
+            const Product& q = p.prod[1];
             const int32_t k = q.k_counted ? max(count, 1) : q.K;
-            const int32_t all = (k + kK - 1) / kK;
-            out.k0 = slot * q.k_per_split;
-            out.stages = q.splits > 1 ? min(q.k_per_split, all - out.k0) : all;
+            const int32_t one = max((k + kK - 1) / kK, q.out_bf16 ? 6 : 12) + 2;
+            if (rest) lead = (p.prod[0].k_per_split + 2 + one / 2) / one;
+        }
+    }
+    __device__ __forceinline__ bool next(const CeParams& p, int32_t count, Tile& t) {
+        const int32_t j = turn++;
+        const int32_t at = cluster + j * clusters;
+        if (at < tiles0) {
+            locate(p, count, 0, at, t);
             return true;
         }
-        t -= per * q.splits;
+        if (KIND != kProducts || tiles1 == 0) return false;
+        const int32_t i = j - (tiles0 / clusters + (cluster < rest ? 1 : 0));
+        const int32_t ahead = clusters - rest;  // clusters that take the lead rounds
+        int32_t lt;
+        if (cluster < rest)
+            lt = lead * ahead + i * clusters + cluster;
+        else if (i < lead)
+            lt = i * ahead + cluster - rest;
+        else
+            lt = lead * ahead + (i - lead) * clusters + cluster;
+        if (lt >= tiles1) return false;
+        locate(p, count, 1, lt, t);
+        return true;
     }
-    return false;
-}
+};
 
 // Lane i writes its row's 64 bytes into a staging box (16-byte piece j of row r at
 // j ^ ((r >> 1) & 3): the 64-byte swizzle, conflict-free).
@@ -289,7 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             uint32_t s = 0, round = 0;
             bool ok = true;
             Tile t;
-            for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+            Walk<KIND> walk;
+            walk.start(p, count, cluster, num_clusters);
+            while (ok && walk.next(p, count, t)) {
                 const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                 const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * (q.tile_n / 2);
                 for (int32_t i = 0; i < t.stages; ++i) {
@@ -339,7 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 uint32_t s = 0, phase = 0, tcount = 0;
                 bool ok = true;
                 Tile t;
-                for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+                Walk<KIND> walk;
+                walk.start(p, count, cluster, num_clusters);
+                while (ok && walk.next(p, count, t)) {
                     const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                     const uint32_t idesc = idesc_bf16(256, (uint32_t)q.tile_n, q.a_mn != 0, q.b_mn != 0);
                     // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
@@ -397,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
         uint32_t tcount = 0;
         bool ok = true;
         Tile t;
-        for (int32_t tile = cluster; ok && locate<KIND>(p, count, tile, t); tile += num_clusters) {
+        Walk<KIND> walk;
+        walk.start(p, count, cluster, num_clusters);
+        while (ok && walk.next(p, count, t)) {
             const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
             const int32_t row0 = t.m0 + (int32_t)rank * 128 + quad * 32;
             const int32_t row = row0 + lane;
@@ -856,19 +903,29 @@ int32_t piece_columns(int32_t padded, int64_t vocab) {
     return (int32_t)((even + kTile - 1) / kTile * kTile);
 }
 
-// Parts that dh's contraction over a piece's columns is cut into.  With fewer tiles than pairs of
-// SMs the parts fill the device; each costs a pass over its fp32 output, written here as four
-// stages of the tile loop.  The number with the shortest schedule is taken, and lowered to the
-// parts that get work; every piece of the vocabulary uses at most as many.
+// Parts that dh's contraction over a piece's columns is cut into, so that its few long tiles fill the
+// device beside dw's many short ones.  A schedule takes the parts' own rounds, or all tiles' stages
+// shared out; a part costs two stages of hand-off and four for the passes over its fp32 output.  How
+// many tokens count is known on the device alone, so the number is taken whose schedule is best
+// over all of them, half and a quarter, each measured against one that is shared out evenly.  Lowered
+// to the parts that get work; every piece uses at most as many.
 int32_t split_count(int32_t padded, int64_t dim, int32_t columns) {
-    const int64_t tiles = (int64_t)(padded / kTile) * ((dim + kTile - 1) / kTile);
+    const int64_t n_tiles = (dim + kTile - 1) / kTile;
+    const int64_t w_tiles = (columns + kTile - 1) / kTile * n_tiles;
     const int32_t stages = (columns + kK - 1) / kK;
-    if (tiles >= kClustersMost) return 1;
     int32_t best = 1;
-    int64_t best_cost = INT64_MAX;
+    double best_cost = 1e30;
     for (int32_t s = 1; s <= 16 && s <= stages; ++s) {
         const int64_t per = (stages + s - 1) / s;
-        const int64_t cost = (tiles * s + kClustersMost - 1) / kClustersMost * (per + 4);
+        double cost = 0;
+        for (int32_t share = 1; share <= 4; share *= 2) {
+            const int32_t rows = pad_rows(padded / share);
+            const int64_t tiles = rows / kTile * n_tiles, others = w_tiles * (std::max(rows / kK, 6) + 2);
+            const int64_t rounds = (tiles * s + kClustersMost - 1) / kClustersMost * (per + 2);
+            const int64_t shared = (tiles * s * (per + 6) + others) / kClustersMost;
+            const int64_t even = (tiles * (stages + 6) + others) / kClustersMost + 1;
+            cost += (double)std::max(rounds, shared) / (double)even;
+        }
         if (cost < best_cost) best = s, best_cost = cost;
     }
     const int32_t per = (stages + best - 1) / best;

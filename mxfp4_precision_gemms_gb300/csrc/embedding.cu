@@ -22,8 +22,7 @@
 #include <algorithm>
 
 #include "element.cuh"
-#include "internal.h"
-#include "ptx.cuh"
+#include "step_ops.cuh"
 
 namespace mx {
 namespace {

@@ -184,12 +184,6 @@ cudaError_t launch_overlapped(Kern kern, dim3 grid, dim3 block, size_t smem, cud
 }
 
 // Host helpers implemented in mxfp4_api.cu.
-mxfp4_status ensure_device();    // current device checked (GB300), status word looked up, context bound
-uint64_t wait_limit_ns();        // this thread's bounded-wait limit
-// 2D tensor map over a row-major bf16 matrix [rows, cols] (leading dimension ld elements):
-// box = box_cols x box_rows, 128-byte swizzle, zero fill outside.
-bool encode_bf16_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, uint32_t box_cols,
-                     uint32_t box_rows);
 uint32_t* device_status_ptr();  // for the current device
 // Records the thread-local message returned by mxfp4_last_error() and returns st.
 mxfp4_status record_error(mxfp4_status st, const char* fmt, ...);

@@ -12,6 +12,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "step_ops.cuh"
 
 namespace mx {
 

@@ -14,8 +14,6 @@ constexpr uint32_t kStatusTimeout = 1u;
 // A kernel found its dynamic shared memory misaligned for its layout and returned
 // without touching memory.
 constexpr uint32_t kStatusSmemLayout = 2u;
-// A token id or target outside the vocabulary (and not the ignored / padding one).
-constexpr uint32_t kStatusBadIndex = 4u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -126,18 +124,9 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until the shared-memory sources of all committed bulk groups have been read.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// The same for all but the N most recently committed groups.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
 // Waits until all committed bulk groups have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Brings `bytes` (a multiple of 16) from a 16-byte aligned global address into L2.
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -257,17 +246,6 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc
         : "memory");
 }
 
-// bf16 operands (kind::f16), fp32 accumulation, issued for a CTA pair.
-__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading / stride
 // byte offsets (16-byte units), version 1, swizzle mode in bits 61-63.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
@@ -292,16 +270,6 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N) {
            | (1u << 23)         // scale type: UE8M0
            | ((M >> 4) << 24);  // M / 16
 }
-// Instruction descriptor for kind::f16 with bf16 A/B and fp32 accumulation.  a_mn / b_mn: that
-// operand's M (N) index runs along its shared-memory rows instead of K.
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
-    return (1u << 4)                // D format: fp32
-           | (1u << 7)              // A format: bf16
-           | (1u << 10)             // B format: bf16
-           | (a_mn << 15) | (b_mn << 16)
-           | ((N >> 3) << 17)       // N / 8
-           | ((M >> 4) << 24);      // M / 16
-}
 __device__ __forceinline__ uint32_t idesc_with_sf_ids(uint32_t idesc, uint32_t a_id, uint32_t b_id) {
     return idesc | (b_id << 4) | (a_id << 29);
 }
@@ -320,22 +288,9 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
           "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-// The same for 8 columns.
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ conversions
-// 2^x (ex2.approx: about 2 ulp, 2^-inf = 0, subnormal results flushed).
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Eight fp32 -> eight E2M1 codes packed in 32 bits (value i in nibble i), round to
 // nearest even, saturating.  A pure conversion (no side effects), so not volatile: the
 // compiler may schedule it among the surrounding arithmetic.

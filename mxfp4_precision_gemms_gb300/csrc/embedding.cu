@@ -18,6 +18,8 @@
 //      the chunk is finished there.  A run that crosses a chunk's border leaves an fp32 partial
 //      sum, so a very frequent token is shared out over many CTAs.
 //   3. Join.  The partial sums of each crossing run are added in chunk order.
+// A few tokens are not sorted: one CTA for each token and slab of columns looks its id up among the
+// others and, where it is the first of its id, adds up their rows.
 // Which additions are made in which order depends on the ids alone, never on timing.
 #include <algorithm>
 
@@ -119,15 +121,18 @@ struct SortParams {
     int32_t clear_vec;   // 16-byte aligned rows of a multiple of 16 bytes
 };
 
+// Whether a token's row belongs to the gradient; one outside the vocabulary is reported.
+__device__ __forceinline__ bool takes_part(int64_t id, int64_t vocab, int64_t padding_id, uint32_t* status) {
+    if (id >= 0 && id == padding_id) return false;
+    if (id >= 0 && id < vocab) return true;
+    atomicOr(status, kStatusBadIndex);
+    return false;
+}
+
 // The key that a token sorts by: its id, or `vocab` (behind every row) when it is left out.
 __device__ __forceinline__ uint32_t token_key(const SortParams& p, uint32_t t) {
     const int64_t id = load_id(p.ids, p.is64, t);
-    if (id == p.padding_id && id >= 0) return (uint32_t)p.vocab;
-    if (id < 0 || id >= p.vocab) {
-        atomicOr(p.status, kStatusBadIndex);
-        return (uint32_t)p.vocab;
-    }
-    return (uint32_t)id;
+    return (uint32_t)(takes_part(id, p.vocab, p.padding_id, p.status) ? id : p.vocab);
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -505,7 +510,96 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, D
     }
 }
 
+// ---------------------------------------------------------------- few tokens
+// At most this many tokens go without the sort: its three launches cost 17 to 21 us whatever their
+// number, the lookup 4.6 us at 23 tokens and 5.4 at 239.  A run of equal ids is added by one CTA here, which at
+// 256 equal ones takes as long as the sort's way; beyond, that would be slower.
+constexpr uint32_t kFewTokens = 512;
+constexpr int kFewAhead = 16;  // rows loaded before they are added
+
+struct FewParams {
+    const void* ids;
+    int32_t is64;
+    uint32_t tokens;
+    int64_t padding_id;
+    uint32_t* status;
+};
+
+template <class DY, class DW, bool VEC>
+__global__ void __launch_bounds__(kSumThreads) few_kernel(const FewParams f, const SumParams p, const DY* dy, DW* dw) {
+    constexpr int U = VEC ? 8 : 1;
+    constexpr int kWords = kFewTokens / 32;
+    __shared__ uint32_t same[kWords];  // bit t: token t has this CTA's id
+    __shared__ uint16_t list[kFewTokens];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t mine = blockIdx.x;
+    const int64_t id = load_id(f.ids, f.is64, mine);
+    if (!takes_part(id, p.vocab, f.padding_id, f.status)) return;
+#pragma unroll
+    for (int w = warp; w < kWords; w += kSumThreads / 32) {
+        const uint32_t t = w * 32 + lane;
+        const uint32_t votes = __ballot_sync(0xffffffffu, t < f.tokens && load_id(f.ids, f.is64, t) == id);
+        if (lane == 0) same[w] = votes;
+    }
+    __syncthreads();
+    uint32_t n = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        if (w * 32 + 31 < mine ? same[w] != 0 : (w * 32 <= mine && (same[w] & ((1u << (mine & 31)) - 1)) != 0))
+            return;  // an earlier token has the id: its CTA adds this row
+        n += __popc(same[w]);
+    }
+    for (uint32_t t = threadIdx.x; t < f.tokens; t += kSumThreads) {
+        if (!(same[t >> 5] >> (t & 31) & 1u)) continue;
+        uint32_t at = __popc(same[t >> 5] & ((1u << (t & 31)) - 1));
+        for (uint32_t w = 0; w < t >> 5; ++w) at += __popc(same[w]);
+        list[at] = (uint16_t)t;
+    }
+    __syncthreads();
+    const int64_t col = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * U;
+    if (col >= p.dim) return;
+    float acc[U] = {};
+    for (uint32_t i0 = 0; i0 < n; i0 += kFewAhead) {
+        Raw8<DY> raw[VEC ? kFewAhead : 1];
+        float one[VEC ? 1 : kFewAhead];
+#pragma unroll
+        for (int a = 0; a < kFewAhead; ++a) {
+            if (i0 + a >= n) break;
+            const DY* src = dy + (int64_t)list[i0 + a] * p.lddy + col;
+            if constexpr (VEC)
+                raw[a] = load8(src);
+            else
+                one[a] = load1(src);
+        }
+#pragma unroll
+        for (int a = 0; a < kFewAhead; ++a) {
+            if (i0 + a >= n) break;
+            if constexpr (VEC) {
+                float v[8];
+                unpack8(raw[a], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += v[j];
+            } else {
+                acc[0] += one[a];
+            }
+        }
+    }
+    if constexpr (VEC)
+        finish8(dw + id * p.lddw + col, acc, p);
+    else
+        finish(dw + id * p.lddw + col, acc[0], p);
+}
+
 // ---------------------------------------------------------------- launches
+template <class DY, class DW, bool VEC>
+cudaError_t launch_few(const FewParams& f, const SumParams& p, const void* dy, void* dw, cudaStream_t s) {
+    constexpr int per = kSumThreads * (VEC ? 8 : 1);
+    return launch_overlapped(few_kernel<DY, DW, VEC>, dim3(f.tokens, (unsigned)((p.dim + per - 1) / per)),
+                             dim3(kSumThreads), 0, s, 1, true, f, p, static_cast<const DY*>(dy), static_cast<DW*>(dw));
+}
+
 template <class W, class Y, bool VEC>
 cudaError_t launch_lookup(const void* ids, int is64, int64_t tokens, const void* w, int64_t vocab, int64_t dim,
                           int64_t ldw, float scale, void* y, int64_t ldy, cudaStream_t s) {
@@ -670,8 +764,9 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     SortParams sp{};
     sp.ids = ids;
     sp.is64 = ids_dtype == MXFP4_IDS_I64;
-    sp.passes = tokens > 0 ? sort_passes(vocab) : 0;
-    sp.tokens = (uint32_t)tokens;
+    const bool few = tokens <= kFewTokens;
+    sp.passes = few ? 0 : sort_passes(vocab);
+    sp.tokens = few ? 0 : (uint32_t)tokens;
     sp.vocab = vocab;
     sp.padding_id = padding_id;
     uint8_t* at = static_cast<uint8_t*>(ws);
@@ -691,13 +786,13 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     sp.clear_vec = base16 && sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0;
     sp.clear = !accumulate;
     const int64_t dsz = esize(dy_dtype);
-    if (accumulate && lddy == dim && reinterpret_cast<uintptr_t>(dy) % 16 == 0) {
+    if (accumulate && !few && lddy == dim && reinterpret_cast<uintptr_t>(dy) % 16 == 0) {
         sp.fetch = static_cast<const uint8_t*>(dy);
         sp.fetch_bytes = std::min<int64_t>(tokens * dim * dsz, kFetchMost) / 16 * 16;
     }
     int sms = 0;
     cudaError_t e = sm_count(&sms);
-    if (e == cudaSuccess) e = launch_sort(sp, sms, s);
+    if (e == cudaSuccess && !(few && accumulate)) e = launch_sort(sp, sms, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s sort launch: %s", what, cudaGetErrorString(e));
     if (tokens == 0) return record_error(MXFP4_OK, "%s", "");
 
@@ -714,9 +809,11 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     p.num_runs = sp.num_runs;
     p.part = reinterpret_cast<float*>(at + 2 * sorted_bytes(tokens) + runs_bytes(tokens));
     const bool vec = vector_rows(dy, lddy, dim, esize(dy_dtype)) && vector_rows(dw, lddw, dim, wsz);
+    const FewParams fp{ids, sp.is64, (uint32_t)tokens, padding_id, sp.status};
     auto go = [&](auto yt, auto wt) {
         using DY = decltype(yt);
         using DW = decltype(wt);
+        if (few) return vec ? launch_few<DY, DW, true>(fp, p, dy, dw, s) : launch_few<DY, DW, false>(fp, p, dy, dw, s);
         return vec ? launch_sum<DY, DW, true>(p, dy, dw, sms, s) : launch_sum<DY, DW, false>(p, dy, dw, sms, s);
     };
     const bool yb = dy_dtype == MXFP4_OUT_BF16, wb = dw_dtype == MXFP4_OUT_BF16;

@@ -109,7 +109,8 @@ def _check_grad(torch, mx, dt, ids, dy, vocab, scale, padding, out, accumulate, 
 
 @pytest.mark.parametrize("kind", ["same", "distinct", "few", "zipf"])
 @pytest.mark.parametrize("tokens,vocab,dim", [(1, 5, 8), (31, 40, 16), (32, 33, 129), (65, 511, 1024),
-                                              (1000, 1200, 1032), (4097, 5000, 64), (9000, 128256, 72)])
+                                              (511, 600, 136), (512, 600, 1032), (513, 600, 136), (545, 600, 33), (1000, 1200, 1032),
+                                              (4097, 5000, 64), (9000, 128256, 72)])
 def test_gradient(kind, tokens, vocab, dim):
     torch, mx, dt = _setup()
     ids = _ids(torch, kind, tokens, vocab, tokens)
@@ -148,6 +149,24 @@ def test_gradient_pitched_and_padding(dyt):
             full = torch.full((300, pitch + 3), 7.0, dtype=dt[out], device="cuda")
             mx.embedding_grad(ids, clean, 300, padding_id=padding, out_dtype=out, dw=full[:, :dim])
             assert torch.equal(full[:, :dim], got) and bool((full[:, dim:] == 7.0).all())
+
+
+@pytest.mark.parametrize("tokens", [200, 700])
+def test_padding_outside_the_vocabulary_and_bad_ids(tokens):
+    """Few tokens and many take different kernels: both leave out padding and bad ids, and report the latter.
+    (The tolerance of a sum of n terms, as above: which terms are added first depends on all ids.)"""
+    torch, mx, _ = _setup()
+    ids = torch.arange(tokens, device="cuda") % 50
+    dy = _rows(torch, tokens, 24, 24, torch.float32, 3)
+    keep = (ids != 4).nonzero()[:, 0]
+    want = torch.zeros(50, 24, dtype=torch.float64, device="cuda").index_put_((ids[keep],), dy.double()[keep], accumulate=True)
+    size = torch.zeros(50, 24, dtype=torch.float64, device="cuda").index_put_((ids[keep],), dy.double()[keep].abs(), accumulate=True)
+    tol = (tokens // 50 + 4) * 2.0 ** -24 * size
+    got = mx.embedding_grad(torch.where(ids == 4, torch.full_like(ids, 70), ids), dy, 50, padding_id=70)
+    assert mx.device_status() == 0 and bool(((got.double() - want).abs() <= tol).all())
+    for bad in (50, -1, -2, 1 << 40):
+        got = mx.embedding_grad(torch.where(ids == 4, torch.full_like(ids, bad), ids), dy, 50, padding_id=-1)
+        assert mx.device_status() == 1 and bool(((got.double() - want).abs() <= tol).all())
 
 
 def test_gradient_without_tokens_and_all_padding():

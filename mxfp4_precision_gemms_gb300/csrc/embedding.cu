@@ -8,11 +8,11 @@
 // the table).  HBM bandwidth bounds every long call, launch latency the short ones.
 //
 // The gradient is three launches.
-//   1. Sort.  One cluster of eight CTAs sorts (id, token) pairs by id, stably, with a
+//   1. Sort.  One CTA, or a cluster of up to eight, sorts (id, token) pairs by id, stably, with a
 //      least-significant-digit radix sort of 9 bits a pass (two passes up to 262143 ids): each
 //      warp owns a contiguous run of tokens and counts its digits with match.any, so that the
-//      order within a digit is the order of the tokens.  The other clusters of the launch
-//      meanwhile clear the table.
+//      order within a digit is the order of the tokens.  The other CTAs of the launch meanwhile
+//      clear the table.
 //   2. Sum.  The sorted tokens are cut into chunks of kChunk.  A CTA owns one chunk and one slab
 //      of columns and adds its rows up in registers; a row of the table whose tokens all lie in
 //      the chunk is finished there.  A run that crosses a chunk's border leaves an fp32 partial
@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kLookupThreads)
 // ---------------------------------------------------------------- sort (and clear)
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCtas = 8;  // the portable cluster size
+constexpr int kSortCtasMost = 8;  // the portable cluster size
+constexpr uint32_t kSortTokens = 2048;  // tokens for each CTA: more CTAs pay for their barriers above that
 constexpr int kBits = 9;
 constexpr int kBins = 1 << kBits;
 // counters [warp][bin], this CTA's bin totals, the cluster-wide offsets, scan scratch
@@ -108,8 +109,7 @@ struct SortParams {
     uint32_t tokens;
     int64_t vocab, padding_id;
     uint2* buf[2];  // (key, token); the last pass writes buf[0]
-    Run* runs;           // short runs from the front, long ones from the back
-    uint32_t* num_runs;  // [2]: short, long
+    uint32_t* num_runs;  // [2]: cleared here, counted by the sums
     uint32_t* status;
     // clearing: rows of row_bytes, pitch_bytes apart
     uint8_t* dw;
@@ -129,10 +129,30 @@ __device__ __forceinline__ bool takes_part(int64_t id, int64_t vocab, int64_t pa
     return false;
 }
 
-// The key that a token sorts by: its id, or `vocab` (behind every row) when it is left out.
-__device__ __forceinline__ uint32_t token_key(const SortParams& p, uint32_t t) {
-    const int64_t id = load_id(p.ids, p.is64, t);
-    return (uint32_t)(takes_part(id, p.vocab, p.padding_id, p.status) ? id : p.vocab);
+// kSortItems (key, token) pairs of a lane, its tokens 32 apart from t0 on: in the first pass the key is
+// the token's id, or `vocab` (behind every row) when it is left out.
+__device__ __forceinline__ void load_pairs(const SortParams& p, const uint2* in, bool first_pass, uint32_t t0,
+                                           uint32_t end, uint2 (&kv)[kSortItems]) {
+    if (!first_pass) {
+#pragma unroll
+        for (int k = 0; k < kSortItems; ++k) {
+            const uint32_t t = t0 + k * 32;
+            kv[k] = t < end ? __ldcg(&in[t]) : make_uint2(0u, 0u);
+        }
+        return;
+    }
+    int64_t id[kSortItems];  // all loads before the first use
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const uint32_t t = t0 + k * 32;
+        id[k] = t < end ? load_id(p.ids, p.is64, t) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const uint32_t t = t0 + k * 32;
+        const bool on = t < end && takes_part(id[k], p.vocab, p.padding_id, p.status);
+        kv[k] = make_uint2((uint32_t)(on ? id[k] : p.vocab), t);
+    }
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -141,40 +161,53 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
-__device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
+// Barrier over the sorting CTAs, with their global writes visible to all of them.
+template <int CTAS>
+__device__ __forceinline__ void sort_sync() {
+    if constexpr (CTAS > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+
+template <int CTAS>
+__device__ void sort_tokens(const SortParams& p, uint32_t* smem) {
     if (p.tokens == 0) return;  // nothing to sort, and no workspace: the launch only clears
     uint32_t* count = smem;                       // [kSortWarps][kBins]
     uint32_t* total = count + kSortWarps * kBins;  // [kBins]
     uint32_t* base = total + kBins;                // [kBins]
     uint32_t* wsum = base + kBins;                 // [32]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = CTAS > 1 ? cluster_ctarank() : 0;
     // contiguous run of tokens of this warp, a multiple of 32 long
-    const uint32_t per_warp = ((p.tokens + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
+    const uint32_t per_warp = ((p.tokens + CTAS * kSortWarps * 32 - 1) / (CTAS * kSortWarps * 32)) * 32;
     const uint64_t first = (uint64_t)(rank * kSortWarps + warp) * per_warp;
     const uint32_t begin = (uint32_t)(first < p.tokens ? first : p.tokens);
     const uint32_t end = (uint32_t)(first + per_warp < p.tokens ? first + per_warp : p.tokens);
+    // warps of this CTA that have tokens
+    const uint64_t mine_from = (uint64_t)rank * kSortWarps * per_warp;
+    const uint32_t warps = mine_from >= p.tokens ? 0u
+                                                  : (uint32_t)min((uint64_t)kSortWarps,
+                                                                  (p.tokens - mine_from + per_warp - 1) / per_warp);
     uint32_t* mine = count + warp * kBins;
+    if (rank == 0 && tid < 2) p.num_runs[tid] = 0;
 
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * kBits;
         const uint2* in = p.buf[(p.passes - pass) & 1];
         uint2* out = p.buf[(p.passes - pass - 1) & 1];
-        for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) count[i] = 0;
+        for (uint32_t i = tid; i < warps * (kBins / 4); i += kSortThreads)
+            reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         for (uint32_t t0 = begin; t0 < end; t0 += 32 * kSortItems) {
-            uint32_t key[kSortItems];
-#pragma unroll
-            for (int k = 0; k < kSortItems; ++k) {
-                const uint32_t t = t0 + k * 32 + lane;
-                key[k] = t < end ? (pass == 0 ? token_key(p, t) : __ldcg(&in[t]).x) : 0u;
-            }
+            uint2 kv[kSortItems];
+            load_pairs(p, in, pass == 0, t0 + lane, end, kv);
 #pragma unroll
             for (int k = 0; k < kSortItems; ++k) {
                 const bool on = t0 + k * 32 + lane < end;
                 const uint32_t mask = __ballot_sync(0xffffffffu, on);
                 if (on) {
-                    const uint32_t d = (key[k] >> shift) & (kBins - 1);
+                    const uint32_t d = (kv[k].x >> shift) & (kBins - 1);
                     const uint32_t peers = __match_any_sync(mask, d);
                     if ((peers & ((1u << lane) - 1)) == 0) mine[d] += __popc(peers);
                 }
@@ -182,27 +215,35 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
             }
         }
         __syncthreads();
+        uint32_t before = 0, all = 0;
         if (tid < kBins) {  // exclusive over the warps of this CTA
             uint32_t run = 0;
-#pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = count[w * kBins + tid];
-                count[w * kBins + tid] = run;
-                run += c;
+            for (uint32_t w0 = 0; w0 < warps; w0 += 8) {
+                uint32_t c[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) c[j] = w0 + j < warps ? count[(w0 + j) * kBins + tid] : 0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (w0 + j < warps) count[(w0 + j) * kBins + tid] = run;
+                    run += c[j];
+                }
             }
             total[tid] = run;
+            all = run;
         }
-        cluster_sync();
-        uint32_t before = 0, all = 0;
-        if (tid < kBins) {
-            const uint32_t a = smem_u32(total + tid);
-            uint32_t c[kSortCtas];
+        if constexpr (CTAS > 1) {  // the other CTAs' totals
+            cluster_sync();
+            if (tid < kBins) {
+                const uint32_t a = smem_u32(total + tid);
+                uint32_t c[CTAS];
 #pragma unroll
-            for (int r = 0; r < kSortCtas; ++r) c[r] = ld_cluster_u32(mapa_shared(a, r));
+                for (int r = 0; r < CTAS; ++r) c[r] = ld_cluster_u32(mapa_shared(a, r));
+                all = 0;
 #pragma unroll
-            for (int r = 0; r < kSortCtas; ++r) {
-                before += r < (int)rank ? c[r] : 0u;
-                all += c[r];
+                for (int r = 0; r < CTAS; ++r) {
+                    before += r < (int)rank ? c[r] : 0u;
+                    all += c[r];
+                }
             }
         }
         // exclusive scan of `all` over the bins (16 warps of 32 bins)
@@ -215,18 +256,14 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
         if (tid < kBins) {
-            uint32_t lower = 0;
-            for (int w = 0; w < warp; ++w) lower += wsum[w];
+            uint32_t lower = lane < warp ? wsum[lane] : 0u;  // warp < 16
+            lower = __reduce_add_sync(0xffffffffu, lower);
             base[tid] = lower + inc - all + before;
         }
         __syncthreads();
         for (uint32_t t0 = begin; t0 < end; t0 += 32 * kSortItems) {
             uint2 kv[kSortItems];
-#pragma unroll
-            for (int k = 0; k < kSortItems; ++k) {
-                const uint32_t t = t0 + k * 32 + lane;
-                kv[k] = t < end ? (pass == 0 ? make_uint2(token_key(p, t), t) : __ldcg(&in[t])) : make_uint2(0u, 0u);
-            }
+            load_pairs(p, in, pass == 0, t0 + lane, end, kv);
 #pragma unroll
             for (int k = 0; k < kSortItems; ++k) {
                 const bool on = t0 + k * 32 + lane < end;
@@ -242,63 +279,10 @@ __device__ void sort_cluster(const SortParams& p, uint32_t* smem) {
                 __syncwarp();
             }
         }
-        // The pass's output is visible to the whole cluster, and no CTA's totals are still
-        // being read, before the next pass starts.
-        cluster_sync();
+        // The pass's output is visible to all of them, and no CTA's totals are still being read,
+        // before the next pass starts.
+        sort_sync<CTAS>();
     }
-    if (rank != 0) return;
-    // The runs that cross a chunk's border, in the order of their ids.
-    const uint2* sorted = p.buf[0];
-    const uint32_t chunks = (p.tokens + kChunk - 1) / kChunk;
-    uint32_t found[2] = {0, 0};
-    for (uint32_t c0 = 0; c0 + 1 < chunks; c0 += kSortThreads) {
-        const uint32_t c = c0 + tid;
-        bool starts = false;
-        uint32_t key = 0, end = 0;
-        if (c + 1 < chunks) {  // the last key of chunk c goes on in the next, and did not come from the one before
-            key = __ldcg(&sorted[(uint64_t)c * kChunk + kChunk - 1]).x;
-            starts = key != (uint32_t)p.vocab && __ldcg(&sorted[(uint64_t)(c + 1) * kChunk]).x == key &&
-                     (c == 0 || __ldcg(&sorted[(uint64_t)c * kChunk - 1]).x != key);
-        }
-        if (starts) {
-            // The first key of chunk lo is `key`, that of chunk hi is not.  Most runs end soon: strides
-            // that double first, then halving between the last two.
-            uint32_t lo = c + 1, hi = chunks;
-            for (uint32_t step = 1; lo + step < hi; step *= 2) {
-                if (__ldcg(&sorted[(uint64_t)(lo + step) * kChunk]).x != key) {
-                    hi = lo + step;
-                    break;
-                }
-                lo += step;
-            }
-            while (hi - lo > 1) {
-                const uint32_t mid = lo + (hi - lo) / 2;
-                if (__ldcg(&sorted[(uint64_t)mid * kChunk]).x == key)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            end = hi;
-        }
-        for (int kind = 0; kind < 2; ++kind) {
-            const bool mine_is = starts && (end - c > kLongRun) == (kind == 1);
-            const uint32_t votes = __ballot_sync(0xffffffffu, mine_is);
-            __syncthreads();  // the round before has read wsum
-            if (lane == 0) wsum[warp] = __popc(votes);
-            __syncthreads();
-            uint32_t lower = 0, all = 0;
-            for (int w = 0; w < kSortWarps; ++w) {
-                lower += w < warp ? wsum[w] : 0u;
-                all += wsum[w];
-            }
-            if (mine_is) {
-                const uint32_t at = found[kind] + lower + __popc(votes & ((1u << lane) - 1));
-                p.runs[kind ? chunks - 1 - at : at] = {key, c, end};
-            }
-            found[kind] += all;
-        }
-    }
-    if (tid < 2) p.num_runs[tid] = found[tid];
 }
 
 // Zeroes the table's part of CTA `part` of `parts`.
@@ -326,7 +310,7 @@ __device__ __forceinline__ void clear_table(const SortParams& p, uint32_t part, 
     }
 }
 
-// While the sort of a call that adds to the table keeps eight SMs busy, the others bring the
+// While the sort of a call that adds to the table keeps a few SMs busy, the others bring the
 // first rows of dy into L2, a CTA's threads kFetchBytes each.
 constexpr int64_t kFetchBytes = 4096;
 constexpr int64_t kFetchMost = int64_t(64) << 20;  // half of L2
@@ -336,16 +320,17 @@ __device__ __forceinline__ void fetch_rows(const SortParams& p, uint32_t part, u
         l2_prefetch(p.fetch + o, (uint32_t)(p.fetch_bytes - o < kFetchBytes ? p.fetch_bytes - o : kFetchBytes));
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads, 2) sort_clear_kernel(const __grid_constant__ SortParams p) {
     extern __shared__ __align__(16) uint32_t smem[];
     grid_dependency_wait();
     allow_dependent_launch();
-    if (blockIdx.x < kSortCtas)
-        sort_cluster(p, smem);
+    if (blockIdx.x < CTAS)
+        sort_tokens<CTAS>(p, smem);
     else if (!p.clear)
-        fetch_rows(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
+        fetch_rows(p, blockIdx.x - CTAS, gridDim.x - CTAS);
     else
-        clear_table(p, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
+        clear_table(p, blockIdx.x - CTAS, gridDim.x - CTAS);
 }
 
 // ---------------------------------------------------------------- sum and join
@@ -359,32 +344,43 @@ struct SumParams {
     float scale;
     int32_t accumulate;
     float* part;  // [chunks][2][dim]: a run that came in from the left, a run that goes out to the right
-    const Run* runs;
-    const uint32_t* num_runs;
+    Run* runs;           // short runs from the front, long ones from the back; in no particular order
+    uint32_t* num_runs;  // [2]: short, long
     uint32_t chunks;
 };
 
-template <class DW>
-__device__ __forceinline__ void finish(DW* dst, float sum, const SumParams& p) {
-    const float v = p.scale * sum;
-    store1(dst, p.accumulate ? load1(dst) + v : v);
-}
-template <class DW>
-__device__ __forceinline__ void finish8(DW* dst, float (&sum)[8], const SumParams& p) {
-    float v[8];
-    if (p.accumulate) {
-        unpack8(load8(dst), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fmaf(p.scale, sum[j], v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p.scale * sum[j];
-    }
-    store8(dst, v);
+// What a row of the table becomes: `old` is what it holds where the gradient is added to it.
+__device__ __forceinline__ float finished(float sum, float old, const SumParams& p) {
+    return p.accumulate ? fmaf(p.scale, sum, old) : p.scale * sum;
 }
 
-// One chunk of sorted tokens x one slab of columns (8 per thread, or one).
-template <class DY, class DW, bool VEC>
+// Enters the run that starts in this chunk and goes on in the next into its list.
+__device__ __forceinline__ void enter_run(const SumParams& p, uint32_t chunk, uint32_t key) {
+    // The first key of chunk lo is `key`, that of chunk hi is not.  Most runs end soon: strides
+    // that double first, then halving between the last two.
+    uint32_t lo = chunk + 1, hi = p.chunks;
+    for (uint32_t step = 1; lo + step < hi; step *= 2) {
+        if (__ldcg(&p.sorted[(uint64_t)(lo + step) * kChunk]).x != key) {
+            hi = lo + step;
+            break;
+        }
+        lo += step;
+    }
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (__ldcg(&p.sorted[(uint64_t)mid * kChunk]).x == key)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const bool is_long = hi - chunk > kLongRun;
+    const uint32_t at = atomicAdd(&p.num_runs[is_long ? 1 : 0], 1u);
+    p.runs[is_long ? p.chunks - 1 - at : at] = {key, chunk, hi};
+}
+
+// One chunk of sorted tokens x one slab of columns (8 per thread, or one).  ACC: dw is added to;
+// the rows that end in the chunk are loaded along with the tokens' rows.
+template <class DY, class DW, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, const DY* dy, DW* dw) {
     constexpr int U = VEC ? 8 : 1;
     __shared__ uint2 kv[kChunk + 2];  // with the neighbours' keys on both sides
@@ -398,27 +394,41 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
         kv[i] = at >= 0 && at < p.tokens ? p.sorted[at] : make_uint2(0xffffffffu, 0);
     }
     __syncthreads();
+    const uint32_t none = (uint32_t)p.vocab;  // the key of tokens that are left out
+    if (kv[1].x == none) return;
+    if (slab == 0 && threadIdx.x == kSumThreads - 1) {
+        const uint32_t key = kv[n].x;
+        if (key != none && kv[n + 1].x == key && kv[0].x != key) enter_run(p, chunk, key);
+    }
     const int64_t col = ((int64_t)slab * kSumThreads + threadIdx.x) * U;
-    if (col >= p.dim || kv[1].x == (uint32_t)p.vocab) return;
+    if (col >= p.dim) return;
 
     float acc[U] = {};
     for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
         Raw8<DY> raw[VEC ? kAhead : 1];
-        float one[VEC ? 1 : kAhead];
+        Raw8<DW> old[VEC && ACC ? kAhead : 1];
+        float one[VEC ? 1 : kAhead], old1[VEC ? 1 : kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-            const bool on = i0 + a < n && kv[1 + i0 + a].x != (uint32_t)p.vocab;
-            const DY* src = dy + (int64_t)kv[1 + (on ? i0 + a : 0)].y * p.lddy + col;
-            if constexpr (VEC) {
-                if (on) raw[a] = load8(src);
-            } else {
-                if (on) one[a] = load1(src);
+            const uint32_t i = i0 + a;
+            if (i >= n || kv[1 + i].x == none) break;
+            const uint32_t key = kv[1 + i].x;
+            const DY* src = dy + (int64_t)kv[1 + i].y * p.lddy + col;
+            if constexpr (VEC)
+                raw[a] = load8(src);
+            else
+                one[a] = load1(src);
+            if (ACC && kv[2 + i].x != key && kv[0].x != key) {
+                if constexpr (VEC)
+                    old[a] = load8(dw + (int64_t)key * p.lddw + col);
+                else
+                    old1[a] = load1(dw + (int64_t)key * p.lddw + col);
             }
         }
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
             const uint32_t i = i0 + a;
-            if (i >= n || kv[1 + i].x == (uint32_t)p.vocab) break;
+            if (i >= n || kv[1 + i].x == none) break;
             if constexpr (VEC) {
                 float v[8];
                 unpack8(raw[a], v);
@@ -434,10 +444,16 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
             // first key and the one before it are the same.
             const bool from_left = kv[0].x == key;
             if (last && !from_left) {
-                if constexpr (VEC)
-                    finish8(dw + (int64_t)key * p.lddw + col, acc, p);
-                else
-                    finish(dw + (int64_t)key * p.lddw + col, acc[0], p);
+                DW* dst = dw + (int64_t)key * p.lddw + col;
+                if constexpr (VEC) {
+                    float v[8] = {};
+                    if constexpr (ACC) unpack8(old[a], v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = finished(acc[j], v[j], p);
+                    store8(dst, v);
+                } else {
+                    store1(dst, finished(acc[0], ACC ? old1[a] : 0.f, p));
+                }
             } else {
                 float* to = p.part + ((int64_t)chunk * 2 + (from_left ? 0 : 1)) * p.dim + col;
                 if constexpr (VEC)
@@ -493,7 +509,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, D
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < kJoinWarps; ++k) sum += part[k][i];
-            finish(dw + (int64_t)run.key * p.lddw + col0 + i, sum, p);
+            DW* dst = dw + (int64_t)run.key * p.lddw + col0 + i;
+            store1(dst, finished(sum, p.accumulate ? load1(dst) : 0.f, p));
         }
     }
     for (uint64_t item = (uint64_t)blockIdx.x * kJoinWarps + warp; item < shorts; item += (uint64_t)gridDim.x * kJoinWarps) {
@@ -501,12 +518,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, D
         const Run run = p.runs[item / slabs];
         const int64_t col = ((int64_t)slab * 32 + lane) * U;
         if (col >= p.dim) continue;
-        float acc[U] = {};
+        DW* dst = dw + (int64_t)run.key * p.lddw + col;
+        float acc[U] = {}, old[U] = {};
+        if (p.accumulate) {
+            if constexpr (VEC)
+                load4(dst, old);
+            else
+                old[0] = load1(dst);
+        }
 #pragma unroll 4
         for (uint32_t c = run.first; c < run.end; ++c) add(acc, run, c, col);
-        DW* dst = dw + (int64_t)run.key * p.lddw + col;
 #pragma unroll
-        for (int j = 0; j < U; ++j) finish(dst + j, acc[j], p);
+        for (int j = 0; j < U; ++j) acc[j] = finished(acc[j], old[j], p);
+        if constexpr (VEC)
+            store4(dst, acc);
+        else
+            store1(dst, acc[0]);
     }
 }
 
@@ -560,7 +587,14 @@ __global__ void __launch_bounds__(kSumThreads) few_kernel(const FewParams f, con
     __syncthreads();
     const int64_t col = ((int64_t)blockIdx.y * kSumThreads + threadIdx.x) * U;
     if (col >= p.dim) return;
-    float acc[U] = {};
+    DW* dst = dw + id * p.lddw + col;
+    float acc[U] = {}, old[U] = {};
+    if (p.accumulate) {
+        if constexpr (VEC)
+            unpack8(load8(dst), old);
+        else
+            old[0] = load1(dst);
+    }
     for (uint32_t i0 = 0; i0 < n; i0 += kFewAhead) {
         Raw8<DY> raw[VEC ? kFewAhead : 1];
         float one[VEC ? 1 : kFewAhead];
@@ -586,10 +620,12 @@ __global__ void __launch_bounds__(kSumThreads) few_kernel(const FewParams f, con
             }
         }
     }
+#pragma unroll
+    for (int j = 0; j < U; ++j) acc[j] = finished(acc[j], old[j], p);
     if constexpr (VEC)
-        finish8(dw + id * p.lddw + col, acc, p);
+        store8(dst, acc);
     else
-        finish(dw + id * p.lddw + col, acc[0], p);
+        store1(dst, acc[0]);
 }
 
 // ---------------------------------------------------------------- launches
@@ -625,7 +661,8 @@ cudaError_t launch_sum(SumParams p, const void* dy, void* dw, int sms, cudaStrea
     p.chunks = (p.tokens + kChunk - 1) / kChunk;
     const int64_t ctas = (int64_t)p.chunks * ((p.dim + per - 1) / per);
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_overlapped(sum_kernel<DY, DW, VEC>, dim3((unsigned)ctas), dim3(kSumThreads), 0, s, 1, true, p,
+    auto kern = p.accumulate ? sum_kernel<DY, DW, VEC, true> : sum_kernel<DY, DW, VEC, false>;
+    cudaError_t e = launch_overlapped(kern, dim3((unsigned)ctas), dim3(kSumThreads), 0, s, 1, true, p,
                                       static_cast<const DY*>(dy), static_cast<DW*>(dw));
     if (e != cudaSuccess || p.chunks < 2) return e;
     constexpr int per_join = 32 * (VEC ? 4 : 1);
@@ -635,21 +672,29 @@ cudaError_t launch_sum(SumParams p, const void* dy, void* dw, int sms, cudaStrea
                              0, s, 1, true, p, static_cast<DW*>(dw), slabs);
 }
 
-cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
+template <int CTAS>
+cudaError_t launch_sort_of(const SortParams& p, int sms, cudaStream_t s) {
+    auto kern = sort_clear_kernel<CTAS>;
     static DeviceSlots slots;
     int set = 0;
     cudaError_t e = per_device_setting(slots, &set, [&](int, int* n) {
         *n = 1;
-        return cudaFuncSetAttribute(sort_clear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     });
     if (e != cudaSuccess) return e;
     const int64_t stretches = (p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes;
     const int64_t clear_ctas = p.clear_flat ? stretches : std::min<int64_t>(stretches, 8 * sms);
     const int64_t fetch_ctas = (p.fetch_bytes + kSortThreads * kFetchBytes - 1) / (kSortThreads * kFetchBytes);
-    const int64_t clusters = 1 + ((p.clear ? clear_ctas : fetch_ctas) + kSortCtas - 1) / kSortCtas;
-    if (clusters * kSortCtas > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_overlapped(sort_clear_kernel, dim3((unsigned)(clusters * kSortCtas)), dim3(kSortThreads), kSortSmem, s, kSortCtas,
-                             true, p);
+    const int64_t clusters = 1 + ((p.clear ? clear_ctas : fetch_ctas) + CTAS - 1) / CTAS;
+    if (clusters * CTAS > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(kern, dim3((unsigned)(clusters * CTAS)), dim3(kSortThreads), kSortSmem, s, CTAS, true, p);
+}
+
+cudaError_t launch_sort(const SortParams& p, int sms, cudaStream_t s) {
+    if (p.tokens <= kSortTokens) return launch_sort_of<1>(p, sms, s);
+    if (p.tokens <= 2 * kSortTokens) return launch_sort_of<2>(p, sms, s);
+    if (p.tokens <= 4 * kSortTokens) return launch_sort_of<4>(p, sms, s);
+    return launch_sort_of<kSortCtasMost>(p, sms, s);
 }
 
 bool valid_float(int t) { return t == MXFP4_OUT_F32 || t == MXFP4_OUT_BF16; }
@@ -774,7 +819,6 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     sp.buf[1] = tokens > 0 ? reinterpret_cast<uint2*>(at + sorted_bytes(tokens)) : nullptr;
     if (tokens > 0) {
         sp.num_runs = reinterpret_cast<uint32_t*>(at + 2 * sorted_bytes(tokens));
-        sp.runs = reinterpret_cast<Run*>(at + 2 * sorted_bytes(tokens) + 16);
     }
     sp.status = device_status_ptr();
     sp.dw = static_cast<uint8_t*>(dw);
@@ -805,7 +849,7 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     p.lddw = lddw;
     p.scale = scale;
     p.accumulate = accumulate;
-    p.runs = sp.runs;
+    p.runs = reinterpret_cast<Run*>(at + 2 * sorted_bytes(tokens) + 16);
     p.num_runs = sp.num_runs;
     p.part = reinterpret_cast<float*>(at + 2 * sorted_bytes(tokens) + runs_bytes(tokens));
     const bool vec = vector_rows(dy, lddy, dim, esize(dy_dtype)) && vector_rows(dw, lddw, dim, wsz);

@@ -114,9 +114,7 @@ struct SortParams {
     // clearing: rows of row_bytes, pitch_bytes apart
     uint8_t* dw;
     int64_t rows, row_bytes, pitch_bytes;
-    int32_t clear;       // otherwise the CTAs beside the sorting ones fetch dy into L2
-    const uint8_t* fetch;
-    int64_t fetch_bytes;
+    int32_t clear;
     int32_t clear_flat;  // contiguous and 16-byte aligned: one run of bytes
     int32_t clear_vec;   // 16-byte aligned rows of a multiple of 16 bytes
 };
@@ -310,16 +308,6 @@ __device__ __forceinline__ void clear_table(const SortParams& p, uint32_t part, 
     }
 }
 
-// While the sort of a call that adds to the table keeps a few SMs busy, the others bring the
-// first rows of dy into L2, a CTA's threads kFetchBytes each.
-constexpr int64_t kFetchBytes = 4096;
-constexpr int64_t kFetchMost = int64_t(64) << 20;  // half of L2
-__device__ __forceinline__ void fetch_rows(const SortParams& p, uint32_t part, uint32_t parts) {
-    for (int64_t o = ((int64_t)part * kSortThreads + threadIdx.x) * kFetchBytes; o < p.fetch_bytes;
-         o += (int64_t)parts * kSortThreads * kFetchBytes)
-        l2_prefetch(p.fetch + o, (uint32_t)(p.fetch_bytes - o < kFetchBytes ? p.fetch_bytes - o : kFetchBytes));
-}
-
 template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads, 2) sort_clear_kernel(const __grid_constant__ SortParams p) {
     extern __shared__ __align__(16) uint32_t smem[];
@@ -327,14 +315,14 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_clear_kernel(const __gri
     allow_dependent_launch();
     if (blockIdx.x < CTAS)
         sort_tokens<CTAS>(p, smem);
-    else if (!p.clear)
-        fetch_rows(p, blockIdx.x - CTAS, gridDim.x - CTAS);
     else
         clear_table(p, blockIdx.x - CTAS, gridDim.x - CTAS);
 }
 
 // ---------------------------------------------------------------- sum and join
-constexpr int kAhead = 8;  // rows loaded before they are added
+// Rows loaded before they are added; with the rows of dw that they are added to, half as many leave
+// registers for six CTAs an SM (32768 tokens into 32000 x 4096 fp32: 136 us with 8, 125 with 4, 127 with 2).
+constexpr int kAhead = 8, kAheadAcc = 4;
 constexpr int kSumThreads = 128;
 
 struct SumParams {
@@ -383,6 +371,7 @@ __device__ __forceinline__ void enter_run(const SumParams& p, uint32_t chunk, ui
 template <class DY, class DW, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, const DY* dy, DW* dw) {
     constexpr int U = VEC ? 8 : 1;
+    constexpr int AHEAD = ACC ? kAheadAcc : kAhead;
     __shared__ uint2 kv[kChunk + 2];  // with the neighbours' keys on both sides
     grid_dependency_wait();
     allow_dependent_launch();
@@ -404,12 +393,12 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
     if (col >= p.dim) return;
 
     float acc[U] = {};
-    for (uint32_t i0 = 0; i0 < n; i0 += kAhead) {
-        Raw8<DY> raw[VEC ? kAhead : 1];
-        Raw8<DW> old[VEC && ACC ? kAhead : 1];
-        float one[VEC ? 1 : kAhead], old1[VEC ? 1 : kAhead];
+    for (uint32_t i0 = 0; i0 < n; i0 += AHEAD) {
+        Raw8<DY> raw[VEC ? AHEAD : 1];
+        Raw8<DW> old[VEC && ACC ? AHEAD : 1];
+        float one[VEC ? 1 : AHEAD], old1[VEC ? 1 : AHEAD];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < AHEAD; ++a) {
             const uint32_t i = i0 + a;
             if (i >= n || kv[1 + i].x == none) break;
             const uint32_t key = kv[1 + i].x;
@@ -426,7 +415,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
             }
         }
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < AHEAD; ++a) {
             const uint32_t i = i0 + a;
             if (i >= n || kv[1 + i].x == none) break;
             if constexpr (VEC) {
@@ -538,9 +527,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SumParams p, D
 }
 
 // ---------------------------------------------------------------- few tokens
-// At most this many tokens go without the sort: its three launches cost 17 to 21 us whatever their
-// number, the lookup 4.6 us at 23 tokens and 5.4 at 239.  A run of equal ids is added by one CTA here, which at
-// 256 equal ones takes as long as the sort's way; beyond, that would be slower.
+// At most this many tokens go without the sort.  Added to a 4000 x 2048 fp32 table, 23 tokens take 2.7 us
+// and 512 5.7, where the sort's three launches take 17 for 513.  512 equal ids are the worst: one CTA
+// a slab adds them all, 31 us against 19.
 constexpr uint32_t kFewTokens = 512;
 constexpr int kFewAhead = 16;  // rows loaded before they are added
 
@@ -684,8 +673,7 @@ cudaError_t launch_sort_of(const SortParams& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t stretches = (p.rows * p.row_bytes + kClearBytes - 1) / kClearBytes;
     const int64_t clear_ctas = p.clear_flat ? stretches : std::min<int64_t>(stretches, 8 * sms);
-    const int64_t fetch_ctas = (p.fetch_bytes + kSortThreads * kFetchBytes - 1) / (kSortThreads * kFetchBytes);
-    const int64_t clusters = 1 + ((p.clear ? clear_ctas : fetch_ctas) + CTAS - 1) / CTAS;
+    const int64_t clusters = 1 + ((p.clear ? clear_ctas : 0) + CTAS - 1) / CTAS;
     if (clusters * CTAS > INT32_MAX) return cudaErrorInvalidConfiguration;
     return launch_overlapped(kern, dim3((unsigned)(clusters * CTAS)), dim3(kSortThreads), kSortSmem, s, CTAS, true, p);
 }
@@ -829,11 +817,6 @@ extern "C" mxfp4_status mxfp4_embedding_grad(const void* ids, int ids_dtype, int
     sp.clear_flat = base16 && sp.pitch_bytes == sp.row_bytes;
     sp.clear_vec = base16 && sp.row_bytes % 16 == 0 && sp.pitch_bytes % 16 == 0;
     sp.clear = !accumulate;
-    const int64_t dsz = esize(dy_dtype);
-    if (accumulate && !few && lddy == dim && reinterpret_cast<uintptr_t>(dy) % 16 == 0) {
-        sp.fetch = static_cast<const uint8_t*>(dy);
-        sp.fetch_bytes = std::min<int64_t>(tokens * dim * dsz, kFetchMost) / 16 * 16;
-    }
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess && !(few && accumulate)) e = launch_sort(sp, sms, s);

@@ -15,7 +15,7 @@
 //             hold cannot reach a sum (left out before the loss of at most 256 tokens)
 //   stats     logits tile by tile; each thread reduces 128 columns of one row to (max, sum)
 //   combine   joins the tiles' statistics, writes lse and the losses
-//   dlogits   logits of one piece again -> dz in bf16
+//   dlogits   logits of one piece again -> dz in bf16 (as the sum of two for at most 128 tokens)
 //   products  dh += dz w and dw = dz^T h of that piece, in one launch
 //   scatter   adds up the parts of dh and puts its rows back in the tokens' order
 //
@@ -101,6 +101,7 @@ struct CeParams {
     const void* targets;
     int32_t col0;           // first vocabulary index of this launch's columns
     int32_t rows;           // pitch of the statistics: padded token count
+    int32_t paired;         // gradient of at most kPaired tokens: see there
     float2* stats;          // [tile * 2 + half][rows]: (max * log2 e, sum of 2^(z log2 e - max))
     float* target_logit;    // [rows]
     const float* lse2;      // [rows] lse * log2 e
@@ -108,6 +109,13 @@ struct CeParams {
     uint32_t* status;
     uint64_t wait_ns;
 };
+
+// dz is rounded to bf16 for the tensor cores, which costs a gradient as much as its own rounding
+// does; over many tokens the errors of their dz average out, over a few they need not (dz - p is
+// near -1 at the target and its error then goes into the whole row of dh).  At most kPaired tokens fill half
+// of a tile's rows, so the other half, idle otherwise, holds their rows again with what the
+// rounding left of dz: both products then sum dz to 16 bits, at no cost.
+constexpr int32_t kPaired = 128;
 
 enum Kind { kStats = 0, kDlogits = 1, kProducts = 2 };
 
@@ -318,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     allow_dependent_launch();
     int32_t count = p.tokens;
     if (KIND != kStats || !p.direct) count = counted_tokens(p.header);
+    const int32_t rows = KIND != kStats && p.paired ? kTile : count;  // that hold something
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs)
@@ -330,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             bool ok = true;
             Tile t;
             Walk<KIND> walk;
-            walk.start(p, count, cluster, num_clusters);
-            while (ok && walk.next(p, count, t)) {
+            walk.start(p, rows, cluster, num_clusters);
+            while (ok && walk.next(p, rows, t)) {
                 const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                 const int32_t ya = t.m0 + (int32_t)rank * 128, yb = t.n0 + (int32_t)rank * (q.tile_n / 2);
                 for (int32_t i = 0; i < t.stages; ++i) {
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 bool ok = true;
                 Tile t;
                 Walk<KIND> walk;
-                walk.start(p, count, cluster, num_clusters);
-                while (ok && walk.next(p, count, t)) {
+                walk.start(p, rows, cluster, num_clusters);
+                while (ok && walk.next(p, rows, t)) {
                     const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
                     const uint32_t idesc = idesc_bf16(256, (uint32_t)q.tile_n, q.a_mn != 0, q.b_mn != 0);
                     // K = 16 further on: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise.
@@ -442,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
         bool ok = true;
         Tile t;
         Walk<KIND> walk;
-        walk.start(p, count, cluster, num_clusters);
-        while (ok && walk.next(p, count, t)) {
+        walk.start(p, rows, cluster, num_clusters);
+        while (ok && walk.next(p, rows, t)) {
             const Product& q = p.prod[KIND == kProducts ? t.prob : 0];
             const int32_t row0 = t.m0 + (int32_t)rank * 128 + quad * 32;
             const int32_t row = row0 + lane;
@@ -451,6 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             // per-row values first: their latency hides behind the wait for the accumulator
             int32_t tgt = -1;
             float lse2 = 0.f, ratio = 0.f;
+            const bool counts = (p.paired ? row & (kPaired - 1) : row) < count;
+            const bool low_half = p.paired && row >= kPaired;
             if constexpr (KIND != kProducts) {
                 if (KIND == kStats && p.direct) {  // one that does not count hits no column, or its value is not used
                     const int64_t y = row < count ? load_id(p.targets, p.is64, row) : -1;
@@ -558,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                                 const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
                                 x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
                             }
-                            w[j] = row < count ? pack_bf16(x[0], x[1]) : 0u;
+                            w[j] = pack_bf16(x[0], x[1]);
+                            if (low_half) w[j] = pack_bf16(x[0] - bf16_lo(w[j]), x[1] - bf16_hi(w[j]));
+                            if (!counts) w[j] = 0u;
                         }
                         boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
                     } else {
@@ -603,6 +616,7 @@ struct GatherParams {
     const bf16* h;
     int64_t ldh;
     int32_t tokens, dim, vocab;
+    int32_t paired;  // each row again kPaired rows further down
     int32_t vec;  // rows of h can be read in 16-byte vectors
     const void* targets;
     int32_t is64;
@@ -698,8 +712,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
                 p.target[r] = y;
                 p.source[r] = t;
                 if constexpr (GRAD) {
-                    p.lse2[r] = p.lse[t] * kLog2e;
-                    p.ratio[r] = p.reduction == MXFP4_REDUCE_NONE ? p.dloss[t] : 1.f;
+                    const float l = p.lse[t] * kLog2e;
+                    const float g = p.reduction == MXFP4_REDUCE_NONE ? p.dloss[t] : 1.f;
+                    p.lse2[r] = l;
+                    p.ratio[r] = g;
+                    if (p.paired) {
+                        p.target[r + kPaired] = y;
+                        p.lse2[r + kPaired] = l;
+                        p.ratio[r + kPaired] = g;
+                    }
                 }
             } else if constexpr (!GRAD) {
                 p.lse_out[t] = 0.f;
@@ -711,29 +732,35 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
         for (int32_t i = warp; i < n_list; i += kGatherWarps) {
             const bf16* src = p.h + (int64_t)list_src[i] * p.ldh;
             bf16* dst = p.rows + (int64_t)(before + i) * p.dim;
-            if (p.vec) {
+            for (int copy = 0; copy <= (GRAD ? p.paired : 0); ++copy, dst += (int64_t)kPaired * p.dim) {
+                if (p.vec) {
 #pragma unroll 8
-                for (int u = lane; u < units; u += 32)
-                    reinterpret_cast<uint4*>(dst)[u] = reinterpret_cast<const uint4*>(src)[u];
-            } else {
-                for (int c = lane; c < p.dim; c += 32) dst[c] = src[c];
+                    for (int u = lane; u < units; u += 32)
+                        reinterpret_cast<uint4*>(dst)[u] = reinterpret_cast<const uint4*>(src)[u];
+                } else {
+                    for (int c = lane; c < p.dim; c += 32) dst[c] = src[c];
+                }
             }
         }
         before += all;
     }
     // Behind the counted rows: their dz is 0 up to the end of the last tile, whatever their logits are,
     // but rows that share dw's last stage with them are multiplied by that 0 and must be finite.
-    const int32_t padded = pad_rows(total), stage_end = (max(total, 1) + kK - 1) / kK * kK;
-    for (int32_t r = total + (int32_t)blockIdx.x * kGatherWarps + warp; r < padded; r += (int32_t)gridDim.x * kGatherWarps) {
-        if (GRAD && r < stage_end) {
-            bf16* dst = p.rows + (int64_t)r * p.dim;
-            for (int u = lane; u < units; u += 32) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0, 0, 0, 0);
+    const bool paired = GRAD && p.paired;
+    const int32_t padded = paired ? kPaired : pad_rows(total);
+    const int32_t stage_end = paired ? kPaired : (max(total, 1) + kK - 1) / kK * kK;
+    for (int32_t r0 = total + (int32_t)blockIdx.x * kGatherWarps + warp; r0 < padded;
+         r0 += (int32_t)gridDim.x * kGatherWarps)
+        for (int32_t r = r0; r <= r0 + (paired ? kPaired : 0); r += kPaired) {
+            if (GRAD && r0 < stage_end) {
+                bf16* dst = p.rows + (int64_t)r * p.dim;
+                for (int u = lane; u < units; u += 32) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0, 0, 0, 0);
+            }
+            if (lane == 0) {
+                p.target[r] = -1;
+                if constexpr (GRAD) p.lse2[r] = 0.f, p.ratio[r] = 0.f;
+            }
         }
-        if (lane == 0) {
-            p.target[r] = -1;
-            if constexpr (GRAD) p.lse2[r] = 0.f, p.ratio[r] = 0.f;
-        }
-    }
 }
 
 // ---------------------------------------------------------------- combine
@@ -854,7 +881,7 @@ constexpr int kScatterThreads = 256;
 template <class DH>
 __global__ void __launch_bounds__(kScatterThreads)
     scatter_kernel(const Header* header, const int32_t* place, const float* parts, int32_t splits, int64_t slot_elems,
-                   int32_t tokens, int32_t dim, uint32_t segs, DH* dh, int64_t lddh, int32_t vec) {
+                   int32_t tokens, int32_t dim, uint32_t segs, DH* dh, int64_t lddh, int32_t vec, int32_t paired) {
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t wid = (int64_t)blockIdx.x * (kScatterThreads / 32) + (threadIdx.x >> 5);
@@ -866,12 +893,14 @@ __global__ void __launch_bounds__(kScatterThreads)
     float v[8] = {};
     if (r >= 0) {
         const float* src = parts + (int64_t)r * dim + u * 8;
-        for (int32_t k = 0; k < splits; ++k) {
-            float x[8];
-            unpack8(load8(src + k * slot_elems), x);
+        for (int half = 0; half <= paired; ++half, src += (int64_t)kPaired * dim)
+#pragma unroll 4
+            for (int32_t k = 0; k < splits; ++k) {
+                float x[8];
+                unpack8(load8(src + k * slot_elems), x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += x[j];
-        }
+                for (int j = 0; j < 8; ++j) v[j] += x[j];
+            }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= gscale;
     }
@@ -1007,12 +1036,13 @@ cudaError_t launch_matrix(const CeParams& p, int64_t tiles, cudaStream_t s) {
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t width) { return ((m + kTile - 1) / kTile) * ((n + width - 1) / width); }
 
-cudaError_t gather_grid(int64_t tokens, int* grid) {
+// Eight tokens to a CTA, two CTAs an SM; for a gradient's few tokens more CTAs share the zero rows behind them.
+cudaError_t gather_grid(int64_t tokens, int least, int* grid) {
     static DeviceSlots slots;
     int sms = 0;
     cudaError_t e = per_device_setting(
         slots, &sms, [&](int dev, int* n) { return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev); });
-    *grid = (int)std::min<int64_t>(2 * sms, std::max<int64_t>(1, (tokens + 7) / 8));
+    *grid = (int)std::min<int64_t>(2 * sms, std::max<int64_t>(least, (tokens + 7) / 8));
     return e;
 }
 
@@ -1147,7 +1177,7 @@ extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t d
         g.lse_out = lse;
         g.status = p.status;
         int grid = 1;
-        e = gather_grid(tokens, &grid);
+        e = gather_grid(tokens, 1, &grid);
         if (e == cudaSuccess)
             e = launch_overlapped(gather_kernel<false>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
         if (e != cudaSuccess) return launch_failed(what, "gather", e);
@@ -1231,6 +1261,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
     g.tokens = (int32_t)tokens;
     g.dim = (int32_t)dim;
     g.vocab = (int32_t)vocab;
+    g.paired = tokens <= kPaired;
     g.vec = vector_rows(h, ldh, dim, 2);
     g.targets = targets;
     g.is64 = ids_dtype == MXFP4_IDS_I64;
@@ -1247,7 +1278,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
     g.ratio = reinterpret_cast<float*>(base + l.ratio);
     g.status = device_status_ptr();
     int grid = 1;
-    e = gather_grid(tokens, &grid);
+    e = gather_grid(tokens, 32, &grid);
     if (e == cudaSuccess)
         e = launch_overlapped(gather_kernel<true>, dim3(grid), dim3(kGatherThreads), 0, s, 1, true, g);
     if (e != cudaSuccess) return launch_failed(what, "gather", e);
@@ -1262,6 +1293,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
         p.target = g.target;
         p.col0 = (int32_t)v0;
             p.rows = l.padded;
+        p.paired = g.paired;
         p.lse2 = g.lse2;
         p.ratio = g.ratio;
         p.status = g.status;
@@ -1339,12 +1371,12 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             e = launch_overlapped(scatter_kernel<bf16>, dim3((unsigned)blocks), dim3(kScatterThreads), 0, s, 1, true,
                                   (const Header*)g.header, (const int32_t*)g.place, (const float*)parts, l.splits, slot,
                                   (int32_t)tokens, (int32_t)dim, segs, static_cast<bf16*>(dh), lddh,
-                                  (int32_t)vector_rows(dh, lddh, dim, 2));
+                                  (int32_t)vector_rows(dh, lddh, dim, 2), g.paired);
         else
             e = launch_overlapped(scatter_kernel<float>, dim3((unsigned)blocks), dim3(kScatterThreads), 0, s, 1, true,
                                   (const Header*)g.header, (const int32_t*)g.place, (const float*)parts, l.splits, slot,
                                   (int32_t)tokens, (int32_t)dim, segs, static_cast<float*>(dh), lddh,
-                                  (int32_t)vector_rows(dh, lddh, dim, 4));
+                                  (int32_t)vector_rows(dh, lddh, dim, 4), g.paired);
         if (e != cudaSuccess) return launch_failed(what, "scatter", e);
     }
     return record_error(MXFP4_OK, "%s", "");

@@ -714,14 +714,14 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
     if len(outs) != n:
         raise ValueError(f"{len(outs)} outs for {n} gradients")
     # Whole-list passes of the tensors' own C methods: a call may come with hundreds of gradients.
-    kinds = [_OUT_OF.get(d) for d in map(_dtype_of, grads)]
+    kinds = list(map(_OUT_OF.get, map(_dtype_of, grads)))
     sizes = list(map(_numel, grads))
     if None in kinds or not all(map(_is_cuda, grads)) or not all(map(_is_contiguous, grads)):
         raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
     at = list(map(_data_ptr, grads))
     to = at
     if outs is not grads:
-        if (kinds != [_OUT_OF.get(d) for d in map(_dtype_of, outs)] or sizes != list(map(_numel, outs))
+        if (kinds != list(map(_OUT_OF.get, map(_dtype_of, outs))) or sizes != list(map(_numel, outs))
                 or not all(map(_is_cuda, outs)) or not all(map(_is_contiguous, outs))):
             raise ValueError("outs must be contiguous CUDA tensors of their gradients' sizes and types")
         to = list(map(_data_ptr, outs))

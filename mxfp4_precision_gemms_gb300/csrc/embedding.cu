@@ -703,6 +703,11 @@ size_t chunks_of(int64_t tokens) { return (size_t)((tokens + kChunk - 1) / kChun
 // the number of runs (16 bytes) and the runs
 size_t runs_bytes(int64_t tokens) { return up256(16 + chunks_of(tokens) * sizeof(Run)); }
 
+// Whether the grids of a call's launches hold: tokens x slabs of the narrowest kind (single elements).
+bool grids_fit(int64_t tokens, int64_t dim) {
+    return tokens * ((dim + kSumThreads - 1) / kSumThreads) / 8 < INT32_MAX / 4;
+}
+
 mxfp4_status check_table(const char* what, int ids_dtype, int64_t tokens, int64_t vocab, int64_t dim) {
     if (ids_dtype != MXFP4_IDS_I32 && ids_dtype != MXFP4_IDS_I64)
         return record_error(MXFP4_ERR_INVALID_ARG, "%s: bad ids_dtype %d", what, ids_dtype);
@@ -710,6 +715,9 @@ mxfp4_status check_table(const char* what, int ids_dtype, int64_t tokens, int64_
     if (tokens > INT32_MAX || vocab >= INT32_MAX || dim > kMaxDim)
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens and vocab must be below 2^31, dim at most %lld",
                             what, (long long)kMaxDim);
+    if (!grids_fit(tokens, dim))
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld tokens of %lld columns are too many", what,
+                            (long long)tokens, (long long)dim);
     return MXFP4_OK;
 }
 

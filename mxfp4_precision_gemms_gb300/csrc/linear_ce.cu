@@ -999,8 +999,10 @@ Layout lay_out(int64_t tokens, int64_t vocab, int64_t dim, bool grad) {
     return l;
 }
 
+// The kernels count rows, columns and tiles in 32 bits.
 bool sizes_fit(int64_t tokens, int64_t vocab, int64_t dim) {
-    return tokens >= 0 && vocab >= 0 && dim >= 0 && tokens <= (1 << 24) && vocab <= (1 << 28) && dim <= (1 << 16);
+    return tokens >= 0 && vocab >= 0 && dim >= 0 && tokens <= (1 << 24) && vocab <= (1 << 28) && dim <= (1 << 16) &&
+           ((tokens + kTile - 1) / kTile) * ((vocab + 127) / 128) <= (1 << 30);
 }
 
 template <int KIND>
@@ -1029,7 +1031,6 @@ cudaError_t launch_matrix(const CeParams& p, int64_t tiles, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorNotSupported;
-    if (tiles > INT32_MAX - 1024) return cudaErrorInvalidConfiguration;  // the kernel counts them in 32 bits
     const int64_t grid = 2 * std::min<int64_t>(tiles, clusters);
     return launch_overlapped(kern, dim3((unsigned)grid), dim3(kThreads), kSmem, s, 2, true, p);
 }
@@ -1058,7 +1059,7 @@ mxfp4_status check_common(const char* what, const void* h, int64_t tokens, int64
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: vocab and dim must be positive", what);
     if (dim % 8) return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: dim (%lld) %% 8 != 0", what, (long long)dim);
     if (!sizes_fit(tokens, vocab, dim))
-        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tokens, 2^28 ids or 2^16 columns", what);
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tokens, 2^28 ids, 2^16 columns or 2^45 logits", what);
     if (!w) return record_error(MXFP4_ERR_INVALID_ARG, "%s: w is NULL", what);
     if (reinterpret_cast<uintptr_t>(w) % 16 || ldw % 8)
         return record_error(MXFP4_ERR_MISALIGNED, "%s: w must be 16-byte aligned with ldw %% 8 == 0", what);

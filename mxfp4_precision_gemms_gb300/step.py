@@ -9,6 +9,7 @@ fp32 number for each token.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as mx
 
@@ -24,6 +25,7 @@ class EmbeddingFunction(torch.autograd.Function):
         return mx.embedding(ids, w, scale=scale, out_dtype=None if out_dtype is None else mx._OUT_OF[out_dtype])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         dy = dy.reshape(-1, dy.shape[-1])
@@ -54,6 +56,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         return loss.reshape(targets.shape if reduction == mx.REDUCE_NONE else ())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         h2, w, y, lse = ctx.saved_tensors
         need_h, need_w = ctx.needs_input_grad[:2]

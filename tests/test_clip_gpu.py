@@ -115,3 +115,16 @@ def test_same_bits_other_stream_and_graph():
     # halving is exact, and so is its effect on every square and sum
     assert torch.equal(n2, n0 * 0.5)
     assert all(((a.double() - b.double()).abs() <= 2.0 ** -7 * a.double().abs()).all() for a, b in zip(o0, outs))
+
+
+def test_tensor_past_2_31_elements():
+    """2.2e9 equal bf16 gradients of 2^-10: fp32 sums of up to 2^24 of their squares (2^-20 each) are exact, which the
+    CTAs' sums are; the additions over the CTAs (8 and 8 levels) and of the one other square round."""
+    torch, mx = _setup()
+    n = 2_200_000_000
+    g = torch.full((n,), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    g[-1] = 4.0
+    want = math.sqrt((n - 1) * 2.0 ** -20 + 16.0)
+    norm = mx.clip_grad_norm([g], want / 2)
+    assert abs(float(norm) - want) <= 12 * 2.0 ** -24 * want
+    assert bool((g[:-1] == 2.0 ** -11).all()) and float(g[-1]) == 2.0

@@ -227,3 +227,33 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(y2, y0.flip(0)) and torch.equal(g2, mx.embedding_grad(ids, dy, 2000))
     assert torch.equal(g2, mx.embedding_grad(ids, dy, 2000)) and mx.device_status() == 0
+
+
+def test_rows_past_2_31_elements():
+    torch, mx, _ = _setup()
+    V, D = 600_000, 4096  # 2.46e9 elements
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(3, D, device="cuda").bfloat16()
+    w[V - 3:] = last
+    ids = torch.tensor([V - 1, 0, V - 3, V - 2], device="cuda")
+    y = mx.embedding(ids, w)
+    assert torch.equal(y, torch.stack([last[2], w[0], last[0], last[1]]))
+    for many in (1, 200):  # few tokens, and enough for the sort
+        dw = mx.embedding_grad(ids.repeat(many), y.repeat(many, 1), V, dw=w, accumulate=True)
+        assert not dw[1:V - 3].any()
+        w[V - 3:] = last
+    full = torch.full((V, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    mx.embedding_grad(ids.repeat(200), y.repeat(200, 1), V, dw=full)
+    assert not full[:V - 3].any() and bool(((full[V - 1].float() - 200 * last[2].float()).abs() <= 2.0 ** -7 * 200 * last[2].float().abs()).all())
+    assert mx.device_status() == 0
+
+
+def test_output_past_2_31_elements():
+    torch, mx, _ = _setup()
+    w = torch.randn(1000, 4096, device="cuda").bfloat16()
+    ids = torch.arange(600_000, device="cuda") % 1000
+    y = mx.embedding(ids, w)
+    assert torch.equal(y[-1000:], w) and torch.equal(y[299_000:300_000], w)
+    # and their gradient: 600 rows of each id, the same every time
+    dw = mx.embedding_grad(ids, y, 1000, out_dtype=mx.OUT_F32)
+    assert bool(((dw - 600 * w.float()).abs() <= 604 * 2.0 ** -24 * 600 * w.float().abs()).all())

@@ -10,6 +10,8 @@ Tolerances, element by element (u = 2^-24):
   dz = p - [target]: p within p * 2 * (el + ez); rounded to bf16, 2^-8 |dz| (half an ulp is at most 2^-8 of the
   value) -- then products added up in fp32 over n terms: 2u * n * sum|dz||x|.
   A bf16 output adds 2^-8 of the result."""
+import math
+
 import pytest
 
 from tests.gpu_util import gpu_ready
@@ -295,4 +297,62 @@ def test_same_bits_other_stream_and_graph():
     loss, lse = mx.linear_ce(h, w, y)
     dh, dw = mx.linear_ce_grad(h, w, y, lse, one)
     assert torch.equal(loss, loss3) and torch.equal(lse, lse3) and torch.equal(dh, dh3) and torch.equal(dw, dw3)
+    assert mx.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [5, 100, 200, 256])
+def test_few_tokens_with_unaligned_rows(T):
+    """Up to 256 tokens the loss reads h where it lies, if its rows are aligned; up to 128 the gradient keeps
+    more of dz.  Rows of an odd pitch must give what aligned ones give."""
+    torch, mx = _setup()
+    h, w, y = _inputs(torch, T, 999, 72, T, 0.4, pitch_h=73)
+    ha = h.contiguous()
+    one = torch.ones(1, device="cuda")
+    ref = _reference(torch, h, w, y)
+    lse = _check_forward(torch, mx, h, w, y, ref)
+    assert torch.equal(lse, mx.linear_ce(ha, w, y)[1])
+    for a, b in zip(mx.linear_ce_grad(h, w, y, lse, one), mx.linear_ce_grad(ha, w, y, lse, one)):
+        assert torch.equal(a, b)
+    _check_grad(torch, mx, h, w, y, lse, ref, mx.REDUCE_NONE, mx.OUT_F32)
+
+
+@pytest.mark.parametrize("T", [1, 3, 128])
+def test_few_tokens_keep_more_of_dz(T):
+    """At most 128 tokens: dz is held to 2^-16, so fp32 gradients are within that of the formula's, far below a
+    bf16 rounding (in the 2-norm; the logits' own error is below 2^-16 here as well)."""
+    torch, mx = _setup()
+    h, w, y = _inputs(torch, T, 3000, 256, T)
+    lse = mx.linear_ce(h, w, y)[1]
+    dh, dw = mx.linear_ce_grad(h, w, y, lse, torch.ones(1, device="cuda"), dh_dtype=mx.OUT_F32, dw_dtype=mx.OUT_F32)
+    hd, wd = h.double(), w.double()
+    dz = torch.softmax(hd @ wd.t(), 1)
+    dz[torch.arange(T, device="cuda"), y] -= 1
+    dz /= T
+    for got, want in ((dh, dz @ wd), (dw, dz.t() @ hd)):
+        assert float((got.double() - want).norm()) <= 2.0 ** -14 * float(want.norm())
+
+
+def test_weights_past_2_31_elements():
+    torch, mx = _setup()
+    T, V, D = 300, 600_000, 4096
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w[-512:] = torch.randn(512, D, device="cuda", generator=g) / 64
+    h = torch.randn(T, D, device="cuda", generator=g).bfloat16()
+    y = torch.randint(V - 512, V, (T,), device="cuda", generator=g)
+    z = h.double() @ w[-512:].double().t()
+    lse = torch.logsumexp(torch.cat([z, torch.full((T, 1), math.log(V - 512), dtype=torch.float64, device="cuda")], 1), 1)
+    want = lse - z.gather(1, y[:, None] - (V - 512))[:, 0]
+    loss, got = mx.linear_ce(h, w, y, reduction=mx.REDUCE_NONE)
+    tol = 2 * U * D * (h.double().abs() @ w[-512:].double().abs().t()).amax(1) + U * (128 + V / 128 + 200)
+    assert bool(((got.double() - lse).abs() <= tol).all()) and bool(((loss.double() - want).abs() <= 2 * tol).all())
+    dh, dw = mx.linear_ce_grad(h, w, y, got, torch.ones(1, device="cuda"), reduction=mx.REDUCE_SUM)
+    dz = torch.exp(z - lse[:, None])
+    dz[torch.arange(T, device="cuda"), y - (V - 512)] -= 1
+    for a, b in ((dh, dz @ w[-512:].double()), (dw[-512:], dz.t() @ h.double())):
+        assert float((a.double() - b).norm()) <= 2.0 ** -7 * float(b.norm())
+    p = torch.exp(-lse)[:, None]  # every other id's probability
+    other = (p * h.double()).sum(0)
+    for v in (0, 12345, V // 2, V - 513):
+        assert float((dw[v].double() - other).norm()) <= 2.0 ** -7 * float(other.norm())
     assert mx.device_status() == 0

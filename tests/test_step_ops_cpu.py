@@ -30,7 +30,7 @@ def _lookup(L, **kw):
     (dict(vocab=-1), INVALID), (dict(dim=-1), INVALID), (dict(ids=None), INVALID), (dict(w=None), INVALID),
     (dict(y=None), INVALID), (dict(ldw=7), INVALID), (dict(ldy=7), INVALID), (dict(vocab=0), SHAPE),
     (dict(n=1 << 31), SHAPE), (dict(vocab=(1 << 31) - 1), SHAPE), (dict(dim=(1 << 20) + 1, ldw=1 << 21, ldy=1 << 21), SHAPE),
-    (dict(ids=0x1004), MISALIGNED), (dict(w=0x2001), MISALIGNED), (dict(y=0x3002, yt=0), MISALIGNED),
+    (dict(n=(1 << 31) - 1, dim=1 << 20, ldw=1 << 20, ldy=1 << 20), SHAPE), (dict(ids=0x1004), MISALIGNED), (dict(w=0x2001), MISALIGNED), (dict(y=0x3002, yt=0), MISALIGNED),
     (dict(n=0), 0), (dict(dim=0, ldw=0, ldy=0), 0)])
 def test_embedding_refuses(L, change, want):
     assert _lookup(L, **change) == want
@@ -108,7 +108,7 @@ def _ce(L, **kw):
 CE_BAD = [(dict(h=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(it=2), INVALID),
           (dict(red=3), INVALID), (dict(red=-1), INVALID), (dict(n=-1), INVALID), (dict(vocab=-1), INVALID),
           (dict(dim=-8), INVALID), (dict(vocab=0), SHAPE), (dict(dim=0), SHAPE), (dict(dim=60), SHAPE),
-          (dict(n=(1 << 24) + 1), SHAPE), (dict(vocab=(1 << 28) + 1), SHAPE), (dict(ldh=63), INVALID),
+          (dict(n=(1 << 24) + 1), SHAPE), (dict(vocab=(1 << 28) + 1), SHAPE), (dict(n=1 << 24, vocab=1 << 28), SHAPE), (dict(ldh=63), INVALID),
           (dict(ldw=56), INVALID), (dict(ldw=68), MISALIGNED), (dict(w=0x2008), MISALIGNED), (dict(h=0x1001), MISALIGNED),
           (dict(y=0x3004), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(wsb=64), WORKSPACE),
           (dict(ws=0x6010), MISALIGNED)]

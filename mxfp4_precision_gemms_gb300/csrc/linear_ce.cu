@@ -102,7 +102,7 @@ struct CeParams {
     int32_t col0;           // first vocabulary index of this launch's columns
     int32_t rows;           // pitch of the statistics: padded token count
     int32_t paired;         // gradient of at most kPaired tokens: see there
-    float2* stats;          // [tile * 2 + half][rows]: (max * log2 e, sum of 2^(z log2 e - max))
+    float2* stats;          // [tile * 2 + half][rows]: (max, sum of exp(z - max))
     float* target_logit;    // [rows]
     const float* lse2;      // [rows] lse * log2 e
     const float* ratio;     // [rows] factor of this token's gradient
@@ -117,15 +117,17 @@ struct CeParams {
 // rounding left of dz: both products then sum dz to 16 bits, at no cost.
 constexpr int32_t kPaired = 128;
 
-enum Kind { kStats = 0, kDlogits = 1, kProducts = 2 };
+enum Kind { kStats = 0, kDlogits = 1, kProducts = 2, kDlogitsFew = 3 };  // kDlogitsFew: paired
 
 // Stages that one accumulator takes.  The tensor cores cut each step's sum off towards zero, and the
 // loss of a long contraction would carry that one-sided error: the logits of dim = 4096 came out
 // smaller by 4.2e-6 of themselves (1.0e-6 at 1024), ten times an fp32 product's error.  So the
 // statistics' logits are summed in runs of K = 512, joined in fp32 by the epilogue, which has the time:
-// a run is 4096 cycles of MMAs and about 500 of read-out.  dz is rounded to bf16 anyway, and the
-// gradients' sums carry that rounding: they are taken in one run.
-constexpr int kStatsRun = 8;
+// a run is 4096 cycles of MMAs and about 500 of read-out.  Runs of 256 halve what error is left (4.5e-7 of a
+// logit) and cost 3 to 6%; they are taken for at most a tile of tokens, where HBM is waited for anyway and
+// few losses average an error out.  dz is rounded to bf16 anyway, and the gradients' sums carry
+// that rounding: they are taken in one run.
+constexpr int kStatsRun = 8, kStatsRunFew = 4;
 
 __host__ __device__ inline int32_t pad_rows(int32_t n) { return n <= 0 ? kTile : (n + kTile - 1) / kTile * kTile; }
 
@@ -273,6 +275,9 @@ struct Boxes {
     }
 };
 
+// Compute-bound for many tokens: 2048 x 65536 x 4096, statistics 0.55 ms, dz 0.56 ms, both products 1.15 ms, with
+// the tensor pipe active in 98.7, 97.3 and 96.0% of the cycles at the 1.70 GHz that the power cap leaves
+// (1.9 to 2.0 PFLOP/s; a cuBLAS product of 8192^3 reached 1.89).
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_constant__ CeParams p) {
     extern __shared__ uint8_t smem[];
@@ -291,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     uint64_t* mma_done = acc_empty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffTmem);
 
-    constexpr int32_t kRun = KIND == kStats ? kStatsRun : 1 << 30;  // stages per accumulator
+    // stages per accumulator, a power of two
+    const int32_t run = KIND != kStats ? 1 << 30 : p.rows <= kTile ? kStatsRunFew : kStatsRun;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int32_t cluster = (int32_t)(blockIdx.x >> 1), num_clusters = (int32_t)(gridDim.x >> 1);
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     const uint32_t a_lbo = q.a_mn ? kOpBytes / 2 : 16, b_lbo = q.b_mn ? kOpBytes / 2 : 16;
                     uint32_t d = 0;
                     for (int32_t i = 0; i < t.stages; ++i) {
-                        const bool first = (i & (kRun - 1)) == 0;
+                        const bool first = (i & (run - 1)) == 0;
                         if (first) {  // a new accumulator
                             const uint32_t ab = tcount & 1u;
                             if (tcount >= 2 &&
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                             s = 0;
                             phase ^= 1u;
                         }
-                        if ((i & (kRun - 1)) == kRun - 1 || i + 1 == t.stages) {
+                        if ((i & (run - 1)) == run - 1 || i + 1 == t.stages) {
                             tc_commit_pair(&acc_full[tcount & 1u], 0x3);
                             ++tcount;
                         }
@@ -460,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             // per-row values first: their latency hides behind the wait for the accumulator
             int32_t tgt = -1;
             float lse2 = 0.f, ratio = 0.f;
-            const bool counts = (p.paired ? row & (kPaired - 1) : row) < count;
-            const bool low_half = p.paired && row >= kPaired;
+            const bool counts = (KIND == kDlogitsFew ? row & (kPaired - 1) : row) < count;
             if constexpr (KIND != kProducts) {
                 if (KIND == kStats && p.direct) {  // one that does not count hits no column, or its value is not used
                     const int64_t y = row < count ? load_id(p.targets, p.is64, row) : -1;
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 } else {
                     tgt = __ldcg(p.target + row) - p.col0;
                 }
-                if constexpr (KIND == kDlogits) {
+                if constexpr (KIND == kDlogits || KIND == kDlogitsFew) {
                     lse2 = __ldcg(p.lse2 + row);
                     ratio = __ldcg(p.ratio + row);
                 }
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
             if constexpr (KIND == kStats) {
                 // The logits are the sums of their runs' accumulators, added up here.
                 uint32_t z[4][32];
-                for (int32_t i = 0; i < t.stages; i += kRun, ++tcount) {
+                for (int32_t i = 0; i < t.stages; i += run, ++tcount) {
                     const uint32_t ab = tcount & 1u;
                     if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) {
                         ok = false;
@@ -529,9 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
 #pragma unroll
                     for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(z[c][j]));
                 }
-                m *= kLog2e;
                 // all -inf: any finite reference leaves the terms 0
-                const float ref = m == -INFINITY ? 0.f : m;
+                const float ref = m == -INFINITY ? 0.f : m * kLog2e;
                 float s4[4] = {};
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -539,6 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     for (int j = 0; j < 32; ++j)
                         s4[j & 3] += exp2_approx(fmaf(__uint_as_float(z[c][j]), kLog2e, -ref));
                 sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                // The terms are 2^(z log2 e - ref).  What rounding took from ref = m log2 e is put back, so that
+                // the sum is that of exp(z - m): a confident token's loss is little more than its logarithm.
+                if (m != -INFINITY) sum = fmaf(sum, -kLn2 * fmaf(m, kLog2e, -ref), sum);
                 if (row < count)
                     p.stats[(int64_t)((t.n0 / q.tile_n) * 2 + half) * p.rows + row] = make_float2(m, sum);
             } else {
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     }
                     const int32_t col = c0 + c * 32;
                     if (half * 128 + c * 32 >= q.tile_n) continue;  // past a narrow tile's columns
-                    if constexpr (KIND == kDlogits) {
+                    if constexpr (KIND == kDlogits || KIND == kDlogitsFew) {
                         const int32_t hit = tgt - col;
                         uint32_t w[16];
 #pragma unroll
@@ -569,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                                 const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
                                 x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
                             }
-                            w[j] = pack_bf16(x[0], x[1]);
-                            if (low_half) w[j] = pack_bf16(x[0] - bf16_lo(w[j]), x[1] - bf16_hi(w[j]));
-                            if (!counts) w[j] = 0u;
+                            w[j] = counts ? pack_bf16(x[0], x[1]) : 0u;
+                            if (KIND == kDlogitsFew && row >= kPaired && counts)
+                                w[j] = pack_bf16(x[0] - bf16_lo(w[j]), x[1] - bf16_hi(w[j]));
                         }
                         boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
                     } else {
@@ -651,7 +658,7 @@ __device__ __forceinline__ int32_t counted_target(const GatherParams& p, int32_t
 
 // Each CTA gathers a contiguous range of tokens.  Where its rows go follows from the number of
 // counted tokens in front of them, which it counts by itself: the targets are short beside
-// the rows, and no CTA waits for another.
+// the rows, and no CTA waits for another.  8 to 10 us at 1531 tokens, latency.
 template <bool GRAD>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
     __shared__ int32_t warp_n[2][kGatherWarps];
@@ -783,7 +790,8 @@ struct CombineParams {
     uint32_t* status;
 };
 
-// kCombineRows rows per CTA, a group of threads to each: the walk over the tiles is a chain of loads.
+// kCombineRows rows per CTA, a group of threads to each: the walk over the tiles is a chain of loads
+// (8 rows x 286 statistics 8 us under ncu, most of it the launch and two trips to L2).
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
     __shared__ float2 sh[kCombineThreads / 32][kCombineRows];
     grid_dependency_wait();
@@ -797,7 +805,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
     auto join = [&](float2 o) {
         const float top = fmaxf(m, o.x);
         const float ref = top == -INFINITY ? 0.f : top;
-        s = s * exp2_approx(m - ref) + o.y * exp2_approx(o.x - ref);
+        s = s * exp2_approx((m - ref) * kLog2e) + o.y * exp2_approx((o.x - ref) * kLog2e);
         m = top;
     };
     if (row < count) {
@@ -823,7 +831,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
     m = sh[0][r].x, s = sh[0][r].y;
 #pragma unroll
     for (int k = 1; k < kCombineThreads / 32; ++k) join(sh[k][r]);
-    float lse = (m + log2f(s)) * kLn2, loss = 0.f;
+    const float ln_s = logf(s);
+    float lse = m + ln_s, loss = 0.f;
     int32_t t = row;
     bool counts = true;
     if (p.direct) {
@@ -834,7 +843,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
         t = p.source[row];
     }
     if (counts)
-        loss = lse - p.target_logit[row];
+        loss = (m - p.target_logit[row]) + ln_s;  // exact difference where the target is the largest
     else
         lse = 0.f;
     p.lse[t] = lse;
@@ -933,10 +942,10 @@ int32_t piece_columns(int32_t padded, int64_t vocab) {
 
 // Parts that dh's contraction over a piece's columns is cut into, so that its few long tiles fill the
 // device beside dw's many short ones.  A schedule takes the parts' own rounds, or all tiles' stages
-// shared out; a part costs two stages of hand-off and four for the passes over its fp32 output.  How
+// shared out; a part costs two stages of hand-off and twelve for the passes over its fp32 output.  How
 // many tokens count is known on the device alone, so the number is taken whose schedule is best
-// over all of them, half and a quarter, each measured against one that is shared out evenly.  Lowered
-// to the parts that get work; every piece uses at most as many.
+// where all of them do (twice) and half of them (once), each against one that is shared out evenly.
+// Lowered to the parts that get work; every piece uses at most as many.
 int32_t split_count(int32_t padded, int64_t dim, int32_t columns) {
     const int64_t n_tiles = (dim + kTile - 1) / kTile;
     const int64_t w_tiles = (columns + kTile - 1) / kTile * n_tiles;
@@ -946,13 +955,13 @@ int32_t split_count(int32_t padded, int64_t dim, int32_t columns) {
     for (int32_t s = 1; s <= 16 && s <= stages; ++s) {
         const int64_t per = (stages + s - 1) / s;
         double cost = 0;
-        for (int32_t share = 1; share <= 4; share *= 2) {
+        for (int32_t share = 1; share <= 2; ++share) {
             const int32_t rows = pad_rows(padded / share);
             const int64_t tiles = rows / kTile * n_tiles, others = w_tiles * (std::max(rows / kK, 6) + 2);
             const int64_t rounds = (tiles * s + kClustersMost - 1) / kClustersMost * (per + 2);
-            const int64_t shared = (tiles * s * (per + 6) + others) / kClustersMost;
-            const int64_t even = (tiles * (stages + 6) + others) / kClustersMost + 1;
-            cost += (double)std::max(rounds, shared) / (double)even;
+            const int64_t shared = (tiles * s * (per + 14) + others) / kClustersMost;
+            const int64_t even = (tiles * (stages + 14) + others) / kClustersMost + 1;
+            cost += (double)std::max(rounds, shared) / (double)even / share;
         }
         if (cost < best_cost) best = s, best_cost = cost;
     }
@@ -1314,7 +1323,8 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
                 !encode_out_map(&q.map_c, dz, l.padded, cols, l.piece, true))
                 return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
             p.count = 1;
-            e = launch_matrix<kDlogits>(p, tiles_of(l.padded, cols, q.tile_n), s);
+            e = p.paired ? launch_matrix<kDlogitsFew>(p, tiles_of(l.padded, cols, q.tile_n), s)
+                         : launch_matrix<kDlogits>(p, tiles_of(l.padded, cols, q.tile_n), s);
             if (e != cudaSuccess) return launch_failed(what, "dlogits", e);
         }
         int n = 0;

@@ -16,6 +16,14 @@ from . import binding as mx
 _REDUCTIONS = {"none": mx.REDUCE_NONE, "sum": mx.REDUCE_SUM, "mean": mx.REDUCE_MEAN}
 
 
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x [..., dim] as a matrix whose rows do not overlap (a broadcast gradient's do) and are contiguous."""
+    x = x.reshape(-1, x.shape[-1])
+    if (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+        x = x.contiguous()
+    return x
+
+
 class EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, w, scale, padding_id, out_dtype):
@@ -28,10 +36,7 @@ class EmbeddingFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
-        dy = dy.reshape(-1, dy.shape[-1])
-        if dy.shape[1] > 1 and dy.stride(1) != 1:
-            dy = dy.contiguous()
-        dw = mx.embedding_grad(ids.reshape(-1), dy, ctx.vocab, scale=ctx.scale, padding_id=ctx.padding_id,
+        dw = mx.embedding_grad(ids.reshape(-1), _rows(dy), ctx.vocab, scale=ctx.scale, padding_id=ctx.padding_id,
                                out_dtype=mx._OUT_OF[ctx.w_dtype])
         return None, dw, None, None, None
 
@@ -46,9 +51,9 @@ def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, padding_id
 class LinearCrossEntropyFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, w, targets, ignore_index, reduction):
-        h2 = h.reshape(-1, h.shape[-1])
-        if h2.shape[1] > 1 and h2.stride(1) != 1:
-            h2 = h2.contiguous()
+        h2, w = _rows(h), _rows(w)
+        if w.data_ptr() % 16 or (w.shape[0] > 1 and w.stride(0) % 8):
+            w = w.contiguous()  # what the library asks of its rows
         y = targets.reshape(-1).contiguous()
         loss, lse = mx.linear_ce(h2, w, y, ignore_index=ignore_index, reduction=reduction)
         ctx.save_for_backward(h2, w, y, lse)

@@ -70,6 +70,69 @@ def test_only_the_gradients_that_are_asked_for():
         linear_cross_entropy(h, w, y, reduction="median")
 
 
+def test_broadcast_and_strided_inputs():
+    """Gradients that arrive broadcast (rows or all elements shared), hidden states that are one row repeated, and
+    weights that are columns of a wider matrix give what contiguous ones give."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import embedding, linear_cross_entropy
+
+    w = torch.randn(50, 24, device="cuda").requires_grad_()
+    ids = torch.randint(0, 50, (4, 9), device="cuda")
+    v = torch.randn(24, device="cuda")
+    for out in (embedding(ids, w), embedding(ids, w) @ torch.diag(v)):
+        w.grad = None
+        out.sum().backward()
+        want = torch.zeros(50, 24, device="cuda").index_add_(0, ids.reshape(-1), (v if out.grad_fn.name() != "EmbeddingFunctionBackward" else torch.ones_like(v)).expand(36, 24))
+        assert torch.allclose(w.grad, want, rtol=1e-6, atol=1e-6)
+    w.grad = None
+    embedding(ids, w).backward(v.expand(4, 9, 24))  # one row for all tokens
+    assert torch.allclose(w.grad, torch.zeros(50, 24, device="cuda").index_add_(0, ids.reshape(-1), v.expand(36, 24)), rtol=1e-5)
+
+    h = torch.randn(1, 64, device="cuda").bfloat16().requires_grad_()
+    wide = torch.randn(300, 99, device="cuda").bfloat16()
+    wo = wide[:, 3:67].detach().requires_grad_()
+    y = torch.randint(0, 300, (40,), device="cuda")
+    linear_cross_entropy(h.expand(40, 64), wo, y, reduction="sum").backward()
+    hc, wc = h.detach().repeat(40, 1).requires_grad_(), wo.detach().contiguous().requires_grad_()
+    linear_cross_entropy(hc, wc, y, reduction="sum").backward()
+    assert torch.equal(wo.grad, wc.grad)
+    assert float((h.grad.float() - hc.grad.float().sum(0)).abs().max()) <= 2.0 ** -7 * float(hc.grad.float().abs().sum(0).max())
+
+
+def test_concurrent_streams():
+    """Calls on three streams at once: each has its own workspace, so each gives what it gives alone."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    g = torch.Generator(device="cuda").manual_seed(5)
+    sets = []
+    for i in range(3):
+        T, V, D = (700, 3000, 256) if i else (2500, 9000, 64)
+        sets.append((torch.randn(T, D, device="cuda", generator=g).bfloat16(),
+                     (torch.randn(V, D, device="cuda", generator=g) / 8).bfloat16(),
+                     torch.randint(0, V, (T,), device="cuda", generator=g)))
+    one = torch.ones(1, device="cuda")
+
+    def work(h, w, y, stream=None):
+        loss, lse = mx.linear_ce(h, w, y, stream=stream)
+        dh, dw = mx.linear_ce_grad(h, w, y, lse, one, stream=stream)
+        de = mx.embedding_grad(y, h, w.shape[0], stream=stream)
+        e = mx.embedding(y, w, stream=stream)
+        norm = mx.clip_grad_norm([dw, dh], 1e-3, stream=stream)
+        return loss, lse, dh, dw, de, e, norm
+
+    alone = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        both = [work(*s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            for x, z in zip(a, b):
+                assert torch.equal(x, z)
+    assert mx.device_status() == 0
+
+
 def test_clip_grad_norm_on_parameters():
     torch = gpu_ready()
     from mxfp4_precision_gemms_gb300.step import clip_grad_norm_

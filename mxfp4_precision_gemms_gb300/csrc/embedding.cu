@@ -693,7 +693,7 @@ bool valid_float(int t) { return t == MXFP4_OUT_F32 || t == MXFP4_OUT_BF16; }
 int64_t esize(int t) { return t == MXFP4_OUT_BF16 ? 2 : 4; }
 bool element_aligned(const void* p, int t) { return reinterpret_cast<uintptr_t>(p) % esize(t) == 0; }
 
-constexpr int64_t kMaxDim = int64_t(1) << 20;  // the slabs of the sum and join grids fit in gridDim.y
+constexpr int64_t kMaxDim = int64_t(1) << 20;  // the slabs of a few tokens fit in gridDim.y
 
 int sort_passes(int64_t vocab) {
     int bits = 1;

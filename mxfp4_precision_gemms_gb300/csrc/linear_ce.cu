@@ -111,8 +111,8 @@ struct CeParams {
 };
 
 // dz is rounded to bf16 for the tensor cores, which costs a gradient as much as its own rounding
-// does; over many tokens the errors of their dz average out, over a few they need not (dz - p is
-// near -1 at the target and its error then goes into the whole row of dh).  At most kPaired tokens fill half
+// does; over many tokens the errors of their dz average out, over a few they need not (dz is largest at
+// the target, and its error there goes into the whole row of dh).  At most kPaired tokens fill half
 // of a tile's rows, so the other half, idle otherwise, holds their rows again with what the
 // rounding left of dz: both products then sum dz to 16 bits, at no cost.
 constexpr int32_t kPaired = 128;
@@ -149,8 +149,8 @@ constexpr int kClustersMost = 76;  // pairs of SMs
 
 // A tile's columns of the vocabulary where the tiles fill the device few times over: the width whose
 // schedule is shortest.  A stage costs two cycles a column, or its bytes at 72 a cycle (what L2
-// gives an SM), and a tile some 600 cycles more.  (64 tokens, 65536 x 4096: 256 tiles of 256 columns are
-// four rounds of 76, 293 of 224 too: 115 -> 101 us.)
+// gives an SM), and a tile some 600 cycles more.  (64 tokens, 65536 x 2048: 256 tiles of 256 columns are
+// four rounds of 76, and so are 293 of 224: 65 -> 61 us.)
 inline int32_t vocab_tile(int64_t num_m, int64_t n, int64_t k) {
     if (num_m * ((n + kTile - 1) / kTile) >= 8 * kClustersMost) return kTile;
     int32_t best = kTile;

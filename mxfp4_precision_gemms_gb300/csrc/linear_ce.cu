@@ -83,6 +83,7 @@ struct Product {
     int32_t k_counted;      // K is the number of counted tokens
     int32_t M, N, K;
     int32_t tile_n;         // columns of a tile: kTile, or less where that divides better (a multiple of 32)
+    int32_t num_n;          // tiles along N
     uint32_t tx;            // bytes of a stage, both CTAs
     int32_t splits;         // K is cut into this many parts, each with its own output
     int32_t k_per_split;    // stages of a part
@@ -133,7 +134,7 @@ __host__ __device__ inline int32_t pad_rows(int32_t n) { return n <= 0 ? kTile :
 
 struct Tile {
     int prob;
-    int32_t m0, n0, k0, stages, slot;
+    int32_t m0, n0, n_tile, k0, stages, slot;
 };
 
 // A tile's columns for N columns in all: as few tiles as 256-column ones, cut evenly.  The MMA's time
@@ -164,35 +165,34 @@ inline int32_t vocab_tile(int64_t num_m, int64_t n, int64_t k) {
     return best;
 }
 
+__device__ __forceinline__ int32_t tiles_m(const Product& q, int32_t count) {
+    return (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
+}
+
 // Tile `lt` of product `i`.  Consecutive tiles (which run at the same time) walk the dimension with
 // fewer tiles first: the operand along it is read in every wave and stays in L2 while the other
 // one streams through once.
 __device__ __forceinline__ void locate(const CeParams& p, int32_t count, int i, int32_t lt, Tile& out) {
     const Product& q = p.prod[i];
-    const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
-    const int32_t num_n = (q.N + q.tile_n - 1) / q.tile_n;
+    const int32_t num_m = tiles_m(q, count), num_n = q.num_n;
     out.prob = i;
     out.slot = 0;
     if (q.splits > 1) {
         out.slot = lt / (num_m * num_n);
         lt -= out.slot * (num_m * num_n);
     }
-    if (num_n > num_m) {
-        out.m0 = (lt % num_m) * kTile;
-        out.n0 = (lt / num_m) * q.tile_n;
-    } else {
-        out.m0 = (lt / num_n) * kTile;
-        out.n0 = (lt % num_n) * q.tile_n;
-    }
+    // one division: it stands before a cluster's first load
+    const int32_t inner = min(num_m, num_n), major = inner > 1 ? lt / inner : lt, minor = lt - major * inner;
+    out.m0 = (num_n > num_m ? minor : major) * kTile;
+    out.n_tile = num_n > num_m ? major : minor;
+    out.n0 = out.n_tile * q.tile_n;
     const int32_t k = q.k_counted ? max(count, 1) : q.K;
     const int32_t all = (k + kK - 1) / kK;
     out.k0 = out.slot * q.k_per_split;
     out.stages = q.splits > 1 ? min(q.k_per_split, all - out.k0) : all;
 }
 __device__ __forceinline__ int32_t tiles_in(const CeParams& p, int32_t count, int i) {
-    const Product& q = p.prod[i];
-    const int32_t num_m = (q.m_counted ? pad_rows(count) : q.M + kTile - 1) / kTile;
-    return num_m * ((q.N + q.tile_n - 1) / q.tile_n) * q.splits;
+    return tiles_m(p.prod[i], count) * p.prod[i].num_n * p.prod[i].splits;
 }
 
 // The tiles of one cluster, in order; every role of both CTAs walks the same ones.  One product:
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 // the sum is that of exp(z - m): a confident token's loss is little more than its logarithm.
                 if (m != -INFINITY) sum = fmaf(sum, -kLn2 * fmaf(m, kLog2e, -ref), sum);
                 if (row < count)
-                    p.stats[(int64_t)((t.n0 / q.tile_n) * 2 + half) * p.rows + row] = make_float2(m, sum);
+                    p.stats[(int64_t)(t.n_tile * 2 + half) * p.rows + row] = make_float2(m, sum);
             } else {
                 const uint32_t ab = tcount & 1u;
                 if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) break;
@@ -1149,6 +1149,7 @@ extern "C" mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t d
     q.M = l.padded;
     q.N = (int32_t)vocab;
     q.tile_n = l.tile_n;
+    q.num_n = (q.N + q.tile_n - 1) / q.tile_n;
     q.tx = stage_bytes(l.tile_n);
     q.K = (int32_t)dim;
     q.splits = 1;
@@ -1314,6 +1315,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.M = l.padded;
             q.N = cols;
             q.tile_n = vocab_tile(l.padded / kTile, cols, dim);
+            q.num_n = (q.N + q.tile_n - 1) / q.tile_n;
             q.tx = stage_bytes(q.tile_n);
             q.K = (int32_t)dim;
             q.splits = 1;
@@ -1337,6 +1339,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.M = l.padded;
             q.N = (int32_t)dim;
             q.tile_n = even_tile(dim);
+            q.num_n = (q.N + q.tile_n - 1) / q.tile_n;
             q.tx = stage_bytes(kTile);
             q.K = cols;
             const int32_t stages = (cols + kK - 1) / kK;
@@ -1358,6 +1361,7 @@ extern "C" mxfp4_status mxfp4_linear_ce_grad(const void* h, int64_t tokens, int6
             q.M = cols;
             q.N = (int32_t)dim;
             q.tile_n = even_tile(dim);
+            q.num_n = (q.N + q.tile_n - 1) / q.tile_n;
             q.tx = stage_bytes(kTile);
             q.K = l.padded;
             q.splits = 1;

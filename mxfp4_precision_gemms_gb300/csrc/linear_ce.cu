@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     const int64_t y = row < count ? load_id(p.targets, p.is64, row) : -1;
                     tgt = y >= 0 && y < q.N ? (int32_t)y : -1;
                 } else {
-                    tgt = __ldcg(p.target + row) - p.col0;
+                    tgt = __ldcg(p.target + row);
+                    if constexpr (KIND != kStats) tgt -= p.col0;
                 }
                 if constexpr (KIND == kDlogits || KIND == kDlogitsFew) {
                     lse2 = __ldcg(p.lse2 + row);
@@ -512,6 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
                 }
                 if (!ok) break;
+                asm volatile("" : "+r"(tgt));  // its load is not waited for earlier (8192 x 65536 x 256: 229 -> 213 us)
+                if (!p.direct) tgt -= p.col0;
                 float m = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {

@@ -492,8 +492,8 @@ size_t mxfp4_clip_grad_norm_workspace_bytes(int n);
  * are clipped in place are left as they are.  A NaN or infinite norm makes c NaN or 0 and
  * goes into every output, as the formula says.  The squares are summed in fp32, in an order
  * fixed by the sizes (a norm above 1.8e19 overflows to infinity).  Any alignment of the element
- * type; n >= 0.  grads is read on the host during the call.  out must be grad or not
- * overlap any gradient.  ws: device, 256-byte aligned. */
+ * type; n >= 0.  grads is read on the host during the call.  No two gradients
+ * overlap; out must be grad or not overlap any gradient.  ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,
                                   size_t ws_bytes, mxfp4_stream_t stream);
 

@@ -706,8 +706,8 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse:
 
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
-    """mxfp4_clip_grad_norm over a sequence of contiguous CUDA fp32 / bf16 tensors: clips them in
-    place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
+    """mxfp4_clip_grad_norm over a sequence of contiguous CUDA fp32 / bf16 tensors that do not
+    overlap: clips them in place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
     norm before clipping as a 1-element fp32 CUDA tensor."""
     outs = grads if outs is None else outs
     n = len(grads)

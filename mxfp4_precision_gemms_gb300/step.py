@@ -85,11 +85,11 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
 @torch.no_grad()
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     """Clips the gradients of `parameters` (one tensor or an iterable; those without a gradient are
-    passed over) to a global 2-norm of max_norm, in place.  Returns the norm before clipping, a
+    passed over, and one that occurs twice, as a tied weight may, counts once) to a global 2-norm of max_norm, in place.  Returns the norm before clipping, a
     1-element fp32 CUDA tensor; nothing is synchronised.  Gradients are fp32 or bf16."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    grads = [p.grad for p in parameters if p.grad is not None]
+    grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]
     # a gradient with other strides (of a transposed parameter) goes through a contiguous copy
     flat = [g if g.is_contiguous() else g.contiguous() for g in grads]
     norm = mx.clip_grad_norm(flat, max_norm)

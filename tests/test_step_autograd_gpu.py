@@ -152,6 +152,22 @@ def test_clip_grad_norm_on_parameters():
     assert float(clip_grad_norm_(ps[0], 1e9)) > 0
 
 
+def test_clip_grad_norm_counts_a_tied_parameter_once():
+    """A weight that is listed twice is scaled once, by the factor of the norm that has it once."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import clip_grad_norm_
+
+    ps = [torch.zeros(1000, 33, device="cuda", requires_grad=True), torch.zeros(10, device="cuda", requires_grad=True)]
+    for p in ps:
+        p.grad = torch.randn(p.shape, device="cuda")
+    before = [p.grad.double().clone() for p in ps]
+    n = math.sqrt(sum(float((b ** 2).sum()) for b in before))
+    norm = clip_grad_norm_([ps[0], ps[1], ps[0]], 2.0)
+    assert abs(float(norm) - n) < 1e-5 * n
+    for p, b in zip(ps, before):
+        assert bool(((p.grad.double() - b * 2.0 / n).abs() <= 1e-5 * (b * 2.0 / n).abs()).all())
+
+
 def test_example_trains():
     """The example's model learns its chain: from about log(vocab) well towards log(4)."""
     gpu_ready()

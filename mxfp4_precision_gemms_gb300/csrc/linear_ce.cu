@@ -115,7 +115,8 @@ struct CeParams {
 // does; over many tokens the errors of their dz average out, over a few they need not (dz is largest at
 // the target, and its error there goes into the whole row of dh).  At most kPaired tokens fill half
 // of a tile's rows, so the other half, idle otherwise, holds their rows again with what the
-// rounding left of dz: both products then sum dz to 16 bits, at no cost.
+// rounding left of dz: both products then sum dz to 16 bits, at no cost.  (dz itself is as exact as lse in
+// fp32 lets p = exp(z - lse) be: 2^-23 |lse| of p, which a confident token's p - 1 feels.)
 constexpr int32_t kPaired = 128;
 
 enum Kind { kStats = 0, kDlogits = 1, kProducts = 2, kDlogitsFew = 3 };  // kDlogitsFew: paired
@@ -123,12 +124,14 @@ enum Kind { kStats = 0, kDlogits = 1, kProducts = 2, kDlogitsFew = 3 };  // kDlo
 // Stages that one accumulator takes.  The tensor cores cut each step's sum off towards zero, and the
 // loss of a long contraction would carry that one-sided error: the logits of dim = 4096 came out
 // smaller by 4.2e-6 of themselves (1.0e-6 at 1024), ten times an fp32 product's error.  So the
-// statistics' logits are summed in runs of K = 512, joined in fp32 by the epilogue, which has the time:
+// logits are summed in runs of K = 512, joined in fp32 by the epilogue, which has the time:
 // a run is 4096 cycles of MMAs and about 500 of read-out.  Runs of 256 halve what error is left (4.5e-7 of a
 // logit) and cost 3 to 6%; they are taken for at most a tile of tokens, where HBM is waited for anyway and
-// few losses average an error out.  dz is rounded to bf16 anyway, and the gradients' sums carry
-// that rounding: they are taken in one run.
-constexpr int kStatsRun = 8, kStatsRunFew = 4;
+// few losses average an error out.  The gradients make the logits again in the same runs, so that z - lse
+// has only lse's rounding: in one run z would be short of the lse that it is subtracted from, and
+// p - 1 at the target of a confident token (logit 30) off by 1.3e-4 whatever it is.  The two gradient
+// products have no such difference to keep, and are taken in one run.
+constexpr int kLogitsRun = 8, kLogitsRunFew = 4;
 
 __host__ __device__ inline int32_t pad_rows(int32_t n) { return n <= 0 ? kTile : (n + kTile - 1) / kTile * kTile; }
 
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffTmem);
 
     // stages per accumulator, a power of two
-    const int32_t run = KIND != kStats ? 1 << 30 : p.rows <= kTile ? kStatsRunFew : kStatsRun;
+    const int32_t run = KIND == kProducts ? 1 << 30 : p.rows <= kTile ? kLogitsRunFew : kLogitsRun;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int32_t cluster = (int32_t)(blockIdx.x >> 1), num_clusters = (int32_t)(gridDim.x >> 1);
@@ -481,9 +484,32 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                 }
             }
             const uint32_t src = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
-            if constexpr (KIND == kStats) {
+            // dz of the 32 columns of chunk c from their logits
+            auto store_dz = [&](int c, const uint32_t (&z)[32]) {
+                const int32_t col = c0 + c * 32, hit = tgt - col;
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float pr = exp2_approx(fmaf(__uint_as_float(z[2 * j + e]), kLog2e, -lse2));
+                        x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
+                    }
+                    w[j] = counts ? pack_bf16(x[0], x[1]) : 0u;
+                    if (KIND == kDlogitsFew && row >= kPaired && counts)
+                        w[j] = pack_bf16(x[0] - bf16_lo(w[j]), x[1] - bf16_hi(w[j]));
+                }
+                boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
+            };
+            const bool runs = KIND == kStats || (KIND != kProducts && t.stages > run);
+            if (runs) {
                 // The logits are the sums of their runs' accumulators, added up here.
                 uint32_t z[4][32];
+                if constexpr (KIND != kStats) {  // added to from the first run on: reading that apart spilled
+#pragma unroll
+                    for (int j = 0; j < 128; ++j) z[j / 32][j % 32] = 0u;
+                }
                 for (int32_t i = 0; i < t.stages; i += run, ++tcount) {
                     const uint32_t ab = tcount & 1u;
                     if (!wait_bounded(&acc_full[ab], (tcount >> 1) & 1u, p.wait_ns, p.status)) {
@@ -491,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                         break;
                     }
                     tc_fence_after();
-                    if (i == 0) {
+                    if (KIND == kStats && i == 0) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(src + ab * 256 + c * 32, z[c]);
                         tmem_ld_wait();
@@ -513,6 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + ab * 8u);
                 }
                 if (!ok) break;
+                if constexpr (KIND != kStats) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (half * 128 + c * 32 >= q.tile_n) break;  // past a narrow tile's columns
+                        store_dz(c, z[c]);
+                    }
+                    continue;
+                }
                 asm volatile("" : "+r"(tgt));  // its load is not waited for earlier (8192 x 65536 x 256: 229 -> 213 us)
                 if (!p.direct) tgt -= p.col0;
                 float m = -INFINITY, sum = 0.f;
@@ -569,21 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_matrix_kernel(const __grid_con
                     const int32_t col = c0 + c * 32;
                     if (half * 128 + c * 32 >= q.tile_n) continue;  // past a narrow tile's columns
                     if constexpr (KIND == kDlogits || KIND == kDlogitsFew) {
-                        const int32_t hit = tgt - col;
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float x[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float pr = exp2_approx(fmaf(__uint_as_float(v[2 * j + e]), kLog2e, -lse2));
-                                x[e] = (2 * j + e == hit ? pr - 1.f : pr) * ratio;
-                            }
-                            w[j] = counts ? pack_bf16(x[0], x[1]) : 0u;
-                            if (KIND == kDlogitsFew && row >= kPaired && counts)
-                                w[j] = pack_bf16(x[0] - bf16_lo(w[j]), x[1] - bf16_hi(w[j]));
-                        }
-                        boxes.store(&q.map_c, lane, w, col, row0, col < q.N, false);
+                        store_dz(c, v);
                     } else {
                         const int32_t y = t.slot * q.slot_rows + row0;
                         const bool in_m = q.m_counted || row0 < q.M;

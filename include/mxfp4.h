@@ -490,9 +490,10 @@ size_t mxfp4_clip_grad_norm_workspace_bytes(int n);
  * c = min(1, max_norm / (norm + 1e-6)), out = c * grad (fp32 arithmetic, rounded once).
  * *norm (device fp32) receives the norm before clipping.  Where c == 1, gradients that
  * are clipped in place are left as they are.  A NaN or infinite norm makes c NaN or 0 and
- * goes into every output, as the formula says.  The squares are summed in fp32, in an order
- * fixed by the sizes (a norm above 1.8e19 overflows to infinity).  Any alignment of the element
- * type; n >= 0.  grads is read on the host during the call.  No two gradients
+ * goes into every output, as the formula says.  The squares are summed in fp32: a norm above
+ * 1.8e19 overflows to infinity, elements below 1e-19 lose bits of their squares and those below
+ * 3e-23 count as 0.  The order of the sum is fixed by the gradients' sizes, types and 16-byte
+ * alignment and the device's number of SMs.  Any alignment of the element type; n >= 0.  grads is read on the host during the call.  No two gradients
  * overlap; out must be grad or not overlap any gradient.  ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,
                                   size_t ws_bytes, mxfp4_stream_t stream);

@@ -67,14 +67,15 @@ __device__ __forceinline__ int find_tensor(const ClipTable<N>& t, uint32_t chunk
 }
 
 
-// Chunk `chunk` of a launch: its tensor and the bytes of it.
+// Chunk `chunk` of a launch: its tensor and the bytes of it.  The sums look at the gradient's alignment alone:
+// where its clipped values go must not change the order of a sum, and so the norm.
 struct Chunk {
     const uint8_t* in;
     uint8_t* out;
     int32_t bytes;
     bool is_bf16, vec;  // vec: 16-byte aligned
 };
-template <int N>
+template <bool WRITES, int N>
 __device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, uint32_t chunk) {
     const int i = find_tensor(t, chunk);
     Chunk c;
@@ -83,7 +84,7 @@ __device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, uint32_t chunk)
     c.in = static_cast<const uint8_t*>(t.in[i]) + at;
     c.out = static_cast<uint8_t*>(t.out[i]) + at;
     c.bytes = (int32_t)min(int64_t(1) << t.chunk_log2, t.numel[i] * (c.is_bf16 ? 2 : 4) - at);
-    c.vec = ((reinterpret_cast<uintptr_t>(c.in) | reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
+    c.vec = ((reinterpret_cast<uintptr_t>(c.in) | (WRITES ? reinterpret_cast<uintptr_t>(c.out) : 0)) & 15u) == 0;
     return c;
 }
 
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     allow_dependent_launch();
     float sum = 0.f;
     const uint32_t chunks = t.first[t.n];
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) sum += chunk_squares(chunk_at(t, c));
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) sum += chunk_squares(chunk_at<false>(t, c));
     sum = cta_sum(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     Chunk c;
     uint4 r[kBatch];
     if (ch >= 0) {
-        c = chunk_at(t, (uint32_t)ch);
+        c = chunk_at<true>(t, (uint32_t)ch);
         if (!t.in_place) load_units(c, r);
     }
     // The norm from the partial sums, the same in every CTA.
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
         if (x != 1.f || c.in != c.out) chunk_scale(c, r, x);
         ch -= gridDim.x;
         if (ch < 0) return;
-        c = chunk_at(t, (uint32_t)ch);
+        c = chunk_at<true>(t, (uint32_t)ch);
         load_units(c, r);
     }
 }

@@ -552,12 +552,21 @@ def linear_backward(dy: torch.Tensor, wT: QTensor, xT: QTensor, cfg: Config, dx:
 # ----------------------------------------------------------------- the ends of a training step
 # These calls may be short, so what a call costs on the host is kept low: a tensor's shape and
 # strides are asked for once, and the current stream is read without an object around it.
+# A kernel runs on the current device, so every tensor of a call has to be there.
 _FLOAT_OF = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16}
 _OUT_OF = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 _IDS_OF = {torch.int32: IDS_I32, torch.int64: IDS_I64}
 _data_ptr, _numel, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
-_dtype_of, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_dtype_of, _device_index = operator.attrgetter("dtype"), torch.Tensor.get_device  # -1: on the host
 _torch_empty = torch.empty
+
+
+def _current_device() -> int:
+    return _raw_device() if _raw_device is not None else torch.cuda.current_device()
+
+
+def _here(x: torch.Tensor) -> bool:
+    return x.is_cuda and x.get_device() == _current_device()
 
 
 def _empty(shape, dtype, device, stream):
@@ -570,21 +579,21 @@ def _empty(shape, dtype, device, stream):
 
 
 def _matrix(x: torch.Tensor, name: str) -> tuple[int, int, int, int]:
-    """Checks a CUDA fp32 / bf16 matrix with unit column stride; returns (rows, columns, leading
-    dimension, dtype)."""
+    """Checks an fp32 / bf16 matrix with unit column stride on the current device; returns (rows,
+    columns, leading dimension, dtype)."""
     kind = _OUT_OF.get(x.dtype)
-    if kind is not None and x.is_cuda and x.dim() == 2:
+    if kind is not None and _here(x) and x.dim() == 2:
         rows, cols = x.shape
         ld, inner = x.stride()
         if inner == 1 or cols <= 1:
             return rows, cols, (ld if rows > 1 else cols), kind  # of a single row the stride has no meaning
-    raise ValueError(f"{name} must be a CUDA fp32 or bf16 matrix with unit column stride")
+    raise ValueError(f"{name} must be an fp32 or bf16 matrix with unit column stride on the current CUDA device")
 
 
 def _token_ids(ids: torch.Tensor, name: str) -> int:
     kind = _IDS_OF.get(ids.dtype)
-    if kind is None or not ids.is_cuda or not ids.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA int32 or int64 tensor")
+    if kind is None or not _here(ids) or not ids.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 or int64 tensor on the current CUDA device")
     return kind
 
 
@@ -679,8 +688,8 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse:
     leaves that gradient out (None is returned for it); accumulate adds to dw (fp32, given)."""
     n, dim, ldh, vocab, ldw, ids_kind = _ce_operands(h, w, targets)
     for x, size, name in ((lse, n, "lse"), (dloss, n if reduction == REDUCE_NONE else 1, "dloss")):
-        if x.dtype is not torch.float32 or not x.is_cuda or not x.is_contiguous() or x.numel() != size:
-            raise ValueError(f"{name} must be {size} contiguous fp32 CUDA elements")
+        if x.dtype is not torch.float32 or not _here(x) or not x.is_contiguous() or x.numel() != size:
+            raise ValueError(f"{name} must be {size} contiguous fp32 elements on the current CUDA device")
     device = h.device
     dh_at = dw_at = None
     lddh = lddw = dim
@@ -706,8 +715,8 @@ def linear_ce_grad(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse:
 
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tensor:
-    """mxfp4_clip_grad_norm over a sequence of contiguous CUDA fp32 / bf16 tensors that do not
-    overlap: clips them in place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
+    """mxfp4_clip_grad_norm over a sequence of contiguous fp32 / bf16 tensors of the current CUDA device that do
+    not overlap: clips them in place, or into `outs` (same sizes and types; gradients left as they are).  Returns the
     norm before clipping as a 1-element fp32 CUDA tensor."""
     outs = grads if outs is None else outs
     n = len(grads)
@@ -716,14 +725,15 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
     # Whole-list passes of the tensors' own C methods: a call may come with hundreds of gradients.
     kinds = list(map(_OUT_OF.get, map(_dtype_of, grads)))
     sizes = list(map(_numel, grads))
-    if None in kinds or not all(map(_is_cuda, grads)) or not all(map(_is_contiguous, grads)):
-        raise ValueError("gradients must be contiguous CUDA fp32 or bf16 tensors")
+    where = set(map(_device_index, grads))
+    if None in kinds or -1 in where or not all(map(_is_contiguous, grads)) or (n and where != {_current_device()}):
+        raise ValueError("gradients must be contiguous fp32 or bf16 tensors on the current CUDA device")
     at = list(map(_data_ptr, grads))
     to = at
     if outs is not grads:
         if (kinds != list(map(_OUT_OF.get, map(_dtype_of, outs))) or sizes != list(map(_numel, outs))
-                or not all(map(_is_cuda, outs)) or not all(map(_is_contiguous, outs))):
-            raise ValueError("outs must be contiguous CUDA tensors of their gradients' sizes and types")
+                or set(map(_device_index, outs)) != where or not all(map(_is_contiguous, outs))):
+            raise ValueError("outs must be contiguous tensors of their gradients' sizes and types on their device")
         to = list(map(_data_ptr, outs))
     # mxfp4_grad entries: two pointers, numel, (dtype, 0)
     table = array.array("q", itertools.chain.from_iterable(zip(at, to, sizes, kinds)))

@@ -1,0 +1,58 @@
+"""What the step operators take and refuse from Python."""
+import pytest
+
+from tests.gpu_util import gpu_ready
+
+pytestmark = pytest.mark.gpu
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Every call wants its tensors on the current device (here: another index is made out to be the current one)."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+    from mxfp4_precision_gemms_gb300 import step
+
+    w = torch.randn(40, 16, device="cuda").bfloat16()
+    ids = torch.randint(0, 40, (9,), device="cuda")
+    h = torch.randn(9, 16, device="cuda").bfloat16()
+    loss, lse = mx.linear_ce(h, w, ids)
+    p = torch.zeros(8, device="cuda", requires_grad=True)
+    p.grad = torch.ones(8, device="cuda")
+    out = torch.empty(8, device="cuda")
+    calls = [lambda: mx.embedding(ids, w), lambda: mx.embedding_grad(ids, h, 40), lambda: mx.linear_ce(h, w, ids),
+             lambda: mx.linear_ce_grad(h, w, ids, lse, loss), lambda: mx.clip_grad_norm([p.grad], 1.0),
+             lambda: mx.clip_grad_norm([p.grad], 1.0, outs=[out]), lambda: step.embedding(ids, w),
+             lambda: step.linear_cross_entropy(h, w, ids), lambda: step.clip_grad_norm_([p], 1.0)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(mx, "_current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
+def test_each_tensor_of_a_call_is_looked_at():
+    """One tensor on the host among those on the device is refused, whichever it is."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    w = torch.randn(40, 16, device="cuda").bfloat16()
+    ids = torch.randint(0, 40, (9,), device="cuda")
+    h = torch.randn(9, 16, device="cuda").bfloat16()
+    loss, lse = mx.linear_ce(h, w, ids)
+    dw, dh = torch.empty(40, 16, device="cuda").bfloat16(), torch.empty_like(h)
+    g = torch.ones(8, device="cuda")
+    for call, args in ((mx.embedding, (ids, w)), (mx.embedding_grad, (ids, h)), (mx.linear_ce, (h, w, ids)),
+                       (mx.linear_ce_grad, (h, w, ids, lse, loss))):
+        extra = {"vocab": 40} if call is mx.embedding_grad else {}
+        call(*args, **extra)
+        for i in range(len(args)):
+            with pytest.raises(ValueError):
+                call(*(x.cpu() if j == i else x for j, x in enumerate(args)), **extra)
+    for bad in (lambda: mx.embedding(ids, w, out=h.cpu()), lambda: mx.embedding_grad(ids, h, 40, dw=dw.cpu()),
+                lambda: mx.linear_ce_grad(h, w, ids, lse, loss, dh=dh.cpu()),
+                lambda: mx.linear_ce_grad(h, w, ids, lse, loss, dw=dw.cpu()),
+                lambda: mx.clip_grad_norm([g, g.cpu()], 1.0), lambda: mx.clip_grad_norm([g], 1.0, outs=[g.cpu()])):
+        with pytest.raises(ValueError):
+            bad()

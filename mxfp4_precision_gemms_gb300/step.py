@@ -8,6 +8,8 @@ fp32 number for each token.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -18,7 +20,7 @@ _REDUCTIONS = {"none": mx.REDUCE_NONE, "sum": mx.REDUCE_SUM, "mean": mx.REDUCE_M
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
     """x [..., dim] as a matrix whose rows do not overlap (a broadcast gradient's do) and are contiguous."""
-    x = x.reshape(-1, x.shape[-1])
+    x = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
     if (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
         x = x.contiguous()
     return x
@@ -30,6 +32,7 @@ class EmbeddingFunction(torch.autograd.Function):
         ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.vocab, ctx.w_dtype, ctx.scale, ctx.padding_id = w.shape[0], w.dtype, scale, padding_id
+        w = _rows(w) if w.dim() == 2 else w  # the library's own check refuses other shapes
         return mx.embedding(ids, w, scale=scale, out_dtype=None if out_dtype is None else mx._OUT_OF[out_dtype])
 
     @staticmethod
@@ -43,8 +46,9 @@ class EmbeddingFunction(torch.autograd.Function):
 
 def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, padding_id: int = -1,
               out_dtype: torch.dtype | None = None) -> torch.Tensor:
-    """scale * w[ids] for a table w [vocab, dim] (fp32 or bf16), in out_dtype (default: w's).  Its gradient is
-    dense, in w's type, with each row's sum in fp32 in a fixed order; tokens with padding_id give none."""
+    """scale * w[ids] for a table w [vocab, dim] (fp32 or bf16; one whose rows are not contiguous is copied), in
+    out_dtype (default: w's).  Its gradient is dense, in w's type, with each row's sum in fp32 in a fixed order;
+    tokens with padding_id give none."""
     return EmbeddingFunction.apply(ids, w, scale, padding_id, out_dtype)
 
 

@@ -6,6 +6,24 @@ from tests.gpu_util import gpu_ready
 pytestmark = pytest.mark.gpu
 
 
+def test_embedding_takes_a_table_with_other_strides():
+    """A transposed table and columns of a wider one give what contiguous ones give, gradients included."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import embedding
+
+    ids = torch.randint(0, 50, (3, 11), device="cuda")
+    base = torch.randn(24, 50, device="cuda")
+    wide = torch.randn(50, 40, device="cuda")
+    for w in (base.t(), wide[:, 5:29], wide[:, ::2], wide[:1, :24].expand(50, 24)):
+        a, b = w.detach().requires_grad_(), w.detach().contiguous().requires_grad_()
+        ya, yb = embedding(ids, a, scale=3.0), embedding(ids, b, scale=3.0)
+        assert torch.equal(ya, yb)
+        dy = torch.randn_like(ya)
+        ya.backward(dy)
+        yb.backward(dy)
+        assert torch.equal(a.grad, b.grad)
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """Every call wants its tensors on the current device (here: another index is made out to be the current one)."""
     torch = gpu_ready()

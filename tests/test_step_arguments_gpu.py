@@ -24,6 +24,26 @@ def test_embedding_takes_a_table_with_other_strides():
         assert torch.equal(a.grad, b.grad)
 
 
+def test_targets_belong_to_their_tokens():
+    """Targets of the hidden states' leading shape, or either of the two laid out flat; nothing else, even of the same
+    number of elements."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import linear_cross_entropy
+
+    h = torch.randn(3, 5, 16, device="cuda").bfloat16()
+    w = torch.randn(40, 16, device="cuda").bfloat16()
+    y = torch.randint(0, 40, (3, 5), device="cuda")
+    want = linear_cross_entropy(h, w, y, reduction="none")
+    assert torch.equal(linear_cross_entropy(h, w, y.reshape(-1), reduction="none"), want.reshape(-1))
+    assert torch.equal(linear_cross_entropy(h.reshape(-1, 16), w, y, reduction="none"), want)
+    for bad in (y.t(), y.reshape(5, 3), y[None], y[:, :4]):
+        with pytest.raises(ValueError):
+            linear_cross_entropy(h, w, bad)
+    for bad in (w[None], w[0]):
+        with pytest.raises(ValueError):
+            linear_cross_entropy(h, bad, y)
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """Every call wants its tensors on the current device (here: another index is made out to be the current one)."""
     torch = gpu_ready()

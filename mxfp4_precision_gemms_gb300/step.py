@@ -49,6 +49,8 @@ def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, padding_id
     """scale * w[ids] for a table w [vocab, dim] (fp32 or bf16; one whose rows are not contiguous is copied), in
     out_dtype (default: w's).  Its gradient is dense, in w's type, with each row's sum in fp32 in a fixed order;
     tokens with padding_id give none."""
+    if out_dtype is not None and out_dtype not in mx._OUT_OF:
+        raise ValueError(f"out_dtype must be one of {list(mx._OUT_OF)}, not {out_dtype}")
     return EmbeddingFunction.apply(ids, w, scale, padding_id, out_dtype)
 
 

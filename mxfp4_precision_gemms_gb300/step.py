@@ -59,7 +59,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     def forward(ctx, h, w, targets, ignore_index, reduction):
         h2, w = _rows(h), _rows(w)
         if w.data_ptr() % 16 or (w.shape[0] > 1 and w.stride(0) % 8):
-            w = w.contiguous()  # what the library asks of its rows
+            w = w.clone(memory_format=torch.contiguous_format)  # what the library asks of its rows
         y = targets.reshape(-1).contiguous()
         loss, lse = mx.linear_ce(h2, w, y, ignore_index=ignore_index, reduction=reduction)
         ctx.save_for_backward(h2, w, y, lse)

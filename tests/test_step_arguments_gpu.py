@@ -94,3 +94,19 @@ def test_each_tensor_of_a_call_is_looked_at():
                 lambda: mx.clip_grad_norm([g, g.cpu()], 1.0), lambda: mx.clip_grad_norm([g], 1.0, outs=[g.cpu()])):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_cross_entropy_takes_weights_off_16_bytes():
+    """Contiguous weights that start anywhere, as a view into a flat buffer may, give what aligned ones give."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import linear_cross_entropy
+
+    h = torch.randn(30, 24, device="cuda").bfloat16()
+    flat = torch.randn(40 * 24 + 8, device="cuda").bfloat16()
+    y = torch.randint(0, 40, (30,), device="cuda")
+    for shift in (1, 3, 4):
+        w = flat[shift:shift + 40 * 24].view(40, 24)
+        a, b = w.detach().requires_grad_(), w.detach().clone().requires_grad_()
+        la, lb = linear_cross_entropy(h, a, y), linear_cross_entropy(h, b, y)
+        la.backward(), lb.backward()
+        assert torch.equal(la, lb) and torch.equal(a.grad, b.grad)

@@ -415,7 +415,9 @@ typedef enum { MXFP4_IDS_I32 = 0, MXFP4_IDS_I64 = 1 } mxfp4_ids_dtype;
 /* Embedding lookup y[t, :] = scale * w[ids[t], :], computed in fp32 and rounded once.
  * ids: device [tokens] (ids_dtype); w: device [vocab, dim] (ldw elements between rows);
  * y: device [tokens, dim] (ldy).  w_dtype / y_dtype: MXFP4_OUT_F32 or MXFP4_OUT_BF16.
- * Any dim and pitch; rows of a multiple of 16 bytes are moved as vectors.  An id outside
+ * Any dim and pitch.  Rows are moved eight elements at a time where both w and y allow it (dim and
+ * pitch multiples of 8, base aligned to 8 elements: 16 bytes of bf16, 32 of fp32), otherwise one
+ * element at a time; the same holds for dy and dw of mxfp4_embedding_grad.  An id outside
  * [0, vocab) gives a row of zeros. */
 mxfp4_status mxfp4_embedding(const void* ids, int ids_dtype, int64_t tokens, const void* w, int w_dtype,
                              int64_t vocab, int64_t dim, int64_t ldw, float scale, void* y, int y_dtype, int64_t ldy,

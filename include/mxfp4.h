@@ -461,9 +461,10 @@ mxfp4_status mxfp4_linear_ce(const void* h, int64_t tokens, int64_t dim, int64_t
 
 /* Gradients of mxfp4_linear_ce.  With dz[t, v] = g[t] (exp(z[t, v] - lse[t]) - [v == targets[t]])
  *   dh = dz w  (rows of ignored tokens are 0),  dw = dz^T h  (added to dw when accumulate is 1).
- * The logits are made again piece by piece of the vocabulary; dz of one piece is held in the
+ * The logits are made again, the same bits, piece by piece of the vocabulary; dz of one piece is held in the
  * workspace, rounded to bf16 before the factor that all tokens share (up to 128 tokens: held as the
- * sum of two bf16 numbers).
+ * sum of two bf16 numbers).  fp32 outputs carry that rounding too.  exp(z - lse) is as exact as lse in
+ * fp32 is: within some 2^-23 |lse| of itself.
  * h, w, targets, ignore_index, reduction, lse: as given to / returned by mxfp4_linear_ce.
  * dloss: device fp32, the gradient of the loss: [tokens] for MXFP4_REDUCE_NONE, else [1].
  * dh: device [tokens, dim] (lddh), fp32 or bf16, or NULL.  dw: device [vocab, dim] (lddw,

@@ -13,7 +13,9 @@
 //      no atomics and no counter to reset, then scales its chunks, last read first: what the 129 MB
 //      L2 still holds from the first pass is read from there.  Gradients that are clipped in
 //      place by c == 1 are left as they are.
-// HBM bandwidth bounds both passes of long calls, the two launches short ones.
+// HBM bandwidth bounds both passes of long calls, the two launches short ones.  A tensor that starts off 16 bytes is
+// moved one element at a time: views into a flat buffer at an odd element, 872 MB of fp32 in 1165 us instead
+// of 408 out of place, 252 instead of 130 where they are within the limit.
 // Out of place, the second pass has a CTA for each chunk: CTAs that take one and end keep the accesses in
 // address order (872 MB: 248 us against 272 for persistent ones and 257 for cudaMemcpy), and each
 // loads its chunk before it adds up the norm.  In place it is persistent and looks at the norm

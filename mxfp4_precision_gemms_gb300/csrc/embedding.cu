@@ -169,7 +169,7 @@ __device__ __forceinline__ void sort_sync() {
         __syncthreads();
 }
 
-// Latency-bound: 13 us for 8192 tokens, 24 us for 32768, most of it barriers and trips to L2 and back.  Nine bits a
+// Latency-bound: 14 us for 8192 tokens, 22 us for 32768, most of it barriers and trips to L2 and back.  Nine bits a
 // pass are two passes for the usual vocabularies; wider digits would not fit their counters.
 template <int CTAS>
 __device__ void sort_tokens(const SortParams& p, uint32_t* smem) {
@@ -370,7 +370,7 @@ __device__ __forceinline__ void enter_run(const SumParams& p, uint32_t chunk, ui
 }
 
 // One chunk of sorted tokens x one slab of columns (8 per thread, or one).  HBM-bound: 8192 rows of 8 KB
-// in 17 us, 32768 of them added to fp32 rows in 95 (563 MB, 5.9 TB/s).  ACC: dw is added to;
+// in 17 us, 32768 of them added to fp32 rows in 91 (563 MB, 6.2 TB/s).  ACC: dw is added to;
 // the rows that end in the chunk are loaded along with the tokens' rows.
 template <class DY, class DW, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, const DY* dy, DW* dw) {
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p, con
 
 // Joins the crossing runs, one run and one slab of 32 units at a time: a short run's chunks are
 // added by one warp in turn, a long run's by the CTA's warps, each taking every eighth, and their
-// sums in the warps' order.  7 us after 8192 tokens, 14 after 32768: a few dependent reads of L2.
+// sums in the warps' order.  5 us after 8192 tokens, 12 after 32768: a few dependent reads of L2.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 

@@ -48,7 +48,8 @@ def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0, padding_id
               out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """scale * w[ids] for a table w [vocab, dim] (fp32 or bf16; one whose rows are not contiguous is copied), in
     out_dtype (default: w's).  Its gradient is dense, in w's type, with each row's sum in fp32 in a fixed order;
-    tokens with padding_id give none."""
+    tokens with padding_id give none.  An id outside the vocabulary gives a row of zeros and no gradient, and no error
+    here, where nothing is synchronised: binding.device_status() reports it."""
     if out_dtype is not None and out_dtype not in mx._OUT_OF:
         raise ValueError(f"out_dtype must be one of {list(mx._OUT_OF)}, not {out_dtype}")
     return EmbeddingFunction.apply(ids, w, scale, padding_id, out_dtype)
@@ -82,7 +83,8 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     """Softmax cross entropy of the logits h w^T at `targets`: h [..., dim] and w [vocab, dim] bf16, targets
     [...] int32 or int64 (of h's leading shape, or either of the two flat); dim a multiple of 8.  `reduction`: "mean" (over the tokens that count; 0 if
     none does), "sum" or "none".  Tokens whose target is ignore_index do not count, and their rows of h
-    may hold anything."""
+    may hold anything.  Other targets outside the vocabulary do not count either, and raise no error here, where nothing
+    is synchronised: binding.device_status() reports them."""
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
     if w.dim() != 2:
@@ -96,8 +98,9 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
 @torch.no_grad()
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     """Clips the gradients of `parameters` (one tensor or an iterable; those without a gradient are
-    passed over, and one that occurs twice, as a tied weight may, counts once) to a global 2-norm of max_norm, in place.  Returns the norm before clipping, a
-    1-element fp32 CUDA tensor; nothing is synchronised.  Gradients are fp32 or bf16."""
+    passed over, and one that occurs twice, as a tied weight may, counts once) to a global 2-norm of max_norm,
+    in place.  Returns the norm before clipping, a 1-element fp32 CUDA tensor; nothing is synchronised.
+    Gradients are fp32 or bf16, on the current device."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]

@@ -131,7 +131,8 @@ enum Kind { kStats = 0, kDlogits = 1, kProducts = 2, kDlogitsFew = 3 };  // kDlo
 // logit) and cost 3 to 6%; they are taken for at most a tile of tokens, where HBM is waited for anyway and
 // few losses average an error out.  The gradients make the logits again in the same runs, so that z - lse
 // has only lse's rounding: in one run z would be short of the lse that it is subtracted from, and
-// p - 1 at the target of a confident token (logit 30) off by 1.3e-4 whatever it is.  The two gradient
+// p - 1 at the target of a confident token (logit 30) off by 1.3e-4 whatever it is.  (That costs the gradients
+// of 8192 tokens 2 to 3% at dim = 640, 1% at 1024 and nothing that shows from 2048 on.)  The two gradient
 // products have no such difference to keep, and are taken in one run.
 constexpr int kLogitsRun = 8, kLogitsRunFew = 4;
 

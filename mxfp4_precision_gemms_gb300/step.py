@@ -81,15 +81,15 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                          reduction: str = "mean") -> torch.Tensor:
     """Softmax cross entropy of the logits h w^T at `targets`: h [..., dim] and w [vocab, dim] bf16, targets
-    [...] int32 or int64 (of h's leading shape, or either of the two flat); dim a multiple of 8.  `reduction`: "mean" (over the tokens that count; 0 if
-    none does), "sum" or "none".  Tokens whose target is ignore_index do not count, and their rows of h
-    may hold anything.  Other targets outside the vocabulary do not count either, and raise no error here, where nothing
+    [...] int32 or int64 (of h's leading shape, or either of the two flat); dim a multiple of 8.
+    `reduction`: "mean" (over the tokens that count; 0 if none does), "sum" or "none".  Tokens whose target is
+    ignore_index do not count, and their rows of h may hold anything.  Other targets outside the vocabulary do not count either, and raise no error here, where nothing
     is synchronised: binding.device_status() reports them."""
     if reduction not in _REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
     if w.dim() != 2:
         raise ValueError(f"w must be a matrix [vocab, dim], not {tuple(w.shape)}")
-    # of the same number of elements in another shape (a batch laid out the other way), a target would be another token's
+    # in another shape of as many elements (a batch laid out the other way) targets would be other tokens'
     if targets.shape != h.shape[:-1] and targets.dim() != 1 and h.dim() != 2:
         raise ValueError(f"targets {tuple(targets.shape)} do not fit h {tuple(h.shape)}")
     return LinearCrossEntropyFunction.apply(h, w, targets, ignore_index, _REDUCTIONS[reduction])

@@ -501,6 +501,103 @@ size_t mxfp4_clip_grad_norm_workspace_bytes(int n);
 mxfp4_status mxfp4_clip_grad_norm(const mxfp4_grad* grads, int n, float max_norm, float* norm, void* ws,
                                   size_t ws_bytes, mxfp4_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Between the query-key-value projection and the output projection of a decoder block: the
+ * norm of each head of queries and keys with the rotation by position, softmax attention over
+ * packed sequences, and the gradients of both.  As above, infinities and NaN go through the
+ * formulas.
+ * ---------------------------------------------------------------------------------- */
+
+/* Heads of a tensor [tokens, heads, head_dim] whose last dimension is contiguous: slices of one
+ * projection's output as well as a tensor of their own.  Inputs and outputs alike. */
+typedef struct {
+    void* data;           /* device */
+    int64_t token_stride; /* elements between tokens (of one token: any) */
+    int64_t head_stride;  /* elements between heads (of one head: any) */
+    int32_t heads;
+    int32_t dtype;        /* MXFP4_OUT_F32 or MXFP4_OUT_BF16 */
+} mxfp4_heads;
+
+/* A rotation: pair i turns by freq[i] radians a position of axis[i].  The arrays are read on the host
+ * during the call. */
+typedef struct {
+    const double* freq;   /* host [pairs], |freq| <= 1e6 */
+    const int32_t* axis;  /* host [pairs]: the row of positions; NULL: row 0 for all */
+    int32_t pairs;        /* the first 2 * pairs elements of a head turn, the others stay */
+    int32_t interleaved;  /* 1: pair i is elements 2i and 2i + 1; 0: elements i and i + pairs */
+} mxfp4_rope;
+
+/* Norm and rotation of queries and keys in one pass: each row x (a token's head) becomes
+ *   n = x / sqrt(mean(x^2) + eps) * gain   (a side whose gain is NULL: n = x)
+ *   pair (a, b) of n -> (a cos - b sin, b cos + a sin), angle = positions[axis][token] * freq
+ * in fp32, rounded once.  Angles are exact to 2^-40 of a turn for positions below 2^24 and to 2^-32
+ * below 2^32, whatever the frequency.
+ * q, k: [tokens, heads, head_dim], both of one type; k NULL: queries alone.  head_dim even, at
+ * most 256; any strides and alignment of the element type (rows of whole 16-byte vectors are
+ * moved faster).  q_gain, k_gain: device fp32 [head_dim] or NULL.
+ * rope: NULL for no rotation.  positions: device [axes, tokens] (ids_dtype), any integers.
+ * q_out, k_out: as many heads and the same type as q and k; each may be its input itself (the same data
+ * and strides), but not overlap an input otherwise. */
+mxfp4_status mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t tokens, int64_t head_dim,
+                                const float* q_gain, const float* k_gain, float eps, const mxfp4_rope* rope,
+                                const void* positions, int ids_dtype, int64_t axes, const mxfp4_heads* q_out,
+                                const mxfp4_heads* k_out, mxfp4_stream_t stream);
+
+/* Workspace bytes of mxfp4_qk_norm_rope_grad (for the gains' gradients). */
+size_t mxfp4_qk_norm_rope_grad_workspace_bytes(int64_t tokens, int64_t head_dim);
+
+/* Gradient of mxfp4_qk_norm_rope.  q, k and what follows them: as given to it (q and k are not read, and
+ * may be NULL, where the side has no gain).  dq, dk: the gradients of its outputs, dk NULL for queries
+ * alone.  dq_in, dk_in: receive the gradients of its inputs; each may be its dq / dk or q / k itself.
+ * All of one type.  dq_gain, dk_gain: device fp32 [head_dim], overwritten with the gains' gradients, or
+ * NULL; summed in fp32 in an order that the sizes, the strides' alignment and the device's number of SMs fix.
+ * ws: device, 256-byte aligned (not needed when dq_gain and dk_gain are NULL). */
+mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* dq,
+                                     const mxfp4_heads* dk, int64_t tokens, int64_t head_dim, const float* q_gain,
+                                     const float* k_gain, float eps, const mxfp4_rope* rope, const void* positions,
+                                     int ids_dtype, int64_t axes, const mxfp4_heads* dq_in,
+                                     const mxfp4_heads* dk_in, float* dq_gain, float* dk_gain, void* ws,
+                                     size_t ws_bytes, mxfp4_stream_t stream);
+
+/* Softmax attention over packed sequences: for each query of a sequence and each of its heads
+ *   z = scale q k^T over the keys that it sees,  lse = log sum exp z,  out = exp(z - lse) v
+ * q: [q_tokens, q_heads, head_dim]; k, v: [k_tokens, k_heads, head_dim]; q_heads a multiple of k_heads
+ * (query head h reads key head h / (q_heads / k_heads)).  All bf16, rows on multiples of 16 bytes;
+ * head_dim a multiple of 8, at most 128.  scale > 0.
+ * Sequences: cu_q and cu_k are device int32 [seqs + 1], the first token of each sequence and the end of the
+ * last; both NULL: `seqs` sequences of equal lengths.  A list that falls or points behind the tensors is cut to
+ * them, and reported by mxfp4_device_status as MXFP4_ERR_INVALID_ARG.  Any lengths, 0 among them, and those of
+ * queries and keys may differ.
+ * causal 1: query i of a sequence of Lq queries and Lk keys sees keys j <= i + Lk - Lq (the last query sees all).
+ * A query that sees no key gets an out of 0 and an lse of -infinity.  What tokens of other sequences and tokens
+ * outside of all hold reaches nothing.  (Of its own sequence, a hidden key's infinite or NaN v may reach
+ * queries up to 127 before it, as 0 times it.)
+ * out: [q_tokens, q_heads, head_dim] bf16; lse: device fp32 [q_heads, q_tokens], natural logarithm, what
+ * mxfp4_attention_grad takes.  Rows outside of all sequences are left as they were, in both.
+ * Products in bf16 on the tensor cores (the probabilities rounded to bf16, relative to 2^8 times a row's
+ * largest at most), sums and softmax statistics in fp32.  The same bits on every run. */
+mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v, int64_t q_tokens,
+                             int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
+                             int64_t seqs, int causal, float scale, const mxfp4_heads* out, float* lse,
+                             mxfp4_stream_t stream);
+
+/* Workspace bytes of mxfp4_attention_grad: two fp32 statistics of each query. */
+size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
+
+/* Gradients of mxfp4_attention.  The probabilities p = exp(z - lse) are made again:
+ *   dv = p^T dout,  dz = p (dout v^T - dout . out),  dq = scale dz k,  dk = scale dz^T q
+ * q to scale: as given to it, out and lse as returned by it; dout: the gradient of out, bf16.
+ * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences are left as they
+ * were.  dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are
+ * rounded to bf16 for the tensor cores.  No atomic additions: the same bits on every run.
+ * ws: device, 256-byte aligned. */
+mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
+                                  const mxfp4_heads* out, const float* lse, const mxfp4_heads* dout, int64_t q_tokens,
+                                  int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
+                                  int64_t seqs, int causal, float scale, const mxfp4_heads* dq,
+                                  const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws, size_t ws_bytes,
+                                  mxfp4_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the current device's status word:
  * MXFP4_OK, MXFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last call,
  * or MXFP4_ERR_CUDA if a GEMM kernel found its shared memory misaligned for its tile

@@ -60,6 +60,18 @@ class PhiloxOptsC(ctypes.Structure):
                 ("stochastic_rounding", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class HeadsC(ctypes.Structure):
+    """mxfp4_heads: heads of a [tokens, heads, head_dim] tensor."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class RopeC(ctypes.Structure):
+    """mxfp4_rope: frequencies and axes of a rotation (host arrays)."""
+    _fields_ = [("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pairs", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 class MxConfigC(ctypes.Structure):
     _fields_ = [("had", ctypes.c_int32), ("mode", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32)]
@@ -123,6 +135,12 @@ def lib():
                                           P, S, P], I),
                 "mxfp4_clip_grad_norm_workspace_bytes": ([I], S),
                 "mxfp4_clip_grad_norm": ([P, I, F, P, P, S, P], I),
+                "mxfp4_qk_norm_rope": ([P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P], I),
+                "mxfp4_qk_norm_rope_grad_workspace_bytes": ([I64, I64], S),
+                "mxfp4_qk_norm_rope_grad": ([P, P, P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P, P, P, S, P], I),
+                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P], I),
+                "mxfp4_attention_grad_workspace_bytes": ([I64, I64], S),
+                "mxfp4_attention_grad": ([P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
                 "mxfp4_set_wait_limit_ns": ([ctypes.c_uint64], None),
                 "mxfp4_test_inject_gemm_fault": ([I], None),
@@ -745,6 +763,229 @@ def clip_grad_norm(grads, max_norm: float, outs=None, stream=None) -> torch.Tens
     _check(L.mxfp4_clip_grad_norm(table.buffer_info()[0], n, max_norm, norm.data_ptr(), ws.data_ptr(), nb,
                                   _stream(stream)))
     return norm
+
+
+# ----------------------------------------------------------------- around attention
+class Rope:
+    """A rotation by position: pair i of a head turns by freq[i] radians a position of row axis[i] of the positions
+    (all of row 0 by default).  interleaved: pair i is elements 2i and 2i + 1, otherwise i and i + pairs.  Laid out once
+    and read on the host during the calls that take it."""
+
+    def __init__(self, freq, axis=None, interleaved: bool = False):
+        self.freq = array.array("d", freq)
+        self.axis = None if axis is None else array.array("i", axis)
+        if self.axis is not None and len(self.axis) != len(self.freq):
+            raise ValueError(f"{len(self.axis)} axes for {len(self.freq)} frequencies")
+        self.axes = 1 + max(self.axis, default=0) if self.axis is not None else 1  # rows of positions it needs
+        self.interleaved = bool(interleaved)
+        self.c = RopeC(self.freq.buffer_info()[0], None if self.axis is None else self.axis.buffer_info()[0],
+                       len(self.freq), int(interleaved))
+        self.ref = ctypes.addressof(self.c)
+
+
+_addressof = ctypes.addressof
+
+
+def _heads(x: torch.Tensor, name: str) -> tuple[HeadsC, tuple]:
+    """A [tokens, heads, head_dim] fp32 / bf16 tensor of the current device as the library takes it, and its shape."""
+    kind = _OUT_OF.get(x.dtype)
+    if kind is not None and x.dim() == 3 and _here(x):
+        shape = x.shape
+        token_stride, head_stride, inner = x.stride()
+        if inner == 1 or shape[2] <= 1:
+            return HeadsC(x.data_ptr(), token_stride, head_stride, shape[1], kind), shape
+    raise ValueError(f"{name} must be an fp32 or bf16 tensor [tokens, heads, head_dim] with unit inner stride on the "
+                     "current CUDA device")
+
+
+def _like(out, shape, kind: int, name: str, device, stream, zero: bool = False) -> tuple[torch.Tensor, HeadsC]:
+    """A caller's output heads, checked, or new ones (zero: filled with zeros, for a call that leaves rows out)."""
+    if out is None:
+        out = _empty(shape, _FLOAT_OF[kind], device, stream)
+        if zero:
+            with torch.cuda.stream(stream):
+                out.zero_()
+        return out, HeadsC(out.data_ptr(), shape[1] * shape[2], shape[2], shape[1], kind)
+    c, got = _heads(out, name)
+    if tuple(got) != tuple(shape) or c.dtype != kind:
+        raise ValueError(f"{name} must be {tuple(shape)} of {_FLOAT_OF[kind]}")
+    return out, c
+
+
+def _gain(gain: torch.Tensor | None, dim: int, name: str):
+    if gain is None:
+        return None
+    if gain.dtype is not torch.float32 or not _here(gain) or not gain.is_contiguous() or gain.numel() != dim:
+        raise ValueError(f"{name} must be {dim} contiguous fp32 elements on the current CUDA device")
+    return gain.data_ptr()
+
+
+def _positions(positions: torch.Tensor | None, rope: Rope | None, tokens: int) -> tuple[int | None, int, int]:
+    """(address, ids dtype, axes) of the positions of a rotation."""
+    if rope is None:
+        return None, 0, 0
+    if positions is None:
+        raise ValueError("a rotation needs positions")
+    kind = _token_ids(positions, "positions")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens or axes < rope.axes:
+        raise ValueError(f"positions must be [{rope.axes}, {tokens}], not {tuple(positions.shape)}")
+    return positions.data_ptr(), kind, axes
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope | None = None,
+                 positions: torch.Tensor | None = None, q_gain: torch.Tensor | None = None,
+                 k_gain: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, stream=None):
+    """mxfp4_qk_norm_rope: each head of q and k [tokens, heads, head_dim] (fp32 or bf16, any strides with contiguous
+    rows; k may be None) divided by its root mean square and multiplied by its gain (fp32 [head_dim]; None: left as it
+    is), then rotated by `rope` at `positions` ([tokens] or [axes, tokens], int32 or int64).  Returns (q_out, k_out); each
+    may be its input, for in place."""
+    cq, shape = _heads(q, "q")
+    n, _, dim = shape
+    device = q.device
+    at, ids_kind, axes = _positions(positions, rope, n)
+    q_out, cqo = _like(q_out, shape, cq.dtype, "q_out", device, stream)
+    ck = cko = None
+    if k is not None:
+        ck, k_shape = _heads(k, "k")
+        if k_shape[0] != n or k_shape[2] != dim or ck.dtype != cq.dtype:
+            raise ValueError(f"q {tuple(shape)} and k {tuple(k_shape)} do not fit together")
+        k_out, cko = _like(k_out, k_shape, cq.dtype, "k_out", device, stream)
+    _check(lib().mxfp4_qk_norm_rope(_addressof(cq), _addressof(ck) if ck else None, n, dim, _gain(q_gain, dim, "q_gain"),
+                                    _gain(k_gain, dim, "k_gain"), eps, rope.ref if rope else None, at, ids_kind, axes,
+                                    _addressof(cqo), _addressof(cko) if cko else None, _stream(stream)))
+    return q_out, (k_out if k is not None else None)
+
+
+def qk_norm_rope_grad(q: torch.Tensor | None, k: torch.Tensor | None, dq: torch.Tensor, dk: torch.Tensor | None,
+                      rope: Rope | None = None, positions: torch.Tensor | None = None,
+                      q_gain: torch.Tensor | None = None, k_gain: torch.Tensor | None = None, eps: float = 1e-6,
+                      dq_in: torch.Tensor | None = None, dk_in: torch.Tensor | None = None, gains: bool = True,
+                      stream=None):
+    """mxfp4_qk_norm_rope_grad: gradients (dq_in, dk_in, dq_gain, dk_gain) of qk_norm_rope's inputs and gains from dq and
+    dk, those of its outputs (dk None: queries alone).  q and k, its inputs, are read where there is a gain and may be
+    None otherwise.  dq_in and dk_in may be dq and dk themselves; gains False leaves the gains' gradients out."""
+    cd, shape = _heads(dq, "dq")
+    n, _, dim = shape
+    device, kind = dq.device, cd.dtype
+    at, ids_kind, axes = _positions(positions, rope, n)
+    sides = []
+    for x, dx, gain, dx_in, name in ((q, dq, q_gain, dq_in, "q"), (k, dk, k_gain, dk_in, "k")):
+        if dx is None:
+            if gain is not None:
+                raise ValueError(f"{name}_gain without d{name}")
+            sides.append((None, None, None, None, None, None, None))
+            continue
+        c, got = _heads(dx, "d" + name)
+        if got[0] != n or got[2] != dim or c.dtype != kind:
+            raise ValueError(f"dq {tuple(shape)} and d{name} {tuple(got)} do not fit together")
+        cx = dgain = None
+        if gain is not None:
+            if x is None:
+                raise ValueError(f"{name}_gain needs {name}")
+            cx, x_shape = _heads(x, name)
+            if tuple(x_shape) != tuple(got) or cx.dtype != kind:
+                raise ValueError(f"{name} must be {tuple(got)} of {_FLOAT_OF[kind]}")
+            if gains:
+                dgain = _empty(dim, torch.float32, device, stream)
+        dx_in, ci = _like(dx_in, got, kind, f"d{name}_in", device, stream)
+        sides.append((c, cx, ci, _gain(gain, dim, name + "_gain"), dx_in, dgain,
+                      None if dgain is None else dgain.data_ptr()))
+    ref = lambda c: None if c is None else _addressof(c)
+    L = lib()
+    nb = L.mxfp4_qk_norm_rope_grad_workspace_bytes(n, dim) if any(s[5] is not None for s in sides) else 0
+    ws = _empty(nb, torch.uint8, device, stream) if nb else None
+    (cdq, cq, cqi, qg, dq_in, dq_gain, dqg), (cdk, ck, cki, kg, dk_in, dk_gain, dkg) = sides
+    _check(L.mxfp4_qk_norm_rope_grad(ref(cq), ref(ck), ref(cdq), ref(cdk), n, dim, qg, kg, eps, rope.ref if rope else None,
+                                     at, ids_kind, axes, ref(cqi), ref(cki), dqg, dkg, ws.data_ptr() if nb else None, nb,
+                                     _stream(stream)))
+    return dq_in, dk_in, dq_gain, dk_gain
+
+
+def _sequences(cu_q, cu_k, seqs: int, same: bool) -> tuple[int | None, int | None, int]:
+    """(address of cu_q, of cu_k, sequences); cu_k defaults to cu_q where there are as many keys as queries."""
+    if cu_q is None:
+        if cu_k is not None:
+            raise ValueError("cu_k without cu_q")
+        return None, None, seqs
+    if cu_k is None:
+        if not same:
+            raise ValueError("cu_q without cu_k, and not as many keys as queries")
+        cu_k = cu_q
+    for x, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        if x.dtype is not torch.int32 or x.dim() != 1 or x.numel() < 1 or not _here(x) or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 vector on the current CUDA device")
+    if cu_q.numel() != cu_k.numel():
+        raise ValueError(f"cu_q has {cu_q.numel()} elements, cu_k {cu_k.numel()}")
+    return cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1
+
+
+def _attention_operands(q, k, v):
+    """(descriptors of q, k and v, q's shape, k's shape) of an attention call, checked."""
+    cq, shape = _heads(q, "q")
+    ck, k_shape = _heads(k, "k")
+    cv, v_shape = _heads(v, "v")
+    if cq.dtype != OUT_BF16 or ck.dtype != OUT_BF16 or cv.dtype != OUT_BF16:
+        raise ValueError("q, k and v must be bf16")
+    if tuple(k_shape) != tuple(v_shape) or shape[2] != k_shape[2]:
+        raise ValueError(f"q {tuple(shape)}, k {tuple(k_shape)} and v {tuple(v_shape)} do not fit together")
+    return cq, ck, cv, shape, k_shape
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True, scale: float | None = None,
+              cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, seqs: int = 1,
+              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """mxfp4_attention: softmax attention of q [q_tokens, q_heads, head_dim] over k and v [k_tokens, k_heads, head_dim],
+    bf16, scale 1 / sqrt(head_dim) by default.  cu_q, cu_k: int32 [sequences + 1], where each sequence starts (cu_k
+    None: as cu_q); None: `seqs` sequences of equal lengths.  Returns (out, lse): out like q, lse fp32
+    [q_heads, q_tokens], which attention_grad takes.  Tokens outside of all sequences: new outputs hold zeros there, given
+    ones are left as they were."""
+    cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
+    n, heads, dim = shape
+    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == k_shape[0])
+    device = q.device
+    out, co = _like(out, shape, OUT_BF16, "out", device, stream, zero=cu_q is not None)
+    if lse is None:
+        lse = _empty((heads, n), torch.float32, device, stream)
+        if cu_q is not None:
+            with torch.cuda.stream(stream):
+                lse.zero_()
+    elif lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
+        raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
+    _check(lib().mxfp4_attention(_addressof(cq), _addressof(ck), _addressof(cv), n, k_shape[0], dim, at_q, at_k, seqs,
+                                 int(causal), dim ** -0.5 if scale is None else scale, _addressof(co), lse.data_ptr(),
+                                 _stream(stream)))
+    return out, lse
+
+
+def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                   dout: torch.Tensor, causal: bool = True, scale: float | None = None,
+                   cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, seqs: int = 1,
+                   dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                   stream=None):
+    """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out and lse
+    as it returned them, the rest as it was given.  dq, dk and dv may be slices of one buffer.  Tokens outside of all
+    sequences: as in attention."""
+    cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
+    n, heads, dim = shape
+    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == k_shape[0])
+    device, zero = q.device, cu_q is not None
+    _, co = _like(out, shape, OUT_BF16, "out", device, stream)
+    _, cd = _like(dout, shape, OUT_BF16, "dout", device, stream)
+    if lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
+        raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
+    dq, cdq = _like(dq, shape, OUT_BF16, "dq", device, stream, zero)
+    dk, cdk = _like(dk, k_shape, OUT_BF16, "dk", device, stream, zero)
+    dv, cdv = _like(dv, k_shape, OUT_BF16, "dv", device, stream, zero)
+    L = lib()
+    nb = L.mxfp4_attention_grad_workspace_bytes(n, heads)
+    ws = _empty(nb, torch.uint8, device, stream)
+    _check(L.mxfp4_attention_grad(_addressof(cq), _addressof(ck), _addressof(cv), _addressof(co), lse.data_ptr(),
+                                  _addressof(cd), n, k_shape[0], dim, at_q, at_k, seqs, int(causal),
+                                  dim ** -0.5 if scale is None else scale, _addressof(cdq), _addressof(cdk),
+                                  _addressof(cdv), ws.data_ptr(), nb, _stream(stream)))
+    return dq, dk, dv
 
 
 DECOMP_KEYS = ("e2", "scale2", "dz2", "grid2", "scale_grid", "n_deadzone", "n")

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
 SOURCES = ("mxfp4_api.cu", "quantize.cu", "quant_fixes.cu", "quant_random.cu", "gemm.cu", "gemm_mbs.cu", "noalloc.cu",
-           "decompose.cu", "peak.cu", "embedding.cu", "clip.cu", "linear_ce.cu")
+           "decompose.cu", "peak.cu", "embedding.cu", "clip.cu", "linear_ce.cu", "rope.cu",
+           "attention.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,1300 @@
+// attention.cu -- softmax attention over packed sequences, and its gradient, which recomputes the probabilities.
+//
+//   z = scale q k^T where the query sees the key,  lse = log sum exp z,  o = exp(z - lse) v
+//   p = exp(z - lse),  dv = p^T do,  dp = do v^T,  delta = do . o,  dz = p (dp - delta)
+//   dq = scale dz k,  dk = scale dz^T q            (dk, dv: summed over the query heads that share the key's)
+//
+// Scores and probabilities live in tensor memory and registers alone.  All products run on the tensor cores in bf16
+// with fp32 sums (tcgen05.mma.kind::f16 on tiles of 128 x 128); p and dz are rounded to bf16 as operands.
+//
+//   forward  a CTA for 256 queries of a head, as two tiles that take turns: while the softmax of one runs, the tensor
+//            cores work on the other
+//   delta    (lse log2 e, do . o) of each query
+//   dkv      a CTA for 128 keys of a key head, over all queries that see them, of all heads that share it: dk and dv stay
+//            in tensor memory, and no two CTAs add to the same number
+//   dq       a CTA for 128 queries of a head, over the keys that they see
+// The scores are made a second time for dq: two products more than a single pass over (keys, queries) would need, which
+// would have to add to dq in memory, in an order that differs from run to run.
+//
+// Operand tiles are 128 rows (tokens) x 64 or 128 columns in shared memory, in blocks of 64 columns, 128-byte rows,
+// 128-byte swizzle: the same tile is read along its columns (q and k of z) or along its rows (v of p v).  A tile reaches
+// past the end of its sequence into the next one's rows; where such rows are summed over they are cleared first, so that
+// nothing that they hold (infinities, NaN) reaches this sequence.
+#include <algorithm>
+#include <cmath>
+
+#include "element.cuh"
+#include "heads.cuh"
+
+namespace mx {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kRows = 128;                // of a tile
+constexpr int kBlockBytes = kRows * 128;  // 64 columns of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// D (+)= A B^T with bf16 operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in tensor memory: row m in lane m, two bf16 in each column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// wait_bounded for a whole warp: what all lanes agree on.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, uint32_t* status) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, limit_ns, status));
+}
+
+// ------------------------------------------------------------------ sequences
+struct Sequences {
+    const int32_t* cu_q;  // [count + 1] first tokens, or NULL: `count` sequences of equal lengths
+    const int32_t* cu_k;
+    int32_t count, tokens_q, tokens_k, len_q, len_k;
+};
+
+struct Place {
+    int32_t q0, k0, len_q, len_k;  // first tokens and lengths of the sequence
+    int32_t tile;                  // of it; -1: nothing to do
+};
+
+// Sequence i's first token and length, whatever the list holds.
+__device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t tokens, int32_t& first, int32_t& len,
+                                         uint32_t* status) {
+    const int32_t a = cu[i], b = cu[i + 1];
+    if (a < 0 || b < a || b > tokens) atomicOr(status, kStatusBadIndex);
+    first = min(max(a, 0), tokens);
+    len = min(max(b, first), tokens) - first;
+}
+
+// The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences.  By one warp.
+template <bool KEYS>
+__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
+    Place p;
+    p.tile = -1;
+    if (!s.cu_q) {
+        const int32_t len = KEYS ? s.len_k : s.len_q, tiles = (len + rows - 1) / rows;
+        if (tiles == 0 || slot / tiles >= s.count) return p;
+        const int32_t i = slot / tiles;
+        p.q0 = i * s.len_q, p.k0 = i * s.len_k, p.len_q = s.len_q, p.len_k = s.len_k;
+        p.tile = slot - i * tiles;
+        return p;
+    }
+    const int lane = threadIdx.x & 31;
+    int32_t before = 0;
+    for (int32_t i0 = 0; i0 < s.count; i0 += 32) {
+        const int32_t i = i0 + lane;
+        Place mine{};
+        if (i < s.count) {
+            range_of(s.cu_q, i, s.tokens_q, mine.q0, mine.len_q, status);
+            range_of(s.cu_k, i, s.tokens_k, mine.k0, mine.len_k, status);
+        }
+        const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows;
+        int32_t upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t t = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += t;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + upto > slot);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+            p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
+            p.tile = slot - before - __shfl_sync(0xffffffffu, upto - tiles, src);
+            return p;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return p;
+}
+
+// ------------------------------------------------------------------ shared pieces
+// K runs along the tile's columns (16 a step).
+__device__ __forceinline__ uint64_t along_columns(uint32_t tile, int step) {
+    return smem_desc(tile + (step >> 2) * kBlockBytes + (step & 3) * 32, 16, 1024, kSwizzle128B);
+}
+// K runs along the tile's rows (16 a step), N along its columns.
+__device__ __forceinline__ uint64_t along_rows(uint32_t tile, int step) {
+    return smem_desc(tile + step * 2048, kBlockBytes, 1024, kSwizzle128B);
+}
+// Tensor-memory column of step `step` of p or dz, which each half of the columns keeps in its own half of the scores'.
+__device__ __forceinline__ uint32_t half_column(int step) { return (step >> 2) * 64 + (step & 3) * 8; }
+
+// Clears rows [from, 128) of a tile, by one warp.
+template <int DP>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int b = 0; b < DP / 64; ++b)
+        for (int i = from * 8 + lane; i < kRows * 8; i += 32)
+            *reinterpret_cast<uint4*>(tile + b * kBlockBytes + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+template <int DP>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int32_t head,
+                                          int32_t token) {
+    mbar_arrive_expect_tx(bar, DP / 64 * kBlockBytes);
+#pragma unroll
+    for (int b = 0; b < DP / 64; ++b) tma_load_3d(dst + b * kBlockBytes, map, bar, b * 64, head, token);
+}
+
+// This lane's row of an accumulator, times `factor`, to memory as bf16 (dim elements, a multiple of 8).
+__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor, bf16* to, bool inside) {
+    for (int c = 0; c < dim; c += 16) {
+        uint32_t v[16], w[8];
+        tmem_ld_32x32b_x16(taddr + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = pack_bf16(__uint_as_float(v[2 * j]) * factor, __uint_as_float(v[2 * j + 1]) * factor);
+        if (inside) {
+            *reinterpret_cast<uint4*>(to + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c + 8 < dim) *reinterpret_cast<uint4*>(to + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+__device__ __forceinline__ void store_zeros(int dim, bf16* to) {
+    for (int c = 0; c < dim; c += 8) *reinterpret_cast<uint4*>(to + c) = make_uint4(0, 0, 0, 0);
+}
+
+struct Rows {  // of an output
+    bf16* data;
+    int64_t token_stride, head_stride;
+    __device__ __forceinline__ bf16* at(int64_t token, int64_t head) const {
+        return data + token * token_stride + head * head_stride;
+    }
+};
+
+// A ring of tiles: the phase of use number i of its stages.
+template <int N>
+struct Ring {
+    static __device__ __forceinline__ int stage(int i) { return i % N; }
+    static __device__ __forceinline__ uint32_t parity(int i) { return (uint32_t)(i / N) & 1u; }
+};
+
+// ------------------------------------------------------------------ forward
+struct ForwardParams {
+    CUtensorMap q, k, v;
+    Rows out;
+    float* lse;  // [q_heads][tokens_q]
+    Sequences seq;
+    int32_t q_heads, group, dim, causal;
+    float scale_log2;  // scale * log2 e
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+template <int DP>
+struct ForwardShape {
+    static constexpr int kTileBytes = DP / 64 * kBlockBytes;
+    static constexpr int kStages = DP == 128 ? 5 : 6;
+    static constexpr int kOffRing = 2 * kTileBytes;
+    static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
+    static constexpr int kBars = 2 + 2 * kStages + 2 + 2 + 2 + 1;
+    static constexpr int kOffPlace = kOffBar + kBars * 8;
+    static constexpr int kSmem = kOffPlace + 32;
+};
+static_assert(ForwardShape<128>::kSmem <= 227 * 1024, "shared memory budget");
+static_assert(2 * ForwardShape<64>::kSmem > 228 * 1024, "one CTA per SM: CTAs do not wait for each other's TMEM");
+constexpr int kForwardThreads = 64 + 256;
+constexpr float kLag = 8.f;  // log2 of how far a row's sum may run ahead of the maximum that it is scaled by
+
+template <int DP>
+__global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __grid_constant__ ForwardParams p) {
+    using Shape = ForwardShape<DP>;
+    constexpr int kStages = Shape::kStages;
+    extern __shared__ uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemLayout);
+        return;
+    }
+    uint8_t* ring = smem + Shape::kOffRing;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar);  // [2]
+    uint64_t* full = q_full + 2;                                            // [kStages]
+    uint64_t* empty = full + kStages;                                       // [kStages]
+    uint64_t* s_full = empty + kStages;                                     // [2] scores of a tile
+    uint64_t* p_full = s_full + 2;                                          // [2] its probabilities
+    uint64_t* o_full = p_full + 2;                                          // [2] its output
+    uint64_t* mma_done = o_full + 2;
+    Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.q_heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.q_heads);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&p.q);
+        prefetch_tmap(&p.k);
+        prefetch_tmap(&p.v);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 0) {
+        const Place w = find_place<false>(p.seq, slot, 2 * kRows, p.status);
+        if (lane == 0) *where = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    Place at = *where;
+    const bool work = at.tile >= 0;
+    // the tiles that see the most keys first
+    if (work && p.causal) at.tile = (at.len_q + 2 * kRows - 1) / (2 * kRows) - 1 - at.tile;
+    const int32_t row0 = at.tile * 2 * kRows;  // first query, in the sequence
+    const int32_t ahead = at.len_k - at.len_q;  // query i sees keys up to i + ahead
+    // key tiles of each query tile
+    int32_t n[2] = {0, 0};
+    if (work) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int32_t first = row0 + i * kRows, last = min(first + kRows, at.len_q) - 1;
+            const int32_t keys = p.causal ? min(at.len_k, max(last + ahead + 1, 0)) : at.len_k;
+            if (first < at.len_q) n[i] = (keys + kRows - 1) / kRows;
+        }
+    }
+    const int32_t most = max(n[0], n[1]);
+
+    if (warp == 0) {
+        // ---------------- TMA producer
+        if (elect_one() && most > 0) {
+            const int32_t key_head = head / p.group;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (n[i] > 0)
+                    load_tile<DP>(smem + i * Shape::kTileBytes, &p.q, &q_full[i], head, at.q0 + row0 + i * kRows);
+            int armed = 0;
+            for (int i = 0; i < 2 * most; ++i) {  // K and V of each key tile in turn
+                const int s = i % kStages;
+                if (i >= kStages && !wait_bounded(&empty[s], (uint32_t)(i / kStages - 1) & 1u, p.wait_ns, p.status)) break;
+                load_tile<DP>(ring + s * Shape::kTileBytes, i & 1 ? &p.v : &p.k, &full[s], key_head,
+                              at.k0 + (i >> 1) * kRows);
+                armed = i + 1;
+            }
+            // everything that was asked for has landed before this CTA ends
+            for (int i = max(0, armed - kStages); i < armed; ++i)
+                wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1u, p.wait_ns, p.status);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (n[i] > 0) wait_bounded(&q_full[i], 0, p.wait_ns, p.status);
+        }
+    } else if (warp == 1) {
+        // ---------------- tensor cores: one lane issues
+        const uint32_t scores = idesc_bf16(kRows, kRows, 0, 0);
+        const uint32_t output = idesc_bf16(kRows, (uint32_t)(p.dim + 15) / 16 * 16, 0, 1);
+        const int steps = (p.dim + 15) / 16;
+        bool ok = true;
+        auto wait_full = [&](int i) {
+            if (ok) ok = warp_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, p.wait_ns, p.status);
+        };
+        auto make_scores = [&](int t, int j) {
+            const uint32_t a = smem_u32(smem + t * Shape::kTileBytes);
+            const uint32_t b = smem_u32(ring + (2 * j) % kStages * Shape::kTileBytes);
+            if (lane == 0) {
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + t * 128, along_columns(a, k), along_columns(b, k), scores, k != 0);
+                tc_commit(&s_full[t]);
+            }
+        };
+        if (most > 0) {
+            wait_full(0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (ok && n[t] > 0) {
+                    ok = warp_wait(&q_full[t], 0, p.wait_ns, p.status);
+                    tc_fence_after();
+                    if (ok) make_scores(t, 0);
+                }
+            if (ok && lane == 0) tc_commit(&empty[0]);
+        }
+        for (int j = 0; ok && j < most; ++j) {
+            const int sv = (2 * j + 1) % kStages;
+            wait_full(2 * j + 1);
+            if (!ok) break;
+            const int left = at.len_k - j * kRows;  // keys of this tile that are the sequence's
+            if (left < kRows) {
+                clear_rows<DP>(ring + sv * Shape::kTileBytes, left);
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (j + 1 < most) wait_full(2 * j + 2);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!ok || j >= n[t]) continue;
+                ok = warp_wait(&p_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
+                if (!ok) continue;
+                tc_fence_after();
+                const uint32_t b = smem_u32(ring + sv * Shape::kTileBytes);
+                if (lane == 0) {
+                    for (int k = 0; k < kRows / 16; ++k)
+                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, along_rows(b, k), output, j != 0 || k != 0);
+                    if (j + 1 == n[t]) tc_commit(&o_full[t]);
+                }
+                // after p v in the pipe, so the scores may take the place of p
+                if (j + 1 < n[t]) make_scores(t, j + 1);
+            }
+            if (ok && lane == 0) {
+                tc_commit(&empty[sv]);
+                if (j + 1 < most) tc_commit(&empty[(2 * j + 2) % kStages]);
+            }
+        }
+        if (lane == 0) tc_commit(mma_done);
+        warp_wait(mma_done, 0, p.wait_ns, p.status);
+    } else {
+        // ---------------- softmax: a warpgroup for each query tile, a thread for each query
+        const int t = (warp - 2) >> 2, quad = warp & 3;
+        const int32_t row = row0 + t * kRows + quad * 32 + lane;
+        const bool inside = work && row < at.len_q;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t src = lanes + t * 128, acc = lanes + 256 + t * 128;
+        const int columns = (p.dim + 15) / 16 * 16;
+        const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
+        // the least of these in the tile: its first query's
+        const int32_t least = p.causal ? min(at.len_k - 1, row0 + t * kRows + ahead) : at.len_k - 1;
+        float top = -INFINITY;  // maximum that the sums are scaled by (of the scores before `scale`)
+        float shift = 0.f;      // top * scale_log2
+        float sum = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n[t]; ++j) {
+            ok = warp_wait(&s_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t z[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(src + c * 32, z[c]);
+            tmem_ld_wait();
+            if (least - j * kRows < kRows - 1) {
+                const int seen = last - j * kRows;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c * 32 + i > seen) z[c][i] = 0xff800000u;
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[c][i]));
+            const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            // A new maximum is taken up only once the old one lags by kLag: p then stays below 2^kLag, which bf16 and
+            // the fp32 sums hold as exactly as values below 1, and the output is seldom scaled again.
+            const bool raise = j == 0 || (m - top) * p.scale_log2 > kLag;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float new_top = raise ? fmaxf(top, m) : top;
+                const float new_shift = new_top == -INFINITY ? 0.f : new_top * p.scale_log2;
+                if (j > 0) {
+                    // the scores' commit came after that of p v: the output holds all tiles before this one
+                    const float by = !raise ? 1.f : top == -INFINITY ? 0.f : exp2_approx(shift - new_shift);
+                    sum *= by;
+                    for (int c = 0; c < columns; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(acc + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+                        tmem_st_32x32b_x16(acc + c, v);
+                    }
+                }
+                top = new_top;
+                shift = new_shift;
+            }
+            float s4[4] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = exp2_approx(fmaf(__uint_as_float(z[c][2 * i]), p.scale_log2, -shift));
+                    const float b = exp2_approx(fmaf(__uint_as_float(z[c][2 * i + 1]), p.scale_log2, -shift));
+                    s4[(2 * i) & 3] += a;
+                    s4[(2 * i + 1) & 3] += b;
+                    w[i] = pack_bf16(a, b);
+                }
+                tmem_st_32x32b_x16(src + c * 16, w);
+            }
+            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        if (work && n[t] > 0) {
+            ok = ok && warp_wait(&o_full[t], 0, p.wait_ns, p.status);
+            if (ok) {
+                tc_fence_after();
+                store_row(acc, p.dim, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head), inside);
+            }
+        } else if (inside) {  // no key at all
+            store_zeros(p.dim, p.out.at(at.q0 + row, head));
+        }
+        if (inside)
+            p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// What the gradients need of each query: (lse log2 e, do . o).  A query that sees nothing gets an infinite lse, and so
+// probabilities of 0.  HBM-bound: reads o and do once.
+struct DeltaParams {
+    const bf16* out;
+    const bf16* dout;
+    int64_t o_token, o_head, d_token, d_head;
+    const float* lse;
+    float2* stats;  // [q_heads][tokens_q]
+    int32_t tokens, heads, dim;
+};
+constexpr int kDeltaThreads = 256;
+
+__global__ void __launch_bounds__(kDeltaThreads) delta_kernel(const __grid_constant__ DeltaParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int li = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * (kDeltaThreads / 16) + (threadIdx.x >> 4);
+    const int64_t t = row / p.heads;
+    const int32_t h = (int32_t)(row - t * p.heads);
+    float v = 0.f;
+    if (t < p.tokens && li * 8 < p.dim) {
+        float a[8], b[8];
+        unpack8(load8(p.out + t * p.o_token + h * p.o_head + li * 8), a);
+        unpack8(load8(p.dout + t * p.d_token + h * p.d_head + li * 8), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v = fmaf(a[i], b[i], v);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (li == 0 && t < p.tokens) {
+        const int64_t at = (int64_t)h * p.tokens + t;
+        const float l = p.lse[at];
+        p.stats[at] = l == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(l * kLog2e, v);
+    }
+}
+
+struct BackwardParams {
+    CUtensorMap q, k, v, dout;
+    Rows dq, dk, dv;
+    const float2* stats;
+    Sequences seq;
+    int32_t heads;  // of this kernel's CTAs: key heads for dkv, query heads for dq
+    int32_t group, dim, causal;
+    float scale, scale_log2;
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+// Both kernels keep two tiles and stream two others: three stages of the one that is used first and last, two of the other.
+template <int DP>
+struct BackwardShape {
+    static constexpr int kTileBytes = DP / 64 * kBlockBytes;
+    static constexpr int kFirst = 3, kSecond = 2;
+    static constexpr int kOffFirst = 2 * kTileBytes;
+    static constexpr int kOffSecond = kOffFirst + kFirst * kTileBytes;
+    static constexpr int kOffStats = kOffSecond + kSecond * kTileBytes;
+    static constexpr int kOffBar = kOffStats + 2 * kRows * 8;
+    static constexpr int kBars = 2 + 2 * kFirst + 2 * kSecond + 4 + 8 + 1;
+    static constexpr int kOffPlace = kOffBar + kBars * 8;
+    static constexpr int kSmem = (kOffPlace + 32 > 120 * 1024 ? kOffPlace + 32 : 120 * 1024);  // one CTA per SM
+};
+static_assert(BackwardShape<128>::kSmem <= 227 * 1024, "shared memory budget");
+
+// Keys' gradients.  The products of block b (128 keys x 128 queries) in the order in which they are issued:
+//   z(b)^T = k q^T | dv += p(b)^T do, z(b+1)^T | dk += dz(b)^T q, dp(b+1)^T = v do^T | ...
+// While p is made from z, the tensor cores run dk and dp; while dz is made from dp, dv and the next z.
+constexpr int kDkvThreads = 96 + 256;
+
+template <int DP>
+__global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __grid_constant__ BackwardParams p) {
+    using Shape = BackwardShape<DP>;
+    using Q = Ring<Shape::kFirst>;
+    using D = Ring<Shape::kSecond>;
+    extern __shared__ uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemLayout);
+        return;
+    }
+    uint8_t* sK = smem;
+    uint8_t* sV = smem + Shape::kTileBytes;
+    uint8_t* sQ = smem + Shape::kOffFirst;
+    uint8_t* sD = smem + Shape::kOffSecond;
+    float4* stats = reinterpret_cast<float4*>(smem + Shape::kOffStats);  // [2][64]: two queries each
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar);  // [2]
+    uint64_t* q_full = kv_full + 2;
+    uint64_t* q_empty = q_full + Shape::kFirst;
+    uint64_t* d_full = q_empty + Shape::kFirst;
+    uint64_t* d_empty = d_full + Shape::kSecond;
+    uint64_t* stats_full = d_empty + Shape::kSecond;  // [2]
+    uint64_t* stats_empty = stats_full + 2;           // [2]
+    uint64_t* z_full = stats_empty + 2;
+    uint64_t* p_full = z_full + 1;
+    uint64_t* dp_full = p_full + 1;
+    uint64_t* dz_full = dp_full + 1;
+    uint64_t* done = dz_full + 1;
+    Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&stats_full[i], 32);
+            mbar_init(&stats_empty[i], 8);
+        }
+        for (int i = 0; i < Shape::kFirst; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
+        for (int i = 0; i < Shape::kSecond; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 1);
+        }
+        mbar_init(z_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(dp_full, 1);
+        mbar_init(dz_full, 8);
+        mbar_init(done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&p.q);
+        prefetch_tmap(&p.k);
+        prefetch_tmap(&p.v);
+        prefetch_tmap(&p.dout);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 0) {
+        const Place w = find_place<true>(p.seq, slot, kRows, p.status);
+        if (lane == 0) *where = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const Place at = *where;
+    const bool work = at.tile >= 0;
+    const int32_t key0 = at.tile * kRows, ahead = at.len_k - at.len_q;
+    // query tiles that see these keys: from the one with the first query that sees the first key
+    int32_t first = 0, tiles = 0;
+    if (work) {
+        first = p.causal ? max(key0 - ahead, 0) / kRows : 0;
+        tiles = max((at.len_q + kRows - 1) / kRows - first, 0);
+    }
+    const int32_t blocks = tiles * p.group;  // tiles of each query head in turn
+    constexpr uint32_t kZ = 0, kDp = 128, kDv = 256, kDk = 384;  // columns of tensor memory
+
+    if (warp == 0) {
+        // ---------------- TMA producer
+        if (elect_one() && blocks > 0) {
+            load_tile<DP>(sK, &p.k, &kv_full[0], head, at.k0 + key0);
+            load_tile<DP>(sV, &p.v, &kv_full[1], head, at.k0 + key0);
+            int q_armed = 0, d_armed = 0;
+            for (int b = 0; b < blocks; ++b) {
+                const int32_t h = head * p.group + b / tiles, token = at.q0 + (first + b % tiles) * kRows;
+                if (b >= Shape::kFirst && !wait_bounded(&q_empty[Q::stage(b)], Q::parity(b - Shape::kFirst), p.wait_ns, p.status))
+                    break;
+                load_tile<DP>(sQ + Q::stage(b) * Shape::kTileBytes, &p.q, &q_full[Q::stage(b)], h, token);
+                q_armed = b + 1;
+                if (b >= Shape::kSecond && !wait_bounded(&d_empty[D::stage(b)], D::parity(b - Shape::kSecond), p.wait_ns, p.status))
+                    break;
+                load_tile<DP>(sD + D::stage(b) * Shape::kTileBytes, &p.dout, &d_full[D::stage(b)], h, token);
+                d_armed = b + 1;
+            }
+            for (int i = 0; i < 2; ++i) wait_bounded(&kv_full[i], 0, p.wait_ns, p.status);
+            for (int b = max(0, q_armed - Shape::kFirst); b < q_armed; ++b)
+                wait_bounded(&q_full[Q::stage(b)], Q::parity(b), p.wait_ns, p.status);
+            for (int b = max(0, d_armed - Shape::kSecond); b < d_armed; ++b)
+                wait_bounded(&d_full[D::stage(b)], D::parity(b), p.wait_ns, p.status);
+        }
+    } else if (warp == 1) {
+        // ---------------- tensor cores
+        const uint32_t scores = idesc_bf16(kRows, kRows, 0, 0);
+        const uint32_t sums = idesc_bf16(kRows, (uint32_t)(p.dim + 15) / 16 * 16, 0, 1);
+        const int steps = (p.dim + 15) / 16;
+        const uint32_t k_tile = smem_u32(sK), v_tile = smem_u32(sV);
+        bool ok = true;
+        // waits for a streamed tile; rows behind the sequence are cleared, as they are summed over
+        auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int b) {
+            ok = ok && warp_wait(bar, parity, p.wait_ns, p.status);
+            if (!ok) return;
+            const int left = at.len_q - (first + b % tiles) * kRows;
+            if (left < kRows) {
+                clear_rows<DP>(tile, left);
+                fence_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+        };
+        auto make_z = [&](int b) {
+            uint8_t* tile = sQ + Q::stage(b) * Shape::kTileBytes;
+            ready(&q_full[Q::stage(b)], Q::parity(b), tile, b);
+            if (ok && lane == 0) {
+                const uint32_t q_tile = smem_u32(tile);
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + kZ, along_columns(k_tile, k), along_columns(q_tile, k), scores, k != 0);
+                tc_commit(z_full);
+            }
+        };
+        auto make_dp = [&](int b) {
+            uint8_t* tile = sD + D::stage(b) * Shape::kTileBytes;
+            ready(&d_full[D::stage(b)], D::parity(b), tile, b);
+            if (ok && lane == 0) {
+                const uint32_t d_tile = smem_u32(tile);
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + kDp, along_columns(v_tile, k), along_columns(d_tile, k), scores, k != 0);
+                tc_commit(dp_full);
+            }
+        };
+        if (blocks > 0) {
+            ok = warp_wait(&kv_full[0], 0, p.wait_ns, p.status);
+            make_z(0);
+            ok = ok && warp_wait(&kv_full[1], 0, p.wait_ns, p.status);
+            make_dp(0);
+        }
+        for (int b = 0; ok && b < blocks; ++b) {
+            ok = warp_wait(p_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t d_tile = smem_u32(sD + D::stage(b) * Shape::kTileBytes);
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_ts(tmem + kDv, tmem + kZ + half_column(k), along_rows(d_tile, k), sums, b != 0 || k != 0);
+                tc_commit(&d_empty[D::stage(b)]);  // dp(b) came before
+            }
+            if (b + 1 < blocks) make_z(b + 1);
+            ok = ok && warp_wait(dz_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t q_tile = smem_u32(sQ + Q::stage(b) * Shape::kTileBytes);
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_ts(tmem + kDk, tmem + kDp + half_column(k), along_rows(q_tile, k), sums, b != 0 || k != 0);
+                tc_commit(&q_empty[Q::stage(b)]);
+            }
+            if (b + 1 < blocks) make_dp(b + 1);
+        }
+        if (lane == 0) tc_commit(done);
+        warp_wait(done, 0, p.wait_ns, p.status);
+    } else if (warp == 2) {
+        // ---------------- the queries' statistics
+        float2* to = reinterpret_cast<float2*>(stats);
+        for (int b = 0; b < blocks; ++b) {
+            const int s = b & 1;
+            if (b >= 2 && !warp_wait(&stats_empty[s], (uint32_t)(b / 2 - 1) & 1u, p.wait_ns, p.status)) break;
+            const int32_t h = head * p.group + b / tiles, q = (first + b % tiles) * kRows;
+            const float2* from = p.stats + (int64_t)h * p.seq.tokens_q + at.q0;
+#pragma unroll
+            for (int i = 0; i < kRows / 32; ++i) {
+                const int r = i * 32 + lane;
+                to[s * kRows + r] = q + r < at.len_q ? from[q + r] : make_float2(INFINITY, 0.f);
+            }
+            mbar_arrive(&stats_full[s]);
+        }
+    } else {
+        // ---------------- p and dz: a lane for each key, a warpgroup for each half of the queries
+        const int half = (warp - 3) >> 2, quad = warp & 3;
+        const int32_t key = key0 + quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t z_at = lanes + kZ + half * 64, dp_at = lanes + kDp + half * 64;
+        bool ok = true;
+        for (int b = 0; b < blocks; ++b) {
+            const int s = b & 1;
+            ok = warp_wait(&stats_full[s], (uint32_t)(b / 2) & 1u, p.wait_ns, p.status) &&
+                 warp_wait(z_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const float4* st = stats + s * 64 + half * 32;
+            float pr[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t z[32];
+                tmem_ld_32x32b_x32(z_at + c * 32, z);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 l = st[c * 16 + i];
+                    pr[c * 32 + 2 * i] = exp2_approx(fmaf(__uint_as_float(z[2 * i]), p.scale_log2, -l.x));
+                    pr[c * 32 + 2 * i + 1] = exp2_approx(fmaf(__uint_as_float(z[2 * i + 1]), p.scale_log2, -l.z));
+                }
+            }
+            const int32_t q = (first + b % tiles) * kRows;
+            if (p.causal && q + ahead < key0 + kRows - 1) {  // queries below key - ahead do not see the key
+                const int hidden = key - ahead - q - half * 64;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (i < hidden) pr[i] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack_bf16(pr[c * 32 + 2 * i], pr[c * 32 + 2 * i + 1]);
+                tmem_st_32x32b_x16(z_at + c * 16, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+            ok = warp_wait(dp_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t dp[2][32];
+            tmem_ld_32x32b_x32(dp_at, dp[0]);
+            tmem_ld_32x32b_x32(dp_at + 32, dp[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 l = st[c * 16 + i];
+                    w[i] = pack_bf16(pr[c * 32 + 2 * i] * (__uint_as_float(dp[c][2 * i]) - l.y),
+                                     pr[c * 32 + 2 * i + 1] * (__uint_as_float(dp[c][2 * i + 1]) - l.w));
+                }
+                tmem_st_32x32b_x16(dp_at + c * 16, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(dz_full);
+                mbar_arrive(&stats_empty[s]);
+            }
+        }
+        const Rows& rows = half ? p.dk : p.dv;
+        const bool inside = work && key < at.len_k;
+        bf16* to = rows.at(at.k0 + key, head);
+        if (blocks > 0) {
+            ok = ok && warp_wait(done, 0, p.wait_ns, p.status);
+            if (ok) {
+                tc_fence_after();
+                store_row(lanes + (half ? kDk : kDv), p.dim, half ? p.scale : 1.f, to, inside);
+            }
+        } else if (inside) {
+            store_zeros(p.dim, to);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Queries' gradients.  z and dp of the next block are made while dz of this one is; z has two places, and dz takes its own
+// block's, so that dp is free again as soon as it has been read.
+constexpr int kDqThreads = 64 + 256;
+
+template <int DP>
+__global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __grid_constant__ BackwardParams p) {
+    using Shape = BackwardShape<DP>;
+    using K = Ring<Shape::kFirst>;
+    using V = Ring<Shape::kSecond>;
+    extern __shared__ uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusSmemLayout);
+        return;
+    }
+    uint8_t* sQ = smem;
+    uint8_t* sD = smem + Shape::kTileBytes;
+    uint8_t* sK = smem + Shape::kOffFirst;
+    uint8_t* sV = smem + Shape::kOffSecond;
+    uint64_t* qd_full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar);  // [2]
+    uint64_t* k_full = qd_full + 2;
+    uint64_t* k_empty = k_full + Shape::kFirst;
+    uint64_t* v_full = k_empty + Shape::kFirst;
+    uint64_t* v_empty = v_full + Shape::kSecond;
+    uint64_t* z_full = v_empty + Shape::kSecond;  // [2]
+    uint64_t* dp_full = z_full + 2;
+    uint64_t* dp_read = dp_full + 1;
+    uint64_t* dz_full = dp_read + 1;
+    uint64_t* done = dz_full + 1;
+    Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qd_full[i], 1);
+            mbar_init(&z_full[i], 1);
+        }
+        for (int i = 0; i < Shape::kFirst; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < Shape::kSecond; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        mbar_init(dp_full, 1);
+        mbar_init(dp_read, 8);
+        mbar_init(dz_full, 8);
+        mbar_init(done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&p.q);
+        prefetch_tmap(&p.k);
+        prefetch_tmap(&p.v);
+        prefetch_tmap(&p.dout);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 0) {
+        const Place w = find_place<false>(p.seq, slot, kRows, p.status);
+        if (lane == 0) *where = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    Place at = *where;
+    const bool work = at.tile >= 0;
+    if (work && p.causal) at.tile = (at.len_q + kRows - 1) / kRows - 1 - at.tile;  // those that see the most keys first
+    const int32_t row0 = at.tile * kRows, ahead = at.len_k - at.len_q;
+    int32_t blocks = 0;
+    if (work) {
+        const int32_t last = min(row0 + kRows, at.len_q) - 1;
+        const int32_t keys = p.causal ? min(at.len_k, max(last + ahead + 1, 0)) : at.len_k;
+        blocks = (keys + kRows - 1) / kRows;
+    }
+    constexpr uint32_t kZ = 0, kDp = 256, kDq = 384;  // columns of tensor memory; z(b) at kZ + (b & 1) * 128
+
+    if (warp == 0) {
+        // ---------------- TMA producer
+        if (elect_one() && blocks > 0) {
+            const int32_t key_head = head / p.group;
+            load_tile<DP>(sQ, &p.q, &qd_full[0], head, at.q0 + row0);
+            int k_armed = 0, v_armed = 0;
+            for (int b = 0; b < blocks; ++b) {
+                const int32_t token = at.k0 + b * kRows;
+                if (b >= Shape::kFirst && !wait_bounded(&k_empty[K::stage(b)], K::parity(b - Shape::kFirst), p.wait_ns, p.status))
+                    break;
+                load_tile<DP>(sK + K::stage(b) * Shape::kTileBytes, &p.k, &k_full[K::stage(b)], key_head, token);
+                k_armed = b + 1;
+                if (b == 0) load_tile<DP>(sD, &p.dout, &qd_full[1], head, at.q0 + row0);
+                if (b >= Shape::kSecond && !wait_bounded(&v_empty[V::stage(b)], V::parity(b - Shape::kSecond), p.wait_ns, p.status))
+                    break;
+                load_tile<DP>(sV + V::stage(b) * Shape::kTileBytes, &p.v, &v_full[V::stage(b)], key_head, token);
+                v_armed = b + 1;
+            }
+            for (int i = 0; i < 2; ++i) wait_bounded(&qd_full[i], 0, p.wait_ns, p.status);
+            for (int b = max(0, k_armed - Shape::kFirst); b < k_armed; ++b)
+                wait_bounded(&k_full[K::stage(b)], K::parity(b), p.wait_ns, p.status);
+            for (int b = max(0, v_armed - Shape::kSecond); b < v_armed; ++b)
+                wait_bounded(&v_full[V::stage(b)], V::parity(b), p.wait_ns, p.status);
+        }
+    } else if (warp == 1) {
+        // ---------------- tensor cores
+        const uint32_t scores = idesc_bf16(kRows, kRows, 0, 0);
+        const uint32_t sums = idesc_bf16(kRows, (uint32_t)(p.dim + 15) / 16 * 16, 0, 1);
+        const int steps = (p.dim + 15) / 16;
+        const uint32_t q_tile = smem_u32(sQ), d_tile = smem_u32(sD);
+        bool ok = true;
+        auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int b) {
+            ok = ok && warp_wait(bar, parity, p.wait_ns, p.status);
+            if (!ok) return;
+            const int left = at.len_k - b * kRows;
+            if (left < kRows) {  // k is summed over, and 0 times what v holds there must be 0
+                clear_rows<DP>(tile, left);
+                fence_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+        };
+        auto make_z = [&](int b) {
+            uint8_t* tile = sK + K::stage(b) * Shape::kTileBytes;
+            ready(&k_full[K::stage(b)], K::parity(b), tile, b);
+            if (ok && lane == 0) {
+                const uint32_t k_tile = smem_u32(tile);
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + kZ + (b & 1) * 128, along_columns(q_tile, k), along_columns(k_tile, k), scores, k != 0);
+                tc_commit(&z_full[b & 1]);
+            }
+        };
+        auto make_dp = [&](int b) {
+            uint8_t* tile = sV + V::stage(b) * Shape::kTileBytes;
+            ready(&v_full[V::stage(b)], V::parity(b), tile, b);
+            if (ok && lane == 0) {
+                const uint32_t v_tile = smem_u32(tile);
+                for (int k = 0; k < steps; ++k)
+                    mma_ss(tmem + kDp, along_columns(d_tile, k), along_columns(v_tile, k), scores, k != 0);
+                tc_commit(dp_full);
+                tc_commit(&v_empty[V::stage(b)]);
+            }
+        };
+        if (blocks > 0) {
+            ok = warp_wait(&qd_full[0], 0, p.wait_ns, p.status);
+            make_z(0);
+            ok = ok && warp_wait(&qd_full[1], 0, p.wait_ns, p.status);
+            make_dp(0);
+        }
+        for (int b = 0; ok && b < blocks; ++b) {
+            if (b + 1 < blocks) {
+                make_z(b + 1);  // over dz(b - 1), which the product before has read
+                ok = ok && warp_wait(dp_read, (uint32_t)b & 1u, p.wait_ns, p.status);
+                tc_fence_after();
+                make_dp(b + 1);
+            }
+            ok = ok && warp_wait(dz_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t k_tile = smem_u32(sK + K::stage(b) * Shape::kTileBytes);
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_ts(tmem + kDq, tmem + kZ + (b & 1) * 128 + half_column(k), along_rows(k_tile, k), sums,
+                           b != 0 || k != 0);
+                tc_commit(&k_empty[K::stage(b)]);
+            }
+        }
+        if (lane == 0) tc_commit(done);
+        warp_wait(done, 0, p.wait_ns, p.status);
+    } else {
+        // ---------------- p and dz: a lane for each query, a warpgroup for each half of the keys
+        const int half = (warp - 2) >> 2, quad = warp & 3;
+        const int32_t row = row0 + quad * 32 + lane;
+        const bool inside = work && row < at.len_q;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t dp_at = lanes + kDp + half * 64;
+        const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
+        const int32_t least = p.causal ? min(at.len_k - 1, row0 + ahead) : at.len_k - 1;
+        float2 stat = make_float2(INFINITY, 0.f);
+        if (inside) stat = p.stats[(int64_t)head * p.seq.tokens_q + at.q0 + row];
+        bool ok = true;
+        for (int b = 0; b < blocks; ++b) {
+            const uint32_t z_at = lanes + kZ + (b & 1) * 128 + half * 64;
+            ok = warp_wait(&z_full[b & 1], (uint32_t)(b / 2) & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            float pr[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t z[32];
+                tmem_ld_32x32b_x32(z_at + c * 32, z);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    pr[c * 32 + i] = exp2_approx(fmaf(__uint_as_float(z[i]), p.scale_log2, -stat.x));
+            }
+            if (least - b * kRows < kRows - 1) {
+                const int seen = last - b * kRows - half * 64;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (i > seen) pr[i] = 0.f;
+            }
+            ok = warp_wait(dp_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t dp[2][32];
+            tmem_ld_32x32b_x32(dp_at, dp[0]);
+            tmem_ld_32x32b_x32(dp_at + 32, dp[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dp_read);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[i] = pack_bf16(pr[c * 32 + 2 * i] * (__uint_as_float(dp[c][2 * i]) - stat.y),
+                                     pr[c * 32 + 2 * i + 1] * (__uint_as_float(dp[c][2 * i + 1]) - stat.y));
+                tmem_st_32x32b_x16(z_at + c * 16, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dz_full);
+        }
+        bf16* to = p.dq.at(at.q0 + row, head);
+        if (blocks > 0) {
+            ok = ok && warp_wait(done, 0, p.wait_ns, p.status);
+            // each half writes its half of the columns
+            if (ok) {
+                tc_fence_after();
+                const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0;
+                store_row(lanes + kDq + from, half ? p.dim - cut : min(cut, p.dim), p.scale, to + from, inside);
+            }
+        } else if (inside && half == 0) {
+            store_zeros(p.dim, to);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host
+struct Call {
+    Heads q, k, v, out;
+    int64_t tokens_q, tokens_k;
+    Sequences seq;
+    int32_t dim, group;
+};
+
+mxfp4_status check_operand(const char* what, const char* name, const mxfp4_heads* given, int64_t tokens, int64_t dim,
+                           bool written, Heads* out) {
+    mxfp4_status st = check_heads(what, name, given, tokens, dim, written, out);
+    if (st) return st;
+    if (out->dtype != MXFP4_OUT_BF16)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: %s must be bf16", what, name);
+    if (tokens > 0 && !heads_aligned(*out, 16))
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: rows of %s must start on multiples of 16 bytes", what, name);
+    return MXFP4_OK;
+}
+
+mxfp4_status check_call(const char* what, const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
+                        int64_t tokens_q, int64_t tokens_k, int64_t dim, const int32_t* cu_q, const int32_t* cu_k,
+                        int64_t seqs, int causal, float scale, Call* c) {
+    if (tokens_q < 0 || tokens_k < 0 || seqs < 0)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: negative size", what);
+    if (tokens_q >= (1 << 30) || tokens_k >= (1 << 30) || seqs >= (1 << 24))
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: tokens must be below 2^30, sequences below 2^24", what);
+    if (dim < 8 || dim > 128 || dim % 8)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %lld must be a multiple of 8, at most 128", what,
+                            (long long)dim);
+    if (causal != 0 && causal != 1) return record_error(MXFP4_ERR_INVALID_ARG, "%s: causal must be 0 or 1", what);
+    if (!(scale > 0.f) || !std::isfinite(scale * kLog2e))
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
+    mxfp4_status st;
+    if ((st = check_operand(what, "q", q, tokens_q, dim, false, &c->q))) return st;
+    if ((st = check_operand(what, "k", k, tokens_k, dim, false, &c->k))) return st;
+    if ((st = check_operand(what, "v", v, tokens_k, dim, false, &c->v))) return st;
+    if (c->k.heads != c->v.heads || c->q.heads % c->k.heads)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: %d query heads, %d of keys and %d of values do not fit", what,
+                            c->q.heads, c->k.heads, c->v.heads);
+    if (!cu_q != !cu_k) return record_error(MXFP4_ERR_INVALID_ARG, "%s: one of cu_q and cu_k is NULL", what);
+    if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) % 4)
+        return record_error(MXFP4_ERR_MISALIGNED, "%s: cu_q or cu_k misaligned", what);
+    if (!cu_q && (seqs == 0 ? tokens_q || tokens_k : tokens_q % seqs || tokens_k % seqs))
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld sequences of equal lengths do not fit", what,
+                            (long long)seqs);
+    // grids: tiles of 128 at most, one more for each sequence
+    if ((tokens_q / kRows + seqs + 1) * c->q.heads > INT32_MAX || (tokens_k / kRows + seqs + 1) * c->k.heads > INT32_MAX)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles", what);
+    c->tokens_q = tokens_q;
+    c->tokens_k = tokens_k;
+    c->dim = (int32_t)dim;
+    c->group = c->q.heads / c->k.heads;
+    c->seq = {cu_q, cu_k, (int32_t)seqs, (int32_t)tokens_q, (int32_t)tokens_k,
+              seqs && !cu_q ? (int32_t)(tokens_q / seqs) : 0, seqs && !cu_q ? (int32_t)(tokens_k / seqs) : 0};
+    return MXFP4_OK;
+}
+
+// Places of tiles of `rows` tokens: no fewer than there are tiles.
+int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
+    if (c.seq.cu_q) return tokens / rows + c.seq.count;
+    return (int64_t)c.seq.count * ((len + rows - 1) / rows);
+}
+
+template <class Params, class Kern>
+cudaError_t launch_tiles(Kern kern, DeviceSlots& ready, const Params& p, int64_t ctas, int threads, int smem,
+                         cudaStream_t s) {
+    if (ctas == 0) return cudaSuccess;
+    int unused = 0;
+    cudaError_t e = per_device_setting(ready, &unused, [&](int, int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kern, dim3((unsigned)ctas), dim3((unsigned)threads), (size_t)smem, s, 1, true, p);
+}
+
+// Tensors of no tokens have no map: no CTA loads from them.
+bool map_of(CUtensorMap* map, const Heads& h, int64_t tokens, int64_t dim) {
+    return tokens == 0 || encode_heads_map(map, h.data, tokens, h.heads, dim, h.token_stride, h.head_stride, kRows);
+}
+
+Rows rows_of(const Heads& h) { return {static_cast<bf16*>(h.data), h.token_stride, h.head_stride}; }
+
+}  // namespace
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
+                                        int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
+                                        const int32_t* cu_k, int64_t seqs, int causal, float scale,
+                                        const mxfp4_heads* out, float* lse, mxfp4_stream_t stream) {
+    const char* what = "attention";
+    Call c{};
+    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
+    if (st) return st;
+    if ((st = check_operand(what, "out", out, q_tokens, head_dim, true, &c.out))) return st;
+    if (c.out.heads != c.q.heads) return record_error(MXFP4_ERR_INVALID_ARG, "%s: out has other heads than q", what);
+    if (q_tokens == 0 || seqs == 0) return record_error(MXFP4_OK, "%s", "");
+    if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
+    if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
+    if ((st = ensure_device())) return st;
+    ForwardParams p{};
+    if (!map_of(&p.q, c.q, q_tokens, head_dim) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
+        !map_of(&p.v, c.v, k_tokens, head_dim))
+        return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+    p.out = rows_of(c.out);
+    p.lse = lse;
+    p.seq = c.seq;
+    p.q_heads = c.q.heads;
+    p.group = c.group;
+    p.dim = c.dim;
+    p.causal = causal;
+    p.scale_log2 = scale * kLog2e;
+    p.status = device_status_ptr();
+    p.wait_ns = wait_limit_ns();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t ctas = places(c, q_tokens, c.seq.len_q, 2 * kRows) * c.q.heads;
+    static DeviceSlots wide, narrow;
+    const cudaError_t e =
+        c.dim > 64 ? launch_tiles(attention_kernel<128>, wide, p, ctas, kForwardThreads, ForwardShape<128>::kSmem, s)
+                   : launch_tiles(attention_kernel<64>, narrow, p, ctas, kForwardThreads, ForwardShape<64>::kSmem, s);
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return record_error(MXFP4_OK, "%s", "");
+}
+
+extern "C" size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads) {
+    if (q_tokens <= 0 || q_heads <= 0 || q_tokens >= (1 << 30) || q_heads > 65535) return 0;
+    return (size_t)q_tokens * (size_t)q_heads * sizeof(float2);
+}
+
+extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
+                                             const mxfp4_heads* out, const float* lse, const mxfp4_heads* dout,
+                                             int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
+                                             const int32_t* cu_k, int64_t seqs, int causal, float scale,
+                                             const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv,
+                                             void* ws, size_t ws_bytes, mxfp4_stream_t stream) {
+    const char* what = "attention_grad";
+    Call c{};
+    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
+    if (st) return st;
+    Heads d{}, gq{}, gk{}, gv{};
+    if ((st = check_operand(what, "out", out, q_tokens, head_dim, false, &c.out))) return st;
+    if ((st = check_operand(what, "dout", dout, q_tokens, head_dim, false, &d))) return st;
+    if ((st = check_operand(what, "dq", dq, q_tokens, head_dim, true, &gq))) return st;
+    if ((st = check_operand(what, "dk", dk, k_tokens, head_dim, true, &gk))) return st;
+    if ((st = check_operand(what, "dv", dv, k_tokens, head_dim, true, &gv))) return st;
+    if (c.out.heads != c.q.heads || d.heads != c.q.heads || gq.heads != c.q.heads || gk.heads != c.k.heads ||
+        gv.heads != c.k.heads)
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: out, dout or a gradient has other heads than its input", what);
+    if (q_tokens > 0) {
+        if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
+        if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
+        const size_t need = mxfp4_attention_grad_workspace_bytes(q_tokens, c.q.heads);
+        if (!ws || ws_bytes < need)
+            return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, need);
+        if (reinterpret_cast<uintptr_t>(ws) % 256)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: workspace not 256-byte aligned", what);
+    }
+    if (q_tokens * c.q.heads > (int64_t)INT32_MAX * (kDeltaThreads / 16))
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: too many queries", what);
+    if ((q_tokens == 0 && k_tokens == 0) || seqs == 0) return record_error(MXFP4_OK, "%s", "");
+    if ((st = ensure_device())) return st;
+    BackwardParams p{};
+    if (!map_of(&p.q, c.q, q_tokens, head_dim) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
+        !map_of(&p.v, c.v, k_tokens, head_dim) || !map_of(&p.dout, d, q_tokens, head_dim))
+        return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
+    p.dq = rows_of(gq);
+    p.dk = rows_of(gk);
+    p.dv = rows_of(gv);
+    p.stats = static_cast<const float2*>(ws);
+    p.seq = c.seq;
+    p.group = c.group;
+    p.dim = c.dim;
+    p.causal = causal;
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.status = device_status_ptr();
+    p.wait_ns = wait_limit_ns();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (q_tokens > 0) {
+        DeltaParams t{static_cast<const bf16*>(c.out.data), static_cast<const bf16*>(d.data), c.out.token_stride,
+                      c.out.head_stride, d.token_stride, d.head_stride, lse, static_cast<float2*>(ws), (int32_t)q_tokens,
+                      c.q.heads, c.dim};
+        const int64_t rows = q_tokens * c.q.heads, per = kDeltaThreads / 16;
+        e = launch_overlapped(delta_kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(kDeltaThreads), 0, s, 1, true, t);
+        if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s delta launch: %s", what, cudaGetErrorString(e));
+    }
+    static DeviceSlots slots[4];
+    const int smem = c.dim > 64 ? BackwardShape<128>::kSmem : BackwardShape<64>::kSmem;
+    p.heads = c.k.heads;
+    int64_t ctas = places(c, k_tokens, c.seq.len_k, kRows) * c.k.heads;
+    e = c.dim > 64 ? launch_tiles(attention_dkv_kernel<128>, slots[0], p, ctas, kDkvThreads, smem, s)
+                   : launch_tiles(attention_dkv_kernel<64>, slots[1], p, ctas, kDkvThreads, smem, s);
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dkv launch: %s", what, cudaGetErrorString(e));
+    p.heads = c.q.heads;
+    ctas = places(c, q_tokens, c.seq.len_q, kRows) * c.q.heads;
+    e = c.dim > 64 ? launch_tiles(attention_dq_kernel<128>, slots[2], p, ctas, kDqThreads, smem, s)
+                   : launch_tiles(attention_dq_kernel<64>, slots[3], p, ctas, kDqThreads, smem, s);
+    if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dq launch: %s", what, cudaGetErrorString(e));
+    return record_error(MXFP4_OK, "%s", "");
+}

@@ -1,0 +1,89 @@
+"""Attention over packed sequences and its gradient against 64 bits: lengths from nothing to several tiles, head sizes and
+groups, masks that leave rows empty, strides, and what may not reach a sequence."""
+import itertools
+
+import pytest
+
+from tests.gpu_util import gpu_ready
+
+pytestmark = pytest.mark.gpu
+
+LENGTHS = [
+    ([1], [1]), ([3], [37]), ([128], [128]), ([129], [129]), ([300], [300]), ([257, 1, 0, 130], [257, 1, 0, 130]),
+    ([5, 200, 0, 64], [300, 7, 9, 0]),  # more keys than queries, fewer, none of one, none of the other
+]
+
+
+def _inputs(torch, q_lens, k_lens, a, b, D, spare, seed, lean=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    Tq, Tk = sum(q_lens) + spare, sum(k_lens) + spare
+    q, k, v, do = rand(Tq, a, D), rand(Tk, b, D), rand(Tk, b, D), rand(Tq, a, D)
+    if Tk and lean:  # some rows point firmly at one key
+        pick = torch.randint(0, Tk, (Tq, 1), device="cuda", generator=g)
+        head = torch.arange(a, device="cuda") // (a // b)
+        q = q + lean * torch.rand(Tq, a, 1, device="cuda", generator=g) ** 2 * k[pick, head]
+    return [x.bfloat16() for x in (q, k, v, do)]
+
+
+def _edges(torch, lens):
+    return torch.tensor([0, *itertools.accumulate(lens)], dtype=torch.int32, device="cuda")
+
+
+def _check(torch, q, k, v, do, q_lens, k_lens, causal, scale=None, listed=True):
+    from mxfp4_precision_gemms_gb300 import binding as mx
+    from tests.attention_reference import assert_close, attend
+
+    kw = dict(causal=causal, scale=scale)
+    if listed:
+        kw |= dict(cu_q=_edges(torch, q_lens), cu_k=_edges(torch, k_lens))
+    else:
+        kw |= dict(seqs=len(q_lens))
+    out, lse = mx.attention(q, k, v, **kw)
+    grads = mx.attention_grad(q, k, v, out, lse, do, **kw)
+    assert mx.device_status() == 0
+    want, tol = attend(q, k, v, q_lens, k_lens, causal, scale or q.shape[2] ** -0.5, do)
+    for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        assert_close(got, want[name], tol[name], name)
+    return (out, lse, *grads)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", LENGTHS, ids=str)
+def test_lengths(lens, D, causal):
+    torch = gpu_ready()
+    q_lens, k_lens = lens
+    q, k, v, do = _inputs(torch, q_lens, k_lens, 4, 2, D, 3, 1)
+    _check(torch, q, k, v, do, q_lens, k_lens, causal)
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 72, 80, 96, 120])
+def test_head_sizes(D):
+    torch = gpu_ready()
+    q, k, v, do = _inputs(torch, [150], [210], 2, 1, D, 0, 2)
+    _check(torch, q, k, v, do, [150], [210], True)
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (7, 1), (6, 3), (5, 5), (12, 2)])
+def test_shared_heads(heads):
+    torch = gpu_ready()
+    q, k, v, do = _inputs(torch, [70, 140], [70, 140], *heads, 64, 0, 3)
+    _check(torch, q, k, v, do, [70, 140], [70, 140], True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_several_tiles(causal):
+    """More tiles of queries and keys than any ring has stages."""
+    torch = gpu_ready()
+    for D in (64, 128):
+        q, k, v, do = _inputs(torch, [1400, 700], [1400, 1300], 2, 1, D, 0, 4, lean=2.0)
+        _check(torch, q, k, v, do, [1400, 700], [1400, 1300], causal)
+
+
+def test_equal_lengths_without_a_list():
+    torch = gpu_ready()
+    q, k, v, do = _inputs(torch, [190] * 3, [260] * 3, 4, 4, 80, 0, 5)
+    a = _check(torch, q, k, v, do, [190] * 3, [260] * 3, True, listed=False)
+    b = _check(torch, q, k, v, do, [190] * 3, [260] * 3, True)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -220,11 +220,12 @@ def _run_own(s):
         dq, dk, dq_gain, dk_gain = mx.qk_norm_rope_grad(s["q"], s["k"], s["dq"], s["dk"], s["rope"], s["positions"],
                                                         q_gain=s["q_gain"], k_gain=s["k_gain"], eps=EPS)
         return {"dq": dq, "dk": dk, "dq_gain": dq_gain, "dk_gain": dk_gain}
-    out, lse = mx.attention(s["q"], s["k"], s["v"], causal=s["causal"], cu_q=s["cu_q"], cu_k=s["cu_k"])
     if op == "attend":
+        out, lse = mx.attention(s["q"], s["k"], s["v"], causal=s["causal"], cu_q=s["cu_q"], cu_k=s["cu_k"])
         return {"out": out, "lse": lse}
+    out, lse, rest = mx.attention(s["q"], s["k"], s["v"], causal=s["causal"], cu_q=s["cu_q"], cu_k=s["cu_k"], rest=True)
     dq, dk, dv = mx.attention_grad(s["q"], s["k"], s["v"], out, lse, s["dout"], causal=s["causal"], cu_q=s["cu_q"],
-                                   cu_k=s["cu_k"])
+                                   cu_k=s["cu_k"], rest=rest)
     return {"out": out, "dq": dq, "dk": dk, "dv": dv}
 
 

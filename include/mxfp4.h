@@ -574,29 +574,32 @@ mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k,
  * queries up to 127 before it, as 0 times it.)
  * out: [q_tokens, q_heads, head_dim] bf16; lse: device fp32 [q_heads, q_tokens], natural logarithm, what
  * mxfp4_attention_grad takes.  Rows outside of all sequences are left as they were, in both.
- * Products in bf16 on the tensor cores (the probabilities rounded to bf16, relative to 2^8 times a row's
- * largest at most), sums and softmax statistics in fp32.  The same bits on every run. */
+ * rest: NULL, or [q_tokens, q_heads, head_dim] bf16, which receives what rounding left of out (out + rest is the
+ * output to 16 bits): what the gradient is exact with.
+ * Products in bf16 on the tensor cores (the probabilities rounded to bf16), sums and softmax statistics in fp32.
+ * The same bits on every run. */
 mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v, int64_t q_tokens,
                              int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
-                             int64_t seqs, int causal, float scale, const mxfp4_heads* out, float* lse,
-                             mxfp4_stream_t stream);
+                             int64_t seqs, int causal, float scale, const mxfp4_heads* out,
+                             const mxfp4_heads* rest, float* lse, mxfp4_stream_t stream);
 
 /* Workspace bytes of mxfp4_attention_grad: two fp32 statistics of each query. */
 size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
 
 /* Gradients of mxfp4_attention.  The probabilities p = exp(z - lse) are made again:
  *   dv = p^T dout,  dz = p (dout v^T - dout . out),  dq = scale dz k,  dk = scale dz^T q
- * q to scale: as given to it, out and lse as returned by it; dout: the gradient of out, bf16.
+ * q to scale: as given to it, out, rest and lse as returned by it; dout: the gradient of out, bf16.  rest may be NULL:
+ * dout . out then carries out's rounding, and dz of a key that has most of a row's probability is off by it.
  * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences are left as they
  * were.  dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are
  * rounded to bf16 for the tensor cores.  No atomic additions: the same bits on every run.
  * ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
-                                  const mxfp4_heads* out, const float* lse, const mxfp4_heads* dout, int64_t q_tokens,
-                                  int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
-                                  int64_t seqs, int causal, float scale, const mxfp4_heads* dq,
-                                  const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws, size_t ws_bytes,
-                                  mxfp4_stream_t stream);
+                                  const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,
+                                  const mxfp4_heads* dout, int64_t q_tokens, int64_t k_tokens, int64_t head_dim,
+                                  const int32_t* cu_q, const int32_t* cu_k, int64_t seqs, int causal, float scale,
+                                  const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws,
+                                  size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the current device's status word:
  * MXFP4_OK, MXFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last call,

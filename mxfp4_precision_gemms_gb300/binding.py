@@ -138,9 +138,9 @@ def lib():
                 "mxfp4_qk_norm_rope": ([P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P], I),
                 "mxfp4_qk_norm_rope_grad_workspace_bytes": ([I64, I64], S),
                 "mxfp4_qk_norm_rope_grad": ([P, P, P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P, P, P, S, P], I),
-                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P], I),
+                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P], I),
                 "mxfp4_attention_grad_workspace_bytes": ([I64, I64], S),
-                "mxfp4_attention_grad": ([P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
+                "mxfp4_attention_grad": ([P, P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
                 "mxfp4_set_wait_limit_ns": ([ctypes.c_uint64], None),
                 "mxfp4_test_inject_gemm_fault": ([I], None),
@@ -935,17 +935,20 @@ def _attention_operands(q, k, v):
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True, scale: float | None = None,
               cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, seqs: int = 1,
-              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, rest: bool = False, stream=None):
     """mxfp4_attention: softmax attention of q [q_tokens, q_heads, head_dim] over k and v [k_tokens, k_heads, head_dim],
     bf16, scale 1 / sqrt(head_dim) by default.  cu_q, cu_k: int32 [sequences + 1], where each sequence starts (cu_k
     None: as cu_q); None: `seqs` sequences of equal lengths.  Returns (out, lse): out like q, lse fp32
-    [q_heads, q_tokens], which attention_grad takes.  Tokens outside of all sequences: new outputs hold zeros there, given
-    ones are left as they were."""
+    [q_heads, q_tokens], which attention_grad takes.  rest: returns (out, lse, rest), rest like out, what rounding left of
+    it, for exact gradients.  Tokens outside of all sequences: new outputs hold zeros there, given ones are left as they
+    were."""
     cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
     n, heads, dim = shape
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == k_shape[0])
     device = q.device
     out, co = _like(out, shape, OUT_BF16, "out", device, stream, zero=cu_q is not None)
+    if rest:
+        left, cr = _like(None, shape, OUT_BF16, "rest", device, stream, zero=cu_q is not None)
     if lse is None:
         lse = _empty((heads, n), torch.float32, device, stream)
         if cu_q is not None:
@@ -954,18 +957,18 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     elif lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
         raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
     _check(lib().mxfp4_attention(_addressof(cq), _addressof(ck), _addressof(cv), n, k_shape[0], dim, at_q, at_k, seqs,
-                                 int(causal), dim ** -0.5 if scale is None else scale, _addressof(co), lse.data_ptr(),
-                                 _stream(stream)))
-    return out, lse
+                                 int(causal), dim ** -0.5 if scale is None else scale, _addressof(co),
+                                 _addressof(cr) if rest else None, lse.data_ptr(), _stream(stream)))
+    return (out, lse, left) if rest else (out, lse)
 
 
 def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
                    dout: torch.Tensor, causal: bool = True, scale: float | None = None,
                    cu_q: torch.Tensor | None = None, cu_k: torch.Tensor | None = None, seqs: int = 1,
                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
-                   stream=None):
-    """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out and lse
-    as it returned them, the rest as it was given.  dq, dk and dv may be slices of one buffer.  Tokens outside of all
+                   rest: torch.Tensor | None = None, stream=None):
+    """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out, lse
+    and rest as it returned them (without rest the gradients carry out's rounding), the others as it was given.  dq, dk and dv may be slices of one buffer.  Tokens outside of all
     sequences: as in attention."""
     cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
     n, heads, dim = shape
@@ -973,6 +976,7 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     device, zero = q.device, cu_q is not None
     _, co = _like(out, shape, OUT_BF16, "out", device, stream)
     _, cd = _like(dout, shape, OUT_BF16, "dout", device, stream)
+    cr = None if rest is None else _like(rest, shape, OUT_BF16, "rest", device, stream)[1]
     if lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
         raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
     dq, cdq = _like(dq, shape, OUT_BF16, "dq", device, stream, zero)
@@ -981,8 +985,8 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     L = lib()
     nb = L.mxfp4_attention_grad_workspace_bytes(n, heads)
     ws = _empty(nb, torch.uint8, device, stream)
-    _check(L.mxfp4_attention_grad(_addressof(cq), _addressof(ck), _addressof(cv), _addressof(co), lse.data_ptr(),
-                                  _addressof(cd), n, k_shape[0], dim, at_q, at_k, seqs, int(causal),
+    _check(L.mxfp4_attention_grad(_addressof(cq), _addressof(ck), _addressof(cv), _addressof(co),
+                                  _addressof(cr) if cr else None, lse.data_ptr(), _addressof(cd), n, k_shape[0], dim, at_q, at_k, seqs, int(causal),
                                   dim ** -0.5 if scale is None else scale, _addressof(cdq), _addressof(cdk),
                                   _addressof(cdv), ws.data_ptr(), nb, _stream(stream)))
     return dq, dk, dv

@@ -179,8 +179,10 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     for (int b = 0; b < DP / 64; ++b) tma_load_3d(dst + b * kBlockBytes, map, bar, b * 64, head, token);
 }
 
-// This lane's row of an accumulator, times `factor`, to memory as bf16 (dim elements, a multiple of 8).
-__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor, bf16* to, bool inside) {
+// This lane's row of an accumulator, times `factor`, to memory as bf16 (dim elements, a multiple of 8), and what the
+// rounding left, as bf16 again, where it is asked for.
+__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor, bf16* to, bool inside,
+                                          bf16* rest = nullptr) {
     for (int c = 0; c < dim; c += 16) {
         uint32_t v[16], w[8];
         tmem_ld_32x32b_x16(taddr + c, v);
@@ -191,6 +193,14 @@ __device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor,
         if (inside) {
             *reinterpret_cast<uint4*>(to + c) = make_uint4(w[0], w[1], w[2], w[3]);
             if (c + 8 < dim) *reinterpret_cast<uint4*>(to + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            if (rest) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = pack_bf16(fmaf(__uint_as_float(v[2 * j]), factor, -bf16_lo(w[j])),
+                                     fmaf(__uint_as_float(v[2 * j + 1]), factor, -bf16_hi(w[j])));
+                *reinterpret_cast<uint4*>(rest + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (c + 8 < dim) *reinterpret_cast<uint4*>(rest + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
         }
     }
 }
@@ -216,8 +226,8 @@ struct Ring {
 // ------------------------------------------------------------------ forward
 struct ForwardParams {
     CUtensorMap q, k, v;
-    Rows out;
-    float* lse;  // [q_heads][tokens_q]
+    Rows out, rest;  // rest.data NULL: not wanted
+    float* lse;      // [q_heads][tokens_q]
     Sequences seq;
     int32_t q_heads, group, dim, causal;
     float scale_log2;  // scale * log2 e
@@ -479,10 +489,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             ok = ok && warp_wait(&o_full[t], 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
-                store_row(acc, p.dim, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head), inside);
+                store_row(acc, p.dim, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head), inside,
+                          p.rest.data ? p.rest.at(at.q0 + row, head) : nullptr);
             }
         } else if (inside) {  // no key at all
             store_zeros(p.dim, p.out.at(at.q0 + row, head));
+            if (p.rest.data) store_zeros(p.dim, p.rest.at(at.q0 + row, head));
         }
         if (inside)
             p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
@@ -498,10 +510,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
 // ------------------------------------------------------------------ backward
 // What the gradients need of each query: (lse log2 e, do . o).  A query that sees nothing gets an infinite lse, and so
 // probabilities of 0.  HBM-bound: reads o and do once.
+// o is what the forward pass rounded to bf16 and, where it was kept, what that left.  Without the latter do . o is off by
+// 2^-8 of its terms, and so is the dz of a key that has most of a row's probability, where dp - do . o cancels: with scores
+// up to 11, dq and dk of 8192 tokens are off by 5.3e-3 of themselves instead of 2.3e-3 (bf16's own rounding: 1.7e-3).
 struct DeltaParams {
     const bf16* out;
+    const bf16* rest;  // or NULL
     const bf16* dout;
-    int64_t o_token, o_head, d_token, d_head;
+    int64_t o_token, o_head, r_token, r_head, d_token, d_head;
     const float* lse;
     float2* stats;  // [q_heads][tokens_q]
     int32_t tokens, heads, dim;
@@ -522,6 +538,11 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_kernel(const __grid_const
         unpack8(load8(p.dout + t * p.d_token + h * p.d_head + li * 8), b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v = fmaf(a[i], b[i], v);
+        if (p.rest) {
+            unpack8(load8(p.rest + t * p.r_token + h * p.r_head + li * 8), a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v = fmaf(a[i], b[i], v);
+        }
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -1097,7 +1118,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
 
 // ------------------------------------------------------------------ host
 struct Call {
-    Heads q, k, v, out;
+    Heads q, k, v, out, rest;
     int64_t tokens_q, tokens_k;
     Sequences seq;
     int32_t dim, group;
@@ -1152,6 +1173,16 @@ mxfp4_status check_call(const char* what, const mxfp4_heads* q, const mxfp4_head
     return MXFP4_OK;
 }
 
+// out, and the rest of its rounding, which may be NULL.
+mxfp4_status check_output(const char* what, const mxfp4_heads* out, const mxfp4_heads* rest, bool written, Call* c) {
+    mxfp4_status st = check_operand(what, "out", out, c->tokens_q, c->dim, written, &c->out);
+    if (!st && rest) st = check_operand(what, "rest", rest, c->tokens_q, c->dim, written, &c->rest);
+    if (st) return st;
+    if (c->out.heads != c->q.heads || (rest && c->rest.heads != c->q.heads))
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: out or rest has other heads than q", what);
+    return MXFP4_OK;
+}
+
 // Places of tiles of `rows` tokens: no fewer than there are tiles.
 int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
     if (c.seq.cu_q) return tokens / rows + c.seq.count;
@@ -1186,13 +1217,13 @@ using namespace mx;
 extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                         int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
                                         const int32_t* cu_k, int64_t seqs, int causal, float scale,
-                                        const mxfp4_heads* out, float* lse, mxfp4_stream_t stream) {
+                                        const mxfp4_heads* out, const mxfp4_heads* rest, float* lse,
+                                        mxfp4_stream_t stream) {
     const char* what = "attention";
     Call c{};
     mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
     if (st) return st;
-    if ((st = check_operand(what, "out", out, q_tokens, head_dim, true, &c.out))) return st;
-    if (c.out.heads != c.q.heads) return record_error(MXFP4_ERR_INVALID_ARG, "%s: out has other heads than q", what);
+    if ((st = check_output(what, out, rest, true, &c))) return st;
     if (q_tokens == 0 || seqs == 0) return record_error(MXFP4_OK, "%s", "");
     if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
     if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
@@ -1202,6 +1233,7 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
         !map_of(&p.v, c.v, k_tokens, head_dim))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     p.out = rows_of(c.out);
+    p.rest = rows_of(c.rest);
     p.lse = lse;
     p.seq = c.seq;
     p.q_heads = c.q.heads;
@@ -1227,8 +1259,8 @@ extern "C" size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t
 }
 
 extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
-                                             const mxfp4_heads* out, const float* lse, const mxfp4_heads* dout,
-                                             int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
+                                             const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,
+                                             const mxfp4_heads* dout, int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
                                              const int32_t* cu_k, int64_t seqs, int causal, float scale,
                                              const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv,
                                              void* ws, size_t ws_bytes, mxfp4_stream_t stream) {
@@ -1237,14 +1269,14 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
     if (st) return st;
     Heads d{}, gq{}, gk{}, gv{};
-    if ((st = check_operand(what, "out", out, q_tokens, head_dim, false, &c.out))) return st;
+    if ((st = check_output(what, out, rest, false, &c))) return st;
     if ((st = check_operand(what, "dout", dout, q_tokens, head_dim, false, &d))) return st;
     if ((st = check_operand(what, "dq", dq, q_tokens, head_dim, true, &gq))) return st;
     if ((st = check_operand(what, "dk", dk, k_tokens, head_dim, true, &gk))) return st;
     if ((st = check_operand(what, "dv", dv, k_tokens, head_dim, true, &gv))) return st;
-    if (c.out.heads != c.q.heads || d.heads != c.q.heads || gq.heads != c.q.heads || gk.heads != c.k.heads ||
+    if (d.heads != c.q.heads || gq.heads != c.q.heads || gk.heads != c.k.heads ||
         gv.heads != c.k.heads)
-        return record_error(MXFP4_ERR_INVALID_ARG, "%s: out, dout or a gradient has other heads than its input", what);
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: dout or a gradient has other heads than its input", what);
     if (q_tokens > 0) {
         if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
         if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
@@ -1277,8 +1309,9 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (q_tokens > 0) {
-        DeltaParams t{static_cast<const bf16*>(c.out.data), static_cast<const bf16*>(d.data), c.out.token_stride,
-                      c.out.head_stride, d.token_stride, d.head_stride, lse, static_cast<float2*>(ws), (int32_t)q_tokens,
+        DeltaParams t{static_cast<const bf16*>(c.out.data), static_cast<const bf16*>(c.rest.data),
+                      static_cast<const bf16*>(d.data), c.out.token_stride, c.out.head_stride, c.rest.token_stride,
+                      c.rest.head_stride, d.token_stride, d.head_stride, lse, static_cast<float2*>(ws), (int32_t)q_tokens,
                       c.q.heads, c.dim};
         const int64_t rows = q_tokens * c.q.heads, per = kDeltaThreads / 16;
         e = launch_overlapped(delta_kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(kDeltaThreads), 0, s, 1, true, t);

@@ -65,9 +65,9 @@ def turn_size(x, angle, interleaved):
 
 
 # ------------------------------------------------------------------ attention
-def attend(q, k, v, q_lens, k_lens, causal, scale, dout=None):
+def attend(q, k, v, q_lens, k_lens, causal, scale, dout=None, kept=True):
     """Values and tolerances, as dicts of the same keys: out, lse and, with dout, dq, dk, dv; rows outside of all sequences
-    hold zeros."""
+    hold zeros.  kept: the gradients get the output with the rest of its rounding."""
     a, b, D = q.shape[1], k.shape[1], q.shape[2]
     dev = q.device
     Q, K, V = q.to(F64), k.to(F64), v.to(F64)
@@ -75,6 +75,7 @@ def attend(q, k, v, q_lens, k_lens, causal, scale, dout=None):
     if dout is not None:
         want |= {"dq": torch.zeros_like(Q), "dk": torch.zeros_like(K), "dv": torch.zeros_like(V)}
     tol = {n: torch.zeros_like(x) for n, x in want.items()}
+    tol["whole"] = torch.zeros_like(Q)  # of out + rest
     q0 = k0 = 0
     for n, m in zip(q_lens, k_lens):
         rows, cols = slice(q0, q0 + n), slice(k0, k0 + m)
@@ -97,8 +98,10 @@ def attend(q, k, v, q_lens, k_lens, causal, scale, dout=None):
             rel = torch.where(see, dz, torch.zeros_like(dz)).amax(1, keepdim=True) if m else dz.sum(1, keepdim=True)
             # p: rounded to bf16, its own error and that of the sum that it is divided by; the sum over the keys
             ep = U_BF16 + 2 * rel + m * TRUNC
-            to = U_BF16 * o.abs() + ep * (1 + U_BF16) * (p @ w.abs())
-            tol["out"][rows, h] = to
+            before = ep * (p @ w.abs())  # rounding
+            whole = U_BF16 ** 2 * (o.abs() + before) + before
+            tol["whole"][rows, h] = whole
+            tol["out"][rows, h] = U_BF16 * o.abs() + (1 + U_BF16) * before
             tol["lse"][h, rows] = (rel[:, 0] + m * U_F32 + 8 * U_F32 * (1 + lse.abs())).nan_to_num(posinf=0.0)
             if dout is None:
                 continue
@@ -110,7 +113,7 @@ def attend(q, k, v, q_lens, k_lens, causal, scale, dout=None):
             want["dk"][cols, g] += scale * ds.T @ x
             want["dv"][cols, g] += p.T @ do
             # dz: rounded to bf16; p's error in it; that of dp and of delta, which the rounded output makes
-            edelta = (do.abs() * to).sum(1, keepdim=True) + D * U_F32 * (do.abs() * o.abs()).sum(1, keepdim=True)
+            edelta = (do.abs() * (whole if kept else tol["out"][rows, h])).sum(1, keepdim=True) + D * U_F32 * (do.abs() * o.abs()).sum(1, keepdim=True)
             eds = (U_BF16 + 2 * rel + m * TRUNC) * ds.abs() + (1 + U_BF16) * p * (
                 D * TRUNC * (do.abs() @ w.abs().T) + edelta + 4 * U_F32 * (dp.abs() + delta.abs()))
             tol["dq"][rows, h] = scale * (eds + m * TRUNC * ds.abs()) @ y.abs()

@@ -30,7 +30,7 @@ def _edges(torch, lens):
     return torch.tensor([0, *itertools.accumulate(lens)], dtype=torch.int32, device="cuda")
 
 
-def _check(torch, q, k, v, do, q_lens, k_lens, causal, scale=None, listed=True):
+def _check(torch, q, k, v, do, q_lens, k_lens, causal, scale=None, listed=True, kept=True):
     from mxfp4_precision_gemms_gb300 import binding as mx
     from tests.attention_reference import assert_close, attend
 
@@ -39,10 +39,11 @@ def _check(torch, q, k, v, do, q_lens, k_lens, causal, scale=None, listed=True):
         kw |= dict(cu_q=_edges(torch, q_lens), cu_k=_edges(torch, k_lens))
     else:
         kw |= dict(seqs=len(q_lens))
-    out, lse = mx.attention(q, k, v, **kw)
-    grads = mx.attention_grad(q, k, v, out, lse, do, **kw)
+    out, lse, rest = mx.attention(q, k, v, **kw, rest=True)
+    grads = mx.attention_grad(q, k, v, out, lse, do, **kw, rest=rest if kept else None)
     assert mx.device_status() == 0
-    want, tol = attend(q, k, v, q_lens, k_lens, causal, scale or q.shape[2] ** -0.5, do)
+    want, tol = attend(q, k, v, q_lens, k_lens, causal, scale or q.shape[2] ** -0.5, do, kept)
+    assert_close(out.double() + rest.double(), want["out"], tol["whole"], "out + rest")
     for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
         assert_close(got, want[name], tol[name], name)
     return (out, lse, *grads)
@@ -56,6 +57,12 @@ def test_lengths(lens, D, causal):
     q_lens, k_lens = lens
     q, k, v, do = _inputs(torch, q_lens, k_lens, 4, 2, D, 3, 1)
     _check(torch, q, k, v, do, q_lens, k_lens, causal)
+
+
+def test_gradients_without_the_rest_of_the_output():
+    torch = gpu_ready()
+    q, k, v, do = _inputs(torch, [300], [300], 4, 2, 128, 0, 6, lean=2.0)
+    _check(torch, q, k, v, do, [300], [300], True, kept=False)
 
 
 @pytest.mark.parametrize("D", [8, 16, 24, 40, 72, 80, 96, 120])

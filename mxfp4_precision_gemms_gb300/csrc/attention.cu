@@ -25,6 +25,7 @@
 
 #include "element.cuh"
 #include "heads.cuh"
+#include "quant_math.cuh"
 
 namespace mx {
 namespace {
@@ -45,22 +46,27 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+// Shared-memory descriptors as their low words (address, and bytes between 64-column blocks): the high word, 1024 bytes
+// between groups of eight rows and the 128-byte swizzle, is the same for all.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
 // D (+)= A B^T with bf16 operands in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 // The same with A in tensor memory: row m in lane m, two bf16 in each column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -81,10 +87,33 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Barriers of a part of the block (id 0 is __syncthreads).
+__device__ __forceinline__ void sync_some(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool any_of_some(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.b32 a, %1, 0;\n\t"
+        "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
+        "selp.b32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
 // wait_bounded for a whole warp: what all lanes agree on.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, uint32_t* status) {
     return __all_sync(0xffffffffu, wait_bounded(bar, parity, limit_ns, status));
 }
+
+// The first lane's value, which the compiler then knows to be the warp's.  The lane that feeds the tensor cores has 64
+// cycles for each instruction, and took 140 where its operands were not known to be the warp's: 8192 tokens of 32 heads
+// of 128, not causal, forward 1044 us.  With the low words of descriptors made once a tile 836, with elect.sync for the
+// choice of the lane 735, with these 680.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // ------------------------------------------------------------------ sequences
 struct Sequences {
@@ -149,17 +178,25 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
     return p;
 }
 
+__device__ __forceinline__ Place place_of(const Place* p) {
+    return {uniform(p->q0), uniform(p->k0), uniform(p->len_q), uniform(p->len_k), uniform(p->tile)};
+}
+
 // ------------------------------------------------------------------ shared pieces
-// K runs along the tile's columns (16 a step).
-__device__ __forceinline__ uint64_t along_columns(uint32_t tile, int step) {
-    return smem_desc(tile + (step >> 2) * kBlockBytes + (step & 3) * 32, 16, 1024, kSwizzle128B);
+// Low words of a tile's descriptors.  K along its columns: 16 columns a step.
+__device__ __forceinline__ uint32_t columns_of(uint32_t tile) { return (tile & 0x3FFFFu) >> 4 | 1u << 16; }
+__host__ __device__ constexpr uint32_t column_step(int k) { return (k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2; }
+// K along its rows: 16 rows a step, N along the columns.
+__device__ __forceinline__ uint32_t rows_of_tile(uint32_t tile) {
+    return (tile & 0x3FFFFu) >> 4 | (uint32_t)(kBlockBytes >> 4) << 16;
 }
-// K runs along the tile's rows (16 a step), N along its columns.
-__device__ __forceinline__ uint64_t along_rows(uint32_t tile, int step) {
-    return smem_desc(tile + step * 2048, kBlockBytes, 1024, kSwizzle128B);
+constexpr uint32_t kRowStep = 2048 >> 4;
+// Tensor-memory column of step `step` (16 columns) of p or dz, which is kept in the place of the scores: each warp's
+// COLUMNS scores become COLUMNS / 2 columns at their beginning.
+template <int COLUMNS>
+__device__ __forceinline__ uint32_t packed_column(int step) {
+    return step * 16 / COLUMNS * COLUMNS + step * 16 % COLUMNS / 2;
 }
-// Tensor-memory column of step `step` of p or dz, which each half of the columns keeps in its own half of the scores'.
-__device__ __forceinline__ uint32_t half_column(int step) { return (step >> 2) * 64 + (step & 3) * 8; }
 
 // Clears rows [from, 128) of a tile, by one warp.
 template <int DP>
@@ -243,11 +280,12 @@ struct ForwardShape {
     static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
     static constexpr int kBars = 2 + 2 * kStages + 2 + 2 + 2 + 1;
     static constexpr int kOffPlace = kOffBar + kBars * 8;
-    static constexpr int kSmem = kOffPlace + 32;
+    static constexpr int kOffShare = kOffPlace + 32;
+    static constexpr int kSmem = kOffShare + 2 * 2 * kRows * 4;
 };
 static_assert(ForwardShape<128>::kSmem <= 227 * 1024, "shared memory budget");
 static_assert(2 * ForwardShape<64>::kSmem > 228 * 1024, "one CTA per SM: CTAs do not wait for each other's TMEM");
-constexpr int kForwardThreads = 64 + 256;
+constexpr int kForwardThreads = 128 + 512;
 constexpr float kLag = 8.f;  // log2 of how far a row's sum may run ahead of the maximum that it is scaled by
 
 template <int DP>
@@ -269,14 +307,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     uint64_t* mma_done = o_full + 2;
     Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
+    float* share = reinterpret_cast<float*>(smem + Shape::kOffShare);  // [tile][half][row]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.q_heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.q_heads);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
             mbar_init(&o_full[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
@@ -302,8 +341,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
-    Place at = *where;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)*tmem_holder);
+    Place at = place_of(where);
     const bool work = at.tile >= 0;
     // the tiles that see the most keys first
     if (work && p.causal) at.tile = (at.len_q + 2 * kRows - 1) / (2 * kRows) - 1 - at.tile;
@@ -354,11 +393,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             if (ok) ok = warp_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, p.wait_ns, p.status);
         };
         auto make_scores = [&](int t, int j) {
-            const uint32_t a = smem_u32(smem + t * Shape::kTileBytes);
-            const uint32_t b = smem_u32(ring + (2 * j) % kStages * Shape::kTileBytes);
-            if (lane == 0) {
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + t * 128, along_columns(a, k), along_columns(b, k), scores, k != 0);
+            const uint32_t a = columns_of(smem_u32(smem + t * Shape::kTileBytes));
+            const uint32_t b = columns_of(smem_u32(ring + (2 * j) % kStages * Shape::kTileBytes));
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) mma_ss(tmem + t * 128, a + column_step(k), b + column_step(k), scores, k != 0);
                 tc_commit(&s_full[t]);
             }
         };
@@ -371,7 +411,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                     tc_fence_after();
                     if (ok) make_scores(t, 0);
                 }
-            if (ok && lane == 0) tc_commit(&empty[0]);
+            if (ok && elect_one()) tc_commit(&empty[0]);
         }
         for (int j = 0; ok && j < most; ++j) {
             const int sv = (2 * j + 1) % kStages;
@@ -390,70 +430,79 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                 ok = warp_wait(&p_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
                 if (!ok) continue;
                 tc_fence_after();
-                const uint32_t b = smem_u32(ring + sv * Shape::kTileBytes);
-                if (lane == 0) {
+                const uint32_t b = rows_of_tile(smem_u32(ring + sv * Shape::kTileBytes));
+                if (elect_one()) {
+#pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, along_rows(b, k), output, j != 0 || k != 0);
+                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + packed_column<64>(k), b + k * kRowStep, output,
+                               j != 0 || k != 0);
                     if (j + 1 == n[t]) tc_commit(&o_full[t]);
                 }
                 // after p v in the pipe, so the scores may take the place of p
                 if (j + 1 < n[t]) make_scores(t, j + 1);
             }
-            if (ok && lane == 0) {
+            if (ok && elect_one()) {
                 tc_commit(&empty[sv]);
                 if (j + 1 < most) tc_commit(&empty[(2 * j + 2) % kStages]);
             }
         }
-        if (lane == 0) tc_commit(mma_done);
+        if (elect_one()) tc_commit(mma_done);
         warp_wait(mma_done, 0, p.wait_ns, p.status);
-    } else {
-        // ---------------- softmax: a warpgroup for each query tile, a thread for each query
-        const int t = (warp - 2) >> 2, quad = warp & 3;
+    } else if (warp >= 4) {
+        // ---------------- softmax: a lane for each query, a warpgroup for each half of the keys of each query tile
+        const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
         const int32_t row = row0 + t * kRows + quad * 32 + lane;
         const bool inside = work && row < at.len_q;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t src = lanes + t * 128, acc = lanes + 256 + t * 128;
+        const uint32_t src = lanes + t * 128 + half * 64, acc = lanes + 256 + t * 128;
+        float* mine = share + (t * 2 + half) * kRows + quad * 32 + lane;
+        const float* other = share + (t * 2 + 1 - half) * kRows + quad * 32 + lane;
         const int columns = (p.dim + 15) / 16 * 16;
         const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
         // the least of these in the tile: its first query's
         const int32_t least = p.causal ? min(at.len_k - 1, row0 + t * kRows + ahead) : at.len_k - 1;
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         float top = -INFINITY;  // maximum that the sums are scaled by (of the scores before `scale`)
         float shift = 0.f;      // top * scale_log2
-        float sum = 0.f;
+        float2 sum2 = make_float2(0.f, 0.f);
         bool ok = true;
         for (int j = 0; j < n[t]; ++j) {
             ok = warp_wait(&s_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
-            if (!ok) break;
             tc_fence_after();
-            uint32_t z[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(src + c * 32, z[c]);
+            uint32_t z[64];
+            tmem_ld_32x32b_x32(src, *reinterpret_cast<uint32_t(*)[32]>(z));
+            tmem_ld_32x32b_x32(src + 32, *reinterpret_cast<uint32_t(*)[32]>(z + 32));
             tmem_ld_wait();
             if (least - j * kRows < kRows - 1) {
-                const int seen = last - j * kRows;
+                const int seen = last - j * kRows - half * 64;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c * 32 + i > seen) z[c][i] = 0xff800000u;
+                for (int i = 0; i < 64; ++i)
+                    if (i > seen) z[i] = 0xff800000u;
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[c][i]));
-            const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[i]));
+            float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             // A new maximum is taken up only once the old one lags by kLag: p then stays below 2^kLag, which bf16 and
-            // the fp32 sums hold as exactly as values below 1, and the output is seldom scaled again.
-            const bool raise = j == 0 || (m - top) * p.scale_log2 > kLag;
-            if (__any_sync(0xffffffffu, raise)) {
+            // the fp32 sums hold as exactly as values below 1, and the output is seldom scaled again.  A timeout
+            // travels with the vote, so that both halves leave together.
+            if (any_of_some(1 + t, 256, !ok || j == 0 || (m - top) * p.scale_log2 > kLag)) {
+                *mine = ok ? m : NAN;
+                sync_some(1 + t, 256);
+                const float theirs = *other;
+                if (any_of_some(1 + t, 256, !ok)) {
+                    ok = false;
+                    break;
+                }
+                m = fmaxf(m, theirs);
+                const bool raise = j == 0 || (m - top) * p.scale_log2 > kLag;
                 const float new_top = raise ? fmaxf(top, m) : top;
                 const float new_shift = new_top == -INFINITY ? 0.f : new_top * p.scale_log2;
                 if (j > 0) {
                     // the scores' commit came after that of p v: the output holds all tiles before this one
                     const float by = !raise ? 1.f : top == -INFINITY ? 0.f : exp2_approx(shift - new_shift);
-                    sum *= by;
-                    for (int c = 0; c < columns; c += 16) {
+                    sum2 = f2_mul(sum2, make_float2(by, by));
+                    for (int c = half * 16; c < columns; c += 32) {
                         uint32_t v[16];
                         tmem_ld_32x32b_x16(acc + c, v);
                         tmem_ld_wait();
@@ -465,38 +514,44 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                 top = new_top;
                 shift = new_shift;
             }
-            float s4[4] = {};
+            const float2 shift2 = make_float2(-shift, -shift);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float a = exp2_approx(fmaf(__uint_as_float(z[c][2 * i]), p.scale_log2, -shift));
-                    const float b = exp2_approx(fmaf(__uint_as_float(z[c][2 * i + 1]), p.scale_log2, -shift));
-                    s4[(2 * i) & 3] += a;
-                    s4[(2 * i + 1) & 3] += b;
-                    w[i] = pack_bf16(a, b);
+                    const int at_z = c * 32 + 2 * i;
+                    const float2 e = f2_fma(make_float2(__uint_as_float(z[at_z]), __uint_as_float(z[at_z + 1])), scale2, shift2);
+                    const float2 x = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    sum2 = f2_add(sum2, x);
+                    w[i] = pack_bf16(x.x, x.y);
                 }
                 tmem_st_32x32b_x16(src + c * 16, w);
             }
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[t]);
         }
-        if (work && n[t] > 0) {
-            ok = ok && warp_wait(&o_full[t], 0, p.wait_ns, p.status);
+        // the halves' sums, in their order
+        float sum = sum2.x + sum2.y;
+        if (ok && n[t] > 0) {
+            *mine = sum;
+            sync_some(1 + t, 256);
+            sum = half ? *other + sum : sum + *other;
+            ok = warp_wait(&o_full[t], 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
-                store_row(acc, p.dim, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head), inside,
-                          p.rest.data ? p.rest.at(at.q0 + row, head) : nullptr);
+                const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0;
+                store_row(acc + from, half ? p.dim - cut : min(cut, p.dim), sum == 0.f ? 0.f : 1.f / sum,
+                          p.out.at(at.q0 + row, head) + from, inside,
+                          p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
             }
-        } else if (inside) {  // no key at all
+        } else if (inside && half == 0 && n[t] == 0) {  // no key at all
             store_zeros(p.dim, p.out.at(at.q0 + row, head));
             if (p.rest.data) store_zeros(p.dim, p.rest.at(at.q0 + row, head));
         }
-        if (inside)
+        if (inside && half == 0)
             p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
     }
     tc_fence_before();
@@ -583,7 +638,7 @@ static_assert(BackwardShape<128>::kSmem <= 227 * 1024, "shared memory budget");
 // Keys' gradients.  The products of block b (128 keys x 128 queries) in the order in which they are issued:
 //   z(b)^T = k q^T | dv += p(b)^T do, z(b+1)^T | dk += dz(b)^T q, dp(b+1)^T = v do^T | ...
 // While p is made from z, the tensor cores run dk and dp; while dz is made from dp, dv and the next z.
-constexpr int kDkvThreads = 96 + 256;
+constexpr int kDkvThreads = 128 + 512;
 
 template <int DP>
 __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __grid_constant__ BackwardParams p) {
@@ -599,7 +654,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     uint8_t* sV = smem + Shape::kTileBytes;
     uint8_t* sQ = smem + Shape::kOffFirst;
     uint8_t* sD = smem + Shape::kOffSecond;
-    float4* stats = reinterpret_cast<float4*>(smem + Shape::kOffStats);  // [2][64]: two queries each
+    float* stats = reinterpret_cast<float*>(smem + Shape::kOffStats);  // [2][lse, delta][128]
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar);  // [2]
     uint64_t* q_full = kv_full + 2;
     uint64_t* q_empty = q_full + Shape::kFirst;
@@ -615,13 +670,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&stats_full[i], 32);
-            mbar_init(&stats_empty[i], 8);
+            mbar_init(&stats_empty[i], 16);
         }
         for (int i = 0; i < Shape::kFirst; ++i) {
             mbar_init(&q_full[i], 1);
@@ -632,9 +687,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             mbar_init(&d_empty[i], 1);
         }
         mbar_init(z_full, 1);
-        mbar_init(p_full, 8);
+        mbar_init(p_full, 16);
         mbar_init(dp_full, 1);
-        mbar_init(dz_full, 8);
+        mbar_init(dz_full, 16);
         mbar_init(done, 1);
         fence_mbar_init();
         prefetch_tmap(&p.q);
@@ -655,8 +710,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
-    const Place at = *where;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)*tmem_holder);
+    const Place at = place_of(where);
     const bool work = at.tile >= 0;
     const int32_t key0 = at.tile * kRows, ahead = at.len_k - at.len_q;
     // query tiles that see these keys: from the one with the first query that sees the first key
@@ -696,7 +751,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         const uint32_t scores = idesc_bf16(kRows, kRows, 0, 0);
         const uint32_t sums = idesc_bf16(kRows, (uint32_t)(p.dim + 15) / 16 * 16, 0, 1);
         const int steps = (p.dim + 15) / 16;
-        const uint32_t k_tile = smem_u32(sK), v_tile = smem_u32(sV);
+        const uint32_t k_tile = columns_of(smem_u32(sK)), v_tile = columns_of(smem_u32(sV));
         bool ok = true;
         // waits for a streamed tile; rows behind the sequence are cleared, as they are summed over
         auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int b) {
@@ -713,20 +768,22 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         auto make_z = [&](int b) {
             uint8_t* tile = sQ + Q::stage(b) * Shape::kTileBytes;
             ready(&q_full[Q::stage(b)], Q::parity(b), tile, b);
-            if (ok && lane == 0) {
-                const uint32_t q_tile = smem_u32(tile);
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + kZ, along_columns(k_tile, k), along_columns(q_tile, k), scores, k != 0);
+            if (ok && elect_one()) {
+                const uint32_t q_tile = columns_of(smem_u32(tile));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) mma_ss(tmem + kZ, k_tile + column_step(k), q_tile + column_step(k), scores, k != 0);
                 tc_commit(z_full);
             }
         };
         auto make_dp = [&](int b) {
             uint8_t* tile = sD + D::stage(b) * Shape::kTileBytes;
             ready(&d_full[D::stage(b)], D::parity(b), tile, b);
-            if (ok && lane == 0) {
-                const uint32_t d_tile = smem_u32(tile);
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + kDp, along_columns(v_tile, k), along_columns(d_tile, k), scores, k != 0);
+            if (ok && elect_one()) {
+                const uint32_t d_tile = columns_of(smem_u32(tile));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) mma_ss(tmem + kDp, v_tile + column_step(k), d_tile + column_step(k), scores, k != 0);
                 tc_commit(dp_full);
             }
         };
@@ -740,29 +797,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             ok = warp_wait(p_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t d_tile = smem_u32(sD + D::stage(b) * Shape::kTileBytes);
+            if (elect_one()) {
+                const uint32_t d_tile = rows_of_tile(smem_u32(sD + D::stage(b) * Shape::kTileBytes));
+#pragma unroll
                 for (int k = 0; k < kRows / 16; ++k)
-                    mma_ts(tmem + kDv, tmem + kZ + half_column(k), along_rows(d_tile, k), sums, b != 0 || k != 0);
+                    mma_ts(tmem + kDv, tmem + kZ + packed_column<32>(k), d_tile + k * kRowStep, sums, b != 0 || k != 0);
                 tc_commit(&d_empty[D::stage(b)]);  // dp(b) came before
             }
             if (b + 1 < blocks) make_z(b + 1);
             ok = ok && warp_wait(dz_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t q_tile = smem_u32(sQ + Q::stage(b) * Shape::kTileBytes);
+            if (elect_one()) {
+                const uint32_t q_tile = rows_of_tile(smem_u32(sQ + Q::stage(b) * Shape::kTileBytes));
+#pragma unroll
                 for (int k = 0; k < kRows / 16; ++k)
-                    mma_ts(tmem + kDk, tmem + kDp + half_column(k), along_rows(q_tile, k), sums, b != 0 || k != 0);
+                    mma_ts(tmem + kDk, tmem + kDp + packed_column<32>(k), q_tile + k * kRowStep, sums, b != 0 || k != 0);
                 tc_commit(&q_empty[Q::stage(b)]);
             }
             if (b + 1 < blocks) make_dp(b + 1);
         }
-        if (lane == 0) tc_commit(done);
+        if (elect_one()) tc_commit(done);
         warp_wait(done, 0, p.wait_ns, p.status);
     } else if (warp == 2) {
         // ---------------- the queries' statistics
-        float2* to = reinterpret_cast<float2*>(stats);
         for (int b = 0; b < blocks; ++b) {
             const int s = b & 1;
             if (b >= 2 && !warp_wait(&stats_empty[s], (uint32_t)(b / 2 - 1) & 1u, p.wait_ns, p.status)) break;
@@ -771,16 +829,19 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
 #pragma unroll
             for (int i = 0; i < kRows / 32; ++i) {
                 const int r = i * 32 + lane;
-                to[s * kRows + r] = q + r < at.len_q ? from[q + r] : make_float2(INFINITY, 0.f);
+                const float2 v = q + r < at.len_q ? from[q + r] : make_float2(INFINITY, 0.f);
+                stats[s * 2 * kRows + r] = v.x;
+                stats[s * 2 * kRows + kRows + r] = v.y;
             }
             mbar_arrive(&stats_full[s]);
         }
-    } else {
-        // ---------------- p and dz: a lane for each key, a warpgroup for each half of the queries
-        const int half = (warp - 3) >> 2, quad = warp & 3;
+    } else if (warp >= 4) {
+        // ---------------- p and dz: a lane for each key, a warpgroup for each quarter of the queries
+        const int part = (warp - 4) >> 2, quad = warp & 3;
         const int32_t key = key0 + quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t z_at = lanes + kZ + half * 64, dp_at = lanes + kDp + half * 64;
+        const uint32_t z_at = lanes + kZ + part * 32, dp_at = lanes + kDp + part * 32;
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (int b = 0; b < blocks; ++b) {
             const int s = b & 1;
@@ -788,34 +849,37 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
                  warp_wait(z_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            const float4* st = stats + s * 64 + half * 32;
-            float pr[64];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            const float4* lse = reinterpret_cast<const float4*>(stats + s * 2 * kRows + part * 32);
+            const float4* delta = lse + kRows / 4;
+            float2 pr[16];
+            {
                 uint32_t z[32];
-                tmem_ld_32x32b_x32(z_at + c * 32, z);
+                tmem_ld_32x32b_x32(z_at, z);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float4 l = st[c * 16 + i];
-                    pr[c * 32 + 2 * i] = exp2_approx(fmaf(__uint_as_float(z[2 * i]), p.scale_log2, -l.x));
-                    pr[c * 32 + 2 * i + 1] = exp2_approx(fmaf(__uint_as_float(z[2 * i + 1]), p.scale_log2, -l.z));
+                for (int i = 0; i < 8; ++i) {
+                    const float4 l = lse[i];
+                    const float2 e = f2_fma(make_float2(__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1])), scale2,
+                                            make_float2(-l.x, -l.y));
+                    const float2 f = f2_fma(make_float2(__uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])), scale2,
+                                            make_float2(-l.z, -l.w));
+                    pr[2 * i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    pr[2 * i + 1] = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                 }
             }
             const int32_t q = (first + b % tiles) * kRows;
             if (p.causal && q + ahead < key0 + kRows - 1) {  // queries below key - ahead do not see the key
-                const int hidden = key - ahead - q - half * 64;
+                const int hidden = key - ahead - q - part * 32;
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i < hidden) pr[i] = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    if (2 * i < hidden) pr[i].x = 0.f;
+                    if (2 * i + 1 < hidden) pr[i].y = 0.f;
+                }
             }
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = pack_bf16(pr[c * 32 + 2 * i], pr[c * 32 + 2 * i + 1]);
-                tmem_st_32x32b_x16(z_at + c * 16, w);
-            }
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(pr[i].x, pr[i].y);
+            tmem_st_32x32b_x16(z_at, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -823,21 +887,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             ok = warp_wait(dp_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            uint32_t dp[2][32];
-            tmem_ld_32x32b_x32(dp_at, dp[0]);
-            tmem_ld_32x32b_x32(dp_at + 32, dp[1]);
+            uint32_t dp[32];
+            tmem_ld_32x32b_x32(dp_at, dp);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float4 l = st[c * 16 + i];
-                    w[i] = pack_bf16(pr[c * 32 + 2 * i] * (__uint_as_float(dp[c][2 * i]) - l.y),
-                                     pr[c * 32 + 2 * i + 1] * (__uint_as_float(dp[c][2 * i + 1]) - l.w));
-                }
-                tmem_st_32x32b_x16(dp_at + c * 16, w);
+            for (int i = 0; i < 8; ++i) {
+                const float4 l = delta[i];
+                const float2 e = f2_mul(pr[2 * i], f2_sub(make_float2(__uint_as_float(dp[4 * i]), __uint_as_float(dp[4 * i + 1])),
+                                                          make_float2(l.x, l.y)));
+                const float2 f = f2_mul(pr[2 * i + 1], f2_sub(make_float2(__uint_as_float(dp[4 * i + 2]), __uint_as_float(dp[4 * i + 3])),
+                                                              make_float2(l.z, l.w)));
+                w[2 * i] = pack_bf16(e.x, e.y);
+                w[2 * i + 1] = pack_bf16(f.x, f.y);
             }
+            tmem_st_32x32b_x16(dp_at, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -846,16 +909,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
                 mbar_arrive(&stats_empty[s]);
             }
         }
-        const Rows& rows = half ? p.dk : p.dv;
+        // two warpgroups for dv, two for dk, each half of the columns
+        const bool keys = part >= 2;
+        const Rows& rows = keys ? p.dk : p.dv;
         const bool inside = work && key < at.len_k;
         bf16* to = rows.at(at.k0 + key, head);
+        const int cut = (p.dim / 2 + 15) / 16 * 16, from = part & 1 ? cut : 0;
         if (blocks > 0) {
             ok = ok && warp_wait(done, 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
-                store_row(lanes + (half ? kDk : kDv), p.dim, half ? p.scale : 1.f, to, inside);
+                store_row(lanes + (keys ? kDk : kDv) + from, part & 1 ? p.dim - cut : min(cut, p.dim), keys ? p.scale : 1.f,
+                          to + from, inside);
             }
-        } else if (inside) {
+        } else if (inside && (part & 1) == 0) {
             store_zeros(p.dim, to);
         }
     }
@@ -869,7 +936,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
 
 // Queries' gradients.  z and dp of the next block are made while dz of this one is; z has two places, and dz takes its own
 // block's, so that dp is free again as soon as it has been read.
-constexpr int kDqThreads = 64 + 256;
+constexpr int kDqThreads = 128 + 512;
 
 template <int DP>
 __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __grid_constant__ BackwardParams p) {
@@ -898,7 +965,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -914,8 +981,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
             mbar_init(&v_empty[i], 1);
         }
         mbar_init(dp_full, 1);
-        mbar_init(dp_read, 8);
-        mbar_init(dz_full, 8);
+        mbar_init(dp_read, 16);
+        mbar_init(dz_full, 16);
         mbar_init(done, 1);
         fence_mbar_init();
         prefetch_tmap(&p.q);
@@ -936,8 +1003,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
-    Place at = *where;
+    const uint32_t tmem = (uint32_t)uniform((int32_t)*tmem_holder);
+    Place at = place_of(where);
     const bool work = at.tile >= 0;
     if (work && p.causal) at.tile = (at.len_q + kRows - 1) / kRows - 1 - at.tile;  // those that see the most keys first
     const int32_t row0 = at.tile * kRows, ahead = at.len_k - at.len_q;
@@ -978,7 +1045,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         const uint32_t scores = idesc_bf16(kRows, kRows, 0, 0);
         const uint32_t sums = idesc_bf16(kRows, (uint32_t)(p.dim + 15) / 16 * 16, 0, 1);
         const int steps = (p.dim + 15) / 16;
-        const uint32_t q_tile = smem_u32(sQ), d_tile = smem_u32(sD);
+        const uint32_t q_tile = columns_of(smem_u32(sQ)), d_tile = columns_of(smem_u32(sD));
         bool ok = true;
         auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int b) {
             ok = ok && warp_wait(bar, parity, p.wait_ns, p.status);
@@ -994,20 +1061,22 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         auto make_z = [&](int b) {
             uint8_t* tile = sK + K::stage(b) * Shape::kTileBytes;
             ready(&k_full[K::stage(b)], K::parity(b), tile, b);
-            if (ok && lane == 0) {
-                const uint32_t k_tile = smem_u32(tile);
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + kZ + (b & 1) * 128, along_columns(q_tile, k), along_columns(k_tile, k), scores, k != 0);
+            if (ok && elect_one()) {
+                const uint32_t k_tile = columns_of(smem_u32(tile));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) mma_ss(tmem + kZ + (b & 1) * 128, q_tile + column_step(k), k_tile + column_step(k), scores, k != 0);
                 tc_commit(&z_full[b & 1]);
             }
         };
         auto make_dp = [&](int b) {
             uint8_t* tile = sV + V::stage(b) * Shape::kTileBytes;
             ready(&v_full[V::stage(b)], V::parity(b), tile, b);
-            if (ok && lane == 0) {
-                const uint32_t v_tile = smem_u32(tile);
-                for (int k = 0; k < steps; ++k)
-                    mma_ss(tmem + kDp, along_columns(d_tile, k), along_columns(v_tile, k), scores, k != 0);
+            if (ok && elect_one()) {
+                const uint32_t v_tile = columns_of(smem_u32(tile));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) mma_ss(tmem + kDp, d_tile + column_step(k), v_tile + column_step(k), scores, k != 0);
                 tc_commit(dp_full);
                 tc_commit(&v_empty[V::stage(b)]);
             }
@@ -1028,68 +1097,70 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
             ok = ok && warp_wait(dz_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t k_tile = smem_u32(sK + K::stage(b) * Shape::kTileBytes);
+            if (elect_one()) {
+                const uint32_t k_tile = rows_of_tile(smem_u32(sK + K::stage(b) * Shape::kTileBytes));
+#pragma unroll
                 for (int k = 0; k < kRows / 16; ++k)
-                    mma_ts(tmem + kDq, tmem + kZ + (b & 1) * 128 + half_column(k), along_rows(k_tile, k), sums,
+                    mma_ts(tmem + kDq, tmem + kZ + (b & 1) * 128 + packed_column<32>(k), k_tile + k * kRowStep, sums,
                            b != 0 || k != 0);
                 tc_commit(&k_empty[K::stage(b)]);
             }
         }
-        if (lane == 0) tc_commit(done);
+        if (elect_one()) tc_commit(done);
         warp_wait(done, 0, p.wait_ns, p.status);
-    } else {
-        // ---------------- p and dz: a lane for each query, a warpgroup for each half of the keys
-        const int half = (warp - 2) >> 2, quad = warp & 3;
+    } else if (warp >= 4) {
+        // ---------------- p and dz: a lane for each query, a warpgroup for each quarter of the keys
+        const int part = (warp - 4) >> 2, quad = warp & 3;
         const int32_t row = row0 + quad * 32 + lane;
         const bool inside = work && row < at.len_q;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t dp_at = lanes + kDp + half * 64;
+        const uint32_t dp_at = lanes + kDp + part * 32;
         const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
         const int32_t least = p.causal ? min(at.len_k - 1, row0 + ahead) : at.len_k - 1;
         float2 stat = make_float2(INFINITY, 0.f);
         if (inside) stat = p.stats[(int64_t)head * p.seq.tokens_q + at.q0 + row];
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 lse2 = make_float2(-stat.x, -stat.x), delta2 = make_float2(stat.y, stat.y);
         bool ok = true;
         for (int b = 0; b < blocks; ++b) {
-            const uint32_t z_at = lanes + kZ + (b & 1) * 128 + half * 64;
+            const uint32_t z_at = lanes + kZ + (b & 1) * 128 + part * 32;
             ok = warp_wait(&z_full[b & 1], (uint32_t)(b / 2) & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            float pr[64];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            float2 pr[16];
+            {
                 uint32_t z[32];
-                tmem_ld_32x32b_x32(z_at + c * 32, z);
+                tmem_ld_32x32b_x32(z_at, z);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    pr[c * 32 + i] = exp2_approx(fmaf(__uint_as_float(z[i]), p.scale_log2, -stat.x));
+                for (int i = 0; i < 16; ++i) {
+                    const float2 e = f2_fma(make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), scale2, lse2);
+                    pr[i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                }
             }
             if (least - b * kRows < kRows - 1) {
-                const int seen = last - b * kRows - half * 64;
+                const int seen = last - b * kRows - part * 32;
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i > seen) pr[i] = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    if (2 * i > seen) pr[i].x = 0.f;
+                    if (2 * i + 1 > seen) pr[i].y = 0.f;
+                }
             }
             ok = warp_wait(dp_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            uint32_t dp[2][32];
-            tmem_ld_32x32b_x32(dp_at, dp[0]);
-            tmem_ld_32x32b_x32(dp_at + 32, dp[1]);
+            uint32_t dp[32], w[16];
+            tmem_ld_32x32b_x32(dp_at, dp);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dp_read);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = pack_bf16(pr[c * 32 + 2 * i] * (__uint_as_float(dp[c][2 * i]) - stat.y),
-                                     pr[c * 32 + 2 * i + 1] * (__uint_as_float(dp[c][2 * i + 1]) - stat.y));
-                tmem_st_32x32b_x16(z_at + c * 16, w);
+            for (int i = 0; i < 16; ++i) {
+                const float2 e = f2_mul(pr[i], f2_sub(make_float2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), delta2));
+                w[i] = pack_bf16(e.x, e.y);
             }
+            tmem_st_32x32b_x16(z_at, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -1098,13 +1169,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         bf16* to = p.dq.at(at.q0 + row, head);
         if (blocks > 0) {
             ok = ok && warp_wait(done, 0, p.wait_ns, p.status);
-            // each half writes its half of the columns
-            if (ok) {
+            if (ok) {  // each warpgroup writes its share of the columns
                 tc_fence_after();
-                const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0;
-                store_row(lanes + kDq + from, half ? p.dim - cut : min(cut, p.dim), p.scale, to + from, inside);
+                const int width = (p.dim / 4 + 15) / 16 * 16, from = part * width;
+                store_row(lanes + kDq + from, min(width, p.dim - from), p.scale, to + from, inside);
             }
-        } else if (inside && half == 0) {
+        } else if (inside && part == 0) {
             store_zeros(p.dim, to);
         }
     }

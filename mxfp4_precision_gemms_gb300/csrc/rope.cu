@@ -5,10 +5,12 @@
 // Backwards, with dz the gradient turned back by the same angles and u = x r:
 //   dx = r (dz gain - u mean(dz gain u)),   dgain = sum over tokens and heads of dz u
 //
-// HBM bandwidth bounds long calls, latency short ones.  A CTA takes a few tokens: first it makes the cosines and sines
-// of each token and pair in shared memory, once for all heads, then groups of lanes take the rows (a token's head).  A
-// lane holds VEC pairs, as two runs of VEC elements (or one of 2 VEC, where a pair's elements are neighbours), and every
-// row is read once and written once.  The elements behind the rotated ones are pairs that do not turn.
+// HBM bandwidth bounds long calls, latency short ones.  A warp takes a token, or a share of its heads where there are few
+// tokens: it makes the cosines and sines of the token's pairs once for all heads (shared memory of its own, no barrier of
+// the block), then goes through the heads of queries and of keys.  Groups of lanes hold a row (a token's head) each, a lane
+// VEC pairs of it, as two runs of VEC elements (or one of 2 VEC, where a pair's elements are neighbours), with turn and gain
+// in registers; the loads of ROWS rows are under way together.  Every row is read once and written once.  The elements
+// behind the rotated ones are pairs that do not turn.
 //
 // Angles.  A position times a frequency in fp32 is off by 2^-24 of itself, which is 0.03 radians at position 500000.  Here a
 // frequency is held as turns per position in 64-bit fixed point, and a product with an integer modulo 2^64 is the exact
@@ -18,6 +20,7 @@
 
 #include "element.cuh"
 #include "heads.cuh"
+#include "quant_math.cuh"
 
 namespace mx {
 namespace {
@@ -25,10 +28,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kRopeThreads = 256;
+constexpr int kWarps = kRopeThreads / 32;
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxPairs = kMaxHeadDim / 2;
-constexpr int kTokens = 8;      // tokens of a CTA's turn
-constexpr int kCtasPerSm = 4;   // partial sums of the gains' gradients: one row for each CTA
 
 struct RopeSide {  // queries or keys
     const void* x;
@@ -41,7 +43,10 @@ struct RopeSide {  // queries or keys
 
 struct RopeParams {
     RopeSide side[2];
-    int32_t tokens, dim, pairs, interleaved, is64, per_turn;
+    int32_t tokens, dim, pairs, is64;
+    int32_t interleaved;
+    int32_t span;    // slices of heads that a warp takes of a token
+    int64_t items;   // tokens times shares of their slices
     float eps;
     const void* positions;  // [axes][tokens]
     float* partial;         // gradient only: [CTA][2][dim]
@@ -49,16 +54,49 @@ struct RopeParams {
     uint8_t axis[kMaxPairs];
 };
 
-// VEC neighbouring elements, aligned to their size in bytes (at most 32).
-template <int VEC, class T>
-__device__ __forceinline__ void load_run(const T* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8)
-        unpack8(load8(p), v);
-    else if constexpr (VEC == 4)
-        load4(p, v);
-    else
+// VEC neighbouring elements as they lie in memory, aligned to their size in bytes (at most 32).
+template <class T, int VEC>
+struct Run {
+    T v[VEC];
+};
+template <>
+struct Run<bf16, 8> {
+    uint4 w;
+};
+template <>
+struct Run<bf16, 4> {
+    uint2 w;
+};
+template <class T, int VEC>
+__device__ __forceinline__ void load_run(const T* p, Run<T, VEC>& r) {
+    if constexpr (sizeof(T) == 2 && VEC >= 4) {
+        r.w = *reinterpret_cast<const decltype(r.w)*>(p);
+    } else if constexpr (VEC == 8) {
+        const Raw8<float> u = load8(p);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = load1(p + i);
+        for (int i = 0; i < 8; ++i) r.v[i] = u.v[i];
+    } else if constexpr (VEC == 4) {
+        load4(p, r.v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.v[i] = p[i];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void unpack_run(const Run<float, VEC>& r, float (&v)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = r.v[i];
+}
+template <int VEC>
+__device__ __forceinline__ void unpack_run(const Run<bf16, VEC>& r, float (&v)[VEC]) {
+    if constexpr (VEC >= 4) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r.w);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(r.v[i]);
+    }
 }
 template <int VEC, class T>
 __device__ __forceinline__ void store_run(T* p, const float (&v)[VEC]) {
@@ -71,71 +109,117 @@ __device__ __forceinline__ void store_run(T* p, const float (&v)[VEC]) {
         for (int i = 0; i < VEC; ++i) store1(p + i, v[i]);
 }
 
-// The pairs [at, at + VEC) of a row: a[i], b[i].
-template <int VEC, class T>
-__device__ __forceinline__ void load_pairs(const T* row, int at_a, int at_b, int interleaved, float (&a)[VEC],
-                                           float (&b)[VEC]) {
-    float u[VEC], v[VEC];
-    load_run<VEC>(row + at_a, u);
-    load_run<VEC>(row + at_b, v);
-    if (interleaved && VEC > 1) {
+// VEC pairs from a row's two runs: a[i], b[i].
+template <bool NEIGHBOURS, class T, int VEC>
+__device__ __forceinline__ void pairs_of(const Run<T, VEC>& ru, const Run<T, VEC>& rv, float (&a)[VEC], float (&b)[VEC]) {
+    float u[2 * VEC];
+    unpack_run<VEC>(ru, *reinterpret_cast<float(*)[VEC]>(u));
+    unpack_run<VEC>(rv, *reinterpret_cast<float(*)[VEC]>(u + VEC));
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            a[i] = 2 * i < VEC ? u[(2 * i) % VEC] : v[(2 * i) % VEC];
-            b[i] = 2 * i + 1 < VEC ? u[(2 * i + 1) % VEC] : v[(2 * i + 1) % VEC];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) a[i] = u[i], b[i] = v[i];
-    }
+    for (int i = 0; i < VEC; ++i) a[i] = u[NEIGHBOURS ? 2 * i : i], b[i] = u[NEIGHBOURS ? 2 * i + 1 : VEC + i];
 }
-template <int VEC, class T>
-__device__ __forceinline__ void store_pairs(T* row, int at_a, int at_b, int interleaved, const float (&a)[VEC],
-                                            const float (&b)[VEC]) {
-    float u[VEC], v[VEC];
-    if (interleaved && VEC > 1) {
+template <bool NEIGHBOURS, int VEC, class T>
+__device__ __forceinline__ void store_pairs(T* row, int at_a, int at_b, const float (&a)[VEC], const float (&b)[VEC]) {
+    float u[2 * VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            u[i] = i % 2 ? b[i / 2] : a[i / 2];
-            v[i] = i % 2 ? b[(VEC + i) / 2] : a[(VEC + i) / 2];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) u[i] = a[i], v[i] = b[i];
-    }
-    store_run<VEC>(row + at_a, u);
-    store_run<VEC>(row + at_b, v);
+    for (int i = 0; i < VEC; ++i) u[NEIGHBOURS ? 2 * i : i] = a[i], u[NEIGHBOURS ? 2 * i + 1 : VEC + i] = b[i];
+    store_run<VEC>(row + at_a, *reinterpret_cast<float(*)[VEC]>(u));
+    store_run<VEC>(row + at_b, *reinterpret_cast<float(*)[VEC]>(u + VEC));
 }
 
-// Sum over the `n` lanes of a row's group, in every one of them (li: this lane's place in it).
-__device__ __forceinline__ float group_sum(float v, int li, int n) {
+// N neighbouring floats of shared memory, aligned to their size (16 bytes at most).
+template <int N>
+__device__ __forceinline__ void load_shared(const float* p, float (&v)[N]) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(p + i);
+            v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+        }
+    } else if constexpr (N == 2) {
+        const float2 w = *reinterpret_cast<const float2*>(p);
+        v[0] = w.x, v[1] = w.y;
+    } else {
+        v[0] = p[0];
+    }
+}
+
+// d = a b + c and the like on N numbers, two in an instruction.
+template <int N>
+__device__ __forceinline__ void mul_n(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+    if constexpr (N == 1) d[0] = a[0] * b[0];
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = f2_mul(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+        d[i] = r.x, d[i + 1] = r.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void fma_n(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+    if constexpr (N == 1) d[0] = fmaf(a[0], b[0], c[0]);
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = f2_fma(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+        d[i] = r.x, d[i + 1] = r.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void scale_n(float (&d)[N], const float (&a)[N], float by) {
+    float b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = by;
+    mul_n(d, a, b);
+}
+template <int N>
+__device__ __forceinline__ float sum_n(const float (&a)[N]) {
+    float v = a[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) v += a[i];
+    return v;
+}
+
+// Sums of two numbers over the `n` lanes of a row's group, in every one of them (li: this lane's place in it).
+__device__ __forceinline__ void group_sums(float (&v)[2], int li, int n) {
+    if ((n & (n - 1)) == 0) {  // groups start on their own size
+        for (int o = n >> 1; o > 0; o >>= 1) {
+            const float a = __shfl_xor_sync(0xffffffffu, v[0], o), b = __shfl_xor_sync(0xffffffffu, v[1], o);
+            v[0] += a, v[1] += b;
+        }
+        return;
+    }
     const int lane = threadIdx.x & 31;
-    for (int o = n <= 1 ? 0 : 1 << (31 - __clz(n - 1)); o > 0; o >>= 1) {
-        const float t = __shfl_down_sync(0xffffffffu, v, o);
-        if (li < o && li + o < n) v += t;
+    for (int o = 1 << (31 - __clz(n - 1)); o > 0; o >>= 1) {
+        const float a = __shfl_down_sync(0xffffffffu, v[0], o), b = __shfl_down_sync(0xffffffffu, v[1], o);
+        if (li < o && li + o < n) v[0] += a, v[1] += b;
     }
-    return __shfl_sync(0xffffffffu, v, lane - li);
+    v[0] = __shfl_sync(0xffffffffu, v[0], lane - li), v[1] = __shfl_sync(0xffffffffu, v[1], lane - li);
 }
 
-// SLOTS: runs of pairs of a lane, 32 lanes apart (rows of more than 32 VEC pairs).
-template <class T, int VEC, int SLOTS, bool GRAD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ float2 turn[kTokens * kMaxPairs];
-    grid_dependency_wait();
-    allow_dependent_launch();
+// Lanes of a row, and rows that a warp takes at once.
+__host__ __device__ inline int row_lanes(int half, int vec) { return half / vec < 32 ? half / vec : 32; }
+
+// SLOTS: runs of pairs of a lane, 32 lanes apart (rows of more than 32 VEC pairs).  ROWS: that a lane has under way.
+template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD>
+__global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 : 3)
+    rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kSums = GRAD ? kRopeThreads * 2 * VEC * SLOTS : 0;  // floats of the groups' sums of gains
+    constexpr int kTurn = kWarps * kMaxPairs * 2;
+    __shared__ __align__(16) float shared[kTurn + 2 * kMaxHeadDim > kSums ? kTurn + 2 * kMaxHeadDim : kSums];
     const int half = p.dim / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lanes = min(32, half / VEC);  // of a row
-    const int per_warp = 32 / lanes;        // rows that a warp takes at once
+    float2* turn = reinterpret_cast<float2*>(shared) + warp * kMaxPairs;
+    float* gains = shared + kTurn;
+    const int lanes = row_lanes(half, VEC), per_warp = 32 / lanes;
+    const bool idle = lane >= lanes * per_warp;
     const int li = lane % lanes, sub = lane / lanes;
-    const bool idle = sub >= per_warp;
-    const int groups = kRopeThreads / 32 * per_warp, group = warp * per_warp + sub;
-    // where this lane's elements are
+    // where this lane's elements are; a run that is past the row is the first one's again, not counted and not written
     int at_a[SLOTS], at_b[SLOTS], pair[SLOTS];
+    bool there[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-        const int c = (li + s * lanes) * VEC;  // first pair
-        pair[s] = c < half ? c : -1;
-        if (p.interleaved) {
+        there[s] = (li + s * lanes) * VEC < half;
+        const int c = there[s] ? (li + s * lanes) * VEC : 0;  // first pair
+        pair[s] = c;
+        if (NEIGHBOURS) {
             at_a[s] = 2 * c, at_b[s] = 2 * c + VEC;
         } else if (c < p.pairs) {
             at_a[s] = c, at_b[s] = c + p.pairs;
@@ -143,146 +227,212 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             at_a[s] = p.pairs + c, at_b[s] = half + c;
         }
     }
-
-    float dgain[GRAD ? 2 : 1][SLOTS][2][VEC] = {};
-    const int turns = (p.tokens + p.per_turn - 1) / p.per_turn;
-    for (int it = blockIdx.x; it < turns; it += gridDim.x) {
-        const int t0 = it * p.per_turn, nt = min(p.per_turn, p.tokens - t0);
-        __syncthreads();  // the cosines of the turn before have been read
-        for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-            const int t = i / half, c = i - t * half;
+    auto element = [&](int s, int which, int i) {  // of pair i of slot s in its row
+        return NEIGHBOURS ? at_a[s] + 2 * i + which : (which ? at_b[s] : at_a[s]) + i;
+    };
+    grid_dependency_wait();
+    allow_dependent_launch();
+    for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeThreads) {
+        const float* gain = p.side[i >= p.dim].gain;
+        gains[i] = gain ? gain[i >= p.dim ? i - p.dim : i] : 1.f;
+    }
+    __syncthreads();
+    float dgain[2][SLOTS][2][VEC] = {};
+    const int slice = per_warp * ROWS;  // heads
+    const int slices0 = (p.side[0].heads + slice - 1) / slice;
+    const int all = slices0 + (p.side[1].heads + slice - 1) / slice, shares = (all + p.span - 1) / p.span;
+    const float mean = 1.f / (float)p.dim;
+    for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < p.items; item += (int64_t)gridDim.x * kWarps) {
+        const int64_t token = item / shares;
+        const int first = (int)(item - token * shares) * p.span, end = min(first + p.span, all);
+        __syncwarp();  // the cosines of the token before have been read
+        for (int i = lane; i < half; i += 32) {
             float2 cs = make_float2(1.f, 0.f);
-            if (c < p.pairs) {
-                const int64_t pos = load_id(p.positions, p.is64, (int64_t)p.axis[c] * p.tokens + t0 + t);
-                const int64_t frac = (int64_t)((uint64_t)pos * p.freq[c]);  // of a turn, times 2^64
-                sincospif((float)frac * 0x1p-63f, &cs.y, &cs.x);
+            if (i < p.pairs) {
+                const int64_t pos = load_id(p.positions, p.is64, (int64_t)p.axis[i] * p.tokens + token);
+                const int64_t frac = (int64_t)((uint64_t)pos * p.freq[i]);  // of a turn, times 2^64
+                sincospif((float)(int32_t)(frac >> 32) * 0x1p-31f, &cs.y, &cs.x);
             }
             turn[i] = cs;
         }
-        __syncthreads();
+        __syncwarp();
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const RopeSide& side = p.side[which];
-            const int rows = nt * side.heads;
-            float gain[SLOTS][2][VEC];
-            if (side.gain) {
+            const bool norm = side.gain != nullptr;
+            const int from = which ? max(first - slices0, 0) : first, to = which ? end - slices0 : min(end, slices0);
+            if (from >= to) continue;
+            // forward: (a, b) -> (a ca - b sb, b cb + a sa), the gains in the factors; backward: the turn alone
+            float ca[SLOTS][VEC], sa[SLOTS][VEC], cb[GRAD ? 1 : SLOTS][VEC], sb[SLOTS][VEC], gain[GRAD ? SLOTS : 1][2][VEC];
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
-                    if (pair[s] >= 0) {
-                        float u[VEC], v[VEC];
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            u[i] = __ldg(side.gain + at_a[s] + (p.interleaved ? 2 * i : i));
-                            v[i] = __ldg(side.gain + (p.interleaved ? at_a[s] + 2 * i + 1 : at_b[s] + i));
-                        }
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) gain[s][0][i] = u[i], gain[s][1][i] = v[i];
-                    }
-            }
-            // whole warps go round together: the sums are over lanes
-            for (int r0 = warp * per_warp; r0 < rows; r0 += groups) {
-                const int r = r0 + sub;
-                const bool on = !idle && r < rows;
-                const int t = on ? r / side.heads : 0, h = on ? r - t * side.heads : 0;
-                const int64_t token = t0 + t;
-                const T* x = static_cast<const T*>(side.x) + token * side.x_token + h * side.x_head;
-                T* y = static_cast<T*>(side.y) + token * side.y_token + h * side.y_head;
-                const float2* cs = turn + t * half;
-                float a[SLOTS][VEC] = {}, b[SLOTS][VEC] = {};
-                float da[SLOTS][VEC] = {}, db[SLOTS][VEC] = {};
-#pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
-                    if (on && pair[s] >= 0) {
-                        if (!GRAD || side.gain) load_pairs<VEC>(x, at_a[s], at_b[s], p.interleaved, a[s], b[s]);
-                        if constexpr (GRAD) {
-                            const T* dy = static_cast<const T*>(side.dy) + token * side.dy_token + h * side.dy_head;
-                            load_pairs<VEC>(dy, at_a[s], at_b[s], p.interleaved, da[s], db[s]);
-                        }
-                    }
-                if (side.gain) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int s = 0; s < SLOTS; ++s)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) ss = fmaf(a[s][i], a[s][i], fmaf(b[s][i], b[s][i], ss));
-                    const float rstd = rsqrtf(group_sum(ss, li, lanes) / (float)p.dim + p.eps);
-#pragma unroll
-                    for (int s = 0; s < SLOTS; ++s)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) a[s][i] *= rstd, b[s][i] *= rstd;
-                    if constexpr (GRAD) {
-                        float dot = 0.f;
-#pragma unroll
-                        for (int s = 0; s < SLOTS; ++s)
-                            if (on && pair[s] >= 0) {
-#pragma unroll
-                                for (int i = 0; i < VEC; ++i) {
-                                    const float2 c = cs[pair[s] + i];
-                                    const float za = fmaf(da[s][i], c.x, db[s][i] * c.y);
-                                    const float zb = fmaf(db[s][i], c.x, -da[s][i] * c.y);
-                                    dgain[which][s][0][i] = fmaf(za, a[s][i], dgain[which][s][0][i]);
-                                    dgain[which][s][1][i] = fmaf(zb, b[s][i], dgain[which][s][1][i]);
-                                    da[s][i] = za * gain[s][0][i], db[s][i] = zb * gain[s][1][i];
-                                    dot = fmaf(da[s][i], a[s][i], fmaf(db[s][i], b[s][i], dot));
-                                }
-                            }
-                        dot = group_sum(dot, li, lanes) / (float)p.dim;
-#pragma unroll
-                        for (int s = 0; s < SLOTS; ++s)
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                a[s][i] = (da[s][i] - a[s][i] * dot) * rstd;
-                                b[s][i] = (db[s][i] - b[s][i] * dot) * rstd;
-                            }
-                    }
+            for (int s = 0; s < SLOTS; ++s) {
+                float cs[2 * VEC], ga[VEC], gb[VEC], g[2 * VEC];
+                load_shared(reinterpret_cast<const float*>(turn + pair[s]), cs);
+                if (NEIGHBOURS) {
+                    load_shared(gains + which * p.dim + at_a[s], g);
+                } else {
+                    load_shared(gains + which * p.dim + at_a[s], *reinterpret_cast<float(*)[VEC]>(g));
+                    load_shared(gains + which * p.dim + at_b[s], *reinterpret_cast<float(*)[VEC]>(g + VEC));
                 }
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
-                    if (on && pair[s] >= 0) {
-                        if constexpr (!GRAD) {
+                for (int i = 0; i < VEC; ++i) {
+                    ga[i] = g[NEIGHBOURS ? 2 * i : i], gb[i] = g[NEIGHBOURS ? 2 * i + 1 : VEC + i];
+                    if constexpr (GRAD) {
+                        ca[s][i] = cs[2 * i], sa[s][i] = cs[2 * i + 1], sb[s][i] = -cs[2 * i + 1];
+                        gain[s][0][i] = ga[i], gain[s][1][i] = gb[i];
+                    } else {
+                        ca[s][i] = cs[2 * i] * ga[i], sa[s][i] = cs[2 * i + 1] * ga[i];
+                        cb[s][i] = cs[2 * i] * gb[i], sb[s][i] = -cs[2 * i + 1] * gb[i];
+                    }
+                }
+            }
+            for (int h0 = from * slice; h0 < min(to * slice, side.heads); h0 += slice) {
+                Run<T, VEC> x[ROWS][SLOTS][2], dy[GRAD ? ROWS : 1][SLOTS][2];
+                int h[ROWS];
+                // Lanes without a row of their own read the last head's, and write nothing.
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                const float2 c = cs[pair[s] + i];
-                                const float u = side.gain ? a[s][i] * gain[s][0][i] : a[s][i];
-                                const float v = side.gain ? b[s][i] * gain[s][1][i] : b[s][i];
-                                a[s][i] = fmaf(u, c.x, -v * c.y), b[s][i] = fmaf(v, c.x, u * c.y);
+                for (int k = 0; k < ROWS; ++k) {
+                    h[k] = h0 + k * per_warp + sub;
+                    const int64_t at = min(h[k], side.heads - 1);
+                    const T* px = static_cast<const T*>(side.x) + token * side.x_token + at * side.x_head;
+                    const T* pd = static_cast<const T*>(side.dy) + token * side.dy_token + at * side.dy_head;
+#pragma unroll
+                    for (int s = 0; s < SLOTS; ++s) {
+                        if (!GRAD || norm) {
+                            load_run<T, VEC>(px + at_a[s], x[k][s][0]);
+                            load_run<T, VEC>(px + at_b[s], x[k][s][1]);
+                        }
+                        if constexpr (GRAD) {
+                            load_run<T, VEC>(pd + at_a[s], dy[k][s][0]);
+                            load_run<T, VEC>(pd + at_b[s], dy[k][s][1]);
+                        }
+                    }
+                    if (idle) h[k] = side.heads;
+                }
+                // two rows together, so that one's sum over lanes is under way while the other's is
+#pragma unroll
+                for (int k0 = 0; k0 < ROWS; k0 += 2) {
+                    if (k0 > 0 && h0 + k0 * per_warp >= side.heads) break;
+                    float a[2][SLOTS][VEC], b[2][SLOTS][VEC], u[2][SLOTS][VEC], v[2][SLOTS][VEC], rstd[2] = {1.f, 1.f};
+                    if (!GRAD || norm) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float ss[VEC] = {};
+#pragma unroll
+                            for (int s = 0; s < SLOTS; ++s) {
+                                pairs_of<NEIGHBOURS, T, VEC>(x[k0 + r][s][0], x[k0 + r][s][1], a[r][s], b[r][s]);
+                                if (SLOTS == 1 || there[s]) {
+                                    fma_n(ss, a[r][s], a[r][s], ss);
+                                    fma_n(ss, b[r][s], b[r][s], ss);
+                                }
                             }
-                        } else if (!side.gain) {
+                            rstd[r] = sum_n(ss);
+                        }
+                        if (norm) {
+                            group_sums(rstd, li, lanes);
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                const float2 c = cs[pair[s] + i];
-                                a[s][i] = fmaf(da[s][i], c.x, db[s][i] * c.y);
-                                b[s][i] = fmaf(db[s][i], c.x, -da[s][i] * c.y);
+                            for (int r = 0; r < 2; ++r) rstd[r] = rsqrtf(fmaf(rstd[r], mean, p.eps));
+                        }
+                    }
+                    if constexpr (!GRAD) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int s = 0; s < SLOTS; ++s) {
+                                mul_n(u[r][s], a[r][s], ca[s]);
+                                mul_n(v[r][s], b[r][s], cb[s]);
+                                fma_n(u[r][s], b[r][s], sb[s], u[r][s]);
+                                fma_n(v[r][s], a[r][s], sa[s], v[r][s]);
+                                if (norm) {
+                                    scale_n(u[r][s], u[r][s], rstd[r]);
+                                    scale_n(v[r][s], v[r][s], rstd[r]);
+                                }
+                            }
+                    } else {
+                        float along[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float dot[VEC] = {};
+                            // rows that are another lane's, and runs that are no lane's, add nothing to the gains' sums
+                            const bool mine = h[k0 + r] < side.heads;
+#pragma unroll
+                            for (int s = 0; s < SLOTS; ++s) {
+                                float da[VEC], db[VEC];
+                                pairs_of<NEIGHBOURS, T, VEC>(dy[k0 + r][s][0], dy[k0 + r][s][1], da, db);
+                                mul_n(u[r][s], da, ca[s]);
+                                mul_n(v[r][s], db, ca[s]);
+                                fma_n(u[r][s], db, sa[s], u[r][s]);
+                                fma_n(v[r][s], da, sb[s], v[r][s]);
+                                if (norm && (SLOTS == 1 || there[s])) {
+                                    if (mine) {
+                                        float ua[VEC], ub[VEC];
+                                        scale_n(ua, a[r][s], rstd[r]);
+                                        scale_n(ub, b[r][s], rstd[r]);
+                                        fma_n(dgain[which][s][0], u[r][s], ua, dgain[which][s][0]);
+                                        fma_n(dgain[which][s][1], v[r][s], ub, dgain[which][s][1]);
+                                    }
+                                    mul_n(u[r][s], u[r][s], gain[s][0]);
+                                    mul_n(v[r][s], v[r][s], gain[s][1]);
+                                    fma_n(dot, u[r][s], a[r][s], dot);
+                                    fma_n(dot, v[r][s], b[r][s], dot);
+                                }
+                            }
+                            along[r] = sum_n(dot);
+                        }
+                        if (norm) {
+                            group_sums(along, li, lanes);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                // (du - u mean(du u)) r with u = x r
+                                const float by1 = -along[r] * mean * rstd[r] * rstd[r];
+                                float by[VEC];
+#pragma unroll
+                                for (int i = 0; i < VEC; ++i) by[i] = by1;
+#pragma unroll
+                                for (int s = 0; s < SLOTS; ++s) {
+                                    fma_n(u[r][s], a[r][s], by, u[r][s]);
+                                    fma_n(v[r][s], b[r][s], by, v[r][s]);
+                                    scale_n(u[r][s], u[r][s], rstd[r]);
+                                    scale_n(v[r][s], v[r][s], rstd[r]);
+                                }
                             }
                         }
-                        store_pairs<VEC>(y, at_a[s], at_b[s], p.interleaved, a[s], b[s]);
                     }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (h[k0 + r] < side.heads) {
+                            T* py = static_cast<T*>(side.y) + token * side.y_token + h[k0 + r] * side.y_head;
+#pragma unroll
+                            for (int s = 0; s < SLOTS; ++s)
+                                if (SLOTS == 1 || there[s])
+                                    store_pairs<NEIGHBOURS, VEC>(py, at_a[s], at_b[s], u[r][s], v[r][s]);
+                        }
+                }
             }
         }
     }
     if constexpr (GRAD) {
         if (!p.partial) return;
         // the groups' sums, added up in their order
-        __shared__ float sums[kRopeThreads / 32 * 32 * VEC * 2 * SLOTS];
+        const int groups = kWarps * per_warp;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
             if (!idle) {
+                float* at = shared + (warp * per_warp + sub) * p.dim;
 #pragma unroll
                 for (int s = 0; s < SLOTS; ++s)
-                    if (pair[s] >= 0) {
+                    if (there[s]) {
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            float* to = sums + group * p.dim;
-                            to[at_a[s] + (p.interleaved ? 2 * i : i)] = dgain[which][s][0][i];
-                            to[p.interleaved ? at_a[s] + 2 * i + 1 : at_b[s] + i] = dgain[which][s][1][i];
-                        }
+                        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) at[element(s, w, i)] = dgain[which][s][w][i];
                     }
             }
             __syncthreads();
             for (int d = threadIdx.x; d < p.dim; d += kRopeThreads) {
                 float v = 0.f;
-                for (int g = 0; g < groups; ++g) v += sums[g * p.dim + d];
+                for (int g = 0; g < groups; ++g) v += shared[g * p.dim + d];
                 p.partial[((int64_t)blockIdx.x * 2 + which) * p.dim + d] = v;
             }
         }
@@ -318,26 +468,37 @@ cudaError_t sm_count(int* sms) {
     });
 }
 
-constexpr int kMaxCtas = 148 * 8;  // bounds the workspace; more SMs than that need no more
+constexpr int kMaxCtas = 1024;  // bounds the gradient's workspace
 
-// CTAs of a call, and how many tokens each takes at a time: as many CTAs as there are turns of kTokens, no fewer than
-// SMs, no more than fit the device at once; then the tokens shared out so that all take as many turns.
-int rope_ctas(int64_t tokens, int sms, int32_t* per_turn) {
-    const int64_t most = std::min<int64_t>(kMaxCtas, (int64_t)sms * kCtasPerSm);
-    const int64_t turns = (tokens + kTokens - 1) / kTokens;
-    const int64_t ctas = std::min(std::max(turns, std::min<int64_t>(tokens, sms)), most);
-    const int64_t rounds = (tokens + ctas * kTokens - 1) / (ctas * kTokens);
-    *per_turn = (int32_t)((tokens + ctas * rounds - 1) / (ctas * rounds));
-    return (int)ctas;
+// Launches the kernel over `ctas` CTAs at most: a warp for each token, or for each share of a token's heads where there are
+// fewer tokens than warps.
+template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD>
+cudaError_t launch_shares(RopeParams p, int sms, int* ctas, cudaStream_t s) {
+    const int slice = 32 / row_lanes(p.dim / 2, VEC) * ROWS;
+    int all = 0;
+    for (const RopeSide& side : p.side) all += (side.heads + slice - 1) / slice;
+    const int most = std::min(kMaxCtas, sms * (GRAD ? 2 : VEC * SLOTS >= 8 ? 2 : 3));  // that fit the device at once
+    const int64_t warps = (int64_t)most * kWarps;
+    p.span = (int32_t)std::min<int64_t>(all, std::max<int64_t>(1, (int64_t)p.tokens * all / warps));
+    p.items = (int64_t)p.tokens * ((all + p.span - 1) / p.span);
+    *ctas = (int)std::min<int64_t>(most, (p.items + kWarps - 1) / kWarps);
+    return launch_overlapped(rope_kernel<T, VEC, SLOTS, ROWS, NEIGHBOURS, GRAD>, dim3((unsigned)*ctas), dim3(kRopeThreads), 0,
+                             s, 1, true, p);
 }
-
-template <class T, bool GRAD>
-cudaError_t launch_rope(const RopeParams& p, int vec, int ctas, cudaStream_t s) {
-    const dim3 grid((unsigned)ctas), block(kRopeThreads);
-    if (vec == 8) return launch_overlapped(rope_kernel<T, 8, 1, GRAD>, grid, block, 0, s, 1, true, p);
-    if (vec == 4) return launch_overlapped(rope_kernel<T, 4, 1, GRAD>, grid, block, 0, s, 1, true, p);
-    if (vec == 2) return launch_overlapped(rope_kernel<T, 2, 2, GRAD>, grid, block, 0, s, 1, true, p);
-    return launch_overlapped(rope_kernel<T, 1, 4, GRAD>, grid, block, 0, s, 1, true, p);
+template <class T, bool NEIGHBOURS, bool GRAD>
+cudaError_t launch_rope(const RopeParams& p, int vec, int sms, int* ctas, cudaStream_t s) {
+    if (!GRAD && sizeof(T) == 2 && vec == 8) return launch_shares<T, 8, 1, 4, NEIGHBOURS, false>(p, sms, ctas, s);
+    if (vec >= 4) return launch_shares<T, 4, 1, GRAD && sizeof(T) == 4 ? 2 : 4, NEIGHBOURS, GRAD>(p, sms, ctas, s);
+    if (vec == 2) return launch_shares<T, 2, 2, 2, NEIGHBOURS, GRAD>(p, sms, ctas, s);
+    return launch_shares<T, 1, 4, 2, NEIGHBOURS, GRAD>(p, sms, ctas, s);
+}
+template <bool GRAD>
+cudaError_t launch_rope(const RopeParams& p, int dtype, int vec, int sms, int* ctas, cudaStream_t s) {
+    if (dtype == MXFP4_OUT_BF16)
+        return p.interleaved ? launch_rope<bf16, true, GRAD>(p, vec, sms, ctas, s)
+                             : launch_rope<bf16, false, GRAD>(p, vec, sms, ctas, s);
+    return p.interleaved ? launch_rope<float, true, GRAD>(p, vec, sms, ctas, s)
+                         : launch_rope<float, false, GRAD>(p, vec, sms, ctas, s);
 }
 
 // Radians per position as the fraction of a turn in 64-bit fixed point, with 1 / (2 pi) as the sum of two doubles.
@@ -450,10 +611,10 @@ extern "C" mxfp4_status mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_hea
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess) {
-        const int vec = pairs_per_lane(p, all, 4), ctas = rope_ctas(tokens, sms, &p.per_turn);
+        const int vec = pairs_per_lane(p, all, 4);
+        int ctas = 0;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-        e = h[0][0].dtype == MXFP4_OUT_BF16 ? launch_rope<bf16, false>(p, vec, ctas, s)
-                                            : launch_rope<float, false>(p, vec, ctas, s);
+        e = launch_rope<false>(p, h[0][0].dtype, vec, sms, &ctas, s);
     }
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
     return record_error(MXFP4_OK, "%s", "");
@@ -461,7 +622,7 @@ extern "C" mxfp4_status mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_hea
 
 extern "C" size_t mxfp4_qk_norm_rope_grad_workspace_bytes(int64_t tokens, int64_t head_dim) {
     if (tokens <= 0 || tokens > INT32_MAX || head_dim < 2 || head_dim > kMaxHeadDim || head_dim % 2) return 0;
-    return (size_t)std::min<int64_t>(kMaxCtas, tokens) * 2 * (size_t)head_dim * sizeof(float);
+    return (size_t)kMaxCtas * 2 * (size_t)head_dim * sizeof(float);
 }
 
 extern "C" mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* dq,
@@ -520,10 +681,10 @@ extern "C" mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp
     int sms = 0;
     e = sm_count(&sms);
     if (e == cudaSuccess) {
-        const int vec = pairs_per_lane(p, all, 6), ctas = rope_ctas(tokens, sms, &p.per_turn);
+        const int vec = pairs_per_lane(p, all, 6);
+        int ctas = 0;
         p.partial = sums ? static_cast<float*>(ws) : nullptr;
-        e = h[0][0].dtype == MXFP4_OUT_BF16 ? launch_rope<bf16, true>(p, vec, ctas, s)
-                                            : launch_rope<float, true>(p, vec, ctas, s);
+        e = launch_rope<true>(p, h[0][0].dtype, vec, sms, &ctas, s);
         if (e == cudaSuccess && sums)
             e = launch_overlapped(rope_gain_kernel, dim3((unsigned)((head_dim + 31) / 32), 2), dim3(1024), 0, s, 1, true,
                                   (const float*)p.partial, ctas, (int)head_dim, dq_gain, dk_gain);

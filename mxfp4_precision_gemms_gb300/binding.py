@@ -60,12 +60,6 @@ class PhiloxOptsC(ctypes.Structure):
                 ("stochastic_rounding", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class HeadsC(ctypes.Structure):
-    """mxfp4_heads: heads of a [tokens, heads, head_dim] tensor."""
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
-
-
 class RopeC(ctypes.Structure):
     """mxfp4_rope: frequencies and axes of a rotation (host arrays)."""
     _fields_ = [("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pairs", ctypes.c_int32),
@@ -783,39 +777,50 @@ class Rope:
         self.ref = ctypes.addressof(self.c)
 
 
-_addressof = ctypes.addressof
-
-
-def _heads(x: torch.Tensor, name: str) -> tuple[HeadsC, tuple]:
-    """A [tokens, heads, head_dim] fp32 / bf16 tensor of the current device as the library takes it, and its shape."""
+def _heads(x: torch.Tensor, name: str, dev: int) -> tuple[int, int, int, int, int, int, int]:
+    """A [tokens, heads, head_dim] fp32 / bf16 tensor of device `dev` as the four words of an mxfp4_heads, and its shape."""
     kind = _OUT_OF.get(x.dtype)
-    if kind is not None and x.dim() == 3 and _here(x):
-        shape = x.shape
+    if kind is not None and x.dim() == 3 and x.get_device() == dev:
+        n, heads, dim = x.shape
         token_stride, head_stride, inner = x.stride()
-        if inner == 1 or shape[2] <= 1:
-            return HeadsC(x.data_ptr(), token_stride, head_stride, shape[1], kind), shape
+        if inner == 1 or dim <= 1:
+            return x.data_ptr(), token_stride, head_stride, heads | kind << 32, n, heads, dim
     raise ValueError(f"{name} must be an fp32 or bf16 tensor [tokens, heads, head_dim] with unit inner stride on the "
                      "current CUDA device")
 
 
-def _like(out, shape, kind: int, name: str, device, stream, zero: bool = False) -> tuple[torch.Tensor, HeadsC]:
-    """A caller's output heads, checked, or new ones (zero: filled with zeros, for a call that leaves rows out)."""
+def _like(out, shape, kind: int, name: str, device, dev: int, stream, zero: bool = False):
+    """A caller's output heads, checked, or new ones (zero: filled with zeros, for a call that leaves rows out), as the
+    tensor and the words of _heads."""
+    n, heads, dim = shape
     if out is None:
         out = _empty(shape, _FLOAT_OF[kind], device, stream)
         if zero:
-            with torch.cuda.stream(stream):
+            if stream is None:
                 out.zero_()
-        return out, HeadsC(out.data_ptr(), shape[1] * shape[2], shape[2], shape[1], kind)
-    c, got = _heads(out, name)
-    if tuple(got) != tuple(shape) or c.dtype != kind:
-        raise ValueError(f"{name} must be {tuple(shape)} of {_FLOAT_OF[kind]}")
-    return out, c
+            else:
+                with torch.cuda.stream(stream):
+                    out.zero_()
+        return out, (out.data_ptr(), heads * dim, dim, heads | kind << 32)
+    words = _heads(out, name, dev)
+    if words[4:] != shape or words[3] >> 32 != kind:
+        raise ValueError(f"{name} must be {shape} of {_FLOAT_OF[kind]}")
+    return out, words[:4]
 
 
-def _gain(gain: torch.Tensor | None, dim: int, name: str):
+def _table(*words) -> tuple[array.array, int]:
+    """The words of several mxfp4_heads one behind the other, and the first one's address (32 bytes each)."""
+    table = array.array("q", itertools.chain.from_iterable(words))
+    return table, table.buffer_info()[0]
+
+
+_NO_HEADS = (0, 0, 0, 0)
+
+
+def _gain(gain: torch.Tensor | None, dim: int, name: str, dev: int):
     if gain is None:
         return None
-    if gain.dtype is not torch.float32 or not _here(gain) or not gain.is_contiguous() or gain.numel() != dim:
+    if gain.dtype is not torch.float32 or gain.get_device() != dev or not gain.is_contiguous() or gain.numel() != dim:
         raise ValueError(f"{name} must be {dim} contiguous fp32 elements on the current CUDA device")
     return gain.data_ptr()
 
@@ -841,21 +846,25 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope | None = No
     rows; k may be None) divided by its root mean square and multiplied by its gain (fp32 [head_dim]; None: left as it
     is), then rotated by `rope` at `positions` ([tokens] or [axes, tokens], int32 or int64).  Returns (q_out, k_out); each
     may be its input, for in place."""
-    cq, shape = _heads(q, "q")
-    n, _, dim = shape
-    device = q.device
+    dev = _current_device()
+    *wq, n, heads, dim = _heads(q, "q", dev)
+    kind, device = wq[3] >> 32, q.device
     at, ids_kind, axes = _positions(positions, rope, n)
-    q_out, cqo = _like(q_out, shape, cq.dtype, "q_out", device, stream)
-    ck = cko = None
+    q_out, wqo = _like(q_out, (n, heads, dim), kind, "q_out", device, dev, stream)
     if k is not None:
-        ck, k_shape = _heads(k, "k")
-        if k_shape[0] != n or k_shape[2] != dim or ck.dtype != cq.dtype:
-            raise ValueError(f"q {tuple(shape)} and k {tuple(k_shape)} do not fit together")
-        k_out, cko = _like(k_out, k_shape, cq.dtype, "k_out", device, stream)
-    _check(lib().mxfp4_qk_norm_rope(_addressof(cq), _addressof(ck) if ck else None, n, dim, _gain(q_gain, dim, "q_gain"),
-                                    _gain(k_gain, dim, "k_gain"), eps, rope.ref if rope else None, at, ids_kind, axes,
-                                    _addressof(cqo), _addressof(cko) if cko else None, _stream(stream)))
-    return q_out, (k_out if k is not None else None)
+        *wk, k_n, k_heads, k_dim = _heads(k, "k", dev)
+        if k_n != n or k_dim != dim or wk[3] >> 32 != kind:
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not fit together")
+        k_out, wko = _like(k_out, (n, k_heads, dim), kind, "k_out", device, dev, stream)
+        table, to = _table(wq, wqo, wk, wko)
+        to_k, to_k_out = to + 64, to + 96
+    else:
+        table, to = _table(wq, wqo)
+        k_out = to_k = to_k_out = None
+    _check(lib().mxfp4_qk_norm_rope(to, to_k, n, dim, _gain(q_gain, dim, "q_gain", dev), _gain(k_gain, dim, "k_gain", dev),
+                                    eps, None if rope is None else rope.ref, at, ids_kind, axes, to + 32, to_k_out,
+                                    _stream(stream)))
+    return q_out, k_out
 
 
 def qk_norm_rope_grad(q: torch.Tensor | None, k: torch.Tensor | None, dq: torch.Tensor, dk: torch.Tensor | None,
@@ -866,44 +875,47 @@ def qk_norm_rope_grad(q: torch.Tensor | None, k: torch.Tensor | None, dq: torch.
     """mxfp4_qk_norm_rope_grad: gradients (dq_in, dk_in, dq_gain, dk_gain) of qk_norm_rope's inputs and gains from dq and
     dk, those of its outputs (dk None: queries alone).  q and k, its inputs, are read where there is a gain and may be
     None otherwise.  dq_in and dk_in may be dq and dk themselves; gains False leaves the gains' gradients out."""
-    cd, shape = _heads(dq, "dq")
-    n, _, dim = shape
-    device, kind = dq.device, cd.dtype
+    dev = _current_device()
+    *wdq, n, heads, dim = _heads(dq, "dq", dev)
+    kind, device = wdq[3] >> 32, dq.device
     at, ids_kind, axes = _positions(positions, rope, n)
     sides = []
     for x, dx, gain, dx_in, name in ((q, dq, q_gain, dq_in, "q"), (k, dk, k_gain, dk_in, "k")):
         if dx is None:
             if gain is not None:
                 raise ValueError(f"{name}_gain without d{name}")
-            sides.append((None, None, None, None, None, None, None))
+            sides.append((_NO_HEADS, _NO_HEADS, _NO_HEADS, None, None, None))
             continue
-        c, got = _heads(dx, "d" + name)
-        if got[0] != n or got[2] != dim or c.dtype != kind:
-            raise ValueError(f"dq {tuple(shape)} and d{name} {tuple(got)} do not fit together")
-        cx = dgain = None
+        *wd, d_n, d_heads, d_dim = _heads(dx, "d" + name, dev)
+        if d_n != n or d_dim != dim or wd[3] >> 32 != kind:
+            raise ValueError(f"dq {tuple(dq.shape)} and d{name} {tuple(dx.shape)} do not fit together")
+        wx, dgain = _NO_HEADS, None
         if gain is not None:
             if x is None:
                 raise ValueError(f"{name}_gain needs {name}")
-            cx, x_shape = _heads(x, name)
-            if tuple(x_shape) != tuple(got) or cx.dtype != kind:
-                raise ValueError(f"{name} must be {tuple(got)} of {_FLOAT_OF[kind]}")
+            wx = _heads(x, name, dev)
+            if wx[4:] != (n, d_heads, dim) or wx[3] >> 32 != kind:
+                raise ValueError(f"{name} must be {(n, d_heads, dim)} of {_FLOAT_OF[kind]}")
+            wx = wx[:4]
             if gains:
                 dgain = _empty(dim, torch.float32, device, stream)
-        dx_in, ci = _like(dx_in, got, kind, f"d{name}_in", device, stream)
-        sides.append((c, cx, ci, _gain(gain, dim, name + "_gain"), dx_in, dgain,
-                      None if dgain is None else dgain.data_ptr()))
-    ref = lambda c: None if c is None else _addressof(c)
+        dx_in, wi = _like(dx_in, (n, d_heads, dim), kind, f"d{name}_in", device, dev, stream)
+        sides.append((wx, wd, wi, _gain(gain, dim, name + "_gain", dev), dx_in, dgain))
     L = lib()
-    nb = L.mxfp4_qk_norm_rope_grad_workspace_bytes(n, dim) if any(s[5] is not None for s in sides) else 0
+    (wq, _, wqi, qg, dq_in, dq_gain), (wk, wdk, wki, kg, dk_in, dk_gain) = sides
+    nb = 0 if dq_gain is None and dk_gain is None else L.mxfp4_qk_norm_rope_grad_workspace_bytes(n, dim)
     ws = _empty(nb, torch.uint8, device, stream) if nb else None
-    (cdq, cq, cqi, qg, dq_in, dq_gain, dqg), (cdk, ck, cki, kg, dk_in, dk_gain, dkg) = sides
-    _check(L.mxfp4_qk_norm_rope_grad(ref(cq), ref(ck), ref(cdq), ref(cdk), n, dim, qg, kg, eps, rope.ref if rope else None,
-                                     at, ids_kind, axes, ref(cqi), ref(cki), dqg, dkg, ws.data_ptr() if nb else None, nb,
+    table, to = _table(wq, wdq, wqi, wk, wdk, wki)
+    keys = dk is not None
+    _check(L.mxfp4_qk_norm_rope_grad(to if qg else None, to + 96 if kg else None, to + 32, to + 128 if keys else None, n, dim,
+                                     qg, kg, eps, None if rope is None else rope.ref, at, ids_kind, axes, to + 64,
+                                     to + 160 if keys else None, None if dq_gain is None else dq_gain.data_ptr(),
+                                     None if dk_gain is None else dk_gain.data_ptr(), ws.data_ptr() if nb else None, nb,
                                      _stream(stream)))
     return dq_in, dk_in, dq_gain, dk_gain
 
 
-def _sequences(cu_q, cu_k, seqs: int, same: bool) -> tuple[int | None, int | None, int]:
+def _sequences(cu_q, cu_k, seqs: int, same: bool, dev: int) -> tuple[int | None, int | None, int]:
     """(address of cu_q, of cu_k, sequences); cu_k defaults to cu_q where there are as many keys as queries."""
     if cu_q is None:
         if cu_k is not None:
@@ -914,23 +926,28 @@ def _sequences(cu_q, cu_k, seqs: int, same: bool) -> tuple[int | None, int | Non
             raise ValueError("cu_q without cu_k, and not as many keys as queries")
         cu_k = cu_q
     for x, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        if x.dtype is not torch.int32 or x.dim() != 1 or x.numel() < 1 or not _here(x) or not x.is_contiguous():
+        if x.dtype is not torch.int32 or x.dim() != 1 or x.numel() < 1 or x.get_device() != dev or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 vector on the current CUDA device")
     if cu_q.numel() != cu_k.numel():
         raise ValueError(f"cu_q has {cu_q.numel()} elements, cu_k {cu_k.numel()}")
     return cu_q.data_ptr(), cu_k.data_ptr(), cu_q.numel() - 1
 
 
-def _attention_operands(q, k, v):
-    """(descriptors of q, k and v, q's shape, k's shape) of an attention call, checked."""
-    cq, shape = _heads(q, "q")
-    ck, k_shape = _heads(k, "k")
-    cv, v_shape = _heads(v, "v")
-    if cq.dtype != OUT_BF16 or ck.dtype != OUT_BF16 or cv.dtype != OUT_BF16:
+def _attention_operands(q, k, v, dev: int):
+    """(words of q, k and v, tokens of q, its heads, head_dim, tokens of k, its heads) of an attention call, checked."""
+    *wq, n, heads, dim = _heads(q, "q", dev)
+    *wk, m, k_heads, k_dim = _heads(k, "k", dev)
+    *wv, v_m, v_heads, v_dim = _heads(v, "v", dev)
+    if wq[3] >> 32 != OUT_BF16 or wk[3] >> 32 != OUT_BF16 or wv[3] >> 32 != OUT_BF16:
         raise ValueError("q, k and v must be bf16")
-    if tuple(k_shape) != tuple(v_shape) or shape[2] != k_shape[2]:
-        raise ValueError(f"q {tuple(shape)}, k {tuple(k_shape)} and v {tuple(v_shape)} do not fit together")
-    return cq, ck, cv, shape, k_shape
+    if m != v_m or k_heads != v_heads or not dim == k_dim == v_dim:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit together")
+    return wq, wk, wv, n, heads, dim, m, k_heads
+
+
+def _check_lse(lse: torch.Tensor, heads: int, n: int, dev: int):
+    if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != (heads, n):
+        raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True, scale: float | None = None,
@@ -942,23 +959,23 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     [q_heads, q_tokens], which attention_grad takes.  rest: returns (out, lse, rest), rest like out, what rounding left of
     it, for exact gradients.  Tokens outside of all sequences: new outputs hold zeros there, given ones are left as they
     were."""
-    cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
-    n, heads, dim = shape
-    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == k_shape[0])
-    device = q.device
-    out, co = _like(out, shape, OUT_BF16, "out", device, stream, zero=cu_q is not None)
-    if rest:
-        left, cr = _like(None, shape, OUT_BF16, "rest", device, stream, zero=cu_q is not None)
+    dev = _current_device()
+    wq, wk, wv, n, heads, dim, m, _ = _attention_operands(q, k, v, dev)
+    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
+    device, zero = q.device, cu_q is not None
+    out, wo = _like(out, (n, heads, dim), OUT_BF16, "out", device, dev, stream, zero)
+    left, wr = _like(None, (n, heads, dim), OUT_BF16, "rest", device, dev, stream, zero) if rest else (None, _NO_HEADS)
     if lse is None:
         lse = _empty((heads, n), torch.float32, device, stream)
-        if cu_q is not None:
+        if zero:
             with torch.cuda.stream(stream):
                 lse.zero_()
-    elif lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
-        raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
-    _check(lib().mxfp4_attention(_addressof(cq), _addressof(ck), _addressof(cv), n, k_shape[0], dim, at_q, at_k, seqs,
-                                 int(causal), dim ** -0.5 if scale is None else scale, _addressof(co),
-                                 _addressof(cr) if rest else None, lse.data_ptr(), _stream(stream)))
+    else:
+        _check_lse(lse, heads, n, dev)
+    table, to = _table(wq, wk, wv, wo, wr)
+    _check(lib().mxfp4_attention(to, to + 32, to + 64, n, m, dim, at_q, at_k, seqs, causal,
+                                 dim ** -0.5 if scale is None else scale, to + 96, to + 128 if rest else None,
+                                 lse.data_ptr(), _stream(stream)))
     return (out, lse, left) if rest else (out, lse)
 
 
@@ -968,27 +985,27 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
                    rest: torch.Tensor | None = None, stream=None):
     """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out, lse
-    and rest as it returned them (without rest the gradients carry out's rounding), the others as it was given.  dq, dk and dv may be slices of one buffer.  Tokens outside of all
-    sequences: as in attention."""
-    cq, ck, cv, shape, k_shape = _attention_operands(q, k, v)
-    n, heads, dim = shape
-    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == k_shape[0])
+    and rest as it returned them (without rest the gradients carry out's rounding), the others as it was given.  dq, dk
+    and dv may be slices of one buffer.  Tokens outside of all sequences: as in attention."""
+    dev = _current_device()
+    wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
+    at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
     device, zero = q.device, cu_q is not None
-    _, co = _like(out, shape, OUT_BF16, "out", device, stream)
-    _, cd = _like(dout, shape, OUT_BF16, "dout", device, stream)
-    cr = None if rest is None else _like(rest, shape, OUT_BF16, "rest", device, stream)[1]
-    if lse.dtype is not torch.float32 or not _here(lse) or not lse.is_contiguous() or lse.shape != (heads, n):
-        raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
-    dq, cdq = _like(dq, shape, OUT_BF16, "dq", device, stream, zero)
-    dk, cdk = _like(dk, k_shape, OUT_BF16, "dk", device, stream, zero)
-    dv, cdv = _like(dv, k_shape, OUT_BF16, "dv", device, stream, zero)
+    shape, k_shape = (n, heads, dim), (m, k_heads, dim)
+    _, wo = _like(out, shape, OUT_BF16, "out", device, dev, stream)
+    _, wd = _like(dout, shape, OUT_BF16, "dout", device, dev, stream)
+    wr = _NO_HEADS if rest is None else _like(rest, shape, OUT_BF16, "rest", device, dev, stream)[1]
+    _check_lse(lse, heads, n, dev)
+    dq, wdq = _like(dq, shape, OUT_BF16, "dq", device, dev, stream, zero)
+    dk, wdk = _like(dk, k_shape, OUT_BF16, "dk", device, dev, stream, zero)
+    dv, wdv = _like(dv, k_shape, OUT_BF16, "dv", device, dev, stream, zero)
     L = lib()
     nb = L.mxfp4_attention_grad_workspace_bytes(n, heads)
     ws = _empty(nb, torch.uint8, device, stream)
-    _check(L.mxfp4_attention_grad(_addressof(cq), _addressof(ck), _addressof(cv), _addressof(co),
-                                  _addressof(cr) if cr else None, lse.data_ptr(), _addressof(cd), n, k_shape[0], dim, at_q, at_k, seqs, int(causal),
-                                  dim ** -0.5 if scale is None else scale, _addressof(cdq), _addressof(cdk),
-                                  _addressof(cdv), ws.data_ptr(), nb, _stream(stream)))
+    table, to = _table(wq, wk, wv, wo, wr, wd, wdq, wdk, wdv)
+    _check(L.mxfp4_attention_grad(to, to + 32, to + 64, to + 96, None if rest is None else to + 128, lse.data_ptr(), to + 160,
+                                  n, m, dim, at_q, at_k, seqs, causal, dim ** -0.5 if scale is None else scale, to + 192,
+                                  to + 224, to + 256, ws.data_ptr(), nb, _stream(stream)))
     return dq, dk, dv
 
 

@@ -559,6 +559,11 @@ mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k,
                                      const mxfp4_heads* dk_in, float* dq_gain, float* dk_gain, void* ws,
                                      size_t ws_bytes, mxfp4_stream_t stream);
 
+/* Workspace bytes of mxfp4_attention: above 0 where the queries are few and their keys are shared out over several
+ * CTAs, whose parts are then joined. */
+size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t head_dim, int64_t q_heads,
+                                       int64_t k_heads, int64_t seqs);
+
 /* Softmax attention over packed sequences: for each query of a sequence and each of its heads
  *   z = scale q k^T over the keys that it sees,  lse = log sum exp z,  out = exp(z - lse) v
  * q: [q_tokens, q_heads, head_dim]; k, v: [k_tokens, k_heads, head_dim]; q_heads a multiple of k_heads
@@ -576,12 +581,13 @@ mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k,
  * mxfp4_attention_grad takes.  Rows outside of all sequences are left as they were, in both.
  * rest: NULL, or [q_tokens, q_heads, head_dim] bf16, which receives what rounding left of out (out + rest is the
  * output to 16 bits): what the gradient is exact with.
+ * ws: device, 256-byte aligned, mxfp4_attention_workspace_bytes bytes (may be NULL where those are 0).
  * Products in bf16 on the tensor cores (the probabilities rounded to bf16), sums and softmax statistics in fp32.
  * The same bits on every run. */
 mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v, int64_t q_tokens,
                              int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
                              int64_t seqs, int causal, float scale, const mxfp4_heads* out,
-                             const mxfp4_heads* rest, float* lse, mxfp4_stream_t stream);
+                             const mxfp4_heads* rest, float* lse, void* ws, size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Workspace bytes of mxfp4_attention_grad: two fp32 statistics of each query. */
 size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);

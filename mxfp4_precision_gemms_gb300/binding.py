@@ -132,7 +132,8 @@ def lib():
                 "mxfp4_qk_norm_rope": ([P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P], I),
                 "mxfp4_qk_norm_rope_grad_workspace_bytes": ([I64, I64], S),
                 "mxfp4_qk_norm_rope_grad": ([P, P, P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P, P, P, S, P], I),
-                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P], I),
+                "mxfp4_attention_workspace_bytes": ([I64, I64, I64, I64, I64, I64], S),
+                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
                 "mxfp4_attention_grad_workspace_bytes": ([I64, I64], S),
                 "mxfp4_attention_grad": ([P, P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
@@ -960,7 +961,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     it, for exact gradients.  Tokens outside of all sequences: new outputs hold zeros there, given ones are left as they
     were."""
     dev = _current_device()
-    wq, wk, wv, n, heads, dim, m, _ = _attention_operands(q, k, v, dev)
+    wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
     device, zero = q.device, cu_q is not None
     out, wo = _like(out, (n, heads, dim), OUT_BF16, "out", device, dev, stream, zero)
@@ -972,10 +973,13 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
                 lse.zero_()
     else:
         _check_lse(lse, heads, n, dev)
+    L = lib()
+    nb = L.mxfp4_attention_workspace_bytes(n, m, dim, heads, k_heads, seqs)
+    ws = _empty(nb, torch.uint8, device, stream) if nb else None
     table, to = _table(wq, wk, wv, wo, wr)
-    _check(lib().mxfp4_attention(to, to + 32, to + 64, n, m, dim, at_q, at_k, seqs, causal,
-                                 dim ** -0.5 if scale is None else scale, to + 96, to + 128 if rest else None,
-                                 lse.data_ptr(), _stream(stream)))
+    _check(L.mxfp4_attention(to, to + 32, to + 64, n, m, dim, at_q, at_k, seqs, causal,
+                             dim ** -0.5 if scale is None else scale, to + 96, to + 128 if rest else None, lse.data_ptr(),
+                             ws.data_ptr() if nb else None, nb, _stream(stream)))
     return (out, lse, left) if rest else (out, lse)
 
 

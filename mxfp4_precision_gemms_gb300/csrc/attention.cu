@@ -125,6 +125,7 @@ struct Sequences {
 struct Place {
     int32_t q0, k0, len_q, len_k;  // first tokens and lengths of the sequence
     int32_t tile;                  // of it; -1: nothing to do
+    int32_t part, parts;           // of the tile's keys, where they are shared out
 };
 
 // Sequence i's first token and length, whatever the list holds.
@@ -136,17 +137,20 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
     len = min(max(b, first), tokens) - first;
 }
 
-// The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences.  By one warp.
+// The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
+// among their parts of that many keys.  By one warp.
 template <bool KEYS>
-__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
-    Place p;
+__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, uint32_t* status) {
+    Place p{};
     p.tile = -1;
     if (!s.cu_q) {
-        const int32_t len = KEYS ? s.len_k : s.len_q, tiles = (len + rows - 1) / rows;
-        if (tiles == 0 || slot / tiles >= s.count) return p;
-        const int32_t i = slot / tiles;
+        p.parts = chunk > 0 ? max((s.len_k + chunk - 1) / chunk, 1) : 1;
+        const int32_t len = KEYS ? s.len_k : s.len_q, places = (len + rows - 1) / rows * p.parts;
+        if (places == 0 || slot / places >= s.count) return p;
+        const int32_t i = slot / places;
         p.q0 = i * s.len_q, p.k0 = i * s.len_k, p.len_q = s.len_q, p.len_k = s.len_k;
-        p.tile = slot - i * tiles;
+        p.tile = (slot - i * places) / p.parts;
+        p.part = slot - i * places - p.tile * p.parts;
         return p;
     }
     const int lane = threadIdx.x & 31;
@@ -158,7 +162,8 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
             range_of(s.cu_q, i, s.tokens_q, mine.q0, mine.len_q, status);
             range_of(s.cu_k, i, s.tokens_k, mine.k0, mine.len_k, status);
         }
-        const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows;
+        mine.parts = chunk > 0 ? max((mine.len_k + chunk - 1) / chunk, 1) : 1;
+        const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows * mine.parts;
         int32_t upto = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -170,7 +175,10 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
             const int src = __ffs(past) - 1;
             p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
             p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
+            p.parts = __shfl_sync(0xffffffffu, mine.parts, src);
             p.tile = slot - before - __shfl_sync(0xffffffffu, upto - tiles, src);
+            p.part = p.tile % p.parts;
+            p.tile /= p.parts;
             return p;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -179,7 +187,8 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
 }
 
 __device__ __forceinline__ Place place_of(const Place* p) {
-    return {uniform(p->q0), uniform(p->k0), uniform(p->len_q), uniform(p->len_k), uniform(p->tile)};
+    return {uniform(p->q0),   uniform(p->k0),   uniform(p->len_q), uniform(p->len_k),
+            uniform(p->tile), uniform(p->part), uniform(p->parts)};
 }
 
 // ------------------------------------------------------------------ shared pieces
@@ -208,10 +217,19 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
             *reinterpret_cast<uint4*>(tile + b * kBlockBytes + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// A tile of queries holds those of `pack` heads that share a key's (a divisor of the group): row r is token r / pack and
+// head r % pack, `tokens` * pack rows in all, 128 or a few less.  Short sequences fill tiles so, and a mask's edge is
+// `tokens` wide.
+struct Packing {
+    int32_t pack, tokens;
+    __device__ __forceinline__ int32_t rows() const { return pack * tokens; }
+};
+
+// `rows`: of the map's box.
 template <int DP>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int32_t head,
-                                          int32_t token) {
-    mbar_arrive_expect_tx(bar, DP / 64 * kBlockBytes);
+                                          int32_t token, int32_t rows = kRows) {
+    mbar_arrive_expect_tx(bar, DP / 64 * rows * 128);
 #pragma unroll
     for (int b = 0; b < DP / 64; ++b) tma_load_3d(dst + b * kBlockBytes, map, bar, b * 64, head, token);
 }
@@ -241,6 +259,19 @@ __device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor,
         }
     }
 }
+// The same in fp32 as it is (rows of a multiple of 8 elements).
+__device__ __forceinline__ void store_part(uint32_t taddr, int dim, float* to, bool inside) {
+    for (int c = 0; c < dim; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + c, v);
+        tmem_ld_wait();
+        if (inside) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                if (c + j < dim) *reinterpret_cast<uint4*>(to + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+    }
+}
 __device__ __forceinline__ void store_zeros(int dim, bf16* to) {
     for (int c = 0; c < dim; c += 8) *reinterpret_cast<uint4*>(to + c) = make_uint4(0, 0, 0, 0);
 }
@@ -266,8 +297,13 @@ struct ForwardParams {
     Rows out, rest;  // rest.data NULL: not wanted
     float* lse;      // [q_heads][tokens_q]
     Sequences seq;
-    int32_t q_heads, group, dim, causal;
-    float scale_log2;  // scale * log2 e
+    Packing packing;
+    int32_t head_blocks;  // query heads / pack
+    int32_t group, dim, causal;
+    int32_t chunk;        // above 0: a CTA takes that many key tiles of a pair of query tiles, and leaves its part to join_kernel
+    float* part;          // [CTA][2][128][dim]
+    float2* part_stats;   // [CTA][2][128]: (log2 of what the part is scaled by, sum)
+    float scale_log2;     // scale * log2 e
     uint32_t* status;
     uint64_t wait_ns;
 };
@@ -310,7 +346,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     float* share = reinterpret_cast<float*>(smem + Shape::kOffShare);  // [tile][half][row]
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.q_heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.q_heads);
+    const int32_t block = (int32_t)(blockIdx.x % (uint32_t)p.head_blocks), head0 = block * p.packing.pack;
+    const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)p.head_blocks);
+    const int32_t tokens = p.packing.tokens;  // of a tile
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -335,7 +373,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * kRows, p.status);
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -345,17 +383,22 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     Place at = place_of(where);
     const bool work = at.tile >= 0;
     // the tiles that see the most keys first
-    if (work && p.causal) at.tile = (at.len_q + 2 * kRows - 1) / (2 * kRows) - 1 - at.tile;
-    const int32_t row0 = at.tile * 2 * kRows;  // first query, in the sequence
+    if (work && p.causal) at.tile = (at.len_q + 2 * tokens - 1) / (2 * tokens) - 1 - at.tile;
+    const int32_t row0 = at.tile * 2 * tokens;  // first query, in the sequence
     const int32_t ahead = at.len_k - at.len_q;  // query i sees keys up to i + ahead
-    // key tiles of each query tile
-    int32_t n[2] = {0, 0};
+    // key tiles of each query tile: n of them from tile j0 on
+    int32_t n[2] = {0, 0}, j0 = 0;
     if (work) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int32_t first = row0 + i * kRows, last = min(first + kRows, at.len_q) - 1;
+            const int32_t first = row0 + i * tokens, last = min(first + tokens, at.len_q) - 1;
             const int32_t keys = p.causal ? min(at.len_k, max(last + ahead + 1, 0)) : at.len_k;
             if (first < at.len_q) n[i] = (keys + kRows - 1) / kRows;
+        }
+        if (p.chunk > 0) {
+            j0 = at.part * p.chunk;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) n[i] = max(min(n[i] - j0, p.chunk), 0);
         }
     }
     const int32_t most = max(n[0], n[1]);
@@ -363,17 +406,18 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     if (warp == 0) {
         // ---------------- TMA producer
         if (elect_one() && most > 0) {
-            const int32_t key_head = head / p.group;
+            const int32_t key_head = head0 / p.group;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (n[i] > 0)
-                    load_tile<DP>(smem + i * Shape::kTileBytes, &p.q, &q_full[i], head, at.q0 + row0 + i * kRows);
+                    load_tile<DP>(smem + i * Shape::kTileBytes, &p.q, &q_full[i], head0, at.q0 + row0 + i * tokens,
+                                  p.packing.rows());
             int armed = 0;
             for (int i = 0; i < 2 * most; ++i) {  // K and V of each key tile in turn
                 const int s = i % kStages;
                 if (i >= kStages && !wait_bounded(&empty[s], (uint32_t)(i / kStages - 1) & 1u, p.wait_ns, p.status)) break;
                 load_tile<DP>(ring + s * Shape::kTileBytes, i & 1 ? &p.v : &p.k, &full[s], key_head,
-                              at.k0 + (i >> 1) * kRows);
+                              at.k0 + (j0 + (i >> 1)) * kRows);
                 armed = i + 1;
             }
             // everything that was asked for has landed before this CTA ends
@@ -417,7 +461,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             const int sv = (2 * j + 1) % kStages;
             wait_full(2 * j + 1);
             if (!ok) break;
-            const int left = at.len_k - j * kRows;  // keys of this tile that are the sequence's
+            const int left = at.len_k - (j0 + j) * kRows;  // keys of this tile that are the sequence's
             if (left < kRows) {
                 clear_rows<DP>(ring + sv * Shape::kTileBytes, left);
                 fence_async_smem();
@@ -451,16 +495,17 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     } else if (warp >= 4) {
         // ---------------- softmax: a lane for each query, a warpgroup for each half of the keys of each query tile
         const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
-        const int32_t row = row0 + t * kRows + quad * 32 + lane;
-        const bool inside = work && row < at.len_q;
+        const int32_t r = quad * 32 + lane, row = row0 + t * tokens + r / p.packing.pack;  // place in the tile, query
+        const int32_t head = head0 + r % p.packing.pack;
+        const bool inside = work && r < p.packing.rows() && row < at.len_q;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t src = lanes + t * 128 + half * 64, acc = lanes + 256 + t * 128;
         float* mine = share + (t * 2 + half) * kRows + quad * 32 + lane;
         const float* other = share + (t * 2 + 1 - half) * kRows + quad * 32 + lane;
         const int columns = (p.dim + 15) / 16 * 16;
-        const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
-        // the least of these in the tile: its first query's
-        const int32_t least = p.causal ? min(at.len_k - 1, row0 + t * kRows + ahead) : at.len_k - 1;
+        // key that this query sees last, from the first tile's first key on, and the least of these in the query tile
+        const int32_t last = (p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1) - j0 * kRows;
+        const int32_t least = (p.causal ? min(at.len_k - 1, row0 + t * tokens + ahead) : at.len_k - 1) - j0 * kRows;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         float top = -INFINITY;  // maximum that the sums are scaled by (of the scores before `scale`)
         float shift = 0.f;      // top * scale_log2
@@ -542,23 +587,89 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             ok = warp_wait(&o_full[t], 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
-                const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0;
-                store_row(acc + from, half ? p.dim - cut : min(cut, p.dim), sum == 0.f ? 0.f : 1.f / sum,
-                          p.out.at(at.q0 + row, head) + from, inside,
-                          p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
+                const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0, width = half ? p.dim - cut : min(cut, p.dim);
+                if (p.chunk > 0)
+                    store_part(acc + from, width, p.part + (((int64_t)blockIdx.x * 2 + t) * kRows + r) * p.dim + from, inside);
+                else
+                    store_row(acc + from, width, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head) + from, inside,
+                              p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
             }
-        } else if (inside && half == 0 && n[t] == 0) {  // no key at all
+        } else if (inside && half == 0 && n[t] == 0 && p.chunk == 0) {  // no key at all
             store_zeros(p.dim, p.out.at(at.q0 + row, head));
             if (p.rest.data) store_zeros(p.dim, p.rest.at(at.q0 + row, head));
         }
-        if (inside && half == 0)
-            p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
+        if (inside && half == 0) {
+            if (p.chunk > 0)
+                p.part_stats[((int64_t)blockIdx.x * 2 + t) * kRows + r] = make_float2(shift, sum);
+            else
+                p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// The parts of a pair of query tiles joined: a warp for each row, a lane for four columns.  Of the parts' places the first
+// one's CTAs do it, several of them, for their rows in turn.
+constexpr int kJoinThreads = 256, kJoinCtas = 4;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ ForwardParams p) {
+    __shared__ Place where;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t block = (int32_t)(blockIdx.x % (uint32_t)p.head_blocks), slot = (int32_t)(blockIdx.x / (uint32_t)p.head_blocks);
+    const int32_t tokens = p.packing.tokens;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 0) {
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        if (lane == 0) where = w;
+    }
+    __syncthreads();
+    Place at = where;
+    if (at.tile < 0 || at.part > 0) return;
+    if (p.causal) at.tile = (at.len_q + 2 * tokens - 1) / (2 * tokens) - 1 - at.tile;
+    const int32_t row0 = at.tile * 2 * tokens, rows = min(2 * tokens, at.len_q - row0) * p.packing.pack;
+    for (int32_t i = blockIdx.y * (kJoinThreads / 32) + warp; i < rows; i += kJoinCtas * kJoinThreads / 32) {
+        const int32_t t = i / p.packing.rows(), r = i - t * p.packing.rows();
+        const int32_t token = at.q0 + row0 + t * tokens + r / p.packing.pack, head = block * p.packing.pack + r % p.packing.pack;
+        // part s of this row
+        auto part = [&](int s) { return (((int64_t)slot + s) * p.head_blocks + block) * 2 * kRows + t * kRows + r; };
+        // what all are scaled by: the largest of the parts' that hold anything (NaN is something)
+        float top = -INFINITY;
+        for (int s = lane; s < at.parts; s += 32) {
+            const float2 st = p.part_stats[part(s)];
+            if (st.y != 0.f) top = fmaxf(top, st.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < at.parts; ++s) {
+            const float2 st = p.part_stats[part(s)];
+            if (st.y == 0.f) continue;
+            const float by = exp2_approx(st.x - top);
+            sum = fmaf(by, st.y, sum);
+            if (lane * 4 < p.dim) {
+                const float4 x = *reinterpret_cast<const float4*>(p.part + part(s) * p.dim + lane * 4);
+                v.x = fmaf(by, x.x, v.x), v.y = fmaf(by, x.y, v.y), v.z = fmaf(by, x.z, v.z), v.w = fmaf(by, x.w, v.w);
+            }
+        }
+        const float one = sum == 0.f ? 0.f : 1.f / sum;
+        if (lane * 4 < p.dim) {
+            const float o[4] = {v.x * one, v.y * one, v.z * one, v.w * one};
+            uint2 w = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+            *reinterpret_cast<uint2*>(p.out.at(token, head) + lane * 4) = w;
+            if (p.rest.data) {
+                w = make_uint2(pack_bf16(o[0] - bf16_lo(w.x), o[1] - bf16_hi(w.x)), pack_bf16(o[2] - bf16_lo(w.y), o[3] - bf16_hi(w.y)));
+                *reinterpret_cast<uint2*>(p.rest.at(token, head) + lane * 4) = w;
+            }
+        }
+        if (lane == 0) p.lse[(int64_t)head * p.seq.tokens_q + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -613,7 +724,8 @@ struct BackwardParams {
     Rows dq, dk, dv;
     const float2* stats;
     Sequences seq;
-    int32_t heads;  // of this kernel's CTAs: key heads for dkv, query heads for dq
+    Packing packing;
+    int32_t heads;  // of this kernel's CTAs: key heads for dkv, packs of query heads for dq
     int32_t group, dim, causal;
     float scale, scale_log2;
     uint32_t* status;
@@ -704,7 +816,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<true>(p.seq, slot, kRows, p.status);
+        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -714,13 +826,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     const Place at = place_of(where);
     const bool work = at.tile >= 0;
     const int32_t key0 = at.tile * kRows, ahead = at.len_k - at.len_q;
+    const int32_t pack = p.packing.pack, tokens = p.packing.tokens;
     // query tiles that see these keys: from the one with the first query that sees the first key
     int32_t first = 0, tiles = 0;
     if (work) {
-        first = p.causal ? max(key0 - ahead, 0) / kRows : 0;
-        tiles = max((at.len_q + kRows - 1) / kRows - first, 0);
+        first = p.causal ? max(key0 - ahead, 0) / tokens : 0;
+        tiles = max((at.len_q + tokens - 1) / tokens - first, 0);
     }
-    const int32_t blocks = tiles * p.group;  // tiles of each query head in turn
+    const int32_t blocks = tiles * (p.group / pack);  // tiles of each pack of query heads in turn
     constexpr uint32_t kZ = 0, kDp = 128, kDv = 256, kDk = 384;  // columns of tensor memory
 
     if (warp == 0) {
@@ -729,15 +842,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             load_tile<DP>(sK, &p.k, &kv_full[0], head, at.k0 + key0);
             load_tile<DP>(sV, &p.v, &kv_full[1], head, at.k0 + key0);
             int q_armed = 0, d_armed = 0;
-            for (int b = 0; b < blocks; ++b) {
-                const int32_t h = head * p.group + b / tiles, token = at.q0 + (first + b % tiles) * kRows;
+            int32_t h = head * p.group, token = at.q0 + first * tokens, tile = 0;
+            for (int b = 0; b < blocks; ++b, token += tokens) {
+                if (tile++ == tiles) {  // the next heads' first
+                    tile = 1;
+                    h += pack;
+                    token = at.q0 + first * tokens;
+                }
                 if (b >= Shape::kFirst && !wait_bounded(&q_empty[Q::stage(b)], Q::parity(b - Shape::kFirst), p.wait_ns, p.status))
                     break;
-                load_tile<DP>(sQ + Q::stage(b) * Shape::kTileBytes, &p.q, &q_full[Q::stage(b)], h, token);
+                load_tile<DP>(sQ + Q::stage(b) * Shape::kTileBytes, &p.q, &q_full[Q::stage(b)], h, token, p.packing.rows());
                 q_armed = b + 1;
                 if (b >= Shape::kSecond && !wait_bounded(&d_empty[D::stage(b)], D::parity(b - Shape::kSecond), p.wait_ns, p.status))
                     break;
-                load_tile<DP>(sD + D::stage(b) * Shape::kTileBytes, &p.dout, &d_full[D::stage(b)], h, token);
+                load_tile<DP>(sD + D::stage(b) * Shape::kTileBytes, &p.dout, &d_full[D::stage(b)], h, token, p.packing.rows());
                 d_armed = b + 1;
             }
             for (int i = 0; i < 2; ++i) wait_bounded(&kv_full[i], 0, p.wait_ns, p.status);
@@ -753,11 +871,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         const int steps = (p.dim + 15) / 16;
         const uint32_t k_tile = columns_of(smem_u32(sK)), v_tile = columns_of(smem_u32(sV));
         bool ok = true;
-        // waits for a streamed tile; rows behind the sequence are cleared, as they are summed over
-        auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int b) {
+        // waits for a streamed tile; rows behind the sequence, and those that no load fills, are cleared, as they are summed
+        // over
+        const int left_last = (at.len_q - (first + tiles - 1) * tokens) * pack, left_else = p.packing.rows();
+        auto ready = [&](uint64_t* bar, uint32_t parity, uint8_t* tile, int at_tile) {
             ok = ok && warp_wait(bar, parity, p.wait_ns, p.status);
             if (!ok) return;
-            const int left = at.len_q - (first + b % tiles) * kRows;
+            const int left = at_tile == tiles - 1 ? left_last : left_else;
             if (left < kRows) {
                 clear_rows<DP>(tile, left);
                 fence_async_smem();
@@ -765,9 +885,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             }
             tc_fence_after();
         };
+        int next = 0;  // query tile of the block whose scores are made next
         auto make_z = [&](int b) {
             uint8_t* tile = sQ + Q::stage(b) * Shape::kTileBytes;
-            ready(&q_full[Q::stage(b)], Q::parity(b), tile, b);
+            ready(&q_full[Q::stage(b)], Q::parity(b), tile, next);
             if (ok && elect_one()) {
                 const uint32_t q_tile = columns_of(smem_u32(tile));
 #pragma unroll
@@ -778,7 +899,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         };
         auto make_dp = [&](int b) {
             uint8_t* tile = sD + D::stage(b) * Shape::kTileBytes;
-            ready(&d_full[D::stage(b)], D::parity(b), tile, b);
+            ready(&d_full[D::stage(b)], D::parity(b), tile, next);
+            next = next + 1 == tiles ? 0 : next + 1;
             if (ok && elect_one()) {
                 const uint32_t d_tile = columns_of(smem_u32(tile));
 #pragma unroll
@@ -821,15 +943,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         warp_wait(done, 0, p.wait_ns, p.status);
     } else if (warp == 2) {
         // ---------------- the queries' statistics
-        for (int b = 0; b < blocks; ++b) {
+        int32_t q = first * tokens, tile = 0, behind[kRows / 32];  // this lane's rows: token in the tile
+        const float2* from[kRows / 32];
+#pragma unroll
+        for (int i = 0; i < kRows / 32; ++i) {
+            const int r = i * 32 + lane;
+            behind[i] = r < p.packing.rows() ? r / pack : 1 << 30;
+            from[i] = p.stats + (int64_t)(head * p.group + r % pack) * p.seq.tokens_q + at.q0 + r / pack;
+        }
+        for (int b = 0; b < blocks; ++b, q += tokens) {
             const int s = b & 1;
+            if (tile++ == tiles) {  // the next heads' first
+                tile = 1;
+                q = first * tokens;
+#pragma unroll
+                for (int i = 0; i < kRows / 32; ++i) from[i] += (int64_t)pack * p.seq.tokens_q;
+            }
             if (b >= 2 && !warp_wait(&stats_empty[s], (uint32_t)(b / 2 - 1) & 1u, p.wait_ns, p.status)) break;
-            const int32_t h = head * p.group + b / tiles, q = (first + b % tiles) * kRows;
-            const float2* from = p.stats + (int64_t)h * p.seq.tokens_q + at.q0;
 #pragma unroll
             for (int i = 0; i < kRows / 32; ++i) {
                 const int r = i * 32 + lane;
-                const float2 v = q + r < at.len_q ? from[q + r] : make_float2(INFINITY, 0.f);
+                float2 v = make_float2(INFINITY, 0.f);
+                if (behind[i] < at.len_q - q) v = from[i][q];
                 stats[s * 2 * kRows + r] = v.x;
                 stats[s * 2 * kRows + kRows + r] = v.y;
             }
@@ -843,8 +978,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
         const uint32_t z_at = lanes + kZ + part * 32, dp_at = lanes + kDp + part * 32;
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        for (int b = 0; b < blocks; ++b) {
+        int32_t q = first * tokens, tile = 0;
+        for (int b = 0; b < blocks; ++b, q += tokens) {
             const int s = b & 1;
+            if (tile++ == tiles) tile = 1, q = first * tokens;
             ok = warp_wait(&stats_full[s], (uint32_t)(b / 2) & 1u, p.wait_ns, p.status) &&
                  warp_wait(z_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
@@ -867,9 +1004,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
                     pr[2 * i + 1] = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                 }
             }
-            const int32_t q = (first + b % tiles) * kRows;
             if (p.causal && q + ahead < key0 + kRows - 1) {  // queries below key - ahead do not see the key
-                const int hidden = key - ahead - q - part * 32;
+                const int hidden = min((key - ahead - q) * pack, kRows) - part * 32;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (2 * i < hidden) pr[i].x = 0.f;
@@ -966,7 +1102,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
+    const int32_t head0 = (int32_t)(blockIdx.x % (uint32_t)p.heads) * p.packing.pack;
+    const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)p.heads), tokens = p.packing.tokens;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qd_full[i], 1);
@@ -997,7 +1134,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, kRows, p.status);
+        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -1006,11 +1143,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     const uint32_t tmem = (uint32_t)uniform((int32_t)*tmem_holder);
     Place at = place_of(where);
     const bool work = at.tile >= 0;
-    if (work && p.causal) at.tile = (at.len_q + kRows - 1) / kRows - 1 - at.tile;  // those that see the most keys first
-    const int32_t row0 = at.tile * kRows, ahead = at.len_k - at.len_q;
+    if (work && p.causal) at.tile = (at.len_q + tokens - 1) / tokens - 1 - at.tile;  // those that see the most keys first
+    const int32_t row0 = at.tile * tokens, ahead = at.len_k - at.len_q;
     int32_t blocks = 0;
     if (work) {
-        const int32_t last = min(row0 + kRows, at.len_q) - 1;
+        const int32_t last = min(row0 + tokens, at.len_q) - 1;
         const int32_t keys = p.causal ? min(at.len_k, max(last + ahead + 1, 0)) : at.len_k;
         blocks = (keys + kRows - 1) / kRows;
     }
@@ -1019,8 +1156,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     if (warp == 0) {
         // ---------------- TMA producer
         if (elect_one() && blocks > 0) {
-            const int32_t key_head = head / p.group;
-            load_tile<DP>(sQ, &p.q, &qd_full[0], head, at.q0 + row0);
+            const int32_t key_head = head0 / p.group;
+            load_tile<DP>(sQ, &p.q, &qd_full[0], head0, at.q0 + row0, p.packing.rows());
             int k_armed = 0, v_armed = 0;
             for (int b = 0; b < blocks; ++b) {
                 const int32_t token = at.k0 + b * kRows;
@@ -1028,7 +1165,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
                     break;
                 load_tile<DP>(sK + K::stage(b) * Shape::kTileBytes, &p.k, &k_full[K::stage(b)], key_head, token);
                 k_armed = b + 1;
-                if (b == 0) load_tile<DP>(sD, &p.dout, &qd_full[1], head, at.q0 + row0);
+                if (b == 0) load_tile<DP>(sD, &p.dout, &qd_full[1], head0, at.q0 + row0, p.packing.rows());
                 if (b >= Shape::kSecond && !wait_bounded(&v_empty[V::stage(b)], V::parity(b - Shape::kSecond), p.wait_ns, p.status))
                     break;
                 load_tile<DP>(sV + V::stage(b) * Shape::kTileBytes, &p.v, &v_full[V::stage(b)], key_head, token);
@@ -1111,8 +1248,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     } else if (warp >= 4) {
         // ---------------- p and dz: a lane for each query, a warpgroup for each quarter of the keys
         const int part = (warp - 4) >> 2, quad = warp & 3;
-        const int32_t row = row0 + quad * 32 + lane;
-        const bool inside = work && row < at.len_q;
+        const int32_t r = quad * 32 + lane, row = row0 + r / p.packing.pack, head = head0 + r % p.packing.pack;
+        const bool inside = work && r < p.packing.rows() && row < at.len_q;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t dp_at = lanes + kDp + part * 32;
         const int32_t last = p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1;  // key that this query sees last
@@ -1192,7 +1329,16 @@ struct Call {
     int64_t tokens_q, tokens_k;
     Sequences seq;
     int32_t dim, group;
+    Packing packing;
 };
+
+// The divisor of the group that fills the most of a tile's 128 rows, the largest of those that fill as many.
+Packing packing_of(int group) {
+    Packing best{1, kRows};
+    for (int d = 2; d <= std::min(group, kRows); ++d)
+        if (group % d == 0 && kRows / d * d >= best.pack * best.tokens) best = {d, kRows / d};
+    return best;
+}
 
 mxfp4_status check_operand(const char* what, const char* name, const mxfp4_heads* given, int64_t tokens, int64_t dim,
                            bool written, Heads* out) {
@@ -1231,13 +1377,15 @@ mxfp4_status check_call(const char* what, const mxfp4_heads* q, const mxfp4_head
     if (!cu_q && (seqs == 0 ? tokens_q || tokens_k : tokens_q % seqs || tokens_k % seqs))
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: %lld sequences of equal lengths do not fit", what,
                             (long long)seqs);
-    // grids: tiles of 128 at most, one more for each sequence
-    if ((tokens_q / kRows + seqs + 1) * c->q.heads > INT32_MAX || (tokens_k / kRows + seqs + 1) * c->k.heads > INT32_MAX)
-        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles", what);
     c->tokens_q = tokens_q;
     c->tokens_k = tokens_k;
     c->dim = (int32_t)dim;
     c->group = c->q.heads / c->k.heads;
+    c->packing = packing_of(c->group);
+    // grids: a place for each tile, and one more for each sequence
+    if ((tokens_q / c->packing.tokens + seqs + 1) * (c->q.heads / c->packing.pack) > INT32_MAX ||
+        (tokens_k / kRows + seqs + 1) * c->k.heads > INT32_MAX)
+        return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: too many tiles", what);
     c->seq = {cu_q, cu_k, (int32_t)seqs, (int32_t)tokens_q, (int32_t)tokens_k,
               seqs && !cu_q ? (int32_t)(tokens_q / seqs) : 0, seqs && !cu_q ? (int32_t)(tokens_k / seqs) : 0};
     return MXFP4_OK;
@@ -1259,6 +1407,31 @@ int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
     return (int64_t)c.seq.count * ((len + rows - 1) / rows);
 }
 
+// Whether the keys of a pair of query tiles are shared out over several CTAs: where the pairs leave more than half of the SMs
+// without one and sequences have eight key tiles or more on the average.  A part is then `chunk` key tiles, so many that
+// there is about one part for each SM (a CTA's start and end cost as much as some five key tiles), but four at least.
+// `places`: of all parts, no fewer than there are whatever the sequences' lengths.
+constexpr int kSms = 152;  // of a GB300: the workspace does not depend on the device
+struct Split {
+    int32_t chunk;  // 0: none
+    int64_t places;
+};
+Split split_of(int64_t q_tokens, int64_t k_tokens, int64_t q_heads, int64_t k_heads, int64_t seqs) {
+    Split s{0, 0};
+    if (q_tokens <= 0 || k_tokens <= 0 || q_heads <= 0 || k_heads <= 0 || seqs <= 0 || q_heads % k_heads) return s;
+    const Packing packing = packing_of((int)std::min<int64_t>(q_heads / k_heads, 65535));
+    const int64_t blocks = q_heads / packing.pack, pairs = q_tokens / (2 * packing.tokens) + seqs;
+    const int64_t tiles = k_tokens / kRows;  // of keys, and one more for each sequence
+    if (2 * pairs * blocks > kSms || tiles < 8 * seqs) return s;
+    // one pair of query tiles in each sequence, or all in one that has all the keys
+    const bool one = q_tokens <= 2 * packing.tokens;
+    const int64_t work = one ? tiles * blocks : tiles * blocks * pairs;
+    s.chunk = (int32_t)std::max<int64_t>(4, (work + kSms - 1) / kSms);
+    s.places = one ? tiles / s.chunk + 2 * seqs : pairs * (tiles / s.chunk + 2);
+    return s;
+}
+size_t part_bytes(int64_t dim) { return 2 * kRows * ((size_t)dim * sizeof(float) + sizeof(float2)); }
+
 template <class Params, class Kern>
 cudaError_t launch_tiles(Kern kern, DeviceSlots& ready, const Params& p, int64_t ctas, int threads, int smem,
                          cudaStream_t s) {
@@ -1273,8 +1446,8 @@ cudaError_t launch_tiles(Kern kern, DeviceSlots& ready, const Params& p, int64_t
 }
 
 // Tensors of no tokens have no map: no CTA loads from them.
-bool map_of(CUtensorMap* map, const Heads& h, int64_t tokens, int64_t dim) {
-    return tokens == 0 || encode_heads_map(map, h.data, tokens, h.heads, dim, h.token_stride, h.head_stride, kRows);
+bool map_of(CUtensorMap* map, const Heads& h, int64_t tokens, int64_t dim, Packing box = {1, kRows}) {
+    return tokens == 0 || encode_heads_map(map, h.data, tokens, h.heads, dim, h.token_stride, h.head_stride, box.pack, box.tokens);
 }
 
 Rows rows_of(const Heads& h) { return {static_cast<bf16*>(h.data), h.token_stride, h.head_stride}; }
@@ -1284,11 +1457,19 @@ Rows rows_of(const Heads& h) { return {static_cast<bf16*>(h.data), h.token_strid
 
 using namespace mx;
 
+extern "C" size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t head_dim, int64_t q_heads,
+                                                  int64_t k_heads, int64_t seqs) {
+    const Split s = split_of(q_tokens, k_tokens, q_heads, k_heads, seqs);
+    if (s.chunk == 0 || head_dim <= 0 || head_dim > 128) return 0;
+    const Packing packing = packing_of((int)std::min<int64_t>(q_heads / k_heads, 65535));
+    return (size_t)(s.places * (q_heads / packing.pack)) * part_bytes(head_dim);
+}
+
 extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                         int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
                                         const int32_t* cu_k, int64_t seqs, int causal, float scale,
-                                        const mxfp4_heads* out, const mxfp4_heads* rest, float* lse,
-                                        mxfp4_stream_t stream) {
+                                        const mxfp4_heads* out, const mxfp4_heads* rest, float* lse, void* ws,
+                                        size_t ws_bytes, mxfp4_stream_t stream) {
     const char* what = "attention";
     Call c{};
     mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
@@ -1297,29 +1478,48 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     if (q_tokens == 0 || seqs == 0) return record_error(MXFP4_OK, "%s", "");
     if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
     if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
+    const Split split = split_of(q_tokens, k_tokens, c.q.heads, c.k.heads, seqs);
+    if (split.chunk > 0) {
+        const size_t need = mxfp4_attention_workspace_bytes(q_tokens, k_tokens, head_dim, c.q.heads, c.k.heads, seqs);
+        if (!ws || ws_bytes < need)
+            return record_error(MXFP4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, need);
+        if (reinterpret_cast<uintptr_t>(ws) % 256)
+            return record_error(MXFP4_ERR_MISALIGNED, "%s: workspace not 256-byte aligned", what);
+    }
     if ((st = ensure_device())) return st;
     ForwardParams p{};
-    if (!map_of(&p.q, c.q, q_tokens, head_dim) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
+    if (!map_of(&p.q, c.q, q_tokens, head_dim, c.packing) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
         !map_of(&p.v, c.v, k_tokens, head_dim))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     p.out = rows_of(c.out);
     p.rest = rows_of(c.rest);
     p.lse = lse;
     p.seq = c.seq;
-    p.q_heads = c.q.heads;
+    p.packing = c.packing;
+    p.head_blocks = c.q.heads / c.packing.pack;
     p.group = c.group;
     p.dim = c.dim;
     p.causal = causal;
+    p.chunk = split.chunk;
+    if (p.chunk > 0) {
+        p.part = static_cast<float*>(ws);
+        p.part_stats = reinterpret_cast<float2*>(p.part + split.places * p.head_blocks * 2 * kRows * head_dim);
+    }
     p.scale_log2 = scale * kLog2e;
     p.status = device_status_ptr();
     p.wait_ns = wait_limit_ns();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t ctas = places(c, q_tokens, c.seq.len_q, 2 * kRows) * c.q.heads;
+    const int64_t ctas =
+        (p.chunk > 0 ? split.places : places(c, q_tokens, c.seq.len_q, 2 * c.packing.tokens)) * p.head_blocks;
     static DeviceSlots wide, narrow;
-    const cudaError_t e =
+    cudaError_t e =
         c.dim > 64 ? launch_tiles(attention_kernel<128>, wide, p, ctas, kForwardThreads, ForwardShape<128>::kSmem, s)
                    : launch_tiles(attention_kernel<64>, narrow, p, ctas, kForwardThreads, ForwardShape<64>::kSmem, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    if (p.chunk > 0) {
+        e = launch_overlapped(join_kernel, dim3((unsigned)ctas, kJoinCtas), dim3(kJoinThreads), 0, s, 1, true, p);
+        if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s join launch: %s", what, cudaGetErrorString(e));
+    }
     return record_error(MXFP4_OK, "%s", "");
 }
 
@@ -1361,14 +1561,15 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     if ((q_tokens == 0 && k_tokens == 0) || seqs == 0) return record_error(MXFP4_OK, "%s", "");
     if ((st = ensure_device())) return st;
     BackwardParams p{};
-    if (!map_of(&p.q, c.q, q_tokens, head_dim) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
-        !map_of(&p.v, c.v, k_tokens, head_dim) || !map_of(&p.dout, d, q_tokens, head_dim))
+    if (!map_of(&p.q, c.q, q_tokens, head_dim, c.packing) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
+        !map_of(&p.v, c.v, k_tokens, head_dim) || !map_of(&p.dout, d, q_tokens, head_dim, c.packing))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     p.dq = rows_of(gq);
     p.dk = rows_of(gk);
     p.dv = rows_of(gv);
     p.stats = static_cast<const float2*>(ws);
     p.seq = c.seq;
+    p.packing = c.packing;
     p.group = c.group;
     p.dim = c.dim;
     p.causal = causal;
@@ -1394,8 +1595,8 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     e = c.dim > 64 ? launch_tiles(attention_dkv_kernel<128>, slots[0], p, ctas, kDkvThreads, smem, s)
                    : launch_tiles(attention_dkv_kernel<64>, slots[1], p, ctas, kDkvThreads, smem, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dkv launch: %s", what, cudaGetErrorString(e));
-    p.heads = c.q.heads;
-    ctas = places(c, q_tokens, c.seq.len_q, kRows) * c.q.heads;
+    p.heads = c.q.heads / c.packing.pack;
+    ctas = places(c, q_tokens, c.seq.len_q, c.packing.tokens) * p.heads;
     e = c.dim > 64 ? launch_tiles(attention_dq_kernel<128>, slots[2], p, ctas, kDqThreads, smem, s)
                    : launch_tiles(attention_dq_kernel<64>, slots[3], p, ctas, kDqThreads, smem, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dq launch: %s", what, cudaGetErrorString(e));

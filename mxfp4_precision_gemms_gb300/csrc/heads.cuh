@@ -6,9 +6,10 @@
 
 namespace mx {
 
-// 3D tensor map over bf16 heads (mxfp4_api.cu): box = 64 elements of one head x box_rows tokens, 128-byte swizzle.
+// 3D tensor map over bf16 heads (mxfp4_api.cu): box = 64 elements x box_heads heads x box_tokens tokens,
+// 128-byte swizzle.
 bool encode_heads_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride,
-                      int64_t head_stride, uint32_t box_rows);
+                      int64_t head_stride, uint32_t box_heads, uint32_t box_tokens);
 
 // A descriptor whose strides have a meaning: that of a single token or head is the row itself.
 struct Heads {

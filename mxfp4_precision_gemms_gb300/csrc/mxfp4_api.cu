@@ -201,17 +201,17 @@ bool encode_bf16_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols
            CUDA_SUCCESS;
 }
 
-// 3D tensor map over bf16 heads [tokens, heads, dim] (strides in elements): box = 64 elements of one head x box_rows
-// tokens, 128-byte swizzle, zero fill outside.
+// 3D tensor map over bf16 heads [tokens, heads, dim] (strides in elements): box = 64 elements x box_heads heads x
+// box_tokens tokens, 128-byte swizzle, zero fill outside.
 bool encode_heads_map(CUtensorMap* map, const void* p, int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride,
-                      int64_t head_stride, uint32_t box_rows) {
+                      int64_t head_stride, uint32_t box_heads, uint32_t box_tokens) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
     // the stride of a dimension of one has no meaning, but has to be a valid one
     const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)((heads > 1 ? head_stride : dim) * 2),
                                    (cuuint64_t)((tokens > 1 ? token_stride : dim) * 2)};
-    const cuuint32_t box[3] = {64, 1, box_rows};
+    const cuuint32_t box[3] = {64, box_heads, box_tokens};
     const cuuint32_t estr[3] = {1, 1, 1};
     return (t_encode_result = f(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

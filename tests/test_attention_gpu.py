@@ -94,3 +94,24 @@ def test_equal_lengths_without_a_list():
     a = _check(torch, q, k, v, do, [190] * 3, [260] * 3, True, listed=False)
     b = _check(torch, q, k, v, do, [190] * 3, [260] * 3, True)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [(8, 2), (3, 3), (7, 1)])
+def test_few_queries_over_many_keys(heads, causal):
+    """Keys shared out over several CTAs, in as many parts for the shortest sequence as for the longest."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    q_lens, k_lens = [1, 1, 0, 5, 1, 2], [2000, 700, 900, 3000, 90, 0]
+    for D in (64, 72, 128):
+        assert mx.lib().mxfp4_attention_workspace_bytes(sum(q_lens), sum(k_lens), D, *heads, len(q_lens)) > 0
+        q, k, v, do = _inputs(torch, q_lens, k_lens, *heads, D, 3, 7, lean=2.0)
+        _check(torch, q, k, v, do, q_lens, k_lens, causal)
+
+
+@pytest.mark.parametrize("heads", [(65, 1), (130, 1), (26, 2), (96, 1), (254, 2)])
+def test_groups_that_fill_no_tile(heads):
+    torch = gpu_ready()
+    q, k, v, do = _inputs(torch, [3, 40], [50, 160], *heads, 32, 0, 8)
+    _check(torch, q, k, v, do, [3, 40], [50, 160], True)

@@ -85,6 +85,22 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 16 lanes x 32 columns: thread t has columns 8i + 2(t % 4) and the next one of lanes t / 4 (r[4i], r[4i + 1]) and
+// t / 4 + 8 (r[4i + 2], r[4i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// 16 lanes x 16 columns: thread t has column 4i + t % 4 of lanes t / 4 (r[2i]) and t / 4 + 8 (r[2i + 1]).
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Barriers of a part of the block (id 0 is __syncthreads).
@@ -766,7 +782,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     uint8_t* sV = smem + Shape::kTileBytes;
     uint8_t* sQ = smem + Shape::kOffFirst;
     uint8_t* sD = smem + Shape::kOffSecond;
-    float* stats = reinterpret_cast<float*>(smem + Shape::kOffStats);  // [2][lse, delta][128]
+    float* stats = reinterpret_cast<float*>(smem + Shape::kOffStats);  // [2][-lse, -delta][128]
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar);  // [2]
     uint64_t* q_full = kv_full + 2;
     uint64_t* q_empty = q_full + Shape::kFirst;
@@ -965,17 +981,23 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
                 const int r = i * 32 + lane;
                 float2 v = make_float2(INFINITY, 0.f);
                 if (behind[i] < at.len_q - q) v = from[i][q];
-                stats[s * 2 * kRows + r] = v.x;
-                stats[s * 2 * kRows + kRows + r] = v.y;
+                stats[s * 2 * kRows + r] = -v.x;
+                stats[s * 2 * kRows + kRows + r] = -v.y;
             }
             mbar_arrive(&stats_full[s]);
         }
     } else if (warp >= 4) {
-        // ---------------- p and dz: a lane for each key, a warpgroup for each quarter of the queries
+        // ---------------- p and dz: a warpgroup for each quarter of the queries, a warp for 32 keys.  A thread holds two
+        // neighbouring queries of every eight, for four keys: the queries' statistics, which differ along a row here, are
+        // then read from shared memory once for four keys instead of for each (8 instead of 48 cycles a warp and block, of
+        // which the tensor cores' operands already take 1536, and the loads 512, in a block of 2048).
         const int part = (warp - 4) >> 2, quad = warp & 3;
         const int32_t key = key0 + quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t z_at = lanes + kZ + part * 32, dp_at = lanes + kDp + part * 32;
+        constexpr uint32_t kLower = 16u << 16;  // the other 16 lanes
+        const int column = 2 * (lane & 3);      // of each eight
+        const int32_t upper = key0 + quad * 32 + (lane >> 2);  // key of the thread's first row; the others 8 apart
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         int32_t q = first * tokens, tile = 0;
@@ -986,57 +1008,64 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
                  warp_wait(z_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            const float4* lse = reinterpret_cast<const float4*>(stats + s * 2 * kRows + part * 32);
-            const float4* delta = lse + kRows / 4;
-            float2 pr[16];
-            {
-                uint32_t z[32];
-                tmem_ld_32x32b_x32(z_at, z);
-                tmem_ld_wait();
+            const float* lse = stats + s * 2 * kRows + part * 32 + column;  // negated
+            const float* delta = lse + kRows;
+            uint32_t z[2][16];
+            tmem_ld_16x256b_x4(z_at, z[0]);
+            tmem_ld_16x256b_x4(z_at + kLower, z[1]);
+            float2 l[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 l = lse[i];
-                    const float2 e = f2_fma(make_float2(__uint_as_float(z[4 * i]), __uint_as_float(z[4 * i + 1])), scale2,
-                                            make_float2(-l.x, -l.y));
-                    const float2 f = f2_fma(make_float2(__uint_as_float(z[4 * i + 2]), __uint_as_float(z[4 * i + 3])), scale2,
-                                            make_float2(-l.z, -l.w));
-                    pr[2 * i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                    pr[2 * i + 1] = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+            for (int i = 0; i < 4; ++i) l[i] = *reinterpret_cast<const float2*>(lse + 8 * i);
+            tmem_ld_wait();
+            float2 pr[4][4];  // [row][eight]
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t* v = z[r >> 1] + 4 * i + 2 * (r & 1);
+                    const float2 e = f2_fma(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale2, l[i]);
+                    pr[r][i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                 }
-            }
             if (p.causal && q + ahead < key0 + kRows - 1) {  // queries below key - ahead do not see the key
-                const int hidden = min((key - ahead - q) * pack, kRows) - part * 32;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (2 * i < hidden) pr[i].x = 0.f;
-                    if (2 * i + 1 < hidden) pr[i].y = 0.f;
+                for (int r = 0; r < 4; ++r) {
+                    const int hidden = min((upper + 8 * r - ahead - q) * pack, kRows) - part * 32 - column;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (8 * i < hidden) pr[r][i].x = 0.f;
+                        if (8 * i + 1 < hidden) pr[r][i].y = 0.f;
+                    }
                 }
             }
-            uint32_t w[16];
+            uint32_t w[2][8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(pr[i].x, pr[i].y);
-            tmem_st_32x32b_x16(z_at, w);
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[r >> 1][2 * i + (r & 1)] = pack_bf16(pr[r][i].x, pr[r][i].y);
+            tmem_st_16x128b_x4(z_at, w[0]);
+            tmem_st_16x128b_x4(z_at + kLower, w[1]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] = *reinterpret_cast<const float2*>(delta + 8 * i);
             ok = warp_wait(dp_full, (uint32_t)b & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
-            uint32_t dp[32];
-            tmem_ld_32x32b_x32(dp_at, dp);
+            tmem_ld_16x256b_x4(dp_at, z[0]);
+            tmem_ld_16x256b_x4(dp_at + kLower, z[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 l = delta[i];
-                const float2 e = f2_mul(pr[2 * i], f2_sub(make_float2(__uint_as_float(dp[4 * i]), __uint_as_float(dp[4 * i + 1])),
-                                                          make_float2(l.x, l.y)));
-                const float2 f = f2_mul(pr[2 * i + 1], f2_sub(make_float2(__uint_as_float(dp[4 * i + 2]), __uint_as_float(dp[4 * i + 3])),
-                                                              make_float2(l.z, l.w)));
-                w[2 * i] = pack_bf16(e.x, e.y);
-                w[2 * i + 1] = pack_bf16(f.x, f.y);
-            }
-            tmem_st_32x32b_x16(dp_at, w);
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t* v = z[r >> 1] + 4 * i + 2 * (r & 1);
+                    const float2 e = f2_mul(pr[r][i], f2_add(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), l[i]));
+                    w[r >> 1][2 * i + (r & 1)] = pack_bf16(e.x, e.y);
+                }
+            tmem_st_16x128b_x4(dp_at, w[0]);
+            tmem_st_16x128b_x4(dp_at + kLower, w[1]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -1409,7 +1438,7 @@ int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
 
 // Whether the keys of a pair of query tiles are shared out over several CTAs: where the pairs leave more than half of the SMs
 // without one and sequences have eight key tiles or more on the average.  A part is then `chunk` key tiles, so many that
-// there is about one part for each SM (a CTA's start and end cost as much as some five key tiles), but four at least.
+// there is a part for each SM at most (a CTA's start and end cost as much as some five key tiles), but four at least.
 // `places`: of all parts, no fewer than there are whatever the sequences' lengths.
 constexpr int kSms = 152;  // of a GB300: the workspace does not depend on the device
 struct Split {
@@ -1425,8 +1454,8 @@ Split split_of(int64_t q_tokens, int64_t k_tokens, int64_t q_heads, int64_t k_he
     if (2 * pairs * blocks > kSms || tiles < 8 * seqs) return s;
     // one pair of query tiles in each sequence, or all in one that has all the keys
     const bool one = q_tokens <= 2 * packing.tokens;
-    const int64_t work = one ? tiles * blocks : tiles * blocks * pairs;
-    s.chunk = (int32_t)std::max<int64_t>(4, (work + kSms - 1) / kSms);
+    const int64_t parts = std::max<int64_t>(1, one ? kSms / blocks - seqs : kSms / (blocks * pairs) - 1);
+    s.chunk = (int32_t)std::max<int64_t>(4, (tiles + parts - 1) / parts);
     s.places = one ? tiles / s.chunk + 2 * seqs : pairs * (tiles / s.chunk + 2);
     return s;
 }

@@ -1100,7 +1100,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
 }
 
 // Queries' gradients.  z and dp of the next block are made while dz of this one is; z has two places, and dz takes its own
-// block's, so that dp is free again as soon as it has been read.
+// block's, so that dp is free again as soon as it has been read.  dz(b + 1) may be ready before the lane that issues looks for
+// dz(b): two barriers, as a barrier's parity tells neighbouring phases apart and no more.
 constexpr int kDqThreads = 128 + 512;
 
 template <int DP>
@@ -1125,8 +1126,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     uint64_t* z_full = v_empty + Shape::kSecond;  // [2]
     uint64_t* dp_full = z_full + 2;
     uint64_t* dp_read = dp_full + 1;
-    uint64_t* dz_full = dp_read + 1;
-    uint64_t* done = dz_full + 1;
+    uint64_t* dz_full = dp_read + 1;  // [2]
+    uint64_t* done = dz_full + 2;
     Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
 
@@ -1137,6 +1138,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qd_full[i], 1);
             mbar_init(&z_full[i], 1);
+            mbar_init(&dz_full[i], 16);
         }
         for (int i = 0; i < Shape::kFirst; ++i) {
             mbar_init(&k_full[i], 1);
@@ -1148,7 +1150,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         }
         mbar_init(dp_full, 1);
         mbar_init(dp_read, 16);
-        mbar_init(dz_full, 16);
         mbar_init(done, 1);
         fence_mbar_init();
         prefetch_tmap(&p.q);
@@ -1260,7 +1261,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
                 tc_fence_after();
                 make_dp(b + 1);
             }
-            ok = ok && warp_wait(dz_full, (uint32_t)b & 1u, p.wait_ns, p.status);
+            ok = ok && warp_wait(&dz_full[b & 1], (uint32_t)(b / 2) & 1u, p.wait_ns, p.status);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -1330,7 +1331,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dz_full);
+            if (lane == 0) mbar_arrive(&dz_full[b & 1]);
         }
         bf16* to = p.dq.at(at.q0 + row, head);
         if (blocks > 0) {

@@ -115,3 +115,23 @@ def test_groups_that_fill_no_tile(heads):
     torch = gpu_ready()
     q, k, v, do = _inputs(torch, [3, 40], [50, 160], *heads, 32, 0, 8)
     _check(torch, q, k, v, do, [3, 40], [50, 160], True)
+
+
+def test_the_same_bits_on_every_run():
+    """Hundreds of short calls one behind the other, in which the warps of a block overtake each other in every way that
+    their barriers allow: no wait runs out, and every call gives what the first gave."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    for D, lens in ((128, [288, 400, 1100]), (64, [290, 129, 520])):
+        q, k, v, do = _inputs(torch, lens, lens, 32, 8, D, 0, 9)
+        cu = _edges(torch, lens)
+        first = None
+        for _ in range(300):
+            out, lse, rest = mx.attention(q, k, v, cu_q=cu, rest=True)
+            got = (out, lse, rest, *mx.attention_grad(q, k, v, out, lse, do, cu_q=cu, rest=rest))
+            if first is None:
+                first = got
+            else:
+                assert all(torch.equal(x, y) for x, y in zip(got, first))
+        assert mx.device_status() == 0

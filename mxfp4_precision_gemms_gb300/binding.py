@@ -778,6 +778,13 @@ class Rope:
         self.ref = ctypes.addressof(self.c)
 
 
+def _device_for(x: torch.Tensor, name: str) -> int:
+    """The current device, for a call whose first tensor is x (there may be none for one on the host)."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return _current_device()
+
+
 def _heads(x: torch.Tensor, name: str, dev: int) -> tuple[int, int, int, int, int, int, int]:
     """A [tokens, heads, head_dim] fp32 / bf16 tensor of device `dev` as the four words of an mxfp4_heads, and its shape."""
     kind = _OUT_OF.get(x.dtype)
@@ -847,7 +854,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: Rope | None = No
     rows; k may be None) divided by its root mean square and multiplied by its gain (fp32 [head_dim]; None: left as it
     is), then rotated by `rope` at `positions` ([tokens] or [axes, tokens], int32 or int64).  Returns (q_out, k_out); each
     may be its input, for in place."""
-    dev = _current_device()
+    dev = _device_for(q, "q")
     *wq, n, heads, dim = _heads(q, "q", dev)
     kind, device = wq[3] >> 32, q.device
     at, ids_kind, axes = _positions(positions, rope, n)
@@ -876,7 +883,7 @@ def qk_norm_rope_grad(q: torch.Tensor | None, k: torch.Tensor | None, dq: torch.
     """mxfp4_qk_norm_rope_grad: gradients (dq_in, dk_in, dq_gain, dk_gain) of qk_norm_rope's inputs and gains from dq and
     dk, those of its outputs (dk None: queries alone).  q and k, its inputs, are read where there is a gain and may be
     None otherwise.  dq_in and dk_in may be dq and dk themselves; gains False leaves the gains' gradients out."""
-    dev = _current_device()
+    dev = _device_for(dq, "dq")
     *wdq, n, heads, dim = _heads(dq, "dq", dev)
     kind, device = wdq[3] >> 32, dq.device
     at, ids_kind, axes = _positions(positions, rope, n)
@@ -960,7 +967,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     [q_heads, q_tokens], which attention_grad takes.  rest: returns (out, lse, rest), rest like out, what rounding left of
     it, for exact gradients.  Tokens outside of all sequences: new outputs hold zeros there, given ones are left as they
     were."""
-    dev = _current_device()
+    dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
     device, zero = q.device, cu_q is not None
@@ -991,7 +998,7 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out, lse
     and rest as it returned them (without rest the gradients carry out's rounding), the others as it was given.  dq, dk
     and dv may be slices of one buffer.  Tokens outside of all sequences: as in attention."""
-    dev = _current_device()
+    dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
     device, zero = q.device, cu_q is not None

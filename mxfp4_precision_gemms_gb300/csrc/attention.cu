@@ -1475,9 +1475,12 @@ cudaError_t launch_tiles(Kern kern, DeviceSlots& ready, const Params& p, int64_t
     return launch_overlapped(kern, dim3((unsigned)ctas), dim3((unsigned)threads), (size_t)smem, s, 1, true, p);
 }
 
-// Tensors of no tokens have no map: no CTA loads from them.
-bool map_of(CUtensorMap* map, const Heads& h, int64_t tokens, int64_t dim, Packing box = {1, kRows}) {
-    return tokens == 0 || encode_heads_map(map, h.data, tokens, h.heads, dim, h.token_stride, h.head_stride, box.pack, box.tokens);
+// Of a tensor of no tokens nothing is loaded: its map is that of `other`.
+bool map_of(CUtensorMap* map, const Heads& h, int64_t tokens, const Heads& other, int64_t other_tokens, int64_t dim,
+            Packing box = {1, kRows}) {
+    const Heads& x = tokens > 0 ? h : other;
+    return encode_heads_map(map, x.data, tokens > 0 ? tokens : other_tokens, x.heads, dim, x.token_stride, x.head_stride,
+                            (uint32_t)box.pack, (uint32_t)box.tokens);
 }
 
 Rows rows_of(const Heads& h) { return {static_cast<bf16*>(h.data), h.token_stride, h.head_stride}; }
@@ -1518,8 +1521,8 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     }
     if ((st = ensure_device())) return st;
     ForwardParams p{};
-    if (!map_of(&p.q, c.q, q_tokens, head_dim, c.packing) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
-        !map_of(&p.v, c.v, k_tokens, head_dim))
+    if (!map_of(&p.q, c.q, q_tokens, c.q, q_tokens, head_dim, c.packing) ||
+        !map_of(&p.k, c.k, k_tokens, c.q, q_tokens, head_dim) || !map_of(&p.v, c.v, k_tokens, c.q, q_tokens, head_dim))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     p.out = rows_of(c.out);
     p.rest = rows_of(c.rest);
@@ -1591,8 +1594,9 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     if ((q_tokens == 0 && k_tokens == 0) || seqs == 0) return record_error(MXFP4_OK, "%s", "");
     if ((st = ensure_device())) return st;
     BackwardParams p{};
-    if (!map_of(&p.q, c.q, q_tokens, head_dim, c.packing) || !map_of(&p.k, c.k, k_tokens, head_dim) ||
-        !map_of(&p.v, c.v, k_tokens, head_dim) || !map_of(&p.dout, d, q_tokens, head_dim, c.packing))
+    if (!map_of(&p.q, c.q, q_tokens, c.k, k_tokens, head_dim, c.packing) ||
+        !map_of(&p.k, c.k, k_tokens, c.q, q_tokens, head_dim) || !map_of(&p.v, c.v, k_tokens, c.q, q_tokens, head_dim) ||
+        !map_of(&p.dout, d, q_tokens, c.k, k_tokens, head_dim, c.packing))
         return record_error(MXFP4_ERR_CUDA, "%s: tensor map encoding failed", what);
     p.dq = rows_of(gq);
     p.dk = rows_of(gk);

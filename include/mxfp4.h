@@ -559,8 +559,8 @@ mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k,
                                      const mxfp4_heads* dk_in, float* dq_gain, float* dk_gain, void* ws,
                                      size_t ws_bytes, mxfp4_stream_t stream);
 
-/* Workspace bytes of mxfp4_attention: above 0 where the queries are few and their keys are shared out over several
- * CTAs, whose parts are then joined. */
+/* Workspace bytes of mxfp4_attention: above 0 where the queries are few and their keys (1024 or more a sequence on the
+ * average) are shared out over several CTAs, whose parts are then joined. */
 size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t head_dim, int64_t q_heads,
                                        int64_t k_heads, int64_t seqs);
 
@@ -578,7 +578,8 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * outside of all hold reaches nothing.  (Of its own sequence, a hidden key's infinite or NaN v may reach
  * queries up to 127 before it, as 0 times it.)
  * out: [q_tokens, q_heads, head_dim] bf16; lse: device fp32 [q_heads, q_tokens], natural logarithm, what
- * mxfp4_attention_grad takes.  Rows outside of all sequences are left as they were, in both.
+ * mxfp4_attention_grad takes.  Rows outside of all sequences (in front of the first and behind the last) are left as
+ * they were in all outputs or, with zero_outside 1, become 0.
  * rest: NULL, or [q_tokens, q_heads, head_dim] bf16, which receives what rounding left of out (out + rest is the
  * output to 16 bits): what the gradient is exact with.
  * ws: device, 256-byte aligned, mxfp4_attention_workspace_bytes bytes (may be NULL where those are 0).
@@ -586,7 +587,7 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * The same bits on every run. */
 mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v, int64_t q_tokens,
                              int64_t k_tokens, int64_t head_dim, const int32_t* cu_q, const int32_t* cu_k,
-                             int64_t seqs, int causal, float scale, const mxfp4_heads* out,
+                             int64_t seqs, int causal, float scale, int zero_outside, const mxfp4_heads* out,
                              const mxfp4_heads* rest, float* lse, void* ws, size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Workspace bytes of mxfp4_attention_grad: two fp32 statistics of each query. */
@@ -596,15 +597,14 @@ size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
  *   dv = p^T dout,  dz = p (dout v^T - dout . out),  dq = scale dz k,  dk = scale dz^T q
  * q to scale: as given to it, out, rest and lse as returned by it; dout: the gradient of out, bf16.  rest may be NULL:
  * dout . out then carries out's rounding, and dz of a key that has most of a row's probability is off by it.
- * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences are left as they
- * were.  dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are
+ * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are
  * rounded to bf16 for the tensor cores.  No atomic additions: the same bits on every run.
  * ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                   const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,
                                   const mxfp4_heads* dout, int64_t q_tokens, int64_t k_tokens, int64_t head_dim,
                                   const int32_t* cu_q, const int32_t* cu_k, int64_t seqs, int causal, float scale,
-                                  const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws,
+                                  int zero_outside, const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws,
                                   size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the current device's status word:

@@ -133,9 +133,9 @@ def lib():
                 "mxfp4_qk_norm_rope_grad_workspace_bytes": ([I64, I64], S),
                 "mxfp4_qk_norm_rope_grad": ([P, P, P, P, I64, I64, P, P, F, P, P, I, I64, P, P, P, P, P, S, P], I),
                 "mxfp4_attention_workspace_bytes": ([I64, I64, I64, I64, I64, I64], S),
-                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
+                "mxfp4_attention": ([P, P, P, I64, I64, I64, P, P, I64, I, F, I, P, P, P, P, S, P], I),
                 "mxfp4_attention_grad_workspace_bytes": ([I64, I64], S),
-                "mxfp4_attention_grad": ([P, P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, P, P, P, P, S, P], I),
+                "mxfp4_attention_grad": ([P, P, P, P, P, P, P, I64, I64, I64, P, P, I64, I, F, I, P, P, P, P, S, P], I),
                 "mxfp4_device_status": ([P], I),
                 "mxfp4_set_wait_limit_ns": ([ctypes.c_uint64], None),
                 "mxfp4_test_inject_gemm_fault": ([I], None),
@@ -797,18 +797,11 @@ def _heads(x: torch.Tensor, name: str, dev: int) -> tuple[int, int, int, int, in
                      "current CUDA device")
 
 
-def _like(out, shape, kind: int, name: str, device, dev: int, stream, zero: bool = False):
-    """A caller's output heads, checked, or new ones (zero: filled with zeros, for a call that leaves rows out), as the
-    tensor and the words of _heads."""
+def _like(out, shape, kind: int, name: str, device, dev: int, stream):
+    """A caller's output heads, checked, or new ones, as the tensor and the words of _heads."""
     n, heads, dim = shape
     if out is None:
         out = _empty(shape, _FLOAT_OF[kind], device, stream)
-        if zero:
-            if stream is None:
-                out.zero_()
-            else:
-                with torch.cuda.stream(stream):
-                    out.zero_()
         return out, (out.data_ptr(), heads * dim, dim, heads | kind << 32)
     words = _heads(out, name, dev)
     if words[4:] != shape or words[3] >> 32 != kind:
@@ -953,6 +946,18 @@ def _attention_operands(q, k, v, dev: int):
     return wq, wk, wv, n, heads, dim, m, k_heads
 
 
+def _zero_new(given, made, stream) -> bool:
+    """Whether the call itself clears the rows outside of all sequences: only where it makes all of its outputs.  Among
+    given ones, which keep theirs, the new ones are filled with zeros here."""
+    if not any(x is not None for x in given):
+        return True
+    with torch.cuda.stream(stream):
+        for x, y in zip(given, made):
+            if x is None and y is not None:
+                y.zero_()
+    return False
+
+
 def _check_lse(lse: torch.Tensor, heads: int, n: int, dev: int):
     if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != (heads, n):
         raise ValueError(f"lse must be contiguous fp32 [{heads}, {n}] on the current CUDA device")
@@ -970,23 +975,22 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
-    device, zero = q.device, cu_q is not None
-    out, wo = _like(out, (n, heads, dim), OUT_BF16, "out", device, dev, stream, zero)
-    left, wr = _like(None, (n, heads, dim), OUT_BF16, "rest", device, dev, stream, zero) if rest else (None, _NO_HEADS)
+    device, given = q.device, (out, lse)
+    out, wo = _like(out, (n, heads, dim), OUT_BF16, "out", device, dev, stream)
+    left, wr = _like(None, (n, heads, dim), OUT_BF16, "rest", device, dev, stream) if rest else (None, _NO_HEADS)
     if lse is None:
         lse = _empty((heads, n), torch.float32, device, stream)
-        if zero:
-            with torch.cuda.stream(stream):
-                lse.zero_()
     else:
         _check_lse(lse, heads, n, dev)
     L = lib()
-    nb = L.mxfp4_attention_workspace_bytes(n, m, dim, heads, k_heads, seqs)
+    # fewer keys are never shared out
+    nb = L.mxfp4_attention_workspace_bytes(n, m, dim, heads, k_heads, seqs) if m >= 1024 * seqs else 0
     ws = _empty(nb, torch.uint8, device, stream) if nb else None
+    zero = cu_q is not None and _zero_new((*given, None), (out, lse, left), stream)
     table, to = _table(wq, wk, wv, wo, wr)
     _check(L.mxfp4_attention(to, to + 32, to + 64, n, m, dim, at_q, at_k, seqs, causal,
-                             dim ** -0.5 if scale is None else scale, to + 96, to + 128 if rest else None, lse.data_ptr(),
-                             ws.data_ptr() if nb else None, nb, _stream(stream)))
+                             dim ** -0.5 if scale is None else scale, zero, to + 96, to + 128 if rest else None,
+                             lse.data_ptr(), ws.data_ptr() if nb else None, nb, _stream(stream)))
     return (out, lse, left) if rest else (out, lse)
 
 
@@ -1001,22 +1005,23 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
-    device, zero = q.device, cu_q is not None
+    device, given = q.device, (dq, dk, dv)
     shape, k_shape = (n, heads, dim), (m, k_heads, dim)
     _, wo = _like(out, shape, OUT_BF16, "out", device, dev, stream)
     _, wd = _like(dout, shape, OUT_BF16, "dout", device, dev, stream)
     wr = _NO_HEADS if rest is None else _like(rest, shape, OUT_BF16, "rest", device, dev, stream)[1]
     _check_lse(lse, heads, n, dev)
-    dq, wdq = _like(dq, shape, OUT_BF16, "dq", device, dev, stream, zero)
-    dk, wdk = _like(dk, k_shape, OUT_BF16, "dk", device, dev, stream, zero)
-    dv, wdv = _like(dv, k_shape, OUT_BF16, "dv", device, dev, stream, zero)
+    dq, wdq = _like(dq, shape, OUT_BF16, "dq", device, dev, stream)
+    dk, wdk = _like(dk, k_shape, OUT_BF16, "dk", device, dev, stream)
+    dv, wdv = _like(dv, k_shape, OUT_BF16, "dv", device, dev, stream)
     L = lib()
     nb = L.mxfp4_attention_grad_workspace_bytes(n, heads)
     ws = _empty(nb, torch.uint8, device, stream)
+    zero = cu_q is not None and _zero_new(given, (dq, dk, dv), stream)
     table, to = _table(wq, wk, wv, wo, wr, wd, wdq, wdk, wdv)
     _check(L.mxfp4_attention_grad(to, to + 32, to + 64, to + 96, None if rest is None else to + 128, lse.data_ptr(), to + 160,
-                                  n, m, dim, at_q, at_k, seqs, causal, dim ** -0.5 if scale is None else scale, to + 192,
-                                  to + 224, to + 256, ws.data_ptr(), nb, _stream(stream)))
+                                  n, m, dim, at_q, at_k, seqs, causal, dim ** -0.5 if scale is None else scale, zero,
+                                  to + 192, to + 224, to + 256, ws.data_ptr(), nb, _stream(stream)))
     return dq, dk, dv
 
 

@@ -154,8 +154,9 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 }
 
 // The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
-// among their parts of that many keys.  By one warp.
-template <bool KEYS>
+// among their parts of that many keys.  DESCENDING: the tiles with the most work come first, as far as 32 sequences go, if
+// those are the first of each sequence.  By one warp.
+template <bool KEYS, bool DESCENDING>
 __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, uint32_t* status) {
     Place p{};
     p.tile = -1;
@@ -170,6 +171,29 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
         return p;
     }
     const int lane = threadIdx.x & 31;
+    if (DESCENDING && chunk == 0 && s.count <= 32) {
+        Place mine{};
+        if (lane < s.count) {
+            range_of(s.cu_q, lane, s.tokens_q, mine.q0, mine.len_q, status);
+            range_of(s.cu_k, lane, s.tokens_k, mine.k0, mine.len_k, status);
+        }
+        const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows;
+        // A tile's rank is its place in its sequence from the end with the least work, from 1 on; sum of max(tiles - v + 1, 0)
+        // tiles have rank v or more.  The greatest v of which there are more than `slot`:
+        if ((int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)tiles) <= slot) return p;
+        int32_t v = 1;
+        for (int32_t step = 1 << (31 - __clz(__reduce_max_sync(0xffffffffu, (uint32_t)tiles))); step > 0; step >>= 1)
+            if ((int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)max(tiles - (v + step) + 1, 0)) > slot) v += step;
+        // of the sequences that have a tile of that rank, the one that is left
+        const int32_t nth = slot - (int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)max(tiles - v, 0));
+        const uint32_t have = __ballot_sync(0xffffffffu, tiles >= v);
+        const int src = __fns(have, 0, nth + 1);
+        p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+        p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
+        p.parts = 1;
+        p.tile = __shfl_sync(0xffffffffu, tiles, src) - v;
+        return p;
+    }
     int32_t before = 0;
     for (int32_t i0 = 0; i0 < s.count; i0 += 32) {
         const int32_t i = i0 + lane;
@@ -200,6 +224,15 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
     return p;
+}
+
+// Clears the rows of the tokens in front of the first sequence and behind the last, by this warp of every CTA in turn.
+// f(token) clears one.
+template <class F>
+__device__ __forceinline__ void clear_outside(const int32_t* cu, int32_t count, int32_t tokens, F&& f) {
+    const int32_t first = min(max(cu[0], 0), tokens), end = min(max(cu[count], 0), tokens);
+    const int32_t n = first + tokens - end;
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) f(i < first ? (int32_t)i : (int32_t)i - first + end);
 }
 
 __device__ __forceinline__ Place place_of(const Place* p) {
@@ -298,6 +331,11 @@ struct Rows {  // of an output
     __device__ __forceinline__ bf16* at(int64_t token, int64_t head) const {
         return data + token * token_stride + head * head_stride;
     }
+    // all heads of a token, by a warp
+    __device__ __forceinline__ void clear(int64_t token, int32_t heads, int32_t dim) const {
+        for (int32_t i = threadIdx.x & 31; i < heads * (dim / 8); i += 32)
+            *reinterpret_cast<uint4*>(at(token, i / (dim / 8)) + i % (dim / 8) * 8) = make_uint4(0, 0, 0, 0);
+    }
 };
 
 // A ring of tiles: the phase of use number i of its stages.
@@ -316,6 +354,7 @@ struct ForwardParams {
     Packing packing;
     int32_t head_blocks;  // query heads / pack
     int32_t group, dim, causal;
+    int32_t clear;        // rows outside of all sequences become 0
     int32_t chunk;        // above 0: a CTA takes that many key tiles of a pair of query tiles, and leaves its part to join_kernel
     float* part;          // [CTA][2][128][dim]
     float2* part_stats;   // [CTA][2][128]: (log2 of what the part is scaled by, sum)
@@ -389,7 +428,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false, true>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -508,6 +547,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         }
         if (elect_one()) tc_commit(mma_done);
         warp_wait(mma_done, 0, p.wait_ns, p.status);
+    } else if (warp == 2) {
+        if (p.clear)
+            clear_outside(p.seq.cu_q, p.seq.count, p.seq.tokens_q, [&](int32_t token) {
+                const int32_t heads = p.head_blocks * p.packing.pack;
+                p.out.clear(token, heads, p.dim);
+                if (p.rest.data) p.rest.clear(token, heads, p.dim);
+                for (int32_t h = lane; h < heads; h += 32) p.lse[(int64_t)h * p.seq.tokens_q + token] = 0.f;
+            });
     } else if (warp >= 4) {
         // ---------------- softmax: a lane for each query, a warpgroup for each half of the keys of each query tile
         const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
@@ -641,7 +688,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false, true>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) where = w;
     }
     __syncthreads();
@@ -742,7 +789,7 @@ struct BackwardParams {
     Sequences seq;
     Packing packing;
     int32_t heads;  // of this kernel's CTAs: key heads for dkv, packs of query heads for dq
-    int32_t group, dim, causal;
+    int32_t group, dim, causal, clear;
     float scale, scale_log2;
     uint32_t* status;
     uint64_t wait_ns;
@@ -832,7 +879,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.status);
+        const Place w = find_place<true, true>(p.seq, slot, kRows, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -986,6 +1033,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             }
             mbar_arrive(&stats_full[s]);
         }
+    } else if (warp == 3) {
+        if (p.clear)
+            clear_outside(p.seq.cu_k, p.seq.count, p.seq.tokens_k, [&](int32_t token) {
+                p.dk.clear(token, p.heads, p.dim);
+                p.dv.clear(token, p.heads, p.dim);
+            });
     } else if (warp >= 4) {
         // ---------------- p and dz: a warpgroup for each quarter of the queries, a warp for 32 keys.  A thread holds two
         // neighbouring queries of every eight, for four keys: the queries' statistics, which differ along a row here, are
@@ -1164,7 +1217,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.status);
+        const Place w = find_place<false, true>(p.seq, slot, tokens, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -1275,6 +1328,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
         }
         if (elect_one()) tc_commit(done);
         warp_wait(done, 0, p.wait_ns, p.status);
+    } else if (warp == 2) {
+        if (p.clear)
+            clear_outside(p.seq.cu_q, p.seq.count, p.seq.tokens_q,
+                          [&](int32_t token) { p.dq.clear(token, p.heads * p.packing.pack, p.dim); });
     } else if (warp >= 4) {
         // ---------------- p and dz: a lane for each query, a warpgroup for each quarter of the keys
         const int part = (warp - 4) >> 2, quad = warp & 3;
@@ -1383,7 +1440,7 @@ mxfp4_status check_operand(const char* what, const char* name, const mxfp4_heads
 
 mxfp4_status check_call(const char* what, const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                         int64_t tokens_q, int64_t tokens_k, int64_t dim, const int32_t* cu_q, const int32_t* cu_k,
-                        int64_t seqs, int causal, float scale, Call* c) {
+                        int64_t seqs, int causal, float scale, int zero_outside, Call* c) {
     if (tokens_q < 0 || tokens_k < 0 || seqs < 0)
         return record_error(MXFP4_ERR_INVALID_ARG, "%s: negative size", what);
     if (tokens_q >= (1 << 30) || tokens_k >= (1 << 30) || seqs >= (1 << 24))
@@ -1391,7 +1448,8 @@ mxfp4_status check_call(const char* what, const mxfp4_heads* q, const mxfp4_head
     if (dim < 8 || dim > 128 || dim % 8)
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %lld must be a multiple of 8, at most 128", what,
                             (long long)dim);
-    if (causal != 0 && causal != 1) return record_error(MXFP4_ERR_INVALID_ARG, "%s: causal must be 0 or 1", what);
+    if ((causal != 0 && causal != 1) || (zero_outside != 0 && zero_outside != 1))
+        return record_error(MXFP4_ERR_INVALID_ARG, "%s: causal and zero_outside must be 0 or 1", what);
     if (!(scale > 0.f) || !std::isfinite(scale * kLog2e))
         return record_error(MXFP4_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
     mxfp4_status st;
@@ -1500,15 +1558,16 @@ extern "C" size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_to
 
 extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                         int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
-                                        const int32_t* cu_k, int64_t seqs, int causal, float scale,
+                                        const int32_t* cu_k, int64_t seqs, int causal, float scale, int zero_outside,
                                         const mxfp4_heads* out, const mxfp4_heads* rest, float* lse, void* ws,
                                         size_t ws_bytes, mxfp4_stream_t stream) {
     const char* what = "attention";
     Call c{};
-    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
+    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, zero_outside, &c);
     if (st) return st;
     if ((st = check_output(what, out, rest, true, &c))) return st;
-    if (q_tokens == 0 || seqs == 0) return record_error(MXFP4_OK, "%s", "");
+    const bool clear = zero_outside && cu_q;  // sequences of equal lengths leave nothing out
+    if (q_tokens == 0 || (seqs == 0 && !clear)) return record_error(MXFP4_OK, "%s", "");
     if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
     if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);
     const Split split = split_of(q_tokens, k_tokens, c.q.heads, c.k.heads, seqs);
@@ -1533,6 +1592,7 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     p.group = c.group;
     p.dim = c.dim;
     p.causal = causal;
+    p.clear = clear;
     p.chunk = split.chunk;
     if (p.chunk > 0) {
         p.part = static_cast<float*>(ws);
@@ -1542,8 +1602,8 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     p.status = device_status_ptr();
     p.wait_ns = wait_limit_ns();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t ctas =
-        (p.chunk > 0 ? split.places : places(c, q_tokens, c.seq.len_q, 2 * c.packing.tokens)) * p.head_blocks;
+    int64_t ctas = (p.chunk > 0 ? split.places : places(c, q_tokens, c.seq.len_q, 2 * c.packing.tokens)) * p.head_blocks;
+    if (clear) ctas = std::max<int64_t>(ctas, 1);
     static DeviceSlots wide, narrow;
     cudaError_t e =
         c.dim > 64 ? launch_tiles(attention_kernel<128>, wide, p, ctas, kForwardThreads, ForwardShape<128>::kSmem, s)
@@ -1565,11 +1625,11 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
                                              const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,
                                              const mxfp4_heads* dout, int64_t q_tokens, int64_t k_tokens, int64_t head_dim, const int32_t* cu_q,
                                              const int32_t* cu_k, int64_t seqs, int causal, float scale,
-                                             const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv,
+                                             int zero_outside, const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv,
                                              void* ws, size_t ws_bytes, mxfp4_stream_t stream) {
     const char* what = "attention_grad";
     Call c{};
-    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, &c);
+    mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, zero_outside, &c);
     if (st) return st;
     Heads d{}, gq{}, gk{}, gv{};
     if ((st = check_output(what, out, rest, false, &c))) return st;
@@ -1591,7 +1651,8 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     }
     if (q_tokens * c.q.heads > (int64_t)INT32_MAX * (kDeltaThreads / 16))
         return record_error(MXFP4_ERR_UNSUPPORTED_SHAPE, "%s: too many queries", what);
-    if ((q_tokens == 0 && k_tokens == 0) || seqs == 0) return record_error(MXFP4_OK, "%s", "");
+    const bool clear = zero_outside && cu_q;
+    if ((q_tokens == 0 && k_tokens == 0) || (seqs == 0 && !clear)) return record_error(MXFP4_OK, "%s", "");
     if ((st = ensure_device())) return st;
     BackwardParams p{};
     if (!map_of(&p.q, c.q, q_tokens, c.k, k_tokens, head_dim, c.packing) ||
@@ -1607,6 +1668,7 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     p.group = c.group;
     p.dim = c.dim;
     p.causal = causal;
+    p.clear = clear;
     p.scale = scale;
     p.scale_log2 = scale * kLog2e;
     p.status = device_status_ptr();
@@ -1626,11 +1688,13 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     const int smem = c.dim > 64 ? BackwardShape<128>::kSmem : BackwardShape<64>::kSmem;
     p.heads = c.k.heads;
     int64_t ctas = places(c, k_tokens, c.seq.len_k, kRows) * c.k.heads;
+    if (clear && k_tokens > 0) ctas = std::max<int64_t>(ctas, 1);
     e = c.dim > 64 ? launch_tiles(attention_dkv_kernel<128>, slots[0], p, ctas, kDkvThreads, smem, s)
                    : launch_tiles(attention_dkv_kernel<64>, slots[1], p, ctas, kDkvThreads, smem, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dkv launch: %s", what, cudaGetErrorString(e));
     p.heads = c.q.heads / c.packing.pack;
     ctas = places(c, q_tokens, c.seq.len_q, c.packing.tokens) * p.heads;
+    if (clear && q_tokens > 0) ctas = std::max<int64_t>(ctas, 1);
     e = c.dim > 64 ? launch_tiles(attention_dq_kernel<128>, slots[2], p, ctas, kDqThreads, smem, s)
                    : launch_tiles(attention_dq_kernel<64>, slots[3], p, ctas, kDqThreads, smem, s);
     if (e != cudaSuccess) return record_error(MXFP4_ERR_CUDA, "%s dq launch: %s", what, cudaGetErrorString(e));

@@ -103,13 +103,13 @@ def test_rotation_gradient_refuses(L, change, want):
 
 def _attention(L, grad=False, **kw):
     a = dict(q=(0x10000, 1536, 128, 8, 1), k=(0x20000, 1536, 128, 2, 1), v=(0x30000, 1536, 128, 2, 1), n=6, m=9, dim=128,
-             cq=0x1000, ck=0x2000, seqs=2, causal=1, scale=0.1, out=(0x40000, 1024, 128, 8, 1), rest=None, lse=0x5000,
+             cq=0x1000, ck=0x2000, seqs=2, causal=1, scale=0.1, zero=0, out=(0x40000, 1024, 128, 8, 1), rest=None, lse=0x5000,
              dout=(0x60000, 1024, 128, 8, 1), dq=(0x70000, 1024, 128, 8, 1), dk=(0x80000, 256, 128, 2, 1),
              dv=(0x90000, 256, 128, 2, 1), ws=0x100000, wsb=1 << 40)
     a.update(kw)
     table, (q, k, v, out, rest, dout, dq, dk, dv) = _table(*(a[x] for x in ("q", "k", "v", "out", "rest", "dout", "dq", "dk",
                                                                            "dv")))
-    tail = (a["n"], a["m"], a["dim"], P(a["cq"]), P(a["ck"]), a["seqs"], a["causal"], a["scale"])
+    tail = (a["n"], a["m"], a["dim"], P(a["cq"]), P(a["ck"]), a["seqs"], a["causal"], a["scale"], a["zero"])
     if grad:
         return L.mxfp4_attention_grad(q, k, v, out, rest, P(a["lse"]), dout, *tail, dq, dk, dv, P(a["ws"]), a["wsb"], None)
     return L.mxfp4_attention(q, k, v, *tail, out, rest, P(a["lse"]), P(a["ws"]), a["wsb"], None)
@@ -118,7 +118,7 @@ def _attention(L, grad=False, **kw):
 ATTENTION = [
     (dict(n=-1), INVALID), (dict(m=-1), INVALID), (dict(seqs=-1), INVALID), (dict(n=1 << 30), SHAPE), (dict(m=1 << 30), SHAPE),
     (dict(seqs=1 << 24), SHAPE), (dict(dim=4), SHAPE), (dict(dim=136), SHAPE), (dict(dim=100), SHAPE),
-    (dict(causal=2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(causal=2), INVALID), (dict(zero=2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(scale=3e38), INVALID), (dict(q=None), INVALID), (dict(v=None), INVALID),
     (dict(q=(0x10000, 1536, 128, 8, 0)), INVALID), (dict(k=(0x20000, 1536, 128, 3, 1)), SHAPE),
     (dict(v=(0x30000, 1536, 128, 1, 1)), SHAPE), (dict(q=(0x10008, 1536, 128, 8, 1)), MISALIGNED),

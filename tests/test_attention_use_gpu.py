@@ -64,6 +64,44 @@ def test_rows_outside_of_all_sequences_are_left():
         assert float((a.float() - b.float()).norm() / b.float().norm()) < 2.0 ** -6
 
 
+@pytest.mark.parametrize("few", [True, False])
+def test_rows_outside_become_zeros(few):
+    """New outputs hold zeros there, whatever was in their memory, and given ones beside new ones are left."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    q_lens, k_lens = ([2, 1], [3000, 1100]) if few else ([300, 4, 90], [300, 4, 90])
+    q, k, v, do = _inputs(torch, q_lens, k_lens, 6, 2, 72, 50, 14)
+    for shift, drop in ((0, 0), (11, 0), (50, 0), (0, 1), (20, len(q_lens))):  # drop: sequences left out at the end
+        a, b = (_edges(torch, x)[:len(x) + 1 - drop] + shift for x in (q_lens, k_lens))
+        junk = [torch.full_like(q, math.nan) for _ in range(6)] + [torch.full_like(k, math.nan) for _ in range(4)]
+        del junk  # what new tensors are made of
+        out, lse, rest = mx.attention(q, k, v, cu_q=a, cu_k=b, rest=True)
+        dq, dk, dv = mx.attention_grad(q, k, v, out, lse, do, cu_q=a, cu_k=b, rest=rest)
+        for x, edges in ((out, a), (rest, a), (lse.t(), a), (dq, a), (dk, b), (dv, b)):
+            assert not x[:edges[0]].any() and not x[edges[-1]:].any()
+            assert torch.isfinite(x[edges[0]:edges[-1]].float()).all()
+        mine = torch.full_like(q, 2.0)
+        _, other = mx.attention(q, k, v, cu_q=a, cu_k=b, out=mine)
+        assert torch.equal(other, lse) and (mine[a[-1]:] == 2).all() and torch.equal(mine[a[0]:a[-1]], out[a[0]:a[-1]])
+        mine = torch.full_like(k, 2.0)
+        got = mx.attention_grad(q, k, v, out, lse, do, cu_q=a, cu_k=b, rest=rest, dv=mine)
+        assert torch.equal(got[0], dq) and torch.equal(got[1], dk) and (mine[b[-1]:] == 2).all()
+    assert mx.device_status() == 0
+
+
+def test_many_sequences():
+    """More than a warp has lanes, in an order of lengths that goes up and down."""
+    torch = gpu_ready()
+    lens = [(37 * i) % 151 for i in range(90)]
+    q, k, v, do = _inputs(torch, lens, lens, 2, 2, 64, 0, 15)
+    _check(torch, q, k, v, do, lens, lens, True)
+    for n in (31, 32, 33):
+        T = sum(lens[:n])
+        _check(torch, q[:T], k[:T], v[:T], do[:T], lens[:n], lens[:n], True)
+        _check(torch, q[:T], k[:T], v[:T], do[:T], lens[:n], lens[:n], False)
+
+
 def test_layouts():
     """Heads of tokens, slices of a projection's output, a tensor with gaps: the same bits."""
     torch = gpu_ready()

@@ -154,10 +154,12 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 }
 
 // The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
-// among their parts of that many keys.  DESCENDING: the tiles with the most work come first, as far as 32 sequences go, if
-// those are the first of each sequence.  By one warp.
-template <bool KEYS, bool DESCENDING>
-__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, uint32_t* status) {
+// among their parts of that many keys.  Of up to 32 sequences the tiles with the most work come first: with `causal` a
+// sequence's first tiles have it, otherwise those of the longest sequences (a batch of lengths from 1 to 2048, 8192 tokens:
+// forward and backward 595 -> 520 us).  By one warp.
+template <bool KEYS>
+__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, int32_t causal,
+                                            uint32_t* status) {
     Place p{};
     p.tile = -1;
     if (!s.cu_q) {
@@ -171,13 +173,29 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
         return p;
     }
     const int lane = threadIdx.x & 31;
-    if (DESCENDING && chunk == 0 && s.count <= 32) {
+    if (chunk == 0 && s.count <= 32) {
         Place mine{};
         if (lane < s.count) {
             range_of(s.cu_q, lane, s.tokens_q, mine.q0, mine.len_q, status);
             range_of(s.cu_k, lane, s.tokens_k, mine.k0, mine.len_k, status);
         }
         const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows;
+        if (!causal) {
+            const int32_t length = KEYS ? mine.len_q : mine.len_k;
+            int32_t longer = 0;  // tiles of longer sequences, and of as long ones before
+            for (int i = 0; i < s.count; ++i) {
+                const int32_t l = __shfl_sync(0xffffffffu, length, i), t = __shfl_sync(0xffffffffu, tiles, i);
+                if (l > length || (l == length && i < lane)) longer += t;
+            }
+            const uint32_t here = __ballot_sync(0xffffffffu, slot >= longer && slot < longer + tiles);
+            if (!here) return p;
+            const int src = __ffs(here) - 1;
+            p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+            p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
+            p.parts = 1;
+            p.tile = slot - __shfl_sync(0xffffffffu, longer, src);
+            return p;
+        }
         // A tile's rank is its place in its sequence from the end with the least work, from 1 on; sum of max(tiles - v + 1, 0)
         // tiles have rank v or more.  The greatest v of which there are more than `slot`:
         if ((int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)tiles) <= slot) return p;
@@ -377,7 +395,7 @@ struct ForwardShape {
 static_assert(ForwardShape<128>::kSmem <= 227 * 1024, "shared memory budget");
 static_assert(2 * ForwardShape<64>::kSmem > 228 * 1024, "one CTA per SM: CTAs do not wait for each other's TMEM");
 constexpr int kForwardThreads = 128 + 512;
-constexpr float kLag = 8.f;  // log2 of how far a row's sum may run ahead of the maximum that it is scaled by
+constexpr float kLag = 16.f;  // log2 of how far a row's probabilities may run ahead of the maximum that they are scaled by
 
 template <int DP>
 __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __grid_constant__ ForwardParams p) {
@@ -428,7 +446,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false, true>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.causal, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -565,7 +583,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         const uint32_t src = lanes + t * 128 + half * 64, acc = lanes + 256 + t * 128;
         float* mine = share + (t * 2 + half) * kRows + quad * 32 + lane;
         const float* other = share + (t * 2 + 1 - half) * kRows + quad * 32 + lane;
-        const int columns = (p.dim + 15) / 16 * 16;
+        const int columns = (p.dim + 15) / 16 * 16, barrier = 1 + t * 4 + quad;
         // key that this query sees last, from the first tile's first key on, and the least of these in the query tile
         const int32_t last = (p.causal ? min(at.len_k - 1, row + ahead) : at.len_k - 1) - j0 * kRows;
         const int32_t least = (p.causal ? min(at.len_k - 1, row0 + t * tokens + ahead) : at.len_k - 1) - j0 * kRows;
@@ -592,13 +610,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[i]));
             float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             // A new maximum is taken up only once the old one lags by kLag: p then stays below 2^kLag, which bf16 and
-            // the fp32 sums hold as exactly as values below 1, and the output is seldom scaled again.  A timeout
-            // travels with the vote, so that both halves leave together.
-            if (any_of_some(1 + t, 256, !ok || j == 0 || (m - top) * p.scale_log2 > kLag)) {
-                *mine = ok ? m : NAN;
-                sync_some(1 + t, 256);
+            // the fp32 sums hold as exactly as values below 1, and the output is seldom scaled again.  The two warps that
+            // share 32 queries agree on it (with all eight of a tile and a lag of 8: 434 us instead of 400 for 8192 tokens
+            // whose scores reach 11).  A timeout travels with the vote, so that both leave together.
+            if (any_of_some(barrier, 64, !ok || j == 0 || (m - top) * p.scale_log2 > kLag)) {
+                *mine = m;
+                sync_some(barrier, 64);
                 const float theirs = *other;
-                if (any_of_some(1 + t, 256, !ok)) {
+                if (any_of_some(barrier, 64, !ok)) {
                     ok = false;
                     break;
                 }
@@ -645,7 +664,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         float sum = sum2.x + sum2.y;
         if (ok && n[t] > 0) {
             *mine = sum;
-            sync_some(1 + t, 256);
+            sync_some(barrier, 64);
             sum = half ? *other + sum : sum + *other;
             ok = warp_wait(&o_full[t], 0, p.wait_ns, p.status);
             if (ok) {
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false, true>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.causal, p.status);
         if (lane == 0) where = w;
     }
     __syncthreads();
@@ -879,7 +898,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<true, true>(p.seq, slot, kRows, 0, p.status);
+        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.causal, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -1217,7 +1236,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false, true>(p.seq, slot, tokens, 0, p.status);
+        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.causal, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();

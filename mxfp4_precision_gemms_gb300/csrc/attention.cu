@@ -387,7 +387,7 @@ struct ForwardShape {
     static constexpr int kStages = DP == 128 ? 5 : 6;
     static constexpr int kOffRing = 2 * kTileBytes;
     static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
-    static constexpr int kBars = 2 + 2 * kStages + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 2 + 2 * kStages + 2 + 4 + 2 + 1;
     static constexpr int kOffPlace = kOffBar + kBars * 8;
     static constexpr int kOffShare = kOffPlace + 32;
     static constexpr int kSmem = kOffShare + 2 * 2 * kRows * 4;
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     uint64_t* full = q_full + 2;                                            // [kStages]
     uint64_t* empty = full + kStages;                                       // [kStages]
     uint64_t* s_full = empty + kStages;                                     // [2] scores of a tile
-    uint64_t* p_full = s_full + 2;                                          // [2] its probabilities
-    uint64_t* o_full = p_full + 2;                                          // [2] its output
+    uint64_t* p_full = s_full + 2;                                          // [2][2] its probabilities, in two parts
+    uint64_t* o_full = p_full + 4;                                          // [2] its output
     uint64_t* mma_done = o_full + 2;
     Place* where = reinterpret_cast<Place*>(smem + Shape::kOffPlace);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(where + 1);
@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 8);
+            mbar_init(&p_full[2 * i], 8);
+            mbar_init(&p_full[2 * i + 1], 8);
             mbar_init(&o_full[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
@@ -544,17 +545,23 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (!ok || j >= n[t]) continue;
-                ok = warp_wait(&p_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
-                if (!ok) continue;
-                tc_fence_after();
                 const uint32_t b = rows_of_tile(smem_u32(ring + sv * Shape::kTileBytes));
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + packed_column<64>(k), b + k * kRowStep, output,
-                               j != 0 || k != 0);
-                    if (j + 1 == n[t]) tc_commit(&o_full[t]);
+                for (int part = 0; part < 2; ++part) {  // the first 32 keys of each half, then the others
+                    ok = ok && warp_wait(&p_full[2 * t + part], (uint32_t)j & 1u, p.wait_ns, p.status);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = part * 2 + (i >> 1) * 4 + (i & 1);
+                            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + packed_column<64>(k), b + k * kRowStep, output,
+                                   j != 0 || part != 0 || i != 0);
+                        }
+                        if (part == 1 && j + 1 == n[t]) tc_commit(&o_full[t]);
+                    }
                 }
+                if (!ok) continue;
                 // after p v in the pipe, so the scores may take the place of p
                 if (j + 1 < n[t]) make_scores(t, j + 1);
             }
@@ -654,11 +661,11 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                     w[i] = pack_bf16(x.x, x.y);
                 }
                 tmem_st_32x32b_x16(src + c * 16, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t + c]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
         }
         // the halves' sums, in their order
         float sum = sum2.x + sum2.y;

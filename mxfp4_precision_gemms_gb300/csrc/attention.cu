@@ -301,27 +301,57 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     for (int b = 0; b < DP / 64; ++b) tma_load_3d(dst + b * kBlockBytes, map, bar, b * 64, head, token);
 }
 
-// This lane's row of an accumulator, times `factor`, to memory as bf16 (dim elements, a multiple of 8), and what the
-// rounding left, as bf16 again, where it is asked for.
-__device__ __forceinline__ void store_row(uint32_t taddr, int dim, float factor, bf16* to, bool inside,
-                                          bf16* rest = nullptr) {
-    for (int c = 0; c < dim; c += 16) {
-        uint32_t v[16], w[8];
-        tmem_ld_32x32b_x16(taddr + c, v);
-        tmem_ld_wait();
+// Word i of lane j of each four to word j of lane i.
+__device__ __forceinline__ void turn4x4(uint32_t (&w)[4], int lane) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j] = pack_bf16(__uint_as_float(v[2 * j]) * factor, __uint_as_float(v[2 * j + 1]) * factor);
-        if (inside) {
-            *reinterpret_cast<uint4*>(to + c) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (c + 8 < dim) *reinterpret_cast<uint4*>(to + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            if (rest) {
+    for (int bit = 1; bit < 4; bit <<= 1) {
+        const bool upper = lane & bit;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = pack_bf16(fmaf(__uint_as_float(v[2 * j]), factor, -bf16_lo(w[j])),
-                                     fmaf(__uint_as_float(v[2 * j + 1]), factor, -bf16_hi(w[j])));
-                *reinterpret_cast<uint4*>(rest + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (c + 8 < dim) *reinterpret_cast<uint4*>(rest + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int i = 0; i < 4; ++i) {
+            if (i & bit) continue;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? w[i] : w[i + bit], bit);
+            if (upper)
+                w[i] = other;
+            else
+                w[i + bit] = other;
+        }
+    }
+}
+
+// A warp's 32 rows of an accumulator, `width` columns (a multiple of 8), to memory as bf16, and what the rounding left, as
+// bf16 again, where it is asked for.  Of its own row each lane gives the factor, the addresses and whether it is there.  Four
+// lanes write 64 neighbouring bytes of a row: with a row for each lane an instruction touched 32 lines, and the stores
+// of a pair of tiles kept the SM's load and store unit busy for some 8000 cycles.
+__device__ __forceinline__ void store_rows(uint32_t taddr, int width, float factor, bf16* to, bool inside,
+                                           bf16* rest = nullptr) {
+    const int lane = threadIdx.x & 31, column = 8 * (lane & 3);
+    for (int c = 0; c < width; c += 32) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            uint32_t z[16];
+            tmem_ld_16x256b_x4(taddr + c + ((uint32_t)hh << 20), z);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int src = hh * 16 + v * 8 + (lane >> 2);  // lane of the row
+                const float f = __shfl_sync(0xffffffffu, factor, src);
+                const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(to), src);
+                const bool on = __shfl_sync(0xffffffffu, (int)inside, src) && c + column < width;
+                uint32_t w[4], u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = __uint_as_float(z[4 * i + 2 * v]) * f, y = __uint_as_float(z[4 * i + 2 * v + 1]) * f;
+                    w[i] = pack_bf16(x, y);
+                    u[i] = pack_bf16(x - bf16_lo(w[i]), y - bf16_hi(w[i]));
+                }
+                turn4x4(w, lane);
+                if (on) *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(at) + c + column) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (rest) {  // the same for all lanes but for the address
+                    const uint64_t left = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rest), src);
+                    turn4x4(u, lane);
+                    if (on)
+                        *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(left) + c + column) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
             }
         }
     }
@@ -680,7 +710,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                 if (p.chunk > 0)
                     store_part(acc + from, width, p.part + (((int64_t)blockIdx.x * 2 + t) * kRows + r) * p.dim + from, inside);
                 else
-                    store_row(acc + from, width, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head) + from, inside,
+                    store_rows(acc + from, width, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head) + from, inside,
                               p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
             }
         } else if (inside && half == 0 && n[t] == 0 && p.chunk == 0) {  // no key at all
@@ -1163,7 +1193,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
             ok = ok && warp_wait(done, 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
-                store_row(lanes + (keys ? kDk : kDv) + from, part & 1 ? p.dim - cut : min(cut, p.dim), keys ? p.scale : 1.f,
+                store_rows(lanes + (keys ? kDk : kDv) + from, part & 1 ? p.dim - cut : min(cut, p.dim), keys ? p.scale : 1.f,
                           to + from, inside);
             }
         } else if (inside && (part & 1) == 0) {
@@ -1422,7 +1452,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
             if (ok) {  // each warpgroup writes its share of the columns
                 tc_fence_after();
                 const int width = (p.dim / 4 + 15) / 16 * 16, from = part * width;
-                store_row(lanes + kDq + from, min(width, p.dim - from), p.scale, to + from, inside);
+                store_rows(lanes + kDq + from, min(width, p.dim - from), p.scale, to + from, inside);
             }
         } else if (inside && part == 0) {
             store_zeros(p.dim, to);

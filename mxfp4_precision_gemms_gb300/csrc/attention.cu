@@ -154,12 +154,9 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 }
 
 // The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
-// among their parts of that many keys.  Of up to 32 sequences the tiles with the most work come first: with `causal` a
-// sequence's first tiles have it, otherwise those of the longest sequences (a batch of lengths from 1 to 2048, 8192 tokens:
-// forward and backward 595 -> 520 us).  By one warp.
+// among their parts of that many keys.  By one warp.
 template <bool KEYS>
-__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, int32_t causal,
-                                            uint32_t* status) {
+__device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, uint32_t* status) {
     Place p{};
     p.tile = -1;
     if (!s.cu_q) {
@@ -173,45 +170,6 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
         return p;
     }
     const int lane = threadIdx.x & 31;
-    if (chunk == 0 && s.count <= 32) {
-        Place mine{};
-        if (lane < s.count) {
-            range_of(s.cu_q, lane, s.tokens_q, mine.q0, mine.len_q, status);
-            range_of(s.cu_k, lane, s.tokens_k, mine.k0, mine.len_k, status);
-        }
-        const int32_t tiles = ((KEYS ? mine.len_k : mine.len_q) + rows - 1) / rows;
-        if (!causal) {
-            const int32_t length = KEYS ? mine.len_q : mine.len_k;
-            int32_t longer = 0;  // tiles of longer sequences, and of as long ones before
-            for (int i = 0; i < s.count; ++i) {
-                const int32_t l = __shfl_sync(0xffffffffu, length, i), t = __shfl_sync(0xffffffffu, tiles, i);
-                if (l > length || (l == length && i < lane)) longer += t;
-            }
-            const uint32_t here = __ballot_sync(0xffffffffu, slot >= longer && slot < longer + tiles);
-            if (!here) return p;
-            const int src = __ffs(here) - 1;
-            p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
-            p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
-            p.parts = 1;
-            p.tile = slot - __shfl_sync(0xffffffffu, longer, src);
-            return p;
-        }
-        // A tile's rank is its place in its sequence from the end with the least work, from 1 on; sum of max(tiles - v + 1, 0)
-        // tiles have rank v or more.  The greatest v of which there are more than `slot`:
-        if ((int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)tiles) <= slot) return p;
-        int32_t v = 1;
-        for (int32_t step = 1 << (31 - __clz(__reduce_max_sync(0xffffffffu, (uint32_t)tiles))); step > 0; step >>= 1)
-            if ((int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)max(tiles - (v + step) + 1, 0)) > slot) v += step;
-        // of the sequences that have a tile of that rank, the one that is left
-        const int32_t nth = slot - (int32_t)__reduce_add_sync(0xffffffffu, (uint32_t)max(tiles - v, 0));
-        const uint32_t have = __ballot_sync(0xffffffffu, tiles >= v);
-        const int src = __fns(have, 0, nth + 1);
-        p.q0 = __shfl_sync(0xffffffffu, mine.q0, src), p.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
-        p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
-        p.parts = 1;
-        p.tile = __shfl_sync(0xffffffffu, tiles, src) - v;
-        return p;
-    }
     int32_t before = 0;
     for (int32_t i0 = 0; i0 < s.count; i0 += 32) {
         const int32_t i = i0 + lane;
@@ -414,7 +372,7 @@ struct ForwardParams {
 template <int DP>
 struct ForwardShape {
     static constexpr int kTileBytes = DP / 64 * kBlockBytes;
-    static constexpr int kStages = DP == 128 ? 5 : 6;
+    static constexpr int kStages = DP == 128 ? 4 : 6;  // of K and V tiles in turn
     static constexpr int kOffRing = 2 * kTileBytes;
     static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
     static constexpr int kBars = 2 + 2 * kStages + 2 + 4 + 2 + 1;
@@ -452,7 +410,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     const int32_t block = (int32_t)(blockIdx.x % (uint32_t)p.head_blocks), head0 = block * p.packing.pack;
     const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)p.head_blocks);
     const int32_t tokens = p.packing.tokens;  // of a tile
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 96) {  // warp 0 looks for its place meanwhile
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&s_full[i], 1);
@@ -477,7 +435,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.causal, p.status);
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -744,7 +702,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.causal, p.status);
+        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) where = w;
     }
     __syncthreads();
@@ -797,7 +755,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // probabilities of 0.  HBM-bound: reads o and do once.
 // o is what the forward pass rounded to bf16 and, where it was kept, what that left.  Without the latter do . o is off by
 // 2^-8 of its terms, and so is the dz of a key that has most of a row's probability, where dp - do . o cancels: with scores
-// up to 11, dq and dk of 8192 tokens are off by 5.3e-3 of themselves instead of 2.3e-3 (bf16's own rounding: 1.7e-3).
+// up to 11, dq and dk of 8192 tokens are off by 5.3e-3 of themselves instead of 2.7e-3 (bf16's own rounding: 1.7e-3).
 struct DeltaParams {
     const bf16* out;
     const bf16* rest;  // or NULL
@@ -903,7 +861,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads), slot = (int32_t)(blockIdx.x / (uint32_t)p.heads);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 96) {  // warp 0 looks for its place meanwhile
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&stats_full[i], 32);
@@ -935,7 +893,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.causal, p.status);
+        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -1243,7 +1201,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t head0 = (int32_t)(blockIdx.x % (uint32_t)p.heads) * p.packing.pack;
     const int32_t slot = (int32_t)(blockIdx.x / (uint32_t)p.heads), tokens = p.packing.tokens;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 96) {  // warp 0 looks for its place meanwhile
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qd_full[i], 1);
             mbar_init(&z_full[i], 1);
@@ -1273,7 +1231,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.causal, p.status);
+        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();

@@ -487,7 +487,8 @@ cudaError_t launch_shares(RopeParams p, int sms, int* ctas, cudaStream_t s) {
 }
 template <class T, bool NEIGHBOURS, bool GRAD>
 cudaError_t launch_rope(const RopeParams& p, int vec, int sms, int* ctas, cudaStream_t s) {
-    if (!GRAD && sizeof(T) == 2 && vec == 8) return launch_shares<T, 8, 1, 4, NEIGHBOURS, false>(p, sms, ctas, s);
+    if constexpr (!GRAD && sizeof(T) == 2)
+        if (vec == 8) return launch_shares<T, 8, 1, 4, NEIGHBOURS, false>(p, sms, ctas, s);
     if (vec >= 4) return launch_shares<T, 4, 1, GRAD && sizeof(T) == 4 ? 2 : 4, NEIGHBOURS, GRAD>(p, sms, ctas, s);
     if (vec == 2) return launch_shares<T, 2, 2, 2, NEIGHBOURS, GRAD>(p, sms, ctas, s);
     return launch_shares<T, 1, 4, 2, NEIGHBOURS, GRAD>(p, sms, ctas, s);

@@ -36,7 +36,7 @@ struct RopeSide {  // queries or keys
     const void* x;
     const void* dy;  // gradient only
     void* y;         // the result: y, or dx
-    int64_t x_token, x_head, dy_token, dy_head, y_token, y_head;
+    int64_t x_token, x_head, dy_token, dy_head, y_token, y_head;  // bytes
     int32_t heads;
     const float* gain;
 };
@@ -178,21 +178,30 @@ __device__ __forceinline__ float sum_n(const float (&a)[N]) {
     return v;
 }
 
-// Sums of two numbers over the `n` lanes of a row's group, in every one of them (li: this lane's place in it).
-__device__ __forceinline__ void group_sums(float (&v)[2], int li, int n) {
+// Sums of N numbers over the `n` lanes of a row's group, in every one of them (li: this lane's place in it).
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], int li, int n) {
     if ((n & (n - 1)) == 0) {  // groups start on their own size
         for (int o = n >> 1; o > 0; o >>= 1) {
-            const float a = __shfl_xor_sync(0xffffffffu, v[0], o), b = __shfl_xor_sync(0xffffffffu, v[1], o);
-            v[0] += a, v[1] += b;
+            float w[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += w[i];
         }
         return;
     }
     const int lane = threadIdx.x & 31;
     for (int o = 1 << (31 - __clz(n - 1)); o > 0; o >>= 1) {
-        const float a = __shfl_down_sync(0xffffffffu, v[0], o), b = __shfl_down_sync(0xffffffffu, v[1], o);
-        if (li < o && li + o < n) v[0] += a, v[1] += b;
+        float w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __shfl_down_sync(0xffffffffu, v[i], o);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (li < o && li + o < n) v[i] += w[i];
     }
-    v[0] = __shfl_sync(0xffffffffu, v[0], lane - li), v[1] = __shfl_sync(0xffffffffu, v[1], lane - li);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], lane - li);
 }
 
 // Lanes of a row, and rows that a warp takes at once.
@@ -286,6 +295,9 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
                     }
                 }
             }
+            const char* rows_x = static_cast<const char*>(side.x) + token * side.x_token;
+            const char* rows_dy = static_cast<const char*>(side.dy) + token * side.dy_token;
+            char* rows_y = static_cast<char*>(side.y) + token * side.y_token;
             for (int h0 = from * slice; h0 < min(to * slice, side.heads); h0 += slice) {
                 Run<T, VEC> x[ROWS][SLOTS][2], dy[GRAD ? ROWS : 1][SLOTS][2];
                 int h[ROWS];
@@ -293,9 +305,9 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
 #pragma unroll
                 for (int k = 0; k < ROWS; ++k) {
                     h[k] = h0 + k * per_warp + sub;
-                    const int64_t at = min(h[k], side.heads - 1);
-                    const T* px = static_cast<const T*>(side.x) + token * side.x_token + at * side.x_head;
-                    const T* pd = static_cast<const T*>(side.dy) + token * side.dy_token + at * side.dy_head;
+                    const uint32_t at = min(h[k], side.heads - 1);
+                    const T* px = reinterpret_cast<const T*>(rows_x + at * side.x_head);
+                    const T* pd = reinterpret_cast<const T*>(rows_dy + at * side.dy_head);
 #pragma unroll
                     for (int s = 0; s < SLOTS; ++s) {
                         if (!GRAD || norm) {
@@ -313,50 +325,21 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
 #pragma unroll
                 for (int k0 = 0; k0 < ROWS; k0 += 2) {
                     if (k0 > 0 && h0 + k0 * per_warp >= side.heads) break;
-                    float a[2][SLOTS][VEC], b[2][SLOTS][VEC], u[2][SLOTS][VEC], v[2][SLOTS][VEC], rstd[2] = {1.f, 1.f};
-                    if (!GRAD || norm) {
+                    float a[2][SLOTS][VEC], b[2][SLOTS][VEC], u[2][SLOTS][VEC], v[2][SLOTS][VEC];
+                    float sums[GRAD ? 4 : 2];  // of x x; and of dz gain x, which needs no norm yet: one trip over the lanes
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float ss[VEC] = {};
+                    for (int r = 0; r < 2; ++r) {
+                        float ss[VEC] = {}, dot[VEC] = {};
 #pragma unroll
-                            for (int s = 0; s < SLOTS; ++s) {
+                        for (int s = 0; s < SLOTS; ++s) {
+                            if (!GRAD || norm) {
                                 pairs_of<NEIGHBOURS, T, VEC>(x[k0 + r][s][0], x[k0 + r][s][1], a[r][s], b[r][s]);
                                 if (SLOTS == 1 || there[s]) {
                                     fma_n(ss, a[r][s], a[r][s], ss);
                                     fma_n(ss, b[r][s], b[r][s], ss);
                                 }
                             }
-                            rstd[r] = sum_n(ss);
-                        }
-                        if (norm) {
-                            group_sums(rstd, li, lanes);
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) rstd[r] = rsqrtf(fmaf(rstd[r], mean, p.eps));
-                        }
-                    }
-                    if constexpr (!GRAD) {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r)
-#pragma unroll
-                            for (int s = 0; s < SLOTS; ++s) {
-                                mul_n(u[r][s], a[r][s], ca[s]);
-                                mul_n(v[r][s], b[r][s], cb[s]);
-                                fma_n(u[r][s], b[r][s], sb[s], u[r][s]);
-                                fma_n(v[r][s], a[r][s], sa[s], v[r][s]);
-                                if (norm) {
-                                    scale_n(u[r][s], u[r][s], rstd[r]);
-                                    scale_n(v[r][s], v[r][s], rstd[r]);
-                                }
-                            }
-                    } else {
-                        float along[2];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float dot[VEC] = {};
-                            // rows that are another lane's, and runs that are no lane's, add nothing to the gains' sums
-                            const bool mine = h[k0 + r] < side.heads;
-#pragma unroll
-                            for (int s = 0; s < SLOTS; ++s) {
+                            if constexpr (GRAD) {  // dz
                                 float da[VEC], db[VEC];
                                 pairs_of<NEIGHBOURS, T, VEC>(dy[k0 + r][s][0], dy[k0 + r][s][1], da, db);
                                 mul_n(u[r][s], da, ca[s]);
@@ -364,44 +347,62 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
                                 fma_n(u[r][s], db, sa[s], u[r][s]);
                                 fma_n(v[r][s], da, sb[s], v[r][s]);
                                 if (norm && (SLOTS == 1 || there[s])) {
-                                    if (mine) {
-                                        float ua[VEC], ub[VEC];
-                                        scale_n(ua, a[r][s], rstd[r]);
-                                        scale_n(ub, b[r][s], rstd[r]);
-                                        fma_n(dgain[which][s][0], u[r][s], ua, dgain[which][s][0]);
-                                        fma_n(dgain[which][s][1], v[r][s], ub, dgain[which][s][1]);
-                                    }
-                                    mul_n(u[r][s], u[r][s], gain[s][0]);
-                                    mul_n(v[r][s], v[r][s], gain[s][1]);
-                                    fma_n(dot, u[r][s], a[r][s], dot);
-                                    fma_n(dot, v[r][s], b[r][s], dot);
+                                    float zx[VEC];
+                                    mul_n(zx, u[r][s], a[r][s]);
+                                    fma_n(dot, zx, gain[s][0], dot);
+                                    mul_n(zx, v[r][s], b[r][s]);
+                                    fma_n(dot, zx, gain[s][1], dot);
                                 }
                             }
-                            along[r] = sum_n(dot);
                         }
-                        if (norm) {
-                            group_sums(along, li, lanes);
+                        sums[r] = sum_n(ss);
+                        if constexpr (GRAD) sums[2 + r] = sum_n(dot);
+                    }
+                    if (norm) group_sums(sums, li, lanes);
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                // (du - u mean(du u)) r with u = x r
-                                const float by1 = -along[r] * mean * rstd[r] * rstd[r];
-                                float by[VEC];
+                    for (int r = 0; r < 2; ++r) {
+                        const float rstd = norm ? rsqrtf(fmaf(sums[r], mean, p.eps)) : 1.f;
+                        if constexpr (!GRAD) {
 #pragma unroll
-                                for (int i = 0; i < VEC; ++i) by[i] = by1;
-#pragma unroll
-                                for (int s = 0; s < SLOTS; ++s) {
-                                    fma_n(u[r][s], a[r][s], by, u[r][s]);
-                                    fma_n(v[r][s], b[r][s], by, v[r][s]);
-                                    scale_n(u[r][s], u[r][s], rstd[r]);
-                                    scale_n(v[r][s], v[r][s], rstd[r]);
+                            for (int s = 0; s < SLOTS; ++s) {
+                                mul_n(u[r][s], a[r][s], ca[s]);
+                                mul_n(v[r][s], b[r][s], cb[s]);
+                                fma_n(u[r][s], b[r][s], sb[s], u[r][s]);
+                                fma_n(v[r][s], a[r][s], sa[s], v[r][s]);
+                                if (norm) {
+                                    scale_n(u[r][s], u[r][s], rstd);
+                                    scale_n(v[r][s], v[r][s], rstd);
                                 }
                             }
+                        } else if (norm) {
+                            // rows that are another lane's, and runs that are no lane's, add nothing to the gains' sums
+                            const bool mine = h[k0 + r] < side.heads;
+                            // (dz gain - u mean(dz gain u)) r with u = x r
+                            const float along = -sums[2 + r] * mean * rstd * rstd;
+                            float by[VEC];
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) by[i] = along;
+#pragma unroll
+                            for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+                                for (int w = 0; w < 2; ++w) {
+                                    float(&x1)[VEC] = w ? b[r][s] : a[r][s];
+                                    float(&dz)[VEC] = w ? v[r][s] : u[r][s];
+                                    float ux[VEC];
+                                    if (mine && (SLOTS == 1 || there[s])) {
+                                        scale_n(ux, x1, rstd);
+                                        fma_n(dgain[which][s][w], dz, ux, dgain[which][s][w]);
+                                    }
+                                    mul_n(dz, dz, gain[s][w]);
+                                    fma_n(dz, x1, by, dz);
+                                    scale_n(dz, dz, rstd);
+                                }
                         }
                     }
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
                         if (h[k0 + r] < side.heads) {
-                            T* py = static_cast<T*>(side.y) + token * side.y_token + h[k0 + r] * side.y_head;
+                            T* py = reinterpret_cast<T*>(rows_y + (uint32_t)h[k0 + r] * side.y_head);
 #pragma unroll
                             for (int s = 0; s < SLOTS; ++s)
                                 if (SLOTS == 1 || there[s])
@@ -561,6 +562,12 @@ mxfp4_status check_gain(const char* what, const char* name, const float* gain) {
     return MXFP4_OK;
 }
 
+RopeSide side_of(const Heads& x, const Heads& dy, const Heads& y, int32_t heads, const float* gain) {
+    const int64_t size = heads_esize(y.dtype);
+    return {x.data, dy.data, y.data, x.token_stride * size, x.head_stride * size, dy.token_stride * size,
+            dy.head_stride * size, y.token_stride * size, y.head_stride * size, heads, gain};
+}
+
 // Pairs that a lane moves as runs of elements: the most that every row of every tensor allows.
 int pairs_per_lane(const RopeParams& p, const Heads* const* all, int n) {
     const int half = p.dim / 2;
@@ -604,8 +611,7 @@ extern "C" mxfp4_status mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_hea
             return record_error(MXFP4_ERR_INVALID_ARG, "%s: %s has other heads or another type than %s or q", what,
                                 names[i][1], names[i][0]);
         if ((st = check_gain(what, i ? "k_gain" : "q_gain", gains[i]))) return st;
-        p.side[i] = {h[i][0].data, nullptr, h[i][1].data, h[i][0].token_stride, h[i][0].head_stride, 0, 0,
-                     h[i][1].token_stride, h[i][1].head_stride, h[i][0].heads, gains[i]};
+        p.side[i] = side_of(h[i][0], Heads{}, h[i][1], h[i][0].heads, gains[i]);
     }
     if (tokens == 0) return record_error(MXFP4_OK, "%s", "");
     if ((st = ensure_device())) return st;
@@ -658,9 +664,7 @@ extern "C" mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp
         if ((st = check_gain(what, i ? "k_gain" : "q_gain", gains[i]))) return st;
         if ((st = check_gain(what, i ? "dk_gain" : "dq_gain", dgains[i]))) return st;
         sums = sums || dgains[i];
-        p.side[i] = {h[i][2].data, h[i][0].data, h[i][1].data, h[i][2].token_stride, h[i][2].head_stride,
-                     h[i][0].token_stride, h[i][0].head_stride, h[i][1].token_stride, h[i][1].head_stride, h[i][0].heads,
-                     gains[i]};
+        p.side[i] = side_of(h[i][2], h[i][0], h[i][1], h[i][0].heads, gains[i]);
     }
     if (sums && tokens > 0) {
         const size_t need = mxfp4_qk_norm_rope_grad_workspace_bytes(tokens, head_dim);

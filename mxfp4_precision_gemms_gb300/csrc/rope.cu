@@ -9,8 +9,11 @@
 // tokens: it makes the cosines and sines of the token's pairs once for all heads (shared memory of its own, no barrier of
 // the block), then goes through the heads of queries and of keys.  Groups of lanes hold a row (a token's head) each, a lane
 // VEC pairs of it, as two runs of VEC elements (or one of 2 VEC, where a pair's elements are neighbours), with turn and gain
-// in registers; the loads of ROWS rows are under way together.  Every row is read once and written once.  The elements
-// behind the rotated ones are pairs that do not turn.
+// in registers; the loads of ROWS rows are under way together, and in long calls (STAGED) the next ROWS are on their way
+// to shared memory while these are worked on.  Every row is read once and written once.  The elements behind the rotated ones
+// are pairs that do not turn.  8192 tokens of 32 and 8 heads of 128: 33.7 us for 168 MB, backwards 56.9 us for 252 MB; a
+// plain copy of as much takes 28.8 us, and a sum of two tensors into a third 39.1.  Half of the issue slots are taken
+// backwards: its arithmetic (nine operations on a pair of elements, besides the conversions) is what is left.
 //
 // Angles.  A position times a frequency in fp32 is off by 2^-24 of itself, which is 0.03 radians at position 500000.  Here a
 // frequency is held as turns per position in 64-bit fixed point, and a product with an integer modulo 2^64 is the exact
@@ -58,6 +61,10 @@ struct RopeParams {
 template <class T, int VEC>
 struct Run {
     T v[VEC];
+};
+template <>
+struct __align__(16) Run<float, 4> {
+    float v[4];
 };
 template <>
 struct Run<bf16, 8> {
@@ -204,13 +211,40 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int li, int n) {
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], lane - li);
 }
 
+// A run's way from global to shared memory without registers, and the wait for all but the last `N` groups of them.
+template <class R>
+__device__ __forceinline__ void copy_run(R* to, const void* from) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (sizeof(R) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(sizeof(R)) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Lanes of a row, and rows that a warp takes at once.
 __host__ __device__ inline int row_lanes(int half, int vec) { return half / vec < 32 ? half / vec : 32; }
 
+// Runs that a thread holds in shared memory for a slice of heads, of x, and of dy in the gradient.
+__host__ __device__ constexpr int staged_runs(bool staged, int rows, bool grad) { return staged ? rows * (grad ? 2 : 1) * 2 : 0; }
+constexpr int kStages = 2;
+// Slices that a warp must have to go through for the next one's copies to be worth their instructions.  32 and 8 heads of
+// 128, with them and without: 16384 tokens 57.5 and 61.9 us, gradient 109 and 113; 8192 tokens 34.3 and 37.1, 59.6 and 64.5;
+// 4096 tokens (5 and 8 slices) 20.3 and 18.7, 39.1 and 39.2; 512 tokens 10.4 and 8.4, 16.5 and 14.6.  Calls in fp32 lose
+// at 5003 tokens of 14 and 2 heads of 72 (20.7 and 18.6, 33.0 and 28.8) and are left without.
+constexpr int kStagedSlices = 10;
+
 // SLOTS: runs of pairs of a lane, 32 lanes apart (rows of more than 32 VEC pairs).  ROWS: that a lane has under way.
-template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD>
+template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD, bool STAGED>
 __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 : 3)
     rope_kernel(const __grid_constant__ RopeParams p) {
+    static_assert(!STAGED || SLOTS == 1);
+    constexpr int kRuns = staged_runs(STAGED, ROWS, GRAD);
+    extern __shared__ __align__(16) uint8_t staged[];
     constexpr int kSums = GRAD ? kRopeThreads * 2 * VEC * SLOTS : 0;  // floats of the groups' sums of gains
     constexpr int kTurn = kWarps * kMaxPairs * 2;
     __shared__ __align__(16) float shared[kTurn + 2 * kMaxHeadDim > kSums ? kTurn + 2 * kMaxHeadDim : kSums];
@@ -239,21 +273,66 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
     auto element = [&](int s, int which, int i) {  // of pair i of slot s in its row
         return NEIGHBOURS ? at_a[s] + 2 * i + which : (which ? at_b[s] : at_a[s]) + i;
     };
+    const int slice = per_warp * ROWS;  // heads
+    const int slices0 = (p.side[0].heads + slice - 1) / slice;
+    const int all = slices0 + (p.side[1].heads + slice - 1) / slice, shares = (all + p.span - 1) / p.span;
+    const int64_t first_item = (int64_t)blockIdx.x * kWarps + warp, step = (int64_t)gridDim.x * kWarps;
+    // The slice that is copied next, and the stage that it goes to.
+    int64_t next_item = first_item, next_token;
+    int next, next_end, next_stage = 0;
+    auto share_of = [&](int64_t item, int64_t& token, int& from, int& to) {
+        token = shares == 1 ? item : item / shares;
+        from = (int)(item - token * shares) * p.span, to = min(from + p.span, all);
+    };
+    share_of(next_item, next_token, next, next_end);
+    auto run_at = [&](int stage, int i) {
+        return reinterpret_cast<Run<T, VEC>*>(staged) + (stage * kRuns + i) * kRopeThreads + threadIdx.x;
+    };
+    auto copy_next = [&] {
+        if (next_item < p.items) {
+            const int which = next >= slices0;
+            const RopeSide& side = p.side[which];
+            const char* rows_x = static_cast<const char*>(side.x) + next_token * side.x_token;
+            const char* rows_dy = static_cast<const char*>(side.dy) + next_token * side.dy_token;
+            const int h0 = (which ? next - slices0 : next) * slice + sub;
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                const uint32_t h = h0 + k * per_warp;
+                if (h >= (uint32_t)side.heads || idle) continue;
+                if (!GRAD || side.gain) {
+                    const T* row = reinterpret_cast<const T*>(rows_x + h * side.x_head);
+                    copy_run(run_at(next_stage, 2 * k), row + at_a[0]);
+                    copy_run(run_at(next_stage, 2 * k + 1), row + at_b[0]);
+                }
+                if constexpr (GRAD) {
+                    const T* row = reinterpret_cast<const T*>(rows_dy + h * side.dy_head);
+                    copy_run(run_at(next_stage, 2 * (ROWS + k)), row + at_a[0]);
+                    copy_run(run_at(next_stage, 2 * (ROWS + k) + 1), row + at_b[0]);
+                }
+            }
+            if (++next == next_end) {
+                next_item += step;
+                share_of(next_item, next_token, next, next_end);
+            }
+            next_stage ^= 1;
+        }
+        end_copies();
+    };
+    int stage = 0;
     grid_dependency_wait();
     allow_dependent_launch();
+    if constexpr (STAGED) copy_next();
     for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeThreads) {
         const float* gain = p.side[i >= p.dim].gain;
         gains[i] = gain ? gain[i >= p.dim ? i - p.dim : i] : 1.f;
     }
     __syncthreads();
     float dgain[2][SLOTS][2][VEC] = {};
-    const int slice = per_warp * ROWS;  // heads
-    const int slices0 = (p.side[0].heads + slice - 1) / slice;
-    const int all = slices0 + (p.side[1].heads + slice - 1) / slice, shares = (all + p.span - 1) / p.span;
     const float mean = 1.f / (float)p.dim;
-    for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < p.items; item += (int64_t)gridDim.x * kWarps) {
-        const int64_t token = item / shares;
-        const int first = (int)(item - token * shares) * p.span, end = min(first + p.span, all);
+    for (int64_t item = first_item; item < p.items; item += step) {
+        int64_t token;
+        int first, end;
+        share_of(item, token, first, end);
         __syncwarp();  // the cosines of the token before have been read
         for (int i = lane; i < half; i += 32) {
             float2 cs = make_float2(1.f, 0.f);
@@ -301,25 +380,41 @@ __global__ void __launch_bounds__(kRopeThreads, GRAD ? 2 : VEC * SLOTS >= 8 ? 2 
             for (int h0 = from * slice; h0 < min(to * slice, side.heads); h0 += slice) {
                 Run<T, VEC> x[ROWS][SLOTS][2], dy[GRAD ? ROWS : 1][SLOTS][2];
                 int h[ROWS];
-                // Lanes without a row of their own read the last head's, and write nothing.
+                if constexpr (STAGED) {
+                    copy_next();
+                    wait_copies<kStages - 1>();  // a lane reads what it copied itself
 #pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
-                    h[k] = h0 + k * per_warp + sub;
-                    const uint32_t at = min(h[k], side.heads - 1);
-                    const T* px = reinterpret_cast<const T*>(rows_x + at * side.x_head);
-                    const T* pd = reinterpret_cast<const T*>(rows_dy + at * side.dy_head);
+                    for (int k = 0; k < ROWS; ++k) {
+                        h[k] = idle ? side.heads : h0 + k * per_warp + sub;
 #pragma unroll
-                    for (int s = 0; s < SLOTS; ++s) {
-                        if (!GRAD || norm) {
-                            load_run<T, VEC>(px + at_a[s], x[k][s][0]);
-                            load_run<T, VEC>(px + at_b[s], x[k][s][1]);
-                        }
-                        if constexpr (GRAD) {
-                            load_run<T, VEC>(pd + at_a[s], dy[k][s][0]);
-                            load_run<T, VEC>(pd + at_b[s], dy[k][s][1]);
+                        for (int i = 0; i < 2; ++i) {
+                            x[k][0][i] = *run_at(stage, 2 * k + i);
+                            if constexpr (GRAD) dy[k][0][i] = *run_at(stage, 2 * (ROWS + k) + i);
                         }
                     }
-                    if (idle) h[k] = side.heads;
+                    stage ^= 1;
+                } else {
+                    // Lanes without a row of their own read the last head's, and write nothing.
+#pragma unroll
+                    for (int k = 0; k < ROWS; ++k) {
+                        if (k > 0 && k % 2 == 0 && h0 + k * per_warp >= side.heads) break;
+                        h[k] = h0 + k * per_warp + sub;
+                        const uint32_t at = min(h[k], side.heads - 1);
+                        const T* px = reinterpret_cast<const T*>(rows_x + at * side.x_head);
+                        const T* pd = reinterpret_cast<const T*>(rows_dy + at * side.dy_head);
+#pragma unroll
+                        for (int s = 0; s < SLOTS; ++s) {
+                            if (!GRAD || norm) {
+                                load_run<T, VEC>(px + at_a[s], x[k][s][0]);
+                                load_run<T, VEC>(px + at_b[s], x[k][s][1]);
+                            }
+                            if constexpr (GRAD) {
+                                load_run<T, VEC>(pd + at_a[s], dy[k][s][0]);
+                                load_run<T, VEC>(pd + at_b[s], dy[k][s][1]);
+                            }
+                        }
+                        if (idle) h[k] = side.heads;
+                    }
                 }
                 // two rows together, so that one's sum over lanes is under way while the other's is
 #pragma unroll
@@ -473,18 +568,29 @@ constexpr int kMaxCtas = 1024;  // bounds the gradient's workspace
 
 // Launches the kernel over `ctas` CTAs at most: a warp for each token, or for each share of a token's heads where there are
 // fewer tokens than warps.
-template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD>
+template <class T, int VEC, int SLOTS, int ROWS, bool NEIGHBOURS, bool GRAD, bool STAGED = false>
 cudaError_t launch_shares(RopeParams p, int sms, int* ctas, cudaStream_t s) {
     const int slice = 32 / row_lanes(p.dim / 2, VEC) * ROWS;
     int all = 0;
     for (const RopeSide& side : p.side) all += (side.heads + slice - 1) / slice;
     const int most = std::min(kMaxCtas, sms * (GRAD ? 2 : VEC * SLOTS >= 8 ? 2 : 3));  // that fit the device at once
     const int64_t warps = (int64_t)most * kWarps;
+    if constexpr (sizeof(T) == 2 && VEC == (GRAD ? 4 : 8) && !STAGED)
+        if ((int64_t)p.tokens * all >= kStagedSlices * warps)
+            return launch_shares<T, VEC, SLOTS, ROWS, NEIGHBOURS, GRAD, true>(p, sms, ctas, s);
     p.span = (int32_t)std::min<int64_t>(all, std::max<int64_t>(1, (int64_t)p.tokens * all / warps));
     p.items = (int64_t)p.tokens * ((all + p.span - 1) / p.span);
     *ctas = (int)std::min<int64_t>(most, (p.items + kWarps - 1) / kWarps);
-    return launch_overlapped(rope_kernel<T, VEC, SLOTS, ROWS, NEIGHBOURS, GRAD>, dim3((unsigned)*ctas), dim3(kRopeThreads), 0,
-                             s, 1, true, p);
+    const auto kernel = rope_kernel<T, VEC, SLOTS, ROWS, NEIGHBOURS, GRAD, STAGED>;
+    const int smem = kStages * staged_runs(STAGED, ROWS, GRAD) * kRopeThreads * (int)sizeof(Run<T, VEC>);
+    static DeviceSlots ready;
+    int unused = 0;
+    const cudaError_t e = per_device_setting(ready, &unused, [&](int, int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, dim3((unsigned)*ctas), dim3(kRopeThreads), (size_t)smem, s, 1, true, p);
 }
 template <class T, bool NEIGHBOURS, bool GRAD>
 cudaError_t launch_rope(const RopeParams& p, int vec, int sms, int* ctas, cudaStream_t s) {

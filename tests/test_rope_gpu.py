@@ -31,6 +31,17 @@ def _case(torch, tokens, a, b, D, P, axes, dtype, norm, seed=0):
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_both_directions(shape, dtype, norm):
+    _both_directions(shape, dtype, norm)
+
+
+# Warps that go through ten slices of heads or more, with head counts that fill no slice.
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("shape", [(5001, 33, 17, 128, 64, False, 1), (5001, 33, 17, 128, 50, True, 2)], ids=str)
+def test_many_tokens(shape, norm):
+    _both_directions(shape, "bfloat16", norm)
+
+
+def _both_directions(shape, dtype, norm):
     torch = gpu_ready()
     from mxfp4_precision_gemms_gb300 import binding as mx
     from tests import attention_reference as ref

@@ -530,8 +530,8 @@ typedef struct {
 /* Norm and rotation of queries and keys in one pass: each row x (a token's head) becomes
  *   n = x / sqrt(mean(x^2) + eps) * gain   (a side whose gain is NULL: n = x)
  *   pair (a, b) of n -> (a cos - b sin, b cos + a sin), angle = positions[axis][token] * freq
- * in fp32, rounded once.  Angles are exact to 2^-40 of a turn for positions below 2^24 and to 2^-32
- * below 2^32, whatever the frequency.
+ * in fp32, rounded once.  Whatever the position and the frequency, the angle is that of their exact product to 2^-31
+ * of a turn (positions below 2^32; twice that for every further bit), rounded to fp32 as a fraction of a half turn.
  * q, k: [tokens, heads, head_dim], both of one type; k NULL: queries alone.  head_dim even, at
  * most 256; any strides and alignment of the element type (rows of whole 16-byte vectors are
  * moved faster).  q_gain, k_gain: device fp32 [head_dim] or NULL.
@@ -560,7 +560,7 @@ mxfp4_status mxfp4_qk_norm_rope_grad(const mxfp4_heads* q, const mxfp4_heads* k,
                                      size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Workspace bytes of mxfp4_attention: above 0 where the queries are few and their keys (1024 or more a sequence on the
- * average) are shared out over several CTAs, whose parts are then joined. */
+ * average) are shared out over several CTAs, whose parts are then joined.  Does not depend on the device. */
 size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t head_dim, int64_t q_heads,
                                        int64_t k_heads, int64_t seqs);
 
@@ -597,15 +597,18 @@ size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
  *   dv = p^T dout,  dz = p (dout v^T - dout . out),  dq = scale dz k,  dk = scale dz^T q
  * q to scale: as given to it, out, rest and lse as returned by it; dout: the gradient of out, bf16.  rest may be NULL:
  * dout . out then carries out's rounding, and dz of a key that has most of a row's probability is off by it.
- * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are
- * rounded to bf16 for the tensor cores.  No atomic additions: the same bits on every run.
+ * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  dk and dv
+ * are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are rounded to bf16 for the
+ * tensor cores.  No atomic additions: the same bits on every run.  Rows of other sequences and rows outside of all
+ * reach nothing; within a sequence an infinite or NaN number of a query or key may reach, as 0 times it, keys or
+ * queries that it does not see, up to 127 places away.
  * ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                   const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,
                                   const mxfp4_heads* dout, int64_t q_tokens, int64_t k_tokens, int64_t head_dim,
                                   const int32_t* cu_q, const int32_t* cu_k, int64_t seqs, int causal, float scale,
-                                  int zero_outside, const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* dv, void* ws,
-                                  size_t ws_bytes, mxfp4_stream_t stream);
+                                  int zero_outside, const mxfp4_heads* dq, const mxfp4_heads* dk,
+                                  const mxfp4_heads* dv, void* ws, size_t ws_bytes, mxfp4_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the current device's status word:
  * MXFP4_OK, MXFP4_ERR_TIMEOUT if a kernel's bounded wait expired since the last call,

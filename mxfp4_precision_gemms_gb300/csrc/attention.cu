@@ -7,12 +7,16 @@
 // Scores and probabilities live in tensor memory and registers alone.  All products run on the tensor cores in bf16
 // with fp32 sums (tcgen05.mma.kind::f16 on tiles of 128 x 128); p and dz are rounded to bf16 as operands.
 //
-//   forward  a CTA for 256 queries of a head, as two tiles that take turns: while the softmax of one runs, the tensor
-//            cores work on the other
+//   forward  a CTA for two tiles of 128 rows that take turns: while the softmax of one runs, the tensor cores work on the
+//            other.  The rows are queries of all the heads that share a key head (Packing): its keys are read once
+//   join     where few queries' keys are shared out over several CTAs: their parts put together
 //   delta    (lse log2 e, do . o) of each query
 //   dkv      a CTA for 128 keys of a key head, over all queries that see them, of all heads that share it: dk and dv stay
 //            in tensor memory, and no two CTAs add to the same number
-//   dq       a CTA for 128 queries of a head, over the keys that they see
+//   dq       a CTA for 128 rows, over the keys that they see
+// Long sequences are bound by the tensor cores (8192 tokens of 32 and 8 heads of 128, causal: forward 0.55 TFLOP in 358 us,
+// backward seven products, 1.92 TFLOP, in 1178), heads of 64 or less by the softmax's instructions between them, few queries
+// by reading the keys and values, short sequences by the steps that wait for each other.
 // The scores are made a second time for dq: two products more than a single pass over (keys, queries) would need, which
 // would have to add to dq in memory, in an order that differs from run to run.
 //
@@ -690,9 +694,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     }
 }
 
-// The parts of a pair of query tiles joined: a warp for each row, a lane for four columns.  Of the parts' places the first
-// one's CTAs do it, several of them, for their rows in turn.
-constexpr int kJoinThreads = 256, kJoinCtas = 4;
+// The parts of a pair of query tiles joined: a warp for each row, a lane for four columns.  The rows are shared out over
+// the CTAs of all the parts' places, kJoinCtas of a place (256 queries of 32 heads over 8192 keys, the whole call: 65.8 us,
+// with 4 of a place 69.8, with 2 74.1; 64 queries, when the first part's four CTAs did all: 80 us, now 28.9).
+constexpr int kJoinThreads = 256, kJoinCtas = 8;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ ForwardParams p) {
     __shared__ Place where;
@@ -707,14 +712,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
     __syncthreads();
     Place at = where;
-    if (at.tile < 0 || at.part > 0) return;
+    if (at.tile < 0) return;
     if (p.causal) at.tile = (at.len_q + 2 * tokens - 1) / (2 * tokens) - 1 - at.tile;
     const int32_t row0 = at.tile * 2 * tokens, rows = min(2 * tokens, at.len_q - row0) * p.packing.pack;
-    for (int32_t i = blockIdx.y * (kJoinThreads / 32) + warp; i < rows; i += kJoinCtas * kJoinThreads / 32) {
+    const int32_t warps = at.parts * kJoinCtas * (kJoinThreads / 32);
+    for (int32_t i = (at.part * kJoinCtas + blockIdx.y) * (kJoinThreads / 32) + warp; i < rows; i += warps) {
         const int32_t t = i / p.packing.rows(), r = i - t * p.packing.rows();
         const int32_t token = at.q0 + row0 + t * tokens + r / p.packing.pack, head = block * p.packing.pack + r % p.packing.pack;
         // part s of this row
-        auto part = [&](int s) { return (((int64_t)slot + s) * p.head_blocks + block) * 2 * kRows + t * kRows + r; };
+        auto part = [&](int s) { return (((int64_t)slot - at.part + s) * p.head_blocks + block) * 2 * kRows + t * kRows + r; };
         // A lane reads the statistics of every 32nd part, so that the loads of all are under way at once (one part after the
         // other took 15 us for 10 parts, of 8 new tokens over 24018 keys).  What all are scaled by: the largest of the parts'
         // that hold anything (NaN is something).
@@ -1518,9 +1524,14 @@ int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
 }
 
 // Whether the keys of a pair of query tiles are shared out over several CTAs: where the pairs leave more than half of the SMs
-// without one and sequences have eight key tiles or more on the average.  A part is then `chunk` key tiles, so many that
-// there is a part for each SM at most (a CTA's start and end cost as much as some five key tiles), but four at least.
+// without one, sequences have eight key tiles or more on the average, and a CTA has at least kSaved tiles fewer to go through
+// (few rows) or kSavedMany (many, whose parts take longer to join).  A part is `chunk` key tiles, so many that there is a part
+// for each SM at most (a CTA's start and end cost as much as some five key tiles), but four at least.
+// 32 and 8 heads of 128, shared out and not: 1 query over 1024 keys 16.5 and 18.6 us, 2048 16.6 and 27.9, 32768 41 and 329;
+// 4 sequences of 4096 24.7 and 47.6; 64 queries over 1024 keys 22.8 and 20.6 (4 tiles fewer), 2048 22.7 and 30.9 (12);
+// 256 queries over 1024 26.9 and 20.6, 4096 43.3 and 53.5 (16).
 // `places`: of all parts, no fewer than there are whatever the sequences' lengths.
+constexpr int kSaved = 4, kSavedMany = 10, kFewRows = 2 * kRows;
 constexpr int kSms = 152;  // of a GB300: the workspace does not depend on the device
 struct Split {
     int32_t chunk;  // 0: none
@@ -1536,7 +1547,10 @@ Split split_of(int64_t q_tokens, int64_t k_tokens, int64_t q_heads, int64_t k_he
     // one pair of query tiles in each sequence, or all in one that has all the keys
     const bool one = q_tokens <= 2 * packing.tokens;
     const int64_t parts = std::max<int64_t>(1, one ? kSms / blocks - seqs : kSms / (blocks * pairs) - 1);
-    s.chunk = (int32_t)std::max<int64_t>(4, (tiles + parts - 1) / parts);
+    const int32_t chunk = (int32_t)std::max<int64_t>(4, (tiles + parts - 1) / parts);
+    const int saved = q_tokens * q_heads <= kFewRows ? kSaved : kSavedMany;
+    if ((chunk + saved) * seqs > tiles) return s;
+    s.chunk = chunk;
     s.places = one ? tiles / s.chunk + 2 * seqs : pairs * (tiles / s.chunk + 2);
     return s;
 }

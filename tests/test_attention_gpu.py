@@ -110,6 +110,18 @@ def test_few_queries_over_many_keys(heads, causal):
         _check(torch, q, k, v, do, q_lens, k_lens, causal)
 
 
+@pytest.mark.parametrize("lens", [([200], [3000]), ([30, 70], [4000, 2500]), ([300, 1], [90, 5000])], ids=str)
+@pytest.mark.parametrize("heads", [(8, 2), (3, 3)])
+def test_many_rows_joined(heads, lens):
+    """Parts of pairs of query tiles whose rows are more than the warps of one part's CTAs that join them."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    assert mx.lib().mxfp4_attention_workspace_bytes(sum(lens[0]) + 2, sum(lens[1]) + 2, 128, *heads, len(lens[0])) > 0
+    q, k, v, do = _inputs(torch, *lens, *heads, 128, 2, 10, lean=2.0)
+    _check(torch, q, k, v, do, *lens, True)
+
+
 @pytest.mark.parametrize("heads", [(65, 1), (130, 1), (26, 2), (96, 1), (254, 2)])
 def test_groups_that_fill_no_tile(heads):
     torch = gpu_ready()

@@ -26,6 +26,7 @@
 // nothing that they hold (infinities, NaN) reaches this sequence.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "element.cuh"
 #include "heads.cuh"
@@ -367,7 +368,7 @@ struct ForwardParams {
     int32_t clear;        // rows outside of all sequences become 0
     int32_t chunk;        // above 0: a CTA takes that many key tiles of a pair of query tiles, and leaves its part to join_kernel
     float* part;          // [CTA][2][128][dim]
-    float2* part_stats;   // [CTA][2][128]: (log2 of what the part is scaled by, sum)
+    float4* part_stats;   // [CTA][2][128]: (log2 of what the part is scaled by, sum, sum of the rounded probabilities, 0)
     float scale_log2;     // scale * log2 e
     uint32_t* status;
     uint64_t wait_ns;
@@ -590,6 +591,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         float top = -INFINITY;  // maximum that the sums are scaled by (of the scores before `scale`)
         float shift = 0.f;      // top * scale_log2
         float2 sum2 = make_float2(0.f, 0.f);
+        float2 off2 = make_float2(0.f, 0.f);  // what rounding to bf16 adds to the sums
         bool ok = true;
         for (int j = 0; j < n[t]; ++j) {
             ok = warp_wait(&s_full[t], (uint32_t)j & 1u, p.wait_ns, p.status);
@@ -620,14 +622,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                     ok = false;
                     break;
                 }
-                m = fmaxf(m, theirs);
-                const bool raise = j == 0 || (m - top) * p.scale_log2 > kLag;
-                const float new_top = raise ? fmaxf(top, m) : top;
+                const float most_of_both = fmaxf(m, theirs);
+                const bool raise = j == 0 || (most_of_both - top) * p.scale_log2 > kLag;
+                const float new_top = raise ? fmaxf(top, most_of_both) : top;
                 const float new_shift = new_top == -INFINITY ? 0.f : new_top * p.scale_log2;
                 if (j > 0) {
                     // the scores' commit came after that of p v: the output holds all tiles before this one
                     const float by = !raise ? 1.f : top == -INFINITY ? 0.f : exp2_approx(shift - new_shift);
                     sum2 = f2_mul(sum2, make_float2(by, by));
+                    off2 = f2_mul(off2, make_float2(by, by));
                     for (int c = half * 16; c < columns; c += 32) {
                         uint32_t v[16];
                         tmem_ld_32x32b_x16(acc + c, v);
@@ -641,18 +644,38 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                 shift = new_shift;
             }
             const float2 shift2 = make_float2(-shift, -shift);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            // The output is divided by the sum of the rounded probabilities that it is made of, lse is that of the exact ones.
+            // A key that has most of a row's probability then gives its v exactly, whatever its rounding, and the gradient's
+            // dp - do . o, which cancels there, is exact: with scores up to 11, dk of 8192 tokens is off by 2.5e-3 of itself
+            // instead of 4.8e-3.  Tiles whose keys all have less than 1/4 of the sum so far are left out: their roundings
+            // add up to less than the gradients' own.
+            // A row's own keys decide for it, so that no other row changes its bits.
+            constexpr float kHeavy = 4.f;
+            const bool heavy = inside && !(exp2_approx(fmaf(m, p.scale_log2, -shift)) * kHeavy < sum2.x + sum2.y);
+            auto probabilities = [&](int c, auto exact) {
                 uint32_t w[16];
+                float2 all = make_float2(0.f, 0.f), rounded = all;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int at_z = c * 32 + 2 * i;
                     const float2 e = f2_fma(make_float2(__uint_as_float(z[at_z]), __uint_as_float(z[at_z + 1])), scale2, shift2);
                     const float2 x = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-                    sum2 = f2_add(sum2, x);
+                    all = f2_add(all, x);
                     w[i] = pack_bf16(x.x, x.y);
+                    if constexpr (decltype(exact)::value) rounded = f2_add(rounded, make_float2(bf16_lo(w[i]), bf16_hi(w[i])));
                 }
+                sum2 = f2_add(sum2, all);
+                if constexpr (decltype(exact)::value)
+                    if (heavy) off2 = f2_add(off2, f2_sub(rounded, all));
                 tmem_st_32x32b_x16(src + c * 16, w);
+            };
+            const bool any_heavy = __any_sync(0xffffffffu, heavy);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (any_heavy)
+                    probabilities(c, std::true_type{});
+                else
+                    probabilities(c, std::false_type{});
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -660,11 +683,17 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             }
         }
         // the halves' sums, in their order
-        float sum = sum2.x + sum2.y;
-        if (ok && n[t] > 0) {
-            *mine = sum;
+        float sum = sum2.x + sum2.y, kept = 0.f;  // kept: of the rounded probabilities
+        auto both_halves = [&](float v) {
+            *mine = v;
             sync_some(barrier, 64);
-            sum = half ? *other + sum : sum + *other;
+            v = half ? *other + v : v + *other;
+            sync_some(barrier, 64);
+            return v;
+        };
+        if (ok && n[t] > 0) {
+            sum = both_halves(sum);
+            kept = sum + both_halves(off2.x + off2.y);
             ok = warp_wait(&o_full[t], 0, p.wait_ns, p.status);
             if (ok) {
                 tc_fence_after();
@@ -672,7 +701,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
                 if (p.chunk > 0)
                     store_part(acc + from, width, p.part + (((int64_t)blockIdx.x * 2 + t) * kRows + r) * p.dim + from, inside);
                 else
-                    store_rows(acc + from, width, sum == 0.f ? 0.f : 1.f / sum, p.out.at(at.q0 + row, head) + from, inside,
+                    store_rows(acc + from, width, sum == 0.f ? 0.f : 1.f / kept, p.out.at(at.q0 + row, head) + from, inside,
                               p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
             }
         } else if (inside && half == 0 && n[t] == 0 && p.chunk == 0) {  // no key at all
@@ -681,7 +710,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
         }
         if (inside && half == 0) {
             if (p.chunk > 0)
-                p.part_stats[((int64_t)blockIdx.x * 2 + t) * kRows + r] = make_float2(shift, sum);
+                p.part_stats[((int64_t)blockIdx.x * 2 + t) * kRows + r] = make_float4(shift, sum, kept, 0.f);
             else
                 p.lse[(int64_t)head * p.seq.tokens_q + at.q0 + row] = sum == 0.f ? -INFINITY : (shift + log2f(sum)) * kLn2;
         }
@@ -724,20 +753,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         // A lane reads the statistics of every 32nd part, so that the loads of all are under way at once (one part after the
         // other took 15 us for 10 parts, of 8 new tokens over 24018 keys).  What all are scaled by: the largest of the parts'
         // that hold anything (NaN is something).
-        auto stats_of = [&](int s) { return s < at.parts ? p.part_stats[part(s)] : make_float2(0.f, 0.f); };
+        auto stats_of = [&](int s) { return s < at.parts ? p.part_stats[part(s)] : make_float4(0.f, 0.f, 0.f, 0.f); };
         float top = -INFINITY;
         for (int s0 = 0; s0 < at.parts; s0 += 32) {
-            const float2 st = stats_of(s0 + lane);
+            const float4 st = stats_of(s0 + lane);
             if (st.y != 0.f) top = fmaxf(top, st.x);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.f;
+        float sum = 0.f, kept = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s0 = 0; s0 < at.parts; s0 += 32) {
-            const float2 st = stats_of(s0 + lane);
+            const float4 st = stats_of(s0 + lane);
             const float by = st.y == 0.f ? 0.f : exp2_approx(st.x - top);
             sum = fmaf(by, st.y, sum);
+            kept = fmaf(by, st.z, kept);
             const int n = min(32, at.parts - s0);
 #pragma unroll 8
             for (int s = 0; s < n; ++s) {
@@ -749,8 +779,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float one = sum == 0.f ? 0.f : 1.f / sum;
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            kept += __shfl_xor_sync(0xffffffffu, kept, o);
+        }
+        const float one = sum == 0.f ? 0.f : 1.f / kept;
         if (lane * 4 < p.dim) {
             const float o[4] = {v.x * one, v.y * one, v.z * one, v.w * one};
             uint2 w = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
@@ -1554,7 +1587,7 @@ Split split_of(int64_t q_tokens, int64_t k_tokens, int64_t q_heads, int64_t k_he
     s.places = one ? tiles / s.chunk + 2 * seqs : pairs * (tiles / s.chunk + 2);
     return s;
 }
-size_t part_bytes(int64_t dim) { return 2 * kRows * ((size_t)dim * sizeof(float) + sizeof(float2)); }
+size_t part_bytes(int64_t dim) { return 2 * kRows * ((size_t)dim * sizeof(float) + sizeof(float4)); }
 
 template <class Params, class Kern>
 cudaError_t launch_tiles(Kern kern, DeviceSlots& ready, const Params& p, int64_t ctas, int threads, int smem,
@@ -1632,7 +1665,7 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     p.chunk = split.chunk;
     if (p.chunk > 0) {
         p.part = static_cast<float*>(ws);
-        p.part_stats = reinterpret_cast<float2*>(p.part + split.places * p.head_blocks * 2 * kRows * head_dim);
+        p.part_stats = reinterpret_cast<float4*>(p.part + split.places * p.head_blocks * 2 * kRows * head_dim);
     }
     p.scale_log2 = scale * kLog2e;
     p.status = device_status_ptr();

@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // probabilities of 0.  HBM-bound: reads o and do once.
 // o is what the forward pass rounded to bf16 and, where it was kept, what that left.  Without the latter do . o is off by
 // 2^-8 of its terms, and so is the dz of a key that has most of a row's probability, where dp - do . o cancels: with scores
-// up to 11, dq and dk of 8192 tokens are off by 5.3e-3 of themselves instead of 2.7e-3 (bf16's own rounding: 1.7e-3).
+// up to 19, dq and dk of 2048 tokens are off by 5.5e-3 of themselves instead of 2.5e-3 (bf16's own rounding: 1.7e-3).
 struct DeltaParams {
     const bf16* out;
     const bf16* rest;  // or NULL

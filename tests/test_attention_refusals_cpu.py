@@ -151,8 +151,8 @@ def test_workspaces(L):
     assert w(8192, 8192, 128, 32, 8, 1) == 0          # queries enough for all SMs
     assert w(1, 500, 128, 32, 8, 1) == 0              # too few keys to share out
     assert w(8, 24000, 128, 32, 8, 4) > 0
-    # whatever the lists say, a part needs 256 rows of a head's size and two numbers
-    assert w(8, 24000, 128, 32, 8, 4) % (256 * (128 * 4 + 8)) == 0
+    # whatever the lists say, a part needs 256 rows of a head's size and four numbers
+    assert w(8, 24000, 128, 32, 8, 4) % (256 * (128 * 4 + 16)) == 0
     assert w(8, 24000, 128, 32, 8, 4) < 256 << 20
     for bad in ((-1, 8, 128, 8, 8, 1), (8, 0, 128, 8, 8, 1), (8, 24000, 0, 8, 8, 1), (8, 24000, 128, 8, 3, 1),
                 (8, 24000, 128, 8, 8, 0), (8, 24000, 128, 0, 8, 1)):

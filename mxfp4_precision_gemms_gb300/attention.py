@@ -71,7 +71,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
     """Each head of q and k divided by its root mean square and multiplied by its gain ([head_dim]; None: left as it is),
     then rotated.  q and k: [tokens, heads, head_dim] or [batch, length, heads, head_dim], fp32 or bf16 both; head_dim even,
     at most 256.  `rope`: Rope(frequencies, axis of each pair, interleaved) or None; positions: int32 or int64 of q's
-    leading shape, behind a dimension of rope.axes (which may be left out where that is 1).  Gradients of q, k and the gains; sums in fp32, the same bits on every run."""
+    leading shape, behind a dimension of rope.axes (which may be left out where that is 1).  Gradients of q, k and the gains;
+    sums in fp32, the same bits on every run."""
     if q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2]:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not fit together")
     if rope is not None:

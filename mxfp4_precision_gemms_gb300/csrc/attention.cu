@@ -198,6 +198,11 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
             p.len_q = __shfl_sync(0xffffffffu, mine.len_q, src), p.len_k = __shfl_sync(0xffffffffu, mine.len_k, src);
             p.parts = __shfl_sync(0xffffffffu, mine.parts, src);
             p.tile = slot - before - __shfl_sync(0xffffffffu, upto - tiles, src);
+            const int32_t most = __shfl_sync(0xffffffffu, tiles, src);
+            if ((uint32_t)p.tile >= (uint32_t)most) {  // a list that falls, whose tiles are more than 2^31
+                p.tile = -1;
+                return p;
+            }
             p.part = p.tile % p.parts;
             p.tile /= p.parts;
             return p;
@@ -741,7 +746,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
     __syncthreads();
     Place at = where;
-    if (at.tile < 0) return;
+    // parts that have no place: a list that falls names more keys than there are
+    if (at.tile < 0 || slot - at.part + at.parts > (int32_t)(gridDim.x / (uint32_t)p.head_blocks)) return;
     if (p.causal) at.tile = (at.len_q + 2 * tokens - 1) / (2 * tokens) - 1 - at.tile;
     const int32_t row0 = at.tile * 2 * tokens, rows = min(2 * tokens, at.len_q - row0) * p.packing.pack;
     const int32_t warps = at.parts * kJoinCtas * (kJoinThreads / 32);

@@ -181,6 +181,22 @@ def test_lists_that_point_outside_are_reported():
     assert mx.device_status() == 0
 
 
+def test_lists_that_fall_where_keys_are_shared_out():
+    """A list that names more keys than there are has more parts than places: it is reported, and reads nothing else."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300 import binding as mx
+
+    q, k, v, do = _inputs(torch, [1, 1, 1], [2000, 2500, 1500], 4, 2, 64, 0, 8)
+    cu_q = _edges(torch, [1, 1, 1])
+    for bad in ([0, 6000, 0, 6000], [6000, 0, 6000, 0], [0, 6000, 6000, 0]):
+        mx.attention(q, k, v, cu_q=cu_q, cu_k=torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert mx.device_status() == 1
+    cu_k = _edges(torch, [2000, 2500, 1500])
+    first = mx.attention(q, k, v, cu_q=cu_q, cu_k=cu_k)
+    assert all(torch.equal(x, y) for x, y in zip(first, mx.attention(q, k, v, cu_q=cu_q, cu_k=cu_k)))
+    assert mx.device_status() == 0
+
+
 def test_streams_and_graphs():
     """Two calls at once on two streams, and a captured pass replayed on new numbers beside an eager one, give what calls one
     by one give."""

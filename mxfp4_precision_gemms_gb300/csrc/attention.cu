@@ -14,9 +14,10 @@
 //   dkv      a CTA for 128 keys of a key head, over all queries that see them, of all heads that share it: dk and dv stay
 //            in tensor memory, and no two CTAs add to the same number
 //   dq       a CTA for 128 rows, over the keys that they see
-// Long sequences are bound by the products, whose operands take all of shared memory's bandwidth (8192 tokens of 32 and 8 heads of 128, causal: forward 0.55 TFLOP in 358 us,
-// backward seven products, 1.92 TFLOP, in 1178), heads of 64 or less by the softmax's instructions between them, few queries
-// by reading the keys and values, short sequences by the steps that wait for each other.
+// Long sequences are bound by the products, whose operands take all of shared memory's bandwidth (8192 tokens of 32 and 8
+// heads of 128, causal: forward 0.55 TFLOP in 358 us, 321 with no softmax; backward seven products, 1.92 TFLOP, in 1170),
+// heads of 64 or less by the softmax's instructions between them, few queries by reading the keys and values, short
+// sequences by the steps that wait for each other.
 // The scores are made a second time for dq: two products more than a single pass over (keys, queries) would need, which
 // would have to add to dq in memory, in an order that differs from run to run.
 //

@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             // A key that has most of a row's probability then gives its v exactly, whatever its rounding, and the gradient's
             // dp - do . o, which cancels there, is exact: with scores up to 11, dk of 8192 tokens is off by 2.5e-3 of itself
             // instead of 4.8e-3.  Tiles whose keys all have less than 1/4 of the sum so far are left out: their roundings
-            // add up to less than the gradients' own.
+            // add up to less than the gradients' own (with 1/16 the errors are the same and 8192 tokens take 367 us instead of 359).
             // A row's own keys decide for it, so that no other row changes its bits.
             constexpr float kHeavy = 4.f;
             const bool heavy = inside && !(exp2_approx(fmaf(m, p.scale_log2, -shift)) * kHeavy < sum2.x + sum2.y);

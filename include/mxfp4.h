@@ -574,9 +574,10 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * them, and reported by mxfp4_device_status as MXFP4_ERR_INVALID_ARG.  Any lengths, 0 among them, and those of
  * queries and keys may differ.
  * causal 1: query i of a sequence of Lq queries and Lk keys sees keys j <= i + Lk - Lq (the last query sees all).
- * A query that sees no key gets an out of 0 and an lse of -infinity.  What tokens of other sequences and tokens
- * outside of all hold reaches nothing.  (Of its own sequence, a hidden key's infinite or NaN v may reach
- * queries up to 127 before it, as 0 times it.)
+ * A query that sees no key, or whose scores are all -infinity, gets an out of 0 and an lse of -infinity, and no
+ * gradient, whatever hidden keys hold; a score of +infinity or NaN makes its out and its lse NaN.
+ * What tokens of other sequences and tokens outside of all hold reaches nothing.  (Of its own sequence, a hidden
+ * key's infinite or NaN v may reach queries up to 127 before it, as 0 times it.)
  * out: [q_tokens, q_heads, head_dim] bf16; lse: device fp32 [q_heads, q_tokens], natural logarithm, what
  * mxfp4_attention_grad takes.  Rows outside of all sequences (in front of the first and behind the last) are left as
  * they were in all outputs or, with zero_outside 1, become 0.

@@ -704,11 +704,19 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             if (ok) {
                 tc_fence_after();
                 const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0, width = half ? p.dim - cut : min(cut, p.dim);
-                if (p.chunk > 0)
+                if (p.chunk > 0) {
                     store_part(acc + from, width, p.part + (((int64_t)blockIdx.x * 2 + t) * kRows + r) * p.dim + from, inside);
-                else
-                    store_rows(acc + from, width, sum == 0.f ? 0.f : 1.f / kept, p.out.at(at.q0 + row, head) + from, inside,
-                              p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
+                } else {
+                    // A row without weight is zeros, not 0 times sums that hidden keys may have made infinite or NaN.
+                    const bool weight = sum != 0.f;
+                    bf16* to = p.out.at(at.q0 + row, head) + from;
+                    bf16* left = p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr;
+                    store_rows(acc + from, width, 1.f / kept, to, inside && weight, left);
+                    if (inside && !weight) {
+                        store_zeros(width, to);
+                        if (left) store_zeros(width, left);
+                    }
+                }
             }
         } else if (inside && half == 0 && n[t] == 0 && p.chunk == 0) {  // no key at all
             store_zeros(p.dim, p.out.at(at.q0 + row, head));
@@ -1464,7 +1472,9 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
             if (ok) {  // each warpgroup writes its share of the columns
                 tc_fence_after();
                 const int width = (p.dim / 4 + 15) / 16 * 16, from = part * width;
-                store_rows(lanes + kDq + from, min(width, p.dim - from), p.scale, to + from, inside);
+                const bool weight = stat.x != INFINITY;  // otherwise zeros, as in the forward pass
+                store_rows(lanes + kDq + from, min(width, p.dim - from), p.scale, to + from, inside && weight);
+                if (inside && !weight) store_zeros(min(width, p.dim - from), to + from);
             }
         } else if (inside && part == 0) {
             store_zeros(p.dim, to);

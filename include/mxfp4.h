@@ -576,8 +576,9 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * causal 1: query i of a sequence of Lq queries and Lk keys sees keys j <= i + Lk - Lq (the last query sees all).
  * A query that sees no key, or whose scores are all -infinity, gets an out of 0 and an lse of -infinity, and no
  * gradient, whatever hidden keys hold; a score of +infinity or NaN makes its out and its lse NaN.
- * What tokens of other sequences and tokens outside of all hold reaches nothing.  (Of its own sequence, a hidden
- * key's infinite or NaN v may reach queries up to 127 before it, as 0 times it.)
+ * What tokens of other sequences and tokens outside of all hold reaches nothing.  Of its own sequence, a hidden
+ * key's infinite or NaN v may reach, as 0 times it, queries up to 254 places before the first one that sees it (tiles
+ * of up to 128 queries go over whole tiles of 128 keys); a hidden key's k, whatever it is, reaches none.
  * out: [q_tokens, q_heads, head_dim] bf16; lse: device fp32 [q_heads, q_tokens], natural logarithm, what
  * mxfp4_attention_grad takes.  Rows outside of all sequences (in front of the first and behind the last) are left as
  * they were in all outputs or, with zero_outside 1, become 0.
@@ -601,8 +602,9 @@ size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
  * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  dk and dv
  * are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are rounded to bf16 for the
  * tensor cores.  No atomic additions: the same bits on every run.  Rows of other sequences and rows outside of all
- * reach nothing; within a sequence an infinite or NaN number of a query or key may reach, as 0 times it, keys or
- * queries that it does not see, up to 127 places away.
+ * reach nothing.  Within a sequence infinities and NaN reach what the formulas say and besides, as 0 times them, of a
+ * key's k or v the dq of queries up to 254 places before the first one that sees the key, and of a query's q or dout
+ * the dk and dv of keys up to 254 places behind the last one that the query sees.
  * ws: device, 256-byte aligned. */
 mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
                                   const mxfp4_heads* out, const mxfp4_heads* rest, const float* lse,

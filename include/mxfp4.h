@@ -584,6 +584,8 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * they were in all outputs or, with zero_outside 1, become 0.
  * rest: NULL, or [q_tokens, q_heads, head_dim] bf16, which receives what rounding left of out (out + rest is the
  * output to 16 bits): what the gradient is exact with.
+ * out and rest must not overlap k, v or each other; each may be q itself (the same data and strides), but not overlap it
+ * otherwise.  What the call sees of this it refuses.
  * ws: device, 256-byte aligned, mxfp4_attention_workspace_bytes bytes (may be NULL where those are 0).
  * Products in bf16 on the tensor cores (the probabilities rounded to bf16), sums and softmax statistics in fp32.
  * The same bits on every run. */
@@ -599,10 +601,12 @@ size_t mxfp4_attention_grad_workspace_bytes(int64_t q_tokens, int64_t q_heads);
  *   dv = p^T dout,  dz = p (dout v^T - dout . out),  dq = scale dz k,  dk = scale dz^T q
  * q to scale: as given to it, out, rest and lse as returned by it; dout: the gradient of out, bf16.  rest may be NULL:
  * dout . out then carries out's rounding, and dz of a key that has most of a row's probability is off by it.
- * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  dk and dv
- * are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are rounded to bf16 for the
- * tensor cores.  No atomic additions: the same bits on every run.  Rows of other sequences and rows outside of all
- * reach nothing.  Within a sequence infinities and NaN reach what the formulas say and besides, as 0 times them, of a
+ * dq, dk, dv: bf16, overwritten (they may be slices of one buffer); rows outside of all sequences as there.  They must
+ * not overlap each other; dk and dv, which are written before dq is made from the inputs, must not overlap q, k, v or
+ * dout, nor dq k or v; dq may be q or dout itself, but not overlap them otherwise.  What the call sees of this it refuses.
+ * dk and dv are summed over the query heads that share a key head, in fp32, rounded once.  p and dz are rounded to bf16
+ * for the tensor cores.  No atomic additions: the same bits on every run.  Rows of other sequences and rows outside of
+ * all reach nothing.  Within a sequence infinities and NaN reach what the formulas say and besides, as 0 times them, of a
  * key's k or v the dq of queries up to 254 places before the first one that sees the key, and of a query's q or dout
  * the dk and dv of keys up to 254 places behind the last one that the query sees.
  * ws: device, 256-byte aligned. */

@@ -970,8 +970,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     bf16, scale 1 / sqrt(head_dim) by default.  cu_q, cu_k: int32 [sequences + 1], where each sequence starts (cu_k
     None: as cu_q); None: `seqs` sequences of equal lengths.  Returns (out, lse): out like q, lse fp32
     [q_heads, q_tokens], which attention_grad takes.  rest: returns (out, lse, rest), rest like out, what rounding left of
-    it, for exact gradients.  Tokens outside of all sequences: new outputs hold zeros there, given ones are left as they
-    were."""
+    it, for exact gradients.  out may be q itself, but must not overlap k, v or q otherwise.  Tokens outside of all
+    sequences: new outputs hold zeros there, given ones are left as they were."""
     dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)
@@ -1001,7 +1001,8 @@ def attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
                    rest: torch.Tensor | None = None, stream=None):
     """mxfp4_attention_grad: gradients (dq, dk, dv) of attention's inputs, bf16, from dout, that of its output; out, lse
     and rest as it returned them (without rest the gradients carry out's rounding), the others as it was given.  dq, dk
-    and dv may be slices of one buffer.  Tokens outside of all sequences: as in attention."""
+    and dv may be slices of one buffer, but must not overlap each other or q, k, v and dout (dq may be q or dout itself).
+    Tokens outside of all sequences: as in attention."""
     dev = _device_for(q, "q")
     wq, wk, wv, n, heads, dim, m, k_heads = _attention_operands(q, k, v, dev)
     at_q, at_k, seqs = _sequences(cu_q, cu_k, seqs, n == m, dev)

@@ -27,6 +27,7 @@
 // nothing that they hold (infinities, NaN) reaches this sequence.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <type_traits>
 
 #include "element.cuh"
@@ -1567,6 +1568,24 @@ mxfp4_status check_output(const char* what, const mxfp4_heads* out, const mxfp4_
     return MXFP4_OK;
 }
 
+struct Named {
+    const char* name;
+    const Heads* heads;
+    int64_t tokens;
+};
+// No output over an input that other CTAs still read, nor over another output.  `own`: inputs of which a CTA reads only the
+// rows that it writes itself, so that the output may be the same tensor.
+mxfp4_status check_apart(const char* what, const Named& written, std::initializer_list<Named> others,
+                         std::initializer_list<Named> own, int64_t dim) {
+    auto overlap = [&](const Named& x) { return heads_overlap(*written.heads, written.tokens, *x.heads, x.tokens, dim); };
+    for (const Named& x : others)
+        if (overlap(x)) return record_error(MXFP4_ERR_INVALID_ARG, "%s: %s overlaps %s", what, written.name, x.name);
+    for (const Named& x : own)
+        if (overlap(x) && !same_heads(*written.heads, *x.heads))
+            return record_error(MXFP4_ERR_INVALID_ARG, "%s: %s overlaps %s and is not the same tensor", what, written.name, x.name);
+    return MXFP4_OK;
+}
+
 // Places of tiles of `rows` tokens: no fewer than there are tiles.
 int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
     if (c.seq.cu_q) return tokens / rows + c.seq.count;
@@ -1652,6 +1671,10 @@ extern "C" mxfp4_status mxfp4_attention(const mxfp4_heads* q, const mxfp4_heads*
     mxfp4_status st = check_call(what, q, k, v, q_tokens, k_tokens, head_dim, cu_q, cu_k, seqs, causal, scale, zero_outside, &c);
     if (st) return st;
     if ((st = check_output(what, out, rest, true, &c))) return st;
+    const Named q_{"q", &c.q, q_tokens}, k_{"k", &c.k, k_tokens}, v_{"v", &c.v, k_tokens};
+    const Named out_{"out", &c.out, q_tokens}, rest_{"rest", &c.rest, q_tokens};
+    if ((st = check_apart(what, out_, {k_, v_, rest_}, {q_}, head_dim))) return st;
+    if ((st = check_apart(what, rest_, {k_, v_}, {q_}, head_dim))) return st;
     const bool clear = zero_outside && cu_q;  // sequences of equal lengths leave nothing out
     if (q_tokens == 0 || (seqs == 0 && !clear)) return record_error(MXFP4_OK, "%s", "");
     if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
@@ -1726,6 +1749,11 @@ extern "C" mxfp4_status mxfp4_attention_grad(const mxfp4_heads* q, const mxfp4_h
     if (d.heads != c.q.heads || gq.heads != c.q.heads || gk.heads != c.k.heads ||
         gv.heads != c.k.heads)
         return record_error(MXFP4_ERR_INVALID_ARG, "%s: dout or a gradient has other heads than its input", what);
+    const Named q_{"q", &c.q, q_tokens}, k_{"k", &c.k, k_tokens}, v_{"v", &c.v, k_tokens}, d_{"dout", &d, q_tokens};
+    const Named dq_{"dq", &gq, q_tokens}, dk_{"dk", &gk, k_tokens}, dv_{"dv", &gv, k_tokens};
+    if ((st = check_apart(what, dk_, {q_, k_, v_, d_, dq_, dv_}, {}, head_dim))) return st;
+    if ((st = check_apart(what, dv_, {q_, k_, v_, d_, dq_}, {}, head_dim))) return st;
+    if ((st = check_apart(what, dq_, {k_, v_}, {q_, d_}, head_dim))) return st;
     if (q_tokens > 0) {
         if (!lse) return record_error(MXFP4_ERR_INVALID_ARG, "%s: lse is NULL", what);
         if (reinterpret_cast<uintptr_t>(lse) % 4) return record_error(MXFP4_ERR_MISALIGNED, "%s: lse misaligned", what);

@@ -2,6 +2,9 @@
 // values (rotation, attention).
 #pragma once
 
+#include <algorithm>
+#include <cstdlib>
+
 #include "step_ops.cuh"
 
 namespace mx {
@@ -53,6 +56,32 @@ inline bool heads_aligned(const Heads& h, int64_t bytes) {
     const int64_t e = heads_esize(h.dtype);
     return reinterpret_cast<uintptr_t>(h.data) % bytes == 0 && h.token_stride * e % bytes == 0 &&
            h.head_stride * e % bytes == 0;
+}
+
+// Whether two checked tensors of one type share an element.  Exact where their token strides and their head strides are the
+// same (slices of one buffer, a tensor and itself); of others that lie in each other's range only a common start is seen.
+inline bool heads_overlap(const Heads& a, int64_t tokens_a, const Heads& b, int64_t tokens_b, int64_t dim) {
+    if (tokens_a <= 0 || tokens_b <= 0 || !a.data || !b.data) return false;
+    const int64_t size = heads_esize(a.dtype), width = dim * size;
+    auto extent = [&](const Heads& h, int64_t tokens) {  // a stride without a meaning is 0
+        return ((tokens - 1) * h.token_stride + (h.heads - 1) * h.head_stride) * size + width;
+    };
+    const int64_t at_a = (int64_t)reinterpret_cast<uintptr_t>(a.data), at_b = (int64_t)reinterpret_cast<uintptr_t>(b.data);
+    if (at_a + extent(a, tokens_a) <= at_b || at_b + extent(b, tokens_b) <= at_a) return false;
+    const int64_t token = (tokens_a > 1 ? a.token_stride : b.token_stride) * size;
+    const int64_t head = (a.heads > 1 ? a.head_stride : b.head_stride) * size;
+    if ((tokens_b > 1 && b.token_stride * size != token) || (b.heads > 1 && b.head_stride * size != head)) return at_a == at_b;
+    // Row (t, h) of b lies `by` + n * token bytes behind row (t - n, h - m) of a: the n that brings them closest.
+    for (int64_t m = 1 - a.heads; m < b.heads; ++m) {
+        const int64_t by = at_b - at_a + m * head, low = 1 - tokens_a, high = tokens_b - 1;
+        int64_t n = token > 0 ? -by / token : 0;
+        for (int64_t i = n - 1; i <= n + 1; ++i)
+            if (std::llabs(by + std::min(std::max(i, low), high) * token) < width) return true;
+    }
+    return false;
+}
+inline bool same_heads(const Heads& a, const Heads& b) {
+    return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride && a.heads == b.heads;
 }
 
 }  // namespace mx

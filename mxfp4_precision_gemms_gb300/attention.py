@@ -52,7 +52,7 @@ class QkNormRopeFunction(torch.autograd.Function):
         ctx.save_for_backward(None if q_gain is None else q3, None if k_gain is None else k3, positions, *gains)
         ctx.rope, ctx.eps, ctx.shapes = rope, eps, (q.shape, k.shape)
         ctx.types = [None if g is None else g.dtype for g in (q_gain, k_gain)]
-        return q_out.reshape(q.shape), k_out.reshape(k.shape)
+        return q_out, k_out  # not as views made here, which torch lets nobody change in place
 
     @staticmethod
     @once_differentiable
@@ -79,7 +79,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
         lead = tuple(q.shape[:-2])
         if positions is None or tuple(positions.shape) not in ((rope.axes, *lead), lead if rope.axes == 1 else None):
             raise ValueError(f"positions must be {(rope.axes, *lead) if rope.axes > 1 else lead}")
-    return QkNormRopeFunction.apply(q, k, rope, positions if rope is not None else None, q_gain, k_gain, eps)
+    q_out, k_out = QkNormRopeFunction.apply(q, k, rope, positions if rope is not None else None, q_gain, k_gain, eps)
+    return (q_out, k_out) if q.dim() == 3 else (q_out.view(q.shape), k_out.view(k.shape))
 
 
 class AttentionFunction(torch.autograd.Function):
@@ -89,7 +90,7 @@ class AttentionFunction(torch.autograd.Function):
         out, lse, rest = mx.attention(q3, k3, v3, causal=causal, scale=scale, cu_q=cu_q, cu_k=cu_k, seqs=seqs, rest=True)
         ctx.save_for_backward(q3, k3, v3, out, lse, rest, cu_q, cu_k)
         ctx.args, ctx.shapes = (causal, scale, seqs), (q.shape, k.shape)
-        return out.reshape(q.shape)
+        return out  # not as a view made here, which torch lets nobody change in place
 
     @staticmethod
     @once_differentiable
@@ -109,7 +110,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     (cu_k None: as cu_q).  bf16; q_heads a multiple of k_heads, query head h reads key head h // (q_heads // k_heads);
     head_dim a multiple of 8, at most 128; scale 1 / sqrt(head_dim) by default.
     causal: query i of Lq sees the keys j <= i + Lk - Lq, so that the last one sees all.  A query that sees none gives zeros
-    and no gradient, and so do tokens outside of all sequences.  Gradients of q, k and v; the same bits on every run."""
+    and no gradient, and so do tokens outside of all sequences.  Gradients of q, k and v; the same bits on every run.  They are made from the result, too: where
+    they are wanted, change a copy of it, not itself."""
     if q.dim() != k.dim() or k.dim() != v.dim() or q.dim() not in (3, 4):
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit together")
     seqs = 1
@@ -119,4 +121,5 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
         if not q.shape[0] == k.shape[0] == v.shape[0]:
             raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit together")
         seqs = q.shape[0]
-    return AttentionFunction.apply(q, k, v, causal, scale, cu_q, cu_k, seqs)
+    out = AttentionFunction.apply(q, k, v, causal, scale, cu_q, cu_k, seqs)
+    return out if q.dim() == 3 else out.view(q.shape)

@@ -18,7 +18,7 @@ from . import binding as mx
 
 
 class MXFP4LinearFunction(torch.autograd.Function):
-    """y = x @ w.T with x [..., K] and w [N, K] bf16 CUDA tensors (unit inner stride)."""
+    """y = x @ w.T with x [..., K] and w [N, K] bf16 CUDA tensors (unit inner stride), as [tokens, N]."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, had: int, mode: int) -> torch.Tensor:
@@ -27,7 +27,7 @@ class MXFP4LinearFunction(torch.autograd.Function):
         cfg = mx.Config(had=had, mode=mode, out_dtype=mx.OUT_BF16)
         y, xT, wT = mx.linear_fprop(x2, w.contiguous(), cfg)
         ctx.xT, ctx.wT, ctx.had, ctx.mode, ctx.lead = xT, wT, had, mode, lead
-        return y.reshape(*lead, w.shape[0])
+        return y  # not as a view made here, which torch lets nobody change in place
 
     @staticmethod
     def backward(ctx, dy: torch.Tensor):
@@ -44,4 +44,5 @@ def mxfp4_linear(x: torch.Tensor, w: torch.Tensor, had: int = mx.HAD_16, mode: i
     along the contraction (H16 by default) and quantise them to MXFP4.  The number of
     tokens (the product of x's leading dimensions) must be a multiple of 32, and so must
     K and N."""
-    return MXFP4LinearFunction.apply(x, w, had, mode)
+    y = MXFP4LinearFunction.apply(x, w, had, mode)
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])

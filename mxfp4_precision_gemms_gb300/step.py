@@ -65,7 +65,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         loss, lse = mx.linear_ce(h2, w, y, ignore_index=ignore_index, reduction=reduction)
         ctx.save_for_backward(h2, w, y, lse)
         ctx.ignore_index, ctx.reduction, ctx.shape = ignore_index, reduction, h.shape
-        return loss.reshape(targets.shape if reduction == mx.REDUCE_NONE else ())
+        return loss  # not as a view made here, which torch lets nobody change in place
 
     @staticmethod
     @once_differentiable
@@ -92,7 +92,9 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     # in another shape of as many elements (a batch laid out the other way) targets would be other tokens'
     if targets.shape != h.shape[:-1] and targets.dim() != 1 and h.dim() != 2:
         raise ValueError(f"targets {tuple(targets.shape)} do not fit h {tuple(h.shape)}")
-    return LinearCrossEntropyFunction.apply(h, w, targets, ignore_index, _REDUCTIONS[reduction])
+    loss = LinearCrossEntropyFunction.apply(h, w, targets, ignore_index, _REDUCTIONS[reduction])
+    shape = targets.shape if reduction == "none" else ()
+    return loss if loss.shape == shape else loss.view(shape)
 
 
 @torch.no_grad()

@@ -53,3 +53,43 @@ def test_attention(batched):
     grad, leaf.grad = leaf.grad, None
     (attention(leaf, k, v) * 2).sum().backward()
     assert torch.equal(grad, leaf.grad)
+
+
+@pytest.mark.parametrize("lead", [(64,), (2, 32)], ids=str)
+def test_linear(lead):
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.linear import mxfp4_linear
+
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(*lead, 128, device="cuda", generator=g).bfloat16()
+    w = torch.randn(96, 128, device="cuda", generator=g).bfloat16()
+    grads = []
+    for in_place in (True, False):
+        leaves = [t.clone().requires_grad_() for t in (x, w)]
+        y = mxfp4_linear(*leaves)
+        y = y.add_(1) if in_place else y + 1
+        assert y.shape == (*lead, 96)
+        y.square().sum().backward()
+        grads.append((y, *(t.grad for t in leaves)))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_loss(reduction):
+    """Divided by the number of micro-batches, say."""
+    torch = gpu_ready()
+    from mxfp4_precision_gemms_gb300.step import linear_cross_entropy
+
+    g = torch.Generator(device="cuda").manual_seed(4)
+    h = torch.randn(2, 24, 64, device="cuda", generator=g).bfloat16()
+    w = (torch.randn(200, 64, device="cuda", generator=g) / 8).bfloat16()
+    targets = torch.randint(0, 200, (2, 24), device="cuda", generator=g)
+    grads = []
+    for in_place in (True, False):
+        leaves = [t.clone().requires_grad_() for t in (h, w)]
+        loss = linear_cross_entropy(*leaves, targets, reduction=reduction)
+        loss = loss.div_(4) if in_place else loss / 4
+        assert loss.shape == (targets.shape if reduction == "none" else ())
+        loss.sum().backward()
+        grads.append((loss, *(t.grad for t in leaves)))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))

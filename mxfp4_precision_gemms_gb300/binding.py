@@ -777,6 +777,9 @@ class Rope:
                        len(self.freq), int(interleaved))
         self.ref = ctypes.addressof(self.c)
 
+    def __reduce__(self):  # copies and pickles are laid out anew: the descriptor's addresses are this object's
+        return Rope, (self.freq, self.axis, self.interleaved)
+
 
 def _device_for(x: torch.Tensor, name: str) -> int:
     """The current device, for a call whose first tensor is x (there may be none for one on the host)."""

@@ -776,6 +776,8 @@ class Rope:
         self.c = RopeC(self.freq.buffer_info()[0], None if self.axis is None else self.axis.buffer_info()[0],
                        len(self.freq), int(interleaved))
         self.ref = ctypes.addressof(self.c)
+        # arrays that are looked at cannot be resized, so that the addresses stay theirs
+        self._held = memoryview(self.freq), None if self.axis is None else memoryview(self.axis)
 
     def __reduce__(self):  # copies and pickles are laid out anew: the descriptor's addresses are this object's
         return Rope, (self.freq, self.axis, self.interleaved)

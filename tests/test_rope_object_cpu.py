@@ -43,3 +43,13 @@ def test_a_module_that_holds_one():
     other = copy.deepcopy(block)
     del block
     assert _read(other.rope) == ([1.0, 0.5], None, 2, 0)
+
+
+def test_its_arrays_stay_where_they_are():
+    """The library reads them at their addresses: they take new numbers, but no other length."""
+    rope = mx.Rope([1.0, 0.5], axis=[0, 1])
+    for change in (lambda: rope.freq.extend([0.0] * 100000), lambda: rope.axis.append(0), lambda: rope.freq.pop()):
+        with pytest.raises(BufferError):
+            change()
+    rope.freq[1] = 0.25
+    assert _read(rope) == ([1.0, 0.25], [0, 1], 2, 0)

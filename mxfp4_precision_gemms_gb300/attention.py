@@ -51,7 +51,7 @@ class QkNormRopeFunction(torch.autograd.Function):
         q_out, k_out = mx.qk_norm_rope(q3, k3, rope, positions, *gains, eps=eps)
         ctx.save_for_backward(None if q_gain is None else q3, None if k_gain is None else k3, positions, *gains)
         ctx.rope, ctx.eps, ctx.shapes = rope, eps, (q.shape, k.shape)
-        ctx.types = [None if g is None else g.dtype for g in (q_gain, k_gain)]
+        ctx.gains = [None if g is None else (g.dtype, g.shape) for g in (q_gain, k_gain)]
         return q_out, k_out  # not as views made here, which torch lets nobody change in place
 
     @staticmethod
@@ -61,7 +61,7 @@ class QkNormRopeFunction(torch.autograd.Function):
         dq, dk = _rows(dq, "dq", dq.element_size()), _rows(dk, "dk", dk.element_size())
         dq, dk, *gains = mx.qk_norm_rope_grad(q, k, dq, dk, ctx.rope, positions, q_gain, k_gain, eps=ctx.eps,
                                               gains=any(ctx.needs_input_grad[4:6]))
-        dq_gain, dk_gain = (None if g is None else g.to(t) for g, t in zip(gains, ctx.types))
+        dq_gain, dk_gain = (None if g is None else g.to(kind[0]).view(kind[1]) for g, kind in zip(gains, ctx.gains))
         return dq.reshape(ctx.shapes[0]), dk.reshape(ctx.shapes[1]), None, None, dq_gain, dk_gain, None
 
 
@@ -70,9 +70,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
                  eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
     """Each head of q and k divided by its root mean square and multiplied by its gain ([head_dim]; None: left as it is),
     then rotated.  q and k: [tokens, heads, head_dim] or [batch, length, heads, head_dim], fp32 or bf16 both; head_dim even,
-    at most 256.  `rope`: Rope(frequencies, axis of each pair, interleaved) or None; positions: int32 or int64 of q's
-    leading shape, behind a dimension of rope.axes (which may be left out where that is 1).  Gradients of q, k and the gains;
-    sums in fp32, the same bits on every run."""
+    at most 256; gains of head_dim elements in any shape.  `rope`: Rope(frequencies, axis of each pair, interleaved) or
+    None; positions: int32 or int64 of q's leading shape, behind a dimension of rope.axes (which may be left out where
+    that is 1).  Gradients of q, k and the gains; sums in fp32, the same bits on every run."""
     if q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2]:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not fit together")
     if rope is not None:

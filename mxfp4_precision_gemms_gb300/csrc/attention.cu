@@ -169,9 +169,9 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 constexpr int32_t kScanned = 64;
 
 // Place `slot` among the tiles of more than kScanned sequences.  A list that falls may lead to any of them, but to no tile that
-// the sequence has not.
+// the sequence has not.  Not inlined: beside the loop of dkv and dq it cost calls of few sequences 0.5%.
 template <bool KEYS>
-__device__ __forceinline__ Place search_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
+__device__ __noinline__ Place search_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
     const int lane = threadIdx.x & 31;
     for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < s.count; i += (int64_t)gridDim.x * 32) {
         int32_t first, len;
@@ -744,17 +744,18 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
             if (ok) {
                 tc_fence_after();
                 const int cut = (p.dim / 2 + 15) / 16 * 16, from = half ? cut : 0, width = half ? p.dim - cut : min(cut, p.dim);
-                if (p.chunk > 0) {
+                if (p.chunk > 0)
                     store_part(acc + from, width, p.part + (((int64_t)blockIdx.x * 2 + t) * kRows + r) * p.dim + from, inside);
-                } else {
-                    // A row without weight is zeros, not 0 times sums that hidden keys may have made infinite or NaN.
-                    const bool weight = sum != 0.f;
-                    bf16* to = p.out.at(at.q0 + row, head) + from;
-                    bf16* left = p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr;
-                    store_rows(acc + from, width, 1.f / kept, to, inside && weight, left);
-                    if (inside && !weight) {
-                        store_zeros(width, to);
-                        if (left) store_zeros(width, left);
+                else
+                    store_rows(acc + from, width, sum == 0.f ? 0.f : 1.f / kept, p.out.at(at.q0 + row, head) + from, inside,
+                              p.rest.data ? p.rest.at(at.q0 + row, head) + from : nullptr);
+                // A row without weight is zeros, not 0 times sums that hidden keys may have made infinite or NaN.
+                const bool none = inside && sum == 0.f && p.chunk == 0;
+                if (__any_sync(0xffffffffu, none)) {  // over what other lanes have just written
+                    __syncwarp();
+                    if (none) {
+                        store_zeros(width, p.out.at(at.q0 + row, head) + from);
+                        if (p.rest.data) store_zeros(width, p.rest.at(at.q0 + row, head) + from);
                     }
                 }
             }

@@ -78,10 +78,6 @@ template <class T, int VEC>
 __device__ __forceinline__ void load_run(const T* p, Run<T, VEC>& r) {
     if constexpr (sizeof(T) == 2 && VEC >= 4) {
         r.w = *reinterpret_cast<const decltype(r.w)*>(p);
-    } else if constexpr (VEC == 8) {
-        const Raw8<float> u = load8(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i] = u.v[i];
     } else if constexpr (VEC == 4) {
         load4(p, r.v);
     } else {

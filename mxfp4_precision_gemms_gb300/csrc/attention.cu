@@ -164,9 +164,9 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 // more, sequence i's tiles begin at place first / rows + i, which leaves room for all of each: the sequence is then found
 // without those before it, in steps that leave a 32nd of them (at most five), where counting would take each CTA a time
 // that grows with the sequences, and the call one that grows with their square.  The list is looked through by all CTAs
-// together.  8192 tokens of 32 and 8 heads of 128, forward and backward, searched and counted: 64 sequences 88.0 / 218 and
-// 86.2 / 215 us, 128 100.5 / 236 and 103.9 / 243, 1024 392 / 738 and 733 / 1385, 4096 1.50 / 2.72 and 6.28 / 11.4 ms.
-constexpr int32_t kScanned = 64;
+// together.  8192 tokens of 32 and 8 heads of 128, forward and backward, searched and counted: 64 sequences 90.3 / 223 and
+// 86.2 / 215 us, 128 104.1 / 242 and 104.7 / 243, 1024 404 / 749 and 735 / 1383, 4096 1.54 / 2.74 and 6.28 / 11.4 ms.
+constexpr int32_t kScanned = 128;
 
 // Place `slot` among the tiles of more than kScanned sequences.  A list that falls may lead to any of them, but to no tile that
 // the sequence has not.  Not inlined: beside the loop of dkv and dq it cost calls of few sequences 0.5%.

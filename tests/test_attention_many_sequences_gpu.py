@@ -17,7 +17,7 @@ def _all(torch, q, k, v, do, **kw):
     return (out, lse.t(), rest, dq), (dk, dv)
 
 
-@pytest.mark.parametrize("count", [63, 64, 65, 1000, 1025])
+@pytest.mark.parametrize("count", [64, 127, 128, 129, 1000, 1025])
 @pytest.mark.parametrize("causal", [True, False])
 def test_as_in_batches_of_thirty(count, causal):
     torch = gpu_ready()

@@ -164,14 +164,14 @@ __device__ __forceinline__ void range_of(const int32_t* cu, int32_t i, int32_t t
 // more, sequence i's tiles begin at place first / rows + i, which leaves room for all of each: the sequence is then found
 // without those before it, in steps that leave a 32nd of them (at most five), where counting would take each CTA a time
 // that grows with the sequences, and the call one that grows with their square.  The list is looked through by all CTAs
-// together.  8192 tokens of 32 and 8 heads of 128, forward and backward, searched and counted: 64 sequences 90.3 / 223 and
-// 86.2 / 215 us, 128 104.1 / 242 and 104.7 / 243, 1024 404 / 749 and 735 / 1383, 4096 1.54 / 2.74 and 6.28 / 11.4 ms.
+// together.  8192 tokens of 32 and 8 heads of 128, forward and backward, searched and counted: 64 sequences 88.3 / 223 and
+// 86.2 / 214 us, 128 100.6 / 242 and 104.7 / 242, 1024 395 / 748 and 735 / 1383, 4096 1.51 / 2.74 and 6.28 / 11.4 ms.
 constexpr int32_t kScanned = 128;
 
 // Place `slot` among the tiles of more than kScanned sequences.  A list that falls may lead to any of them, but to no tile that
-// the sequence has not.  Not inlined: beside the loop of dkv and dq it cost calls of few sequences 0.5%.
+// the sequence has not.
 template <bool KEYS>
-__device__ __noinline__ Place search_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
+__device__ __forceinline__ Place search_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
     const int lane = threadIdx.x & 31;
     for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < s.count; i += (int64_t)gridDim.x * 32) {
         int32_t first, len;
@@ -198,9 +198,17 @@ __device__ __noinline__ Place search_place(const Sequences& s, int32_t slot, int
     return p;
 }
 
-// The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
-// (and then few sequences) among their parts of that many keys.  By one warp.
 template <bool KEYS>
+__device__ __noinline__ Place call_search_place(const Sequences& s, int32_t slot, int32_t rows, uint32_t* status) {
+    return search_place<KEYS>(s, slot, rows, status);
+}
+
+// The sequence and tile (of `rows` queries, or keys) of place `slot` among the tiles of all sequences; with `chunk` above 0
+// (and then few sequences) among their parts of that many keys.  By one warp.  How the search is reached matters to calls that
+// do not need it: inlined it costs dkv and dq 0.5% of a batch of 13 sequences, as a call the forward pass up to 3% of 8 new
+// tokens over 24018 keys.
+enum class Search { kNone, kInline, kCall };
+template <bool KEYS, Search HOW>
 __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, int32_t rows, int32_t chunk, uint32_t* status) {
     Place p{};
     p.tile = -1;
@@ -214,7 +222,8 @@ __device__ __forceinline__ Place find_place(const Sequences& s, int32_t slot, in
         p.part = slot - i * places - p.tile * p.parts;
         return p;
     }
-    if (s.count > kScanned && chunk == 0) return search_place<KEYS>(s, slot, rows, status);
+    if (HOW != Search::kNone && s.count > kScanned && chunk == 0)
+        return HOW == Search::kInline ? search_place<KEYS>(s, slot, rows, status) : call_search_place<KEYS>(s, slot, rows, status);
     const int lane = threadIdx.x & 31;
     int32_t before = 0;
     for (int32_t i0 = 0; i0 < s.count; i0 += 32) {
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) attention_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false, Search::kInline>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -791,7 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
+        const Place w = find_place<false, Search::kNone>(p.seq, slot, 2 * tokens, p.chunk * kRows, p.status);
         if (lane == 0) where = w;
     }
     __syncthreads();
@@ -996,7 +1005,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) attention_dkv_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<true>(p.seq, slot, kRows, 0, p.status);
+        const Place w = find_place<true, Search::kCall>(p.seq, slot, kRows, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();
@@ -1334,7 +1343,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) attention_dq_kernel(const __gri
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
-        const Place w = find_place<false>(p.seq, slot, tokens, 0, p.status);
+        const Place w = find_place<false, Search::kCall>(p.seq, slot, tokens, 0, p.status);
         if (lane == 0) *where = w;
     }
     tc_fence_before();

@@ -572,7 +572,7 @@ size_t mxfp4_attention_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64
  * Sequences: cu_q and cu_k are device int32 [seqs + 1], the first token of each sequence and the end of the
  * last; both NULL: `seqs` sequences of equal lengths.  A list that falls or points behind the tensors is cut to
  * them, and reported by mxfp4_device_status as MXFP4_ERR_INVALID_ARG.  Any lengths, 0 among them, and those of
- * queries and keys may differ.
+ * queries and keys may differ: room between the texts of a cache is a sequence of keys without queries.
  * causal 1: query i of a sequence of Lq queries and Lk keys sees keys j <= i + Lk - Lq (the last query sees all).
  * A query that sees no key, or whose scores are all -infinity, gets an out of 0 and an lse of -infinity, and no
  * gradient, whatever hidden keys hold; a score of +infinity or NaN makes its out and its lse NaN.

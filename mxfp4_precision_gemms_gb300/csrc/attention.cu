@@ -17,14 +17,16 @@
 // Long sequences are bound by the products, whose operands take all of shared memory's bandwidth (8192 tokens of 32 and 8
 // heads of 128, causal: forward 0.55 TFLOP in 358 us, 321 with no softmax; backward seven products, 1.92 TFLOP, in 1170),
 // heads of 64 or less by the softmax's instructions between them, few queries by reading the keys and values, short
-// sequences by the steps that wait for each other.
+// sequences by a CTA's start and end, which take as long as six tiles of keys (8192 tokens, not causal, in 1024 CTAs with 1, 2,
+// 4, 8 and 16 tiles each: 70, 77, 95, 134 and 211 us).
 // The scores are made a second time for dq: two products more than a single pass over (keys, queries) would need, which
 // would have to add to dq in memory, in an order that differs from run to run.
 //
 // Operand tiles are 128 rows (tokens) x 64 or 128 columns in shared memory, in blocks of 64 columns, 128-byte rows,
 // 128-byte swizzle: the same tile is read along its columns (q and k of z) or along its rows (v of p v).  A tile reaches
 // past the end of its sequence into the next one's rows; where such rows are summed over they are cleared first, so that
-// nothing that they hold (infinities, NaN) reaches this sequence.
+// nothing that they hold (infinities, NaN) reaches this sequence.  Keys of the sequence that are hidden from a query are
+// summed over with p = 0, as far as its tile goes: what they reach is said at the entry points.
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
@@ -1644,7 +1646,7 @@ int64_t places(const Call& c, int64_t tokens, int32_t len, int rows) {
 // Whether the keys of a pair of query tiles are shared out over several CTAs: where the pairs leave more than half of the SMs
 // without one, sequences have eight key tiles or more on the average, and a CTA has at least kSaved tiles fewer to go through
 // (few rows) or kSavedMany (many, whose parts take longer to join).  A part is `chunk` key tiles, so many that there is a part
-// for each SM at most (a CTA's start and end cost as much as some five key tiles), but four at least.
+// for each SM at most (a CTA's start and end cost as much as some six key tiles), but four at least.
 // 32 and 8 heads of 128, shared out and not: 1 query over 1024 keys 16.5 and 18.6 us, 2048 16.6 and 27.9, 32768 41 and 329;
 // 4 sequences of 4096 24.7 and 47.6; 64 queries over 1024 keys 22.8 and 20.6 (4 tiles fewer), 2048 22.7 and 30.9 (12);
 // 256 queries over 1024 26.9 and 20.6, 4096 43.3 and 53.5 (16).
